@@ -440,6 +440,114 @@ ssd_status ssd_decode_graph_create(const ssd_dims *dims, int64_t conv_width, int
 ssd_status ssd_decode_graph_launch(ssd_decode_graph *graph, cudaStream_t stream);
 ssd_status ssd_decode_graph_destroy(ssd_decode_graph *graph);
 
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: a scan whose state is corrected along the key before it is
+ * written. Per batch b and head h, q and k of group i = h / (nheads/ngroups),
+ * state S [P, N] (P = headdim, N = dstate), a_t = exp(g_t):
+ *
+ *     u_t = beta_t (v_t - a_t S_{t-1} k_t)
+ *     S_t = a_t S_{t-1} + u_t k_t^T
+ *     y_t = scale * S_t q_t
+ *
+ * g is the logarithm of the decay (normally <= 0) and beta the step towards v
+ * (normally in [0, 1]); q and k are used as given (rows of norm 1 keep the
+ * update a contraction). States and all sums are float32.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The rule over a whole sequence.
+ *   q, k       [B, L, G, N]  io_dtype
+ *   v          [B, L, H, P]  io_dtype
+ *   g, beta    [B, L, H]     io_dtype
+ *   init_state [B, H, P, N]  float32, may be NULL (zero)
+ *   seqlens    [B]           int32 on the device, may be NULL (L for every b):
+ *              sequence b is its first seqlens[b] tokens (values outside
+ *              [0, L] are brought into it). What q, k, v, g and beta hold past
+ *              them is not used, y is zero there.
+ *   scale      finite
+ *   y          [B, L, H, P]  io_dtype, written
+ *   final_state[B, H, P, N]  float32, the state after the last token of each
+ *              sequence; may be NULL, may be the same buffer as init_state
+ *   workspace  ssd_gated_delta_workspace_size(dims) bytes, 256-byte aligned;
+ *              its status word is read by ssd_workspace_status
+ * dims->flags: SSD_FLAG_SIMT keeps bf16 inputs on the CUDA cores. Limits:
+ * dstate <= 256, headdim <= 65535, batch * seqlen < 2^31.
+ */
+size_t ssd_gated_delta_workspace_size(const ssd_dims *dims);
+ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const void *k, const void *v, const void *g,
+                                   const void *beta, const float *init_state, const int32_t *seqlens, float scale,
+                                   void *y, float *final_state, void *workspace, size_t ws_bytes,
+                                   cudaStream_t stream);
+
+/*
+ * Backward of ssd_gated_delta_chunked: the gradients of
+ *     <dy, y> + <dfinal_state, final_state>
+ * with respect to every input, the states recomputed from the inputs.
+ * Deterministic (fixed-order sums, no atomics).
+ *   dy           [B, L, H, P]  io_dtype     dfinal_state [B, H, P, N] float32, may be NULL (0)
+ *   dq, dk       [B, L, G, N]  io_dtype, sums over the heads of each group
+ *   dv           [B, L, H, P]  io_dtype     dg, dbeta    [B, L, H]    io_dtype
+ *   dinit_state  [B, H, P, N]  float32, may be NULL (not written)
+ *   workspace    ssd_gated_delta_chunked_bwd_workspace_size(dims) bytes, 256-byte aligned
+ * Gradients past a sequence's length are zero. The other arguments and limits
+ * as for ssd_gated_delta_chunked.
+ */
+size_t ssd_gated_delta_chunked_bwd_workspace_size(const ssd_dims *dims);
+ssd_status ssd_gated_delta_chunked_bwd(const ssd_dims *dims, const void *q, const void *k, const void *v,
+                                       const void *g, const void *beta, const float *init_state,
+                                       const int32_t *seqlens, float scale, const void *dy,
+                                       const float *dfinal_state, void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                                       float *dinit_state, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * One token of the rule for a batch of sequences whose states lie in a pool.
+ *   state      [nslots, H, P, N] float32
+ *   q, k [B, G, N], v [B, H, P], g, beta [B, H]  io_dtype
+ *   slots      [B] int32 on the device, may be NULL (row b uses state b, and
+ *              nslots >= batch): row b uses state slots[b]. A value outside
+ *              [0, nslots) marks an idle row: its y is zero and no state is
+ *              touched. Two rows of one call must not name the same state.
+ *   new_state  [nslots, H, P, N] float32, the new states, written at the same
+ *              slots; may be the same buffer as state (update in place)
+ *   y          [B, H, P] io_dtype, written
+ * dims->seqlen is ignored. Limit: dstate <= 256.
+ */
+ssd_status ssd_gated_delta_step(const ssd_dims *dims, int64_t nslots, const float *state, const void *q,
+                                const void *k, const void *v, const void *g, const void *beta, const int32_t *slots,
+                                float scale, float *new_state, void *y, cudaStream_t stream);
+
+/*
+ * Block norm: the gate, the norm after a block, the scaled residual addition
+ * and the norm before the next block, per row of dim channels:
+ *     u = y * silu(z)                                   (z NULL: u = y)
+ *     n = u / sqrt(mean u^2 + eps) * post_weight        (post_weight NULL: n = u)
+ *     res_out = res + scale * n                         (scale NULL: 1)
+ *     out = res_out / sqrt(mean res_out^2 + eps) * pre_weight
+ * out is formed from the unrounded res_out.
+ *   y, z, out    [rows, dim]  io_dtype (out may alias y or z)
+ *   res, res_out [rows, dim]  res_dtype: SSD_F32 or io_dtype (res_out may alias res)
+ *   post_weight, scale, pre_weight [dim] float32
+ * Limits: dim <= 16384, eps >= 0.
+ */
+ssd_status ssd_block_norm(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype, const void *y,
+                          const void *res, const void *z, const float *post_weight, const float *scale,
+                          const float *pre_weight, float eps, void *out, void *res_out, cudaStream_t stream);
+
+/*
+ * Backward of ssd_block_norm from its inputs (no saved statistics).
+ *   dout [rows, dim] io_dtype      dres_out [rows, dim] res_dtype, may be NULL (0)
+ *   dy, dz [rows, dim] io_dtype (dz only with z)      dres [rows, dim] res_dtype
+ *   dpre_weight, dpost_weight (with post_weight), dscale (with scale) [dim] float32
+ *   workspace  ssd_block_norm_bwd_workspace_size(...) bytes, 256-byte aligned
+ * The outputs may not alias the inputs. Deterministic (fixed-order sums).
+ */
+size_t ssd_block_norm_bwd_workspace_size(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype);
+ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype, const void *y,
+                              const void *res, const void *z, const float *post_weight, const float *scale,
+                              const float *pre_weight, float eps, const void *dout, const void *dres_out, void *dy,
+                              void *dz, void *dres, float *dpre_weight, float *dpost_weight, float *dscale,
+                              void *workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* Thread-local description of the last error returned on this thread. */
 const char *ssd_last_error(void);
 

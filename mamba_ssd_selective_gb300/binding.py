@@ -10,6 +10,7 @@ not been built, or does not load, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -85,6 +86,20 @@ def load() -> ctypes.CDLL:
             lib.ssd_decode_graph_destroy.argtypes = [vp]
             for f in (lib.ssd_conv1d_step, lib.ssd_gated_rmsnorm, lib.ssd_decode_layer_step,
                       lib.ssd_decode_graph_create, lib.ssd_decode_graph_launch, lib.ssd_decode_graph_destroy):
+                f.restype = ctypes.c_int
+            lib.ssd_gated_delta_workspace_size.argtypes = [dp]
+            lib.ssd_gated_delta_workspace_size.restype = sz
+            lib.ssd_gated_delta_chunked.argtypes = [dp] + [vp] * 7 + [f32, vp, vp, vp, sz, vp]
+            lib.ssd_gated_delta_chunked_bwd_workspace_size.argtypes = [dp]
+            lib.ssd_gated_delta_chunked_bwd_workspace_size.restype = sz
+            lib.ssd_gated_delta_chunked_bwd.argtypes = [dp] + [vp] * 7 + [f32] + [vp] * 9 + [sz, vp]
+            lib.ssd_gated_delta_step.argtypes = [dp, i64] + [vp] * 7 + [f32, vp, vp, vp]
+            lib.ssd_block_norm.argtypes = [i64, i64, i32, i32] + [vp] * 6 + [f32, vp, vp, vp]
+            lib.ssd_block_norm_bwd_workspace_size.argtypes = [i64, i64, i32, i32]
+            lib.ssd_block_norm_bwd_workspace_size.restype = sz
+            lib.ssd_block_norm_bwd.argtypes = [i64, i64, i32, i32] + [vp] * 6 + [f32] + [vp] * 9 + [sz, vp]
+            for f in (lib.ssd_gated_delta_chunked, lib.ssd_gated_delta_chunked_bwd, lib.ssd_gated_delta_step,
+                      lib.ssd_block_norm, lib.ssd_block_norm_bwd):
                 f.restype = ctypes.c_int
             lib.ssd_scan_chunked.argtypes = [dp] + [vp] * 7 + [ctypes.c_int, vp, vp, vp, sz, vp]
             lib.ssd_scan_chunked_noalloc.argtypes = [dp] + [vp] * 7 + [ctypes.c_int, vp, vp, vp]
@@ -523,3 +538,167 @@ class DecodeGraph:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------- gated delta rule
+
+def _delta_sizes(q, k, v, g, beta, lead):
+    """Checks the token tensors of a delta-rule call (leading dimensions `lead`); returns H, G, P, N."""
+    if q.dim() != len(lead) + 2 or v.dim() != len(lead) + 2:
+        raise ValueError("q, k must be [..., G, N] and v [..., H, P]")
+    dev, io = v.device, v.dtype
+    G, N = q.shape[-2:]
+    H, P = v.shape[-2:]
+    _need(q, "q", (*lead, G, N), io, dev)
+    _need(k, "k", (*lead, G, N), io, dev)
+    _need(v, "v", (*lead, H, P), io, dev)
+    _need(g, "g", (*lead, H), io, dev)
+    _need(beta, "beta", (*lead, H), io, dev)
+    return H, G, P, N
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, device)
+    return workspace
+
+
+def gated_delta_chunked(q, k, v, g, beta, init_state=None, seqlens=None, scale=None, y=None, final_state=None,
+                        workspace=None, stream=None, want_final_state=True, simt=False):
+    """The gated delta rule over a sequence: with a_t = exp(g_t), per head,
+    S_t = a_t S_{t-1} + beta_t (v_t - a_t S_{t-1} k_t) k_t^T and y_t = scale S_t q_t.
+    q/k[B,L,G,N], v[B,L,H,P], g/beta[B,L,H] (float32 or bfloat16; head h reads
+    group h // (H // G)), init_state[B,H,P,N] (float32). seqlens[B] (int32, on
+    the device) are the tokens of right-padded sequences; y is zero past them.
+    scale defaults to 1/sqrt(N). simt=True keeps bf16 inputs on the CUDA cores.
+    Returns (y[B,L,H,P], final_state[B,H,P,N])."""
+    Bsz, L = v.shape[:2]
+    H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz, L))
+    dev, io = v.device, v.dtype
+    _need(init_state, "init_state", (Bsz, H, P, N), torch.float32, dev)
+    _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
+    d = _dims(Bsz, L, H, P, N, G, _io_code(io), SSD_FLAG_SIMT if simt else 0)
+    if y is None:
+        y = torch.empty_like(v)
+    _need(y, "y", (Bsz, L, H, P), io, dev)
+    if final_state is None and want_final_state:
+        final_state = torch.empty((Bsz, H, P, N), dtype=torch.float32, device=dev)
+    _need(final_state, "final_state", (Bsz, H, P, N), torch.float32, dev)
+    lib = load()
+    workspace = _workspace(workspace, int(lib.ssd_gated_delta_workspace_size(ctypes.byref(d))), dev)
+    _check(lib.ssd_gated_delta_chunked(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                       _ptr(init_state), _ptr(seqlens), 1.0 / math.sqrt(N) if scale is None else scale,
+                                       _ptr(y), _ptr(final_state), _ptr(workspace), workspace.numel(),
+                                       _stream(stream, dev)))
+    return y, final_state
+
+
+def gated_delta_chunked_bwd(q, k, v, g, beta, dy, init_state=None, dfinal_state=None, seqlens=None, scale=None,
+                            workspace=None, stream=None, want_dinit=True, simt=False):
+    """Gradients of <dy, y> + <dfinal_state, final_state> for the inputs of
+    gated_delta_chunked. Returns a dict of dq, dk, dv, dg, dbeta (the inputs'
+    type) and dinit (float32; None unless want_dinit)."""
+    Bsz, L = v.shape[:2]
+    H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz, L))
+    dev, io = v.device, v.dtype
+    _need(dy, "dy", (Bsz, L, H, P), io, dev)
+    _need(init_state, "init_state", (Bsz, H, P, N), torch.float32, dev)
+    _need(dfinal_state, "dfinal_state", (Bsz, H, P, N), torch.float32, dev)
+    _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
+    d = _dims(Bsz, L, H, P, N, G, _io_code(io), SSD_FLAG_SIMT if simt else 0)
+    out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), dg=torch.empty_like(g),
+               dbeta=torch.empty_like(beta),
+               dinit=torch.empty((Bsz, H, P, N), dtype=torch.float32, device=dev) if want_dinit else None)
+    lib = load()
+    workspace = _workspace(workspace, int(lib.ssd_gated_delta_chunked_bwd_workspace_size(ctypes.byref(d))), dev)
+    _check(lib.ssd_gated_delta_chunked_bwd(
+        ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(init_state), _ptr(seqlens),
+        1.0 / math.sqrt(N) if scale is None else scale, _ptr(dy), _ptr(dfinal_state), _ptr(out["dq"]), _ptr(out["dk"]),
+        _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out["dinit"]), _ptr(workspace), workspace.numel(),
+        _stream(stream, dev)))
+    return out
+
+
+def gated_delta_step(state, q, k, v, g, beta, slots=None, new_state=None, scale=None, y=None, stream=None):
+    """One token of the gated delta rule. state[S,H,P,N] (float32) is a pool of
+    states, updated in place or written to new_state; q/k[B,G,N], v[B,H,P],
+    g/beta[B,H]. Row b uses state slots[b] (int32, on the device; a value
+    outside the pool marks an idle row: y is zero, no state is touched), or
+    state b without slots. Returns y[B,H,P]."""
+    Bsz = v.shape[0]
+    H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz,))
+    dev, io = v.device, v.dtype
+    S = state.shape[0]
+    _need(state, "state", (S, H, P, N), torch.float32, dev)
+    _need(slots, "slots", (Bsz,), torch.int32, dev)
+    if slots is None and S < Bsz:
+        raise ValueError(f"state holds {S} states for {Bsz} rows")
+    if new_state is None:
+        new_state = state
+    _need(new_state, "new_state", (S, H, P, N), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(v)
+    _need(y, "y", (Bsz, H, P), io, dev)
+    d = _dims(Bsz, 1, H, P, N, G, _io_code(io))
+    _check(load().ssd_gated_delta_step(ctypes.byref(d), S, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                       _ptr(slots), 1.0 / math.sqrt(N) if scale is None else scale, _ptr(new_state),
+                                       _ptr(y), _stream(stream, dev)))
+    return y
+
+
+# ---------------------------------------------------------------- block norm
+
+def _norm_args(y, res, pre_weight, post_weight, z, scale):
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, dim]")
+    R, D = y.shape
+    dev, io = y.device, y.dtype
+    if res.dtype not in (io, torch.float32):
+        raise TypeError(f"res: expected dtype {io} or torch.float32, got {res.dtype}")
+    _need(y, "y", (R, D), io, dev)
+    _need(res, "res", (R, D), res.dtype, dev)
+    _need(z, "z", (R, D), io, dev)
+    for w, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight"), (scale, "scale")):
+        _need(w, name, (D,), torch.float32, dev)
+    return R, D, _io_code(io), _io_code(res.dtype)
+
+
+def block_norm(y, res, pre_weight, post_weight=None, z=None, scale=None, eps=1e-5, out=None, res_out=None,
+               stream=None):
+    """What stands between two blocks, per row: u = y silu(z), n = u / sqrt(mean
+    u^2 + eps) post_weight, res_out = res + scale n, out = res_out / sqrt(mean
+    res_out^2 + eps) pre_weight; without z, post_weight or scale that factor (and
+    its norm) is left out. y/z[rows, dim] float32 or bfloat16, res of the same
+    type or float32, weights and scale [dim] float32. Returns (out, res_out)."""
+    R, D, io, rio = _norm_args(y, res, pre_weight, post_weight, z, scale)
+    if out is None:
+        out = torch.empty_like(y)
+    if res_out is None:
+        res_out = torch.empty_like(res)
+    _need(out, "out", (R, D), y.dtype, y.device)
+    _need(res_out, "res_out", (R, D), res.dtype, y.device)
+    _check(load().ssd_block_norm(R, D, io, rio, _ptr(y), _ptr(res), _ptr(z), _ptr(post_weight), _ptr(scale),
+                                 _ptr(pre_weight), float(eps), _ptr(out), _ptr(res_out), _stream(stream, y.device)))
+    return out, res_out
+
+
+def block_norm_bwd(y, res, dout, pre_weight, dres_out=None, post_weight=None, z=None, scale=None, eps=1e-5,
+                   workspace=None, stream=None):
+    """Gradients of <dout, out> + <dres_out, res_out> for block_norm's inputs.
+    Returns a dict of dy, dz (y's type), dres (res's type), dpre_weight,
+    dpost_weight and dscale (float32); None for an input that was not given."""
+    R, D, io, rio = _norm_args(y, res, pre_weight, post_weight, z, scale)
+    dev = y.device
+    _need(dout, "dout", (R, D), y.dtype, dev)
+    _need(dres_out, "dres_out", (R, D), res.dtype, dev)
+    w = lambda on: torch.empty(D, dtype=torch.float32, device=dev) if on is not None else None  # noqa: E731
+    g = dict(dy=torch.empty_like(y), dz=None if z is None else torch.empty_like(y), dres=torch.empty_like(res),
+             dpre_weight=w(pre_weight), dpost_weight=w(post_weight), dscale=w(scale))
+    lib = load()
+    workspace = _workspace(workspace, int(lib.ssd_block_norm_bwd_workspace_size(R, D, io, rio)), dev)
+    _check(lib.ssd_block_norm_bwd(R, D, io, rio, _ptr(y), _ptr(res), _ptr(z), _ptr(post_weight), _ptr(scale),
+                                  _ptr(pre_weight), float(eps), _ptr(dout), _ptr(dres_out), _ptr(g["dy"]),
+                                  _ptr(g["dz"]), _ptr(g["dres"]), _ptr(g["dpre_weight"]), _ptr(g["dpost_weight"]),
+                                  _ptr(g["dscale"]), _ptr(workspace), workspace.numel(), _stream(stream, dev)))
+    return g

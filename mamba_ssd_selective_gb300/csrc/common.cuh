@@ -73,6 +73,11 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Tokens of sequence b: seqlens[b] brought into [0, L], or L without seqlens.
+__device__ __forceinline__ int64_t seq_len(const int32_t *seqlens, int64_t b, int64_t L) {
+    return seqlens ? imin<int64_t>(L, imax<int64_t>(0, seqlens[b])) : L;
+}
+
 // Inclusive prefix sum over a[0..n) held one value per thread (threads >= n
 // hold 0), for blockDim.x a multiple of 32 of at least 256 and n <= 256.
 // Result written to out[0..n). Fixed association (warp shuffle scan, then a

@@ -139,6 +139,65 @@ struct NormArgs {
 };
 cudaError_t launch_gated_rmsnorm(int io, const NormArgs &a, cudaStream_t stream);
 
+// One token of the gated delta rule (layouts as in ssd_gated_delta_step).
+struct DeltaStepArgs {
+    int64_t B, H, G, P, N, nslots;
+    const float *state;
+    float *new_state;
+    const void *q, *k, *v, *g, *beta;
+    const int32_t *slots;  // may be null: row b uses state b
+    float scale;
+    void *y;
+};
+cudaError_t launch_delta_step(int io, const DeltaStepArgs &a, cudaStream_t stream);
+
+// The gated delta rule over a sequence (layouts as in ssd_gated_delta_chunked).
+struct DeltaArgs {
+    int64_t B, L, H, G, P, N;
+    int io;
+    const void *q, *k, *v, *g, *beta;
+    const float *init;       // may be null
+    const int32_t *seqlens;  // may be null
+    float scale;
+    void *y;                 // null in the backward's forward pass
+    float *final_state;      // may be null
+    int *status;             // SSD_OK, or SSD_ERR_TIMEOUT when a bounded wait gave up
+};
+cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream);
+
+// Its backward (layouts as in ssd_gated_delta_chunked_bwd).
+struct DeltaBwdArgs {
+    DeltaArgs f;
+    const void *dy;
+    const float *dfinal;                        // may be null
+    void *dq, *dk, *dv, *dg, *dbeta;
+    float *dinit;                               // may be null
+    // recurrent path's workspace: states entering every delta_ckpt_len-th
+    // token [B, H, ceil(L / len), P, N], parts [B, L, H, row blocks, N] and
+    // [B, L, H, row blocks]
+    float *ckpt, *dq_part, *dk_part, *dg_part, *db_part;
+};
+int delta_ckpt_len(int64_t N);
+int delta_row_blocks(int64_t P);
+cudaError_t launch_delta_recurrent_bwd(const DeltaBwdArgs &a, cudaStream_t stream);
+
+// Block norm and its backward (layouts as in ssd_block_norm, ssd_block_norm_bwd).
+struct BlockNormArgs {
+    int64_t rows, dim;
+    float eps;
+    const void *y, *z, *res;                    // z may be null
+    const float *post_w, *scale, *pre_w;        // post_w, scale may be null
+    void *out, *res_out;
+    // backward
+    const void *dout, *dres_out;                // dres_out may be null
+    void *dy, *dz, *dres;
+    float *dpre_w, *dpost_w, *dscale;
+    float *part;                                // [block_norm_bwd_parts][3][dim]
+};
+cudaError_t launch_block_norm(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream);
+int block_norm_bwd_parts(int64_t rows, int64_t dim);
+cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream);
+
 // Forward chunk states and entering states only (CUDA-core chunk state, then
 // the float32 state pass in place): a.states holds h_in(c), a.chunk_sum the
 // chunk decays. Used by the backward to recompute the forward.

@@ -1,10 +1,13 @@
 // C ABI of libssdscan.so (declared in include/ssd_scan.h): argument
 // validation, workspace carving and kernel launch order. No allocation, no
 // host synchronisation (except ssd_workspace_status, which exists to wait).
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <new>
+#include <utility>
 
 #include "launch.h"
 #include "ssd_scan.h"
@@ -682,6 +685,231 @@ ssd_status ssd_decode_graph_destroy(ssd_decode_graph *graph) {
     delete graph;
     if (e1 != cudaSuccess) return cuda_fail(e1, "ssd_decode_graph_destroy");
     if (e2 != cudaSuccess) return cuda_fail(e2, "ssd_decode_graph_destroy");
+    return ok();
+}
+
+// ---- gated delta rule ----
+
+namespace {
+
+// Sizes of a delta-rule call; the flags of ssd_dims other than SSD_FLAG_SIMT are the scan's.
+ssd_status check_delta(const ssd_dims *d, bool need_seqlen, float scale) {
+    ssd_status s = check_dims(d, need_seqlen);
+    if (s != SSD_OK) return s;
+    if (d->flags & ~SSD_FLAG_SIMT)
+        return fail(SSD_ERR_INVALID_ARG, "the delta rule takes no flag but SSD_FLAG_SIMT (got 0x%x)", d->flags);
+    if (!isfinite(scale)) return fail(SSD_ERR_INVALID_ARG, "scale must be finite");
+    if (d->dstate > 256) return fail(SSD_ERR_UNSUPPORTED, "dstate must be <= 256 (got %lld)", (long long)d->dstate);
+    if (d->headdim > 65535) return fail(SSD_ERR_UNSUPPORTED, "headdim must be <= 65535");
+    if (d->batch * d->nheads > 0x7fffffffLL) return fail(SSD_ERR_UNSUPPORTED, "batch * nheads too large");
+    if (need_seqlen && d->batch > 0 && d->seqlen > 0x7fffffffLL / d->batch)
+        return fail(SSD_ERR_UNSUPPORTED, "batch * seqlen must be below 2^31");
+    return SSD_OK;
+}
+
+ssd_status check_aligned(std::initializer_list<std::pair<const void *, const char *>> ptrs) {
+    for (const auto &p : ptrs)
+        if (p.first && !aligned(p.first, 16)) return fail(SSD_ERR_INVALID_ARG, "%s is not 16-byte aligned", p.second);
+    return SSD_OK;
+}
+
+ssd_status check_ws(const void *ws, size_t bytes, size_t need) {
+    if (!ws) return fail(SSD_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned(ws, 256)) return fail(SSD_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    if (bytes < need) return fail(SSD_ERR_INVALID_ARG, "workspace of %zu bytes is too small: %zu needed", bytes, need);
+    return SSD_OK;
+}
+
+ssd::DeltaArgs delta_args(const ssd_dims *d, const void *q, const void *k, const void *v, const void *g,
+                          const void *beta, const float *init, const int32_t *seqlens, float scale) {
+    ssd::DeltaArgs a{};
+    a.B = d->batch, a.L = d->seqlen, a.H = d->nheads, a.G = d->ngroups, a.P = d->headdim, a.N = d->dstate;
+    a.io = d->io_dtype == SSD_BF16 ? ssd::IO_BF16 : ssd::IO_F32;
+    a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta;
+    a.init = init, a.seqlens = seqlens, a.scale = scale;
+    return a;
+}
+
+struct DeltaBwdWs {
+    size_t ckpt, dq, dk, dg, db, total;
+};
+DeltaBwdWs delta_bwd_ws(const ssd_dims *d) {
+    const int64_t ck = ssd::delta_ckpt_len(d->dstate), nrb = ssd::delta_row_blocks(d->headdim);
+    const size_t small = round256((size_t)(d->batch * d->seqlen * d->nheads * nrb) * sizeof(float));
+    const size_t part = round256((size_t)(d->batch * d->seqlen * d->nheads * nrb * d->dstate) * sizeof(float));
+    DeltaBwdWs w{};
+    w.ckpt = 256;
+    w.dq = w.ckpt + round256((size_t)(d->batch * d->nheads * ((d->seqlen + ck - 1) / ck) * d->headdim * d->dstate) *
+                             sizeof(float));
+    w.dk = w.dq + part;
+    w.dg = w.dk + part;
+    w.db = w.dg + small;
+    w.total = w.db + small;
+    return w;
+}
+
+}  // namespace
+
+size_t ssd_gated_delta_workspace_size(const ssd_dims *dims) {
+    return check_delta(dims, true, 1.f) == SSD_OK ? 256 : 0;
+}
+
+ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const void *k, const void *v, const void *g,
+                                   const void *beta, const float *init_state, const int32_t *seqlens, float scale,
+                                   void *y, float *final_state, void *workspace, size_t ws_bytes,
+                                   cudaStream_t stream) {
+    ssd_status s = check_delta(dims, true, scale);
+    if (s != SSD_OK) return s;
+    const bool has_tokens = dims->batch > 0 && dims->seqlen > 0;
+    if (has_tokens && (!q || !k || !v || !g || !beta || !y))
+        return fail(SSD_ERR_INVALID_ARG, "q, k, v, g, beta and y must be non-NULL");
+    s = check_aligned({{q, "q"}, {k, "k"}, {v, "v"}, {g, "g"}, {beta, "beta"}, {init_state, "init_state"},
+                       {seqlens, "seqlens"}, {y, "y"}, {final_state, "final_state"}});
+    if (s != SSD_OK) return s;
+    if (dims->batch == 0) return ok();
+    if ((s = check_ws(workspace, ws_bytes, ssd_gated_delta_workspace_size(dims))) != SSD_OK) return s;
+    ssd::DeltaArgs a = delta_args(dims, q, k, v, g, beta, init_state, seqlens, scale);
+    a.y = y;
+    a.final_state = final_state;
+    a.status = static_cast<int *>(workspace);
+    cudaError_t e = ssd::launch_delta_recurrent(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_delta_chunked");
+    return ok();
+}
+
+size_t ssd_gated_delta_chunked_bwd_workspace_size(const ssd_dims *dims) {
+    return check_delta(dims, true, 1.f) == SSD_OK ? delta_bwd_ws(dims).total : 0;
+}
+
+ssd_status ssd_gated_delta_chunked_bwd(const ssd_dims *dims, const void *q, const void *k, const void *v,
+                                       const void *g, const void *beta, const float *init_state,
+                                       const int32_t *seqlens, float scale, const void *dy,
+                                       const float *dfinal_state, void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                                       float *dinit_state, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    ssd_status s = check_delta(dims, true, scale);
+    if (s != SSD_OK) return s;
+    const bool has_tokens = dims->batch > 0 && dims->seqlen > 0;
+    if (has_tokens && (!q || !k || !v || !g || !beta || !dy || !dq || !dk || !dv || !dg || !dbeta))
+        return fail(SSD_ERR_INVALID_ARG, "q, k, v, g, beta, dy, dq, dk, dv, dg and dbeta must be non-NULL");
+    s = check_aligned({{q, "q"}, {k, "k"}, {v, "v"}, {g, "g"}, {beta, "beta"}, {init_state, "init_state"},
+                       {seqlens, "seqlens"}, {dy, "dy"}, {dfinal_state, "dfinal_state"}, {dq, "dq"}, {dk, "dk"},
+                       {dv, "dv"}, {dg, "dg"}, {dbeta, "dbeta"}, {dinit_state, "dinit_state"}});
+    if (s != SSD_OK) return s;
+    if (dims->batch == 0) return ok();
+    if ((s = check_ws(workspace, ws_bytes, ssd_gated_delta_chunked_bwd_workspace_size(dims))) != SSD_OK) return s;
+    const DeltaBwdWs w = delta_bwd_ws(dims);
+    char *base = static_cast<char *>(workspace);
+    ssd::DeltaBwdArgs a{};
+    a.f = delta_args(dims, q, k, v, g, beta, init_state, seqlens, scale);
+    a.f.status = static_cast<int *>(workspace);
+    a.dy = dy, a.dfinal = dfinal_state;
+    a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dinit = dinit_state;
+    a.ckpt = reinterpret_cast<float *>(base + w.ckpt);
+    a.dq_part = reinterpret_cast<float *>(base + w.dq);
+    a.dk_part = reinterpret_cast<float *>(base + w.dk);
+    a.dg_part = reinterpret_cast<float *>(base + w.dg);
+    a.db_part = reinterpret_cast<float *>(base + w.db);
+    cudaError_t e = ssd::launch_delta_recurrent_bwd(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_delta_chunked_bwd");
+    return ok();
+}
+
+ssd_status ssd_gated_delta_step(const ssd_dims *dims, int64_t nslots, const float *state, const void *q,
+                                const void *k, const void *v, const void *g, const void *beta, const int32_t *slots,
+                                float scale, float *new_state, void *y, cudaStream_t stream) {
+    ssd_status s = check_delta(dims, false, scale);
+    if (s != SSD_OK) return s;
+    if (nslots < 0 || (!slots && nslots < dims->batch))
+        return fail(SSD_ERR_INVALID_ARG, "nslots (%lld) must hold a state for each row without slots",
+                    (long long)nslots);
+    if (dims->batch == 0) return ok();
+    if (!q || !k || !v || !g || !beta || !y || (nslots > 0 && (!state || !new_state)))
+        return fail(SSD_ERR_INVALID_ARG, "state, q, k, v, g, beta, new_state and y must be non-NULL");
+    s = check_aligned({{state, "state"}, {q, "q"}, {k, "k"}, {v, "v"}, {g, "g"}, {beta, "beta"}, {slots, "slots"},
+                       {new_state, "new_state"}, {y, "y"}});
+    if (s != SSD_OK) return s;
+    ssd::DeltaStepArgs a{};
+    a.B = dims->batch, a.H = dims->nheads, a.G = dims->ngroups, a.P = dims->headdim, a.N = dims->dstate;
+    a.nslots = nslots;
+    a.state = state, a.new_state = new_state;
+    a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta;
+    a.slots = slots, a.scale = scale, a.y = y;
+    cudaError_t e = ssd::launch_delta_step(dims->io_dtype == SSD_BF16 ? ssd::IO_BF16 : ssd::IO_F32, a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_delta_step");
+    return ok();
+}
+
+// ---- block norm ----
+
+namespace {
+ssd_status check_norm(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype, float eps) {
+    if (rows < 0 || dim < 1)
+        return fail(SSD_ERR_INVALID_ARG, "rows must be >= 0 and dim >= 1 (got %lld, %lld)", (long long)rows,
+                    (long long)dim);
+    if (io_dtype != SSD_F32 && io_dtype != SSD_BF16)
+        return fail(SSD_ERR_INVALID_ARG, "io_dtype must be SSD_F32 or SSD_BF16 (got %d)", io_dtype);
+    if (res_dtype != SSD_F32 && res_dtype != io_dtype)
+        return fail(SSD_ERR_INVALID_ARG, "res_dtype must be SSD_F32 or io_dtype (got %d)", res_dtype);
+    if (!(eps >= 0.f)) return fail(SSD_ERR_INVALID_ARG, "eps must be >= 0");
+    if (rows > 0x7fffffffLL) return fail(SSD_ERR_UNSUPPORTED, "rows must be below 2^31");
+    if (dim > 16384) return fail(SSD_ERR_UNSUPPORTED, "dim must be <= 16384 (got %lld)", (long long)dim);
+    return SSD_OK;
+}
+int io_of(int32_t dtype) { return dtype == SSD_BF16 ? ssd::IO_BF16 : ssd::IO_F32; }
+}  // namespace
+
+ssd_status ssd_block_norm(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype, const void *y,
+                          const void *res, const void *z, const float *post_weight, const float *scale,
+                          const float *pre_weight, float eps, void *out, void *res_out, cudaStream_t stream) {
+    ssd_status s = check_norm(rows, dim, io_dtype, res_dtype, eps);
+    if (s != SSD_OK) return s;
+    if (rows == 0) return ok();
+    if (!y || !res || !pre_weight || !out || !res_out)
+        return fail(SSD_ERR_INVALID_ARG, "y, res, pre_weight, out and res_out must be non-NULL");
+    s = check_aligned({{y, "y"}, {res, "res"}, {z, "z"}, {post_weight, "post_weight"}, {scale, "scale"},
+                       {pre_weight, "pre_weight"}, {out, "out"}, {res_out, "res_out"}});
+    if (s != SSD_OK) return s;
+    ssd::BlockNormArgs a{};
+    a.rows = rows, a.dim = dim, a.eps = eps;
+    a.y = y, a.z = z, a.res = res, a.post_w = post_weight, a.scale = scale, a.pre_w = pre_weight;
+    a.out = out, a.res_out = res_out;
+    cudaError_t e = ssd::launch_block_norm(io_of(io_dtype), io_of(res_dtype), a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_block_norm");
+    return ok();
+}
+
+size_t ssd_block_norm_bwd_workspace_size(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype) {
+    if (check_norm(rows, dim, io_dtype, res_dtype, 0.f) != SSD_OK) return 0;
+    return 256 + round256((size_t)ssd::block_norm_bwd_parts(rows, dim) * 3 * dim * sizeof(float));
+}
+
+ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype, const void *y,
+                              const void *res, const void *z, const float *post_weight, const float *scale,
+                              const float *pre_weight, float eps, const void *dout, const void *dres_out, void *dy,
+                              void *dz, void *dres, float *dpre_weight, float *dpost_weight, float *dscale,
+                              void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    ssd_status s = check_norm(rows, dim, io_dtype, res_dtype, eps);
+    if (s != SSD_OK) return s;
+    if (rows > 0 && (!y || !res || !pre_weight || !dout || !dy || !dres))
+        return fail(SSD_ERR_INVALID_ARG, "y, res, pre_weight, dout, dy and dres must be non-NULL");
+    if (!dpre_weight || (post_weight && !dpost_weight) || (scale && !dscale) || (rows > 0 && z && !dz))
+        return fail(SSD_ERR_INVALID_ARG, "dpre_weight, and dpost_weight, dscale and dz with their inputs, must be non-NULL");
+    s = check_aligned({{y, "y"}, {res, "res"}, {z, "z"}, {post_weight, "post_weight"}, {scale, "scale"},
+                       {pre_weight, "pre_weight"}, {dout, "dout"}, {dres_out, "dres_out"}, {dy, "dy"}, {dz, "dz"},
+                       {dres, "dres"}, {dpre_weight, "dpre_weight"}, {dpost_weight, "dpost_weight"},
+                       {dscale, "dscale"}});
+    if (s != SSD_OK) return s;
+    if ((s = check_ws(workspace, ws_bytes, ssd_block_norm_bwd_workspace_size(rows, dim, io_dtype, res_dtype))) != SSD_OK)
+        return s;
+    ssd::BlockNormArgs a{};
+    a.rows = rows, a.dim = dim, a.eps = eps;
+    a.y = y, a.z = z, a.res = res, a.post_w = post_weight, a.scale = scale, a.pre_w = pre_weight;
+    a.dout = dout, a.dres_out = dres_out;
+    a.dy = dy, a.dz = dz, a.dres = dres;
+    a.dpre_w = dpre_weight, a.dpost_w = post_weight ? dpost_weight : nullptr, a.dscale = scale ? dscale : nullptr;
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
+    cudaError_t e = ssd::launch_block_norm_bwd(io_of(io_dtype), io_of(res_dtype), a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_block_norm_bwd");
     return ok();
 }
 

@@ -228,3 +228,36 @@ WORKLOADS = {
     "mamba1_B1_L4096_D1024_softplus": dict(kind="diag", batch=1, seqlen=4096, dim=1024, dstate=16,
                                            io_dtype="bf16", chunk=2048, delta_softplus=True),
 }
+
+
+# ------------------------------------------------ gated delta rule, block norm
+
+def delta_inputs(batch, seqlen, nheads, ngroups, headdim, dstate, io_dtype="bf16", seed=0, init_state=False,
+                 rate=1.0, mean_key=0.0) -> dict:
+    """q, k (rows of norm 1; mean_key > 0 gives the keys a common direction), v,
+    g = -rate A_h dt (A uniform in [1, 16], dt log-uniform in [1e-3, 1e-1]),
+    beta = sigmoid of a normal, and init; float64 arrays exact in io_dtype."""
+    r = _rng(seed, 40)
+    lead = (batch, seqlen)
+
+    def unit(x):
+        return x / np.sqrt((x * x).sum(-1, keepdims=True))
+
+    q = unit(r.standard_normal((*lead, ngroups, dstate)))
+    k = unit(r.standard_normal((*lead, ngroups, dstate)) + mean_key)
+    v = r.standard_normal((*lead, nheads, headdim))
+    A, dt = r.uniform(1, 16, nheads), np.exp(r.uniform(np.log(1e-3), np.log(1e-1), (*lead, nheads)))
+    beta = 1 / (1 + np.exp(-r.standard_normal((*lead, nheads))))
+    d = {n: round_to(x, io_dtype) for n, x in dict(q=q, k=k, v=v, g=-rate * A * dt, beta=beta).items()}
+    d["init"] = round_to(0.2 * r.standard_normal((batch, nheads, headdim, dstate)), "f32") if init_state else None
+    return d
+
+
+def block_norm_inputs(rows, dim, io_dtype="bf16", res_dtype="bf16", seed=0) -> dict:
+    """y, z, res, dout, dres and the weights pre, post, scale of a block norm; float64 arrays exact in their types."""
+    r = _rng(seed, 41)
+    x = {n: round_to(r.standard_normal((rows, dim)), io_dtype) for n in ("y", "z", "dout")}
+    x["res"], x["dres"] = (round_to(s * r.standard_normal((rows, dim)), res_dtype) for s in (2.0, 1.0))
+    for n, m in (("pre", 1.0), ("post", 1.0), ("scale", 0.5)):
+        x[n] = round_to(m + 0.1 * r.standard_normal(dim), "f32")
+    return x
