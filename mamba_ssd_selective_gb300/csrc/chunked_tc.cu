@@ -1145,6 +1145,19 @@ bool tma_map_tokens_f32(CUtensorMap *out, const void *base, int64_t inner, int64
     return map_tokens(out, base, inner, L, B, box_rows, box_cols, true);
 }
 
+bool tma_map_heads(CUtensorMap *out, const void *base, int64_t inner, int64_t heads, int64_t L, int64_t B, int box_cols,
+                   int box_rows, bool swizzle128) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)inner * 2, (cuuint64_t)(heads * inner) * 2,
+                                   (cuuint64_t)(L * heads * inner) * 2};
+    const cuuint32_t box[4] = {(cuuint32_t)box_cols, 1, (cuuint32_t)box_rows, 1}, estr[4] = {1, 1, 1, 1};
+    return enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_cc_major_cached() { return device_cc_major(); }
 
 int sm_count(int fallback) {

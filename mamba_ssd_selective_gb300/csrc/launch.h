@@ -164,6 +164,9 @@ struct DeltaArgs {
     int *status;             // SSD_OK, or SSD_ERR_TIMEOUT when a bounded wait gave up
 };
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream);
+// The same in chunks of 64 tokens on the tensor cores.
+bool delta_tc_supported(int io, int64_t L, int64_t P, int64_t N);
+cudaError_t launch_delta_tc(const DeltaArgs &a, cudaStream_t stream);
 
 // Its backward (layouts as in ssd_gated_delta_chunked_bwd).
 struct DeltaBwdArgs {

@@ -772,7 +772,8 @@ ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const vo
     a.y = y;
     a.final_state = final_state;
     a.status = static_cast<int *>(workspace);
-    cudaError_t e = ssd::launch_delta_recurrent(a, stream);
+    const bool tc = !(dims->flags & SSD_FLAG_SIMT) && ssd::delta_tc_supported(a.io, a.L, a.P, a.N);
+    cudaError_t e = tc ? ssd::launch_delta_tc(a, stream) : ssd::launch_delta_recurrent(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_delta_chunked");
     return ok();
 }
