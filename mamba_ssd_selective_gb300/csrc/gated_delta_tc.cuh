@@ -1,0 +1,110 @@
+// What the tensor-core kernels of the gated delta rule share: the chunk's
+// tiles and scalars in the workspace, packed float32 arithmetic, bounded waits.
+//
+// Within a chunk of 64 tokens, with c the inclusive sums of g, S0 the entering
+// state, D_tj = exp(c_t - c_j) and s the output scale, the rule is a triangular
+// solve for w (u_t = beta_t w_t is what is added along k_t):
+//     A_tj = D_tj (k_t . k_j) beta_j, j < t            T = (I + A)^-1
+//     R = V - exp(c) K S0^T                            w = T R
+//     Y = s exp(c) Q S0^T + M w                        M_tj = s D_tj (q_t . k_j) beta_j, j <= t
+//     S1 = exp(c_63) S0 + (exp(c_63 - c) beta w)^T K
+// With beta on the columns of A nothing is divided by it, whatever its value.
+// T and M T depend on the inputs alone: delta_prep_kernel forms them for every
+// (b, head, chunk) at once, and the chains of chunks, forward and backward, read them.
+#pragma once
+#include "common.cuh"
+#include "launch.h"
+#include "ssd_scan.h"
+#include "tc_host.h"
+#include "tc_ptx.cuh"
+
+namespace ssd {
+namespace delta {
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kC = 64;  // tokens per chunk
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Workspace: for item (b, head, chunk) = (b H + h) nc + chunk the tiles T hi, M T
+// hi, T lo and (backward) M T lo, 64 x 64 bf16 each in the 128-byte swizzle,
+// and the scalars below, one float per token each, then exp(c_63).
+constexpr uint32_t kTile = 8192, kTilesFwd = 3 * kTile, kTilesBwd = 4 * kTile;
+enum { SC_EG, SC_NEG, SC_BETA, SC_BTAIL, SC_ROWS };  // exp(c), -exp(c), beta, beta exp(c_63 - c)
+constexpr int kScal = SC_ROWS * kC + 4;
+
+struct PrepArgs {
+    DeltaArgs a;
+    int64_t nc;
+    uint8_t *tiles;  // [B][H][nc][tile_bytes]
+    float *scal;     // [B][H][nc][kScal]
+    uint32_t tile_bytes;
+};
+cudaError_t launch_prep(const PrepArgs &p, cudaStream_t stream);
+// The chain over the chunks: y and the final state (each may be null), and for the backward the
+// states entering each chunk [B][H][nc + 1][P][N] (the final one last) and w [B, L, H, P], in bf16.
+cudaError_t launch_chain(const PrepArgs &p, __nv_bfloat16 *states, __nv_bfloat16 *w, cudaStream_t stream);
+
+// Whether a CTA takes two heads of a group.
+inline bool pair_heads(const DeltaArgs &a) {
+    return a.P <= 64 && (a.H / a.G) % 2 == 0 && a.B * (a.H / 2) >= (int64_t)sm_count(152);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+// Two float32 in one 64-bit register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void un2(uint64_t v, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// A pair as bf16 pairs hi and lo, hi + lo within 2^-17 of each.
+__device__ __forceinline__ void split2(uint64_t v, uint32_t &hi, uint32_t &lo) {
+    float x, y;
+    un2(v, x, y);
+    hi = pack2(x, y);
+    un2(fma2(f2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), f2(-1.f, -1.f), v), x, y);
+    lo = pack2(x, y);
+}
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) { split2(f2(x, y), hi, lo); }
+
+// Waits for the phase of `parity`; gives up after kWaitNs or once *fail is set.
+// The part that really waits is out of line, so that the roles' loops stay small
+// in the instruction cache, and looks at the clock once in 32 polls.
+static __device__ __noinline__ bool wait_long(uint32_t addr, uint32_t parity, volatile int *fail) {
+    const uint64_t t0 = tc::global_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int k = 0; k < 32; ++k)
+            if (tc::mbar_try_wait(addr, parity)) return true;
+        if (*fail) return false;
+        if (tc::global_ns() - t0 > kWaitNs) {
+            *fail = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *fail) {
+    const uint32_t addr = tc::smem_u32(bar);
+    return tc::mbar_try_wait(addr, parity) || wait_long(addr, parity, fail);
+}
+
+// Byte offset of 16-byte piece `pc` of row `row` of a tile of 64 bf16 columns in the 128-byte swizzle.
+__device__ __forceinline__ uint32_t piece(int row, int pc) { return (uint32_t)(row * 128 + ((pc ^ (row & 7)) << 4)); }
+
+}  // namespace delta
+}  // namespace ssd

@@ -730,6 +730,13 @@ ssd::DeltaArgs delta_args(const ssd_dims *d, const void *q, const void *k, const
     return a;
 }
 
+// Whether the sequence is taken in chunks on the tensor cores.
+bool delta_on_tc(const ssd_dims *d) {
+    return !(d->flags & SSD_FLAG_SIMT) &&
+           ssd::delta_tc_supported(d->io_dtype == SSD_BF16 ? ssd::IO_BF16 : ssd::IO_F32, d->batch, d->seqlen, d->nheads,
+                                   d->headdim, d->dstate);
+}
+
 struct DeltaBwdWs {
     size_t ckpt, dq, dk, dg, db, total;
 };
@@ -751,7 +758,8 @@ DeltaBwdWs delta_bwd_ws(const ssd_dims *d) {
 }  // namespace
 
 size_t ssd_gated_delta_workspace_size(const ssd_dims *dims) {
-    return check_delta(dims, true, 1.f) == SSD_OK ? 256 : 0;
+    if (check_delta(dims, true, 1.f) != SSD_OK) return 0;
+    return delta_on_tc(dims) ? ssd::delta_tc_workspace(dims->batch, dims->seqlen, dims->nheads) : 256;
 }
 
 ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const void *k, const void *v, const void *g,
@@ -772,8 +780,7 @@ ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const vo
     a.y = y;
     a.final_state = final_state;
     a.status = static_cast<int *>(workspace);
-    const bool tc = !(dims->flags & SSD_FLAG_SIMT) && ssd::delta_tc_supported(a.io, a.L, a.P, a.N);
-    cudaError_t e = tc ? ssd::launch_delta_tc(a, stream) : ssd::launch_delta_recurrent(a, stream);
+    cudaError_t e = delta_on_tc(dims) ? ssd::launch_delta_tc(a, workspace, stream) : ssd::launch_delta_recurrent(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_delta_chunked");
     return ok();
 }
