@@ -89,15 +89,19 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(PrepArgs p) {
         for (int e = 0; e < 2; ++e) {
             const double c2 = (e ? sum : sum - (double)gv[1]) * (double)kLog2e;  // base-2 units
             const float hi = (float)c2, lo = (float)(c2 - (double)hi), eg = exp2f((float)c2);
+            const float row = exp2f(lo), inv = bv[e] * exp2f(-lo);
             sc[S_HI * kC + 2 * lane + e] = hi;
-            sc[S_ROW * kC + 2 * lane + e] = exp2f(lo);
-            sc[S_INV * kC + 2 * lane + e] = bv[e] * exp2f(-lo);
+            sc[S_ROW * kC + 2 * lane + e] = row;
+            sc[S_INV * kC + 2 * lane + e] = inv;
             o[SC_EG * kC + e] = eg;
             o[SC_NEG * kC + e] = -eg;
             o[SC_BETA * kC + e] = bv[e];
             o[SC_BTAIL * kC + e] = bv[e] * exp2f((float)(end - c2));
+            o[kScalDecay + e] = hi;
+            o[kScalDecay + kC + e] = row;
+            o[kScalDecay + 2 * kC + e] = inv;
         }
-        if (lane == 0) p.scal[item * kScal + SC_ROWS * kC] = exp2f((float)end);
+        if (lane == 0) p.scal[item * kScal + kScalEnd] = exp2f((float)end);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();

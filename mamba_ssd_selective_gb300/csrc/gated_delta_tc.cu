@@ -60,7 +60,7 @@ constexpr uint32_t kOffV = 65536;         // 2 stages of 16 KB: [32-row block][t
 constexpr uint32_t kOffW = kOffV + 32768; // SAVE: w in the same layout
 constexpr uint32_t kOffT = kOffW + 16384; // 2 stages of NH x 24 KB: T hi, M T, T lo
 __host__ __device__ constexpr uint32_t off_scal(int NH) { return kOffT + 2 * NH * kTilesFwd; }
-__host__ __device__ constexpr uint32_t off_bar(int NH) { return off_scal(NH) + 2 * NH * kScal * 4; }
+__host__ __device__ constexpr uint32_t off_bar(int NH) { return off_scal(NH) + 2 * NH * kScalBytes; }
 enum {
     BAR_KQ_FULL = 0,   // [2]
     BAR_KQ_EMPTY = 2,  // [2] last product of the chunk
@@ -144,11 +144,11 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                     tc::tma_load_4d(d + k * 16384 + 8192, &prm.mk, bar, 64 * k, grp, c * kC, (int)b);
                 }
                 bar = &bars[BAR_T_FULL + s];
-                tc::mbar_arrive_expect_tx(bar, NH * (kTilesFwd + kScal * 4));
+                tc::mbar_arrive_expect_tx(bar, NH * (kTilesFwd + kScalBytes));
                 for (int hf = 0; hf < NH; ++hf) {
                     const int64_t item = (b * a.H + h0 + hf) * prm.nc + c;
                     tc::bulk_load(sT + (s * NH + hf) * kTilesFwd, prm.tiles + item * prm.tile_bytes, kTilesFwd, bar);
-                    tc::bulk_load(scal + (s * NH + hf) * kScal, prm.scal + item * kScal, kScal * 4, bar);
+                    tc::bulk_load(scal + (s * NH + hf) * kScalDecay, prm.scal + item * kScal, kScalBytes, bar);
                 }
                 done = c + 1;
                 if (!wait_on(&bars[BAR_V_EMPTY + s], ph, fail)) break;  // y of the stage's last chunk has left
@@ -270,7 +270,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
             float eq = 0.f;
             if (nc > 0) {
                 wait_on(&bars[BAR_T_FULL], 0, fail);
-                eq = scal[hf * kScal + SC_ROWS * kC];
+                eq = scal[hf * kScalDecay + kScalEnd];
             }
             __syncwarp();
             if (nc > 0 || SAVE) {
@@ -294,7 +294,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
             for (int c = 0; c < nc; ++c) {
                 const int s = c & 1;
                 const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
-                const float *sc = scal + (s * NH + hf) * kScal + 32 * ch;
+                const float *sc = scal + (s * NH + hf) * kScalDecay + 32 * ch;
                 // R^T = v - exp(c) (K S0^T)^T; vt is this thread's column of the warp's [32 tokens][32 rows]
                 __nv_bfloat16 *vt = reinterpret_cast<__nv_bfloat16 *>(sV + s * 16384 + q * 4096 + ch * 2048) + lane;
                 wait_on(&bars[BAR_V_FULL + s], ph2, fail);
@@ -361,7 +361,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 if (lane == 0) tc::mbar_arrive(&bars[BAR_T_EMPTY + s]);
                 // the state that enters the next chunk
                 if (c + 1 < nc) wait_on(&bars[BAR_T_FULL + (s ^ 1)], ((c + 1) >> 1) & 1, fail);
-                const float eqn = c + 1 < nc ? scal[((s ^ 1) * NH + hf) * kScal + SC_ROWS * kC] : 0.f;
+                const float eqn = c + 1 < nc ? scal[((s ^ 1) * NH + hf) * kScalDecay + kScalEnd] : 0.f;
                 wait_on(&bars[BAR_C_DONE], ph, fail);
                 __syncwarp();
                 tc::tc_fence_after();
@@ -419,7 +419,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
         if (NH == 2 || p32 < P) {
             for (int c = 0; c < nc; ++c) {
                 const int s = c & 1;
-                const float *sc = scal + (s * NH + hf) * kScal + 32 * ch;
+                const float *sc = scal + (s * NH + hf) * kScalDecay + 32 * ch;
                 uint16_t *vt = reinterpret_cast<uint16_t *>(sV + s * 16384 + q * 4096 + ch * 2048) + lane;
                 uint16_t *wt = reinterpret_cast<uint16_t *>(sW + q * 4096 + ch * 2048) + lane;
                 wait_on(&bars[BAR_B_DONE], c & 1, fail);

@@ -29,8 +29,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 // hi, T lo and (backward) M T lo, 64 x 64 bf16 each in the 128-byte swizzle,
 // and the scalars below, one float per token each, then exp(c_63).
 constexpr uint32_t kTile = 8192, kTilesFwd = 3 * kTile, kTilesBwd = 4 * kTile;
-enum { SC_EG, SC_NEG, SC_BETA, SC_BTAIL, SC_ROWS };  // exp(c), -exp(c), beta, beta exp(c_63 - c)
-constexpr int kScal = SC_ROWS * kC + 4;
+enum {
+    SC_EG,     // exp(c)
+    SC_NEG,    // -exp(c)
+    SC_BETA,
+    SC_BTAIL,  // beta exp(c_63 - c)
+    SC_CHAIN,  // the chains read the rows up to here, and exp(c_63) behind them
+    SC_HI = SC_CHAIN,  // c in base-2 units, rounded to float32
+    SC_ROW,    // 2^(c - hi)
+    SC_INV,    // beta 2^(hi - c): D_tj beta_j = 2^(hi_t - hi_j) ROW_t INV_j
+    SC_ROWS
+};
+constexpr int kScalEnd = SC_CHAIN * kC, kScalDecay = kScalEnd + 4;  // exp(c_63); the last three rows
+constexpr uint32_t kScalBytes = kScalDecay * 4;                     // what the chains load
+constexpr int kScal = kScalDecay + 3 * kC;
 
 struct PrepArgs {
     DeltaArgs a;

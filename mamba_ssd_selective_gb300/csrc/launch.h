@@ -184,6 +184,9 @@ struct DeltaBwdArgs {
 int delta_ckpt_len(int64_t N);
 int delta_row_blocks(int64_t P);
 cudaError_t launch_delta_recurrent_bwd(const DeltaBwdArgs &a, cudaStream_t stream);
+bool delta_bwd_tc_supported(int io, int64_t B, int64_t L, int64_t H, int64_t P, int64_t N);
+size_t delta_bwd_tc_workspace(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N);
+cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &a, void *workspace, cudaStream_t stream);
 
 // Block norm and its backward (layouts as in ssd_block_norm, ssd_block_norm_bwd).
 struct BlockNormArgs {

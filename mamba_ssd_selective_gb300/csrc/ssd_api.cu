@@ -737,6 +737,12 @@ bool delta_on_tc(const ssd_dims *d) {
                                    d->headdim, d->dstate);
 }
 
+bool delta_bwd_on_tc(const ssd_dims *d) {
+    return !(d->flags & SSD_FLAG_SIMT) &&
+           ssd::delta_bwd_tc_supported(d->io_dtype == SSD_BF16 ? ssd::IO_BF16 : ssd::IO_F32, d->batch, d->seqlen, d->nheads,
+                                       d->headdim, d->dstate);
+}
+
 struct DeltaBwdWs {
     size_t ckpt, dq, dk, dg, db, total;
 };
@@ -786,7 +792,9 @@ ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const vo
 }
 
 size_t ssd_gated_delta_chunked_bwd_workspace_size(const ssd_dims *dims) {
-    return check_delta(dims, true, 1.f) == SSD_OK ? delta_bwd_ws(dims).total : 0;
+    if (check_delta(dims, true, 1.f) != SSD_OK) return 0;
+    return delta_bwd_on_tc(dims) ? ssd::delta_bwd_tc_workspace(dims->batch, dims->seqlen, dims->nheads, dims->headdim, dims->dstate)
+                                 : delta_bwd_ws(dims).total;
 }
 
 ssd_status ssd_gated_delta_chunked_bwd(const ssd_dims *dims, const void *q, const void *k, const void *v,
@@ -817,7 +825,8 @@ ssd_status ssd_gated_delta_chunked_bwd(const ssd_dims *dims, const void *q, cons
     a.dk_part = reinterpret_cast<float *>(base + w.dk);
     a.dg_part = reinterpret_cast<float *>(base + w.dg);
     a.db_part = reinterpret_cast<float *>(base + w.db);
-    cudaError_t e = ssd::launch_delta_recurrent_bwd(a, stream);
+    cudaError_t e = delta_bwd_on_tc(dims) ? ssd::launch_delta_bwd_tc(a, workspace, stream)
+                                          : ssd::launch_delta_recurrent_bwd(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_delta_chunked_bwd");
     return ok();
 }

@@ -315,3 +315,20 @@ def test_example_block(ssd):
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     assert m.main() < 2e-2
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("P", [64, 128])
+def test_backward_where_beta_is_zero(ssd, io, P):
+    """Tokens that write nothing still have a gradient with respect to beta."""
+    d = inputs.delta_inputs(2, 140, 4, 2, P, 128, io, seed=17, init_state=True)
+    d["beta"][:, ::5] = 0.0
+    d["beta"][1] = 0.0
+    r = np.random.default_rng(18)
+    dy = inputs.round_to(r.standard_normal(d["v"].shape), io)
+    df = inputs.round_to(0.1 * r.standard_normal(d["init"].shape), "f32")
+    want = delta.delta_seq_bwd(*(d[n] for n in NAMES), dy, d["init"], df)
+    got = ssd.gated_delta_chunked_bwd(**tokens(d, io), dy=dev(dy, IO_TORCH[io]), init_state=dev(d["init"]),
+                                      dfinal_state=dev(df))
+    for n in GRADS:
+        near(got[n], want[n], io, n)
