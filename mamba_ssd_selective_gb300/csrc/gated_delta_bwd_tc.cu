@@ -54,6 +54,8 @@ struct ReverseParams {
     float *dinit;           // may be null
     __nv_bfloat16 *cot;     // [B][H][nc][P][N] E of each chunk
     __nv_bfloat16 *dv;
+    int *flags;             // per chain
+    float *carry;           // [B][H][P][N]
     int64_t nc;
     int units_per_b, pblocks;
 };
@@ -108,12 +110,26 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const int64_t b = blockIdx.x / prm.units_per_b;
-    const int un = (int)(blockIdx.x % prm.units_per_b);
-    const int h0 = NH == 2 ? 2 * un : un / prm.pblocks;
-    const int prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;
-    const int grp = h0 / (int)(a.H / a.G);
-    const int row_warps = NH == 2 ? 8 : 2 * imin(4, (P - prow0 + 31) / 32);
+    const int row_warps = NH == 2 || P >= 128 ? 8 : 2 * ((P + 31) / 32);
+    __shared__ Segments seg;
+    // item k: its steps [c0, c1), step i being chunk nc - 1 - i, and where its rows are
+    struct Item {
+        int64_t b, len;
+        int unit, h0, prow0, grp, c0, c1, nc;
+    };
+    auto get = [&](int k) {
+        Item m;
+        seg.item(k, (int)prm.nc, m.unit, m.c0, m.c1);
+        m.b = m.unit / prm.units_per_b;
+        const int un = m.unit % prm.units_per_b;
+        m.h0 = NH == 2 ? 2 * un : un / prm.pblocks;
+        m.prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;
+        m.grp = m.h0 / (int)(a.H / a.G);
+        m.len = seq_len(a.seqlens, m.b, a.L);
+        m.nc = (int)((m.len + kC - 1) / kC);
+        m.c1 = imin(m.c1, m.nc);
+        return m;
+    };
 
     if (tid == 0) {
         for (int k = 0; k < kBars; ++k) {
@@ -125,6 +141,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
         }
         tc::fence_mbar_init();
         *fail = 0;
+        seg.set(a.B * prm.units_per_b, prm.nc);
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, 512);
@@ -135,15 +152,19 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
     const uint32_t tmem = *tmem_slot;
     const uint32_t tX = tmem, tD = tmem + 64, tE = tmem + 128, tOp = tmem + 256, tY = tmem + 384, tYe = tmem + 448;
     pdl_wait();
-    const int64_t len = seq_len(a.seqlens, b, a.L);
-    const int nc = (int)((len + kC - 1) / kC);
+    const int items = seg.items();
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
         if (lane == 0) {
             int n[4] = {0, 0, 0, 0};  // of K and Q with scalars, M T, dY, T
-            for (int it = 0; it < nc; ++it) {
-                const int s = it & 1, c = nc - 1 - it;
+            int it = 0;
+            for (int kk = 0; kk < items && !*fail; ++kk) {
+            const Item m = get(kk);
+            const int64_t b = m.b;
+            const int h0 = m.h0;
+            for (int i = m.c0; i < m.c1; ++i, ++it) {
+                const int s = it & 1, c = m.nc - 1 - i;
                 const uint32_t ph2 = ((it >> 1) & 1) ^ 1, ph = (it & 1) ^ 1;
                 const int64_t item0 = (b * a.H + h0) * prm.nc + c;
                 if (!wait_on(&bars[BAR_SC_EMPTY + s], ph2, fail) || !wait_on(&bars[BAR_KQ_EMPTY + s], ph2, fail)) break;
@@ -151,8 +172,8 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                 uint8_t *d = sKQ + s * 32768;
                 tc::mbar_arrive_expect_tx(bar, 32768u);
                 for (int k = 0; k < 2; ++k) {
-                    tc::tma_load_4d(d + k * 16384, &prm.mq, bar, 64 * k, grp, c * kC, (int)b);
-                    tc::tma_load_4d(d + k * 16384 + 8192, &prm.mk, bar, 64 * k, grp, c * kC, (int)b);
+                    tc::tma_load_4d(d + k * 16384, &prm.mq, bar, 64 * k, m.grp, c * kC, (int)b);
+                    tc::tma_load_4d(d + k * 16384 + 8192, &prm.mk, bar, 64 * k, m.grp, c * kC, (int)b);
                 }
                 bar = &bars[BAR_SC_FULL + s];
                 tc::mbar_arrive_expect_tx(bar, NH * kScalBytes);
@@ -163,7 +184,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                 bar = &bars[BAR_DY_FULL + s];
                 tc::mbar_arrive_expect_tx(bar, 16384u);
                 for (int k = 0; k < 4; ++k) {
-                    const int hh = NH == 2 ? h0 + (k >> 1) : h0, p = NH == 2 ? 32 * (k & 1) : prow0 + 32 * k;
+                    const int hh = NH == 2 ? h0 + (k >> 1) : h0, p = NH == 2 ? 32 * (k & 1) : m.prow0 + 32 * k;
                     tc::tma_load_4d(sDY + s * 16384 + k * 4096, &prm.mdy, bar, p, hh, c * kC, (int)b);
                 }
                 n[2] = it + 1;
@@ -183,6 +204,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                                       &bars[BAR_T_FULL]);
                 n[3] = it + 1;
             }
+            }
             // no copy outlives the block, even where a wait gave up
             for (int k = imax(0, n[0] - 2); k < n[0]; ++k) {
                 tc::mbar_wait(&bars[BAR_KQ_FULL + (k & 1)], (k >> 1) & 1, kWaitNs);
@@ -200,8 +222,12 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
         const uint64_t dT = tc::sdesc_sw128(tc::smem_u32(sT), 16, 1024), dM = tc::sdesc_sw128(tc::smem_u32(sM), 16, 1024);
         const uint64_t dK = tc::sdesc_sw128(tc::smem_u32(sKQ) + 8192, 16, 1024);      // rows of K
         const uint64_t dQm = tc::sdesc_sw128(tc::smem_u32(sKQ), 16384, 1024);         // Q and K by columns
-        for (int it = 0; it < nc; ++it) {
-            const int s = it & 1, c = nc - 1 - it;
+        int it = 0;
+        for (int kk = 0; kk < items; ++kk) {
+        const Item m = get(kk);
+        const int64_t len = m.len;
+        for (int i = m.c0; i < m.c1; ++i, ++it) {
+            const int s = it & 1, c = m.nc - 1 - i;
             const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
             const uint64_t kr = dK + (uint64_t)(s * 2048), qm = dQm + (uint64_t)(s * 2048), km = qm + 512;
             wait_on(&bars[BAR_KQ_FULL + s], ph2, fail);
@@ -274,19 +300,23 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
             tc::mma_commit_if(one, &bars[BAR_C_DONE]);
             tc::mma_commit_if(one, &bars[BAR_KQ_EMPTY + s]);
         }
+        }
         tc::mma_commit_if(one, &bars[BAR_DRAIN]);
         tc::mbar_wait(&bars[BAR_DRAIN], 0, kWaitNs);
         __syncwarp();
     } else if (warp >= kChainWarp0 && warp < kOutWarp0) {
         // ---------------------------------------- elementwise steps of the chain
         const int cw = warp - kChainWarp0, q = cw & 3, ch = cw >> 2;
-        const int hf = NH == 2 ? q >> 1 : 0, h = h0 + hf;
-        const int p32 = NH == 2 ? 32 * (q & 1) : prow0 + 32 * q, p = p32 + lane;
+        const int hf = NH == 2 ? q >> 1 : 0;
         const uint32_t lq = (uint32_t)(32 * q) << 16;
-        const int64_t srow = ((b * a.H + h) * a.P + p) * a.N;
-        if (NH == 2 || p32 < P) {
+        int it = 0;
+        for (int kk = 0; kk < (2 * q < row_warps ? items : 0); ++kk) {
+            const Item m = get(kk);
+            const int64_t b = m.b;
+            const int h = m.h0 + hf, p = (NH == 2 ? 32 * (q & 1) : m.prow0 + 32 * q) + lane;
+            const int64_t srow = ((b * a.H + h) * a.P + p) * a.N;
             // 16 columns of E of chunk c: operands, scaled for the next accumulation, and kept for the gradients
-            auto put_state = [&](const float (&v)[16], int c0, float eq, int64_t c) {
+            auto put_state = [&](const float (&v)[16], int c0, float eq, int c) {
                 uint32_t hi[8], lo[8], sc[16];
                 const uint64_t e2 = f2(eq, eq);
 #pragma unroll
@@ -306,29 +336,47 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                     if (c0 + 8 < N) o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
                 }
             };
-            if (nc > 0) {
-                wait_on(&bars[BAR_SC_FULL], 0, fail);
-                const float eq = scal[hf * kScalDecay + kScalEnd];
-                __syncwarp();
-#pragma unroll 1
-                for (int k4 = 0; k4 < 4; ++k4) {
-                    const int c0 = 64 * ch + 16 * k4;
-                    float v[16];
+            auto get_state = [&](float (&v)[16], const float *from, int c0) {
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (prm.dfinal && p < P && c0 + k < N) x = *reinterpret_cast<const float4 *>(prm.dfinal + srow + c0 + k);
-                        v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
-                    }
-                    put_state(v, c0, eq, nc - 1);
+                for (int k = 0; k < 16; k += 4) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (from && p < P && c0 + k < N) x = __ldcg(reinterpret_cast<const float4 *>(from + srow + c0 + k));
+                    v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
                 }
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&bars[BAR_E_FULL]);
-                tc::mbar_arrive(&bars[BAR_E_FULL + 1]);
+            };
+            auto out_state = [&](const float (&v)[16], float *to, int c0) {
+                if (p >= P || !to) return;
+#pragma unroll
+                for (int k = 0; k < 16; k += 4)
+                    if (c0 + k < N)
+                        *reinterpret_cast<float4 *>(to + srow + c0 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            };
+            if (m.c0 >= m.c1) {  // no token, or none left
+                if (m.nc == 0 && m.c0 == 0)
+                    for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
+                        float v[16];
+                        get_state(v, prm.dfinal, c0);
+                        out_state(v, prm.dinit, c0);
+                    }
+                continue;
             }
-            for (int it = 0; it < nc; ++it) {
-                const int s = it & 1, c = nc - 1 - it;
+            if (m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
+            wait_on(&bars[BAR_SC_FULL + (it & 1)], (it >> 1) & 1, fail);
+            const float eq0 = scal[((it & 1) * NH + hf) * kScalDecay + kScalEnd];
+            __syncwarp();
+#pragma unroll 1
+            for (int k4 = 0; k4 < 4; ++k4) {
+                const int c0 = 64 * ch + 16 * k4;
+                float v[16];
+                get_state(v, m.c0 > 0 ? prm.carry : prm.dfinal, c0);
+                put_state(v, c0, eq0, m.nc - 1 - m.c0);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars[BAR_E_FULL]);
+            tc::mbar_arrive(&bars[BAR_E_FULL + 1]);
+            for (int i = m.c0; i < m.c1; ++i, ++it) {
+                const int s = it & 1, c = m.nc - 1 - i;
                 const uint32_t ph = it & 1;
                 const float *sc = scal + (s * NH + hf) * kScalDecay + 32 * ch;
                 // z
@@ -388,12 +436,13 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                 }
                 if (lane == 0) tc::mbar_arrive(&bars[BAR_SC_EMPTY + s]);
                 // E of the chunk before
-                if (c > 0) wait_on(&bars[BAR_SC_FULL + (s ^ 1)], ((it + 1) >> 1) & 1, fail);
-                const float eq = c > 0 ? scal[((s ^ 1) * NH + hf) * kScalDecay + kScalEnd] : 0.f;
+                const bool next = i + 1 < m.c1;
+                if (next) wait_on(&bars[BAR_SC_FULL + (s ^ 1)], ((it + 1) >> 1) & 1, fail);
+                const float eq = next ? scal[((s ^ 1) * NH + hf) * kScalDecay + kScalEnd] : 0.f;
                 wait_on(&bars[BAR_C_DONE], ph, fail);
                 __syncwarp();
                 tc::tc_fence_after();
-                if (c > 0) {
+                if (next) {
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const int c0 = 64 * ch + 16 * half;
@@ -407,41 +456,39 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                         tc::tc_fence_before();
                         tc::mbar_arrive(&bars[BAR_E_FULL + half]);
                     }
-                } else if (prm.dinit) {
+                } else {
+                    const bool last = m.c1 == m.nc;
 #pragma unroll 1
                     for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
                         float v0[16];
                         tc::tmem_ld16(tE + lq + c0, v0);
                         tc::tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            if (p < P && c0 + k < N)
-                                *reinterpret_cast<float4 *>(prm.dinit + srow + c0 + k) =
-                                    make_float4(v0[k], v0[k + 1], v0[k + 2], v0[k + 3]);
+                        out_state(v0, last ? prm.dinit : prm.carry, c0);
                     }
                     tc::tc_fence_before();
+                    if (!last) {  // handed on to the next CTA
+                        __threadfence();
+                        asm volatile("bar.sync 1, %0;" ::"r"(32 * row_warps) : "memory");
+                        if (cw == 0 && lane == 0) flag_set(prm.flags + m.unit);
+                    }
                 }
             }
-            if (nc == 0 && prm.dinit && p < P)
-                for (int n = 64 * ch; n < imin(N, 64 * ch + 64); n += 4)
-                    *reinterpret_cast<float4 *>(prm.dinit + srow + n) =
-                        prm.dfinal ? *reinterpret_cast<const float4 *>(prm.dfinal + srow + n) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     } else if (warp >= kOutWarp0) {
         // -------------------------------------------- the operands of dY, and dv
         const int cw = warp - kOutWarp0, q = cw & 3, ch = cw >> 2;
-        const int hf = NH == 2 ? q >> 1 : 0, h = h0 + hf;
-        const int p32 = NH == 2 ? 32 * (q & 1) : prow0 + 32 * q, p = p32 + lane;
+        const int hf = NH == 2 ? q >> 1 : 0;
         const uint32_t lq = (uint32_t)(32 * q) << 16;
-        if (NH == 2 || p32 < P) {
+        if (2 * q < row_warps) {
             if (NH == 2) {  // zeros in the other head's operand, for good
                 uint32_t z[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) z[k] = 0u;
                 tc::tmem_st16(tY + 32 * (hf ^ 1) + lq + 16 * ch, z);
             }
-            auto put_dy = [&](int it) {
-                const int s = it & 1, c = nc - 1 - it;
+            // the operands of dY for chunk c, the `it`-th of this CTA
+            auto put_dy = [&](int it, int c, int64_t len) {
+                const int s = it & 1;
                 const float *sc = scal + (s * NH + hf) * kScalDecay + 32 * ch;
                 const uint16_t *yt = reinterpret_cast<const uint16_t *>(sDY + s * 16384 + q * 4096 + ch * 2048) + lane;
                 const int valid = (int)imin<int64_t>(32, len - (int64_t)c * kC - 32 * ch);
@@ -480,40 +527,45 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                     tc::mbar_arrive(&bars[BAR_SC_EMPTY + s]);
                 }
             };
-            if (nc > 0) put_dy(0);
             uint16_t *vt = reinterpret_cast<uint16_t *>(sDV + q * 4096 + ch * 2048) + lane;
-            for (int it = 0; it < nc; ++it) {
-                const int c = nc - 1 - it;
-                if (it + 1 < nc) put_dy(it + 1);
-                wait_on(&bars[BAR_B_DONE], it & 1, fail);
-                __syncwarp();
-                tc::tc_fence_after();
-                float x[32];
-                tc::tmem_ld32(tD + lq + 32 * ch, x);
-                tc::tmem_ld_wait();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive(&bars[BAR_D_READ]);
-                    tc::bulk_wait_read_all();  // the previous chunk's dv has left the buffer
-                }
-                __syncwarp();
+            int it = 0;
+            for (int kk = 0; kk < items; ++kk) {
+                const Item m = get(kk);
+                const int h = m.h0 + hf, p32 = NH == 2 ? 32 * (q & 1) : m.prow0 + 32 * q, p = p32 + lane;
+                if (m.c0 < m.c1) put_dy(it, m.nc - 1 - m.c0, m.len);
+                for (int i = m.c0; i < m.c1; ++i, ++it) {
+                    const int c = m.nc - 1 - i;
+                    if (i + 1 < m.c1) put_dy(it + 1, c - 1, m.len);
+                    wait_on(&bars[BAR_B_DONE], it & 1, fail);
+                    __syncwarp();
+                    tc::tc_fence_after();
+                    float x[32];
+                    tc::tmem_ld32(tD + lq + 32 * ch, x);
+                    tc::tmem_ld_wait();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive(&bars[BAR_D_READ]);
+                        tc::bulk_wait_read_all();  // the previous chunk's dv has left the buffer
+                    }
+                    __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const uint32_t y = pack2(x[k], x[k + 1]);
-                    vt[32 * k] = (uint16_t)y;
-                    vt[32 * k + 32] = (uint16_t)(y >> 16);
+                    for (int k = 0; k < 32; k += 2) {
+                        const uint32_t y = pack2(x[k], x[k + 1]);
+                        vt[32 * k] = (uint16_t)y;
+                        vt[32 * k + 32] = (uint16_t)(y >> 16);
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && p32 < P) {
+                        tc::tma_store_4d(&prm.mdv, vt, p32, h, c * kC + 32 * ch, (int)m.b);
+                        tc::bulk_commit();
+                    }
                 }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && p32 < P) {
-                    tc::tma_store_4d(&prm.mdv, vt, p32, h, c * kC + 32 * ch, (int)b);
-                    tc::bulk_commit();
-                }
+                if (p < P && m.c0 == 0)  // zero past the last chunk
+                    for (int64_t t = (int64_t)m.nc * kC + ch; t < a.L; t += 2)
+                        prm.dv[((m.b * a.L + t) * a.H + h) * P + p] = __float2bfloat16_rn(0.f);
             }
-            if (p < P)  // zero past the last chunk
-                for (int64_t t = (int64_t)nc * kC + ch; t < a.L; t += 2)
-                    prm.dv[((b * a.L + t) * a.H + h) * P + p] = __float2bfloat16_rn(0.f);
             if (lane == 0) tc::bulk_wait_all();
         }
     }
@@ -973,7 +1025,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
 
 template <int NH> cudaError_t launch_reverse(ReverseParams &p, cudaStream_t stream) {
     const DeltaArgs &a = p.a;
-    p.pblocks = (int)((a.P + 127) / 128);
+    p.pblocks = (int)row_blocks(a.P);
     p.units_per_b = (int)(NH == 2 ? a.H / 2 : a.H * p.pblocks);
     static DeviceOnce configured;
     int dev = 0;
@@ -986,8 +1038,7 @@ template <int NH> cudaError_t launch_reverse(ReverseParams &p, cudaStream_t stre
     } else if (e != cudaSuccess) {
         return e;
     }
-    return launch_programmatic(delta_reverse_kernel<NH>, dim3((unsigned)(a.B * p.units_per_b)), dim3(rev::kThreads),
-                               rev::smem_bytes(NH), stream, p);
+    return launch_chains(delta_reverse_kernel<NH>, p, a.B * p.units_per_b, p.nc, rev::kThreads, rev::smem_bytes(NH), stream);
 }
 
 template <int NPAN> cudaError_t launch_grad(const GradParams &p, cudaStream_t stream) {
@@ -1009,14 +1060,16 @@ template <int NPAN> cudaError_t launch_grad(const GradParams &p, cudaStream_t st
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct BwdWs {
-    size_t tiles, scal, states, cot, w, total;
+    size_t tiles, scal, flags, carry, states, cot, w, total;
 };
 BwdWs bwd_ws(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N) {
     const size_t nc = (size_t)((L + kC - 1) / kC), items = (size_t)(B * H) * nc;
     BwdWs s{};
     s.tiles = 256;
     s.scal = s.tiles + items * kTilesBwd;
-    s.states = s.scal + up256(items * kScal * 4);
+    s.flags = s.scal + up256(items * kScal * 4);
+    s.carry = s.flags + up256((size_t)(B * H * row_blocks(P)) * 8);
+    s.states = s.carry + up256((size_t)(B * H * P * N) * 4);
     s.cot = s.states + up256((items + (size_t)(B * H)) * P * N * 2);
     s.w = s.cot + up256(items * P * N * 2);
     s.total = s.w + up256((size_t)(B * L * H * P) * 2);
@@ -1046,6 +1099,8 @@ cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &args, void *workspace, cudaS
     p.tiles = base + s.tiles;
     p.scal = reinterpret_cast<float *>(base + s.scal);
     p.tile_bytes = kTilesBwd;
+    p.flags = reinterpret_cast<int *>(base + s.flags);
+    p.carry = reinterpret_cast<float *>(base + s.carry);
     cudaError_t e = launch_prep(p, stream);
     if (e == cudaSuccess) e = launch_chain(p, bf(s.states), bf(s.w), stream);
     if (e != cudaSuccess) return e;
@@ -1063,6 +1118,8 @@ cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &args, void *workspace, cudaS
     rp.dinit = args.dinit;
     rp.cot = bf(s.cot);
     rp.dv = static_cast<__nv_bfloat16 *>(args.dv);
+    rp.flags = p.flags + a.B * a.H * row_blocks(a.P);
+    rp.carry = p.carry;
     rp.nc = p.nc;
     e = pair_heads(a) ? launch_reverse<2>(rp, stream) : launch_reverse<1>(rp, stream);
     if (e != cudaSuccess) return e;

@@ -53,6 +53,10 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(PrepArgs p) {
     const int64_t bc = blockIdx.x / H, c = bc % p.nc, b = bc / p.nc;
     const int grp = h / (int)(a.H / a.G);
     const int64_t len = seq_len(a.seqlens, b, a.L), t0 = c * kC;
+    if (c == 0) {
+        const int pb = (int)row_blocks(a.P);
+        for (int x = tid; x < 2 * pb; x += kThreads) p.flags[((x / pb) * a.B * H + b * H + h) * pb + x % pb] = 0;
+    }
     if (t0 >= len) return;
     const int64_t item = (b * H + h) * p.nc + c;
     const int NK = N <= 64 ? 64 : 128;

@@ -27,6 +27,8 @@
 // Warps: 0 loads; 1 products; 4-11 the chain's elementwise steps (two warps per
 // 32 rows, half of the tokens or columns each); 12-19 y (and w for the backward).
 //
+// Where there are more chains than SMs they are cut into equal segments (Segments).
+//
 // Bound by the latency of the chain. A product of 16 columns of K takes 64
 // cycles whatever N, 36 of them a chunk (NH = 1); the rest is the elementwise steps
 // between them.
@@ -49,6 +51,8 @@ struct ChainParams {
     const float *scal;
     uint32_t tile_bytes;
     __nv_bfloat16 *states;  // SAVE: [B][H][nc + 1][P][N] states entering each chunk, then the final one
+    int *flags;             // per chain
+    float *carry;           // [B][H][P][N]
     int64_t nc;
     int units_per_b;  // NH = 2: head pairs; NH = 1: heads times blocks of 128 rows
     int pblocks;      // NH = 1: ceil(P / 128)
@@ -95,13 +99,27 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const int64_t b = blockIdx.x / prm.units_per_b;
-    const int un = (int)(blockIdx.x % prm.units_per_b);
-    const int h0 = NH == 2 ? 2 * un : un / prm.pblocks;
-    const int prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;  // state row of lane 0
-    const int grp = h0 / (int)(a.H / a.G);
-    // warps with rows of the state; those whose rows lie past P (NH = 1) take no part
-    const int row_warps = NH == 2 ? 8 : 2 * imin(4, (P - prow0 + 31) / 32);
+    // warps with rows of the state; those whose rows lie past P take no part
+    const int row_warps = NH == 2 || P >= 128 ? 8 : 2 * ((P + 31) / 32);
+    __shared__ Segments seg;
+    // item k: its chunks [c0, c1) that hold tokens, and where its rows are; false: no chunk
+    struct Item {
+        int64_t b, len;
+        int unit, h0, prow0, grp, c0, c1, nc;
+    };
+    auto get = [&](int k) {
+        Item m;
+        seg.item(k, (int)prm.nc, m.unit, m.c0, m.c1);
+        m.b = m.unit / prm.units_per_b;
+        const int un = m.unit % prm.units_per_b;
+        m.h0 = NH == 2 ? 2 * un : un / prm.pblocks;
+        m.prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;  // state row of lane 0
+        m.grp = m.h0 / (int)(a.H / a.G);
+        m.len = seq_len(a.seqlens, m.b, a.L);
+        m.nc = (int)((m.len + kC - 1) / kC);
+        m.c1 = imin(m.c1, m.nc);
+        return m;
+    };
 
     if (tid == 0) {
         for (int k = 0; k < kBars; ++k) {
@@ -113,6 +131,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
         }
         tc::fence_mbar_init();
         *fail = 0;
+        seg.set(a.B * prm.units_per_b, prm.nc);
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, 512);
@@ -123,42 +142,44 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     const uint32_t tmem = *tmem_slot;
     const uint32_t tQS = tmem, tU = tmem + 64, tO = tmem + 128, tS = tmem + 256, tOp = tmem + 384;
     pdl_wait();
-    const int64_t len = seq_len(a.seqlens, b, a.L);
-    const int nc = (int)((len + kC - 1) / kC);
     if (blockIdx.x == 0 && tid == 0) *a.status = SSD_OK;
+    const int items = seg.items();
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
         if (lane == 0) {
-            int done = 0, v_done = 0;
-            for (int c = 0; c < nc; ++c) {
-                const int s = c & 1;
-                const uint32_t ph = ((c >> 1) & 1) ^ 1;
-                if (!wait_on(&bars[BAR_T_EMPTY + s], ph, fail)) break;
-                if (!wait_on(&bars[BAR_KQ_EMPTY + s], ph, fail)) break;
-                uint64_t *bar = &bars[BAR_KQ_FULL + s];
-                uint8_t *d = sKQ + s * 32768;
-                tc::mbar_arrive_expect_tx(bar, 32768u);
-                for (int k = 0; k < 2; ++k) {
-                    tc::tma_load_4d(d + k * 16384, &prm.mq, bar, 64 * k, grp, c * kC, (int)b);
-                    tc::tma_load_4d(d + k * 16384 + 8192, &prm.mk, bar, 64 * k, grp, c * kC, (int)b);
+            int it = 0, done = 0, v_done = 0;
+            for (int k = 0; k < items; ++k) {
+                const Item m = get(k);
+                for (int c = m.c0; c < m.c1; ++c, ++it) {
+                    const int s = it & 1;
+                    const uint32_t ph = ((it >> 1) & 1) ^ 1;
+                    if (!wait_on(&bars[BAR_T_EMPTY + s], ph, fail) || !wait_on(&bars[BAR_KQ_EMPTY + s], ph, fail)) break;
+                    uint64_t *bar = &bars[BAR_KQ_FULL + s];
+                    uint8_t *d = sKQ + s * 32768;
+                    tc::mbar_arrive_expect_tx(bar, 32768u);
+                    for (int e = 0; e < 2; ++e) {
+                        tc::tma_load_4d(d + e * 16384, &prm.mq, bar, 64 * e, m.grp, c * kC, (int)m.b);
+                        tc::tma_load_4d(d + e * 16384 + 8192, &prm.mk, bar, 64 * e, m.grp, c * kC, (int)m.b);
+                    }
+                    bar = &bars[BAR_T_FULL + s];
+                    tc::mbar_arrive_expect_tx(bar, NH * (kTilesFwd + kScalBytes));
+                    for (int hf = 0; hf < NH; ++hf) {
+                        const int64_t item = (m.b * a.H + m.h0 + hf) * prm.nc + c;
+                        tc::bulk_load(sT + (s * NH + hf) * kTilesFwd, prm.tiles + item * prm.tile_bytes, kTilesFwd, bar);
+                        tc::bulk_load(scal + (s * NH + hf) * kScalDecay, prm.scal + item * kScal, kScalBytes, bar);
+                    }
+                    done = it + 1;
+                    if (!wait_on(&bars[BAR_V_EMPTY + s], ph, fail)) break;  // y of the stage's last chunk has left
+                    bar = &bars[BAR_V_FULL + s];
+                    tc::mbar_arrive_expect_tx(bar, 16384u);
+                    for (int e = 0; e < 4; ++e) {
+                        const int hh = NH == 2 ? m.h0 + (e >> 1) : m.h0, p = NH == 2 ? 32 * (e & 1) : m.prow0 + 32 * e;
+                        tc::tma_load_4d(sV + s * 16384 + e * 4096, &prm.mv, bar, p, hh, c * kC, (int)m.b);
+                    }
+                    v_done = it + 1;
                 }
-                bar = &bars[BAR_T_FULL + s];
-                tc::mbar_arrive_expect_tx(bar, NH * (kTilesFwd + kScalBytes));
-                for (int hf = 0; hf < NH; ++hf) {
-                    const int64_t item = (b * a.H + h0 + hf) * prm.nc + c;
-                    tc::bulk_load(sT + (s * NH + hf) * kTilesFwd, prm.tiles + item * prm.tile_bytes, kTilesFwd, bar);
-                    tc::bulk_load(scal + (s * NH + hf) * kScalDecay, prm.scal + item * kScal, kScalBytes, bar);
-                }
-                done = c + 1;
-                if (!wait_on(&bars[BAR_V_EMPTY + s], ph, fail)) break;  // y of the stage's last chunk has left
-                bar = &bars[BAR_V_FULL + s];
-                tc::mbar_arrive_expect_tx(bar, 16384u);
-                for (int k = 0; k < 4; ++k) {
-                    const int hh = NH == 2 ? h0 + (k >> 1) : h0, p = NH == 2 ? 32 * (k & 1) : prow0 + 32 * k;
-                    tc::tma_load_4d(sV + s * 16384 + k * 4096, &prm.mv, bar, p, hh, c * kC, (int)b);
-                }
-                v_done = c + 1;
+                if (*fail) break;
             }
             // no copy outlives the block, even where a wait gave up
             for (int c = imax(0, done - 2); c < done; ++c) {
@@ -177,9 +198,13 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
         const uint64_t dT = tc::sdesc_sw128(tc::smem_u32(sT), 16, 1024);
         const uint64_t dKQ = tc::sdesc_sw128(tc::smem_u32(sKQ), 16, 1024);
         const uint64_t dK = tc::sdesc_sw128(tc::smem_u32(sKQ) + 8192, 16384, 1024);  // K's rows, columns contiguous
-        for (int c = 0; c < nc; ++c) {
-            const int s = c & 1;
-            const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
+        int it = 0;
+        for (int k = 0; k < items; ++k) {
+        const Item m = get(k);
+        const int64_t len = m.len;
+        for (int c = m.c0; c < m.c1; ++c, ++it) {
+            const int s = it & 1;
+            const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
             const uint64_t kq = dKQ + (uint64_t)(s * 2048), kk = dK + (uint64_t)(s * 2048);
             wait_on(&bars[BAR_KQ_FULL + s], ph2, fail);
             __syncwarp();
@@ -190,7 +215,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 tc::fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (c > 0) wait_on(&bars[BAR_O_READ], ph ^ 1, fail);
+            if (it > 0) wait_on(&bars[BAR_O_READ], ph ^ 1, fail);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 wait_on(&bars[BAR_S_FULL + half], ph, fail);
@@ -235,19 +260,23 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
             tc::mma_commit_if(one, &bars[BAR_C_DONE]);
             tc::mma_commit_if(one, &bars[BAR_KQ_EMPTY + s]);
         }
+        }
         tc::mma_commit_if(one, &bars[BAR_DRAIN]);
         tc::mbar_wait(&bars[BAR_DRAIN], 0, kWaitNs);
         __syncwarp();
     } else if (warp >= kChainWarp0 && warp < kOutWarp0) {
         // ---------------------------------------- elementwise steps of the chain
         const int cw = warp - kChainWarp0, q = cw & 3, ch = cw >> 2;
-        const int hf = NH == 2 ? q >> 1 : 0, h = h0 + hf;
-        const int p32 = NH == 2 ? 32 * (q & 1) : prow0 + 32 * q, p = p32 + lane;  // the warp's first row, this thread's
+        const int hf = NH == 2 ? q >> 1 : 0;
         const uint32_t lq = (uint32_t)(32 * q) << 16;
-        const int64_t srow = ((b * a.H + h) * a.P + p) * a.N;
-        if (NH == 2 || p32 < P) {
+        int it = 0;
+        for (int kk = 0; kk < (2 * q < row_warps ? items : 0); ++kk) {
+            const Item m = get(kk);
+            const int64_t b = m.b, len = m.len;
+            const int h = m.h0 + hf, p = (NH == 2 ? 32 * (q & 1) : m.prow0 + 32 * q) + lane;  // this thread's row
+            const int64_t srow = ((b * a.H + h) * a.P + p) * a.N;
             // 16 columns of the state as hi + lo operands, and scaled for the next accumulation
-            auto put_state = [&](const float (&v)[16], int c0, float eq, int64_t c) {
+            auto put_state = [&](const float (&v)[16], int c0, float eq, int c) {
                 uint32_t hi[8], lo[8], sc[16];
                 const uint64_t e2 = f2(eq, eq);
 #pragma unroll
@@ -267,33 +296,57 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                     if (c0 + 8 < N) o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
                 }
             };
-            float eq = 0.f;
-            if (nc > 0) {
-                wait_on(&bars[BAR_T_FULL], 0, fail);
-                eq = scal[hf * kScalDecay + kScalEnd];
-            }
-            __syncwarp();
-            if (nc > 0 || SAVE) {
-#pragma unroll 1
-                for (int k4 = 0; k4 < 4; ++k4) {
-                    const int c0 = 64 * ch + 16 * k4;
-                    float v[16];
+            // 16 columns of the state from float32 rows, which may be null (zero)
+            auto get_state = [&](float (&v)[16], const float *from, int c0) {
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (a.init && p < P && c0 + k < N) x = *reinterpret_cast<const float4 *>(a.init + srow + c0 + k);
-                        v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
-                    }
-                    put_state(v, c0, eq, 0);
+                for (int k = 0; k < 16; k += 4) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (from && p < P && c0 + k < N) x = __ldcg(reinterpret_cast<const float4 *>(from + srow + c0 + k));
+                    v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
                 }
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&bars[BAR_S_FULL]);
-                tc::mbar_arrive(&bars[BAR_S_FULL + 1]);
+            };
+            // and to them; with SAVE the final state in bf16 as well
+            auto out_state = [&](const float (&v)[16], float *to, int c0, bool last) {
+                if (p >= P) return;
+                if (to)
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4)
+                        if (c0 + k < N)
+                            *reinterpret_cast<float4 *>(to + srow + c0 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                if (SAVE && last) {
+                    uint4 *o = reinterpret_cast<uint4 *>(prm.states + (((b * a.H + h) * (prm.nc + 1) + m.nc) * P + p) * N + c0);
+                    if (c0 < N) o[0] = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+                    if (c0 + 8 < N)
+                        o[1] = make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]), pack2(v[14], v[15]));
+                }
+            };
+            if (m.c0 >= m.c1) {  // no token, or none left
+                if (m.nc == 0 && m.c0 == 0)
+                    for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
+                        float v[16];
+                        get_state(v, a.init, c0);
+                        out_state(v, a.final_state, c0, true);
+                    }
+                continue;
             }
-            for (int c = 0; c < nc; ++c) {
-                const int s = c & 1;
-                const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
+            if (m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
+            wait_on(&bars[BAR_T_FULL + (it & 1)], (it >> 1) & 1, fail);
+            const float eq0 = scal[((it & 1) * NH + hf) * kScalDecay + kScalEnd];
+            __syncwarp();
+#pragma unroll 1
+            for (int k4 = 0; k4 < 4; ++k4) {
+                const int c0 = 64 * ch + 16 * k4;
+                float v[16];
+                get_state(v, m.c0 > 0 ? prm.carry : a.init, c0);
+                put_state(v, c0, eq0, m.c0);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars[BAR_S_FULL]);
+            tc::mbar_arrive(&bars[BAR_S_FULL + 1]);
+            for (int c = m.c0; c < m.c1; ++c, ++it) {
+                const int s = it & 1;
+                const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
                 const float *sc = scal + (s * NH + hf) * kScalDecay + 32 * ch;
                 // R^T = v - exp(c) (K S0^T)^T; vt is this thread's column of the warp's [32 tokens][32 rows]
                 __nv_bfloat16 *vt = reinterpret_cast<__nv_bfloat16 *>(sV + s * 16384 + q * 4096 + ch * 2048) + lane;
@@ -360,12 +413,13 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 }
                 if (lane == 0) tc::mbar_arrive(&bars[BAR_T_EMPTY + s]);
                 // the state that enters the next chunk
-                if (c + 1 < nc) wait_on(&bars[BAR_T_FULL + (s ^ 1)], ((c + 1) >> 1) & 1, fail);
-                const float eqn = c + 1 < nc ? scal[((s ^ 1) * NH + hf) * kScalDecay + kScalEnd] : 0.f;
+                const bool next = c + 1 < m.c1;
+                if (next) wait_on(&bars[BAR_T_FULL + (s ^ 1)], ((it + 1) >> 1) & 1, fail);
+                const float eqn = next ? scal[((s ^ 1) * NH + hf) * kScalDecay + kScalEnd] : 0.f;
                 wait_on(&bars[BAR_C_DONE], ph, fail);
                 __syncwarp();
                 tc::tc_fence_after();
-                if (c + 1 < nc || SAVE) {
+                if (next) {
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const int c0 = 64 * ch + 16 * half;
@@ -373,56 +427,47 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                         tc::tmem_ld16(tS + lq + c0, v0);
                         tc::tmem_ld16(tS + lq + c0 + 32, v1);
                         tc::tmem_ld_wait();
-                        if (c + 1 == nc && a.final_state && p < P) {
-#pragma unroll
-                            for (int k = 0; k < 16; k += 4) {
-                                if (c0 + k < N)
-                                    *reinterpret_cast<float4 *>(a.final_state + srow + c0 + k) =
-                                        make_float4(v0[k], v0[k + 1], v0[k + 2], v0[k + 3]);
-                                if (c0 + 32 + k < N)
-                                    *reinterpret_cast<float4 *>(a.final_state + srow + c0 + 32 + k) =
-                                        make_float4(v1[k], v1[k + 1], v1[k + 2], v1[k + 3]);
-                            }
-                        }
                         put_state(v0, c0, eqn, c + 1);
                         put_state(v1, c0 + 32, eqn, c + 1);
                         tc::tmem_st_wait();
                         tc::tc_fence_before();
                         tc::mbar_arrive(&bars[BAR_S_FULL + half]);
                     }
-                } else if (a.final_state) {
+                } else {
+                    const bool last = m.c1 == m.nc;
+                    float *to = last ? a.final_state : prm.carry;
 #pragma unroll 1
                     for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
                         float v0[16];
                         tc::tmem_ld16(tS + lq + c0, v0);
                         tc::tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            if (p < P && c0 + k < N)
-                                *reinterpret_cast<float4 *>(a.final_state + srow + c0 + k) =
-                                    make_float4(v0[k], v0[k + 1], v0[k + 2], v0[k + 3]);
+                        out_state(v0, to, c0, last);
                     }
                     tc::tc_fence_before();
+                    if (!last) {  // handed on to the next CTA
+                        __threadfence();
+                        asm volatile("bar.sync 1, %0;" ::"r"(32 * row_warps) : "memory");
+                        if (cw == 0 && lane == 0) flag_set(prm.flags + m.unit);
+                    }
                 }
             }
-            if (nc == 0 && a.final_state && p < P)
-                for (int n = 64 * ch; n < imin(N, 64 * ch + 64); n += 4)
-                    *reinterpret_cast<float4 *>(a.final_state + srow + n) =
-                        a.init ? *reinterpret_cast<const float4 *>(a.init + srow + n) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     } else if (warp >= kOutWarp0) {
         // ------------------------------------------------------------ y, and w
         const int cw = warp - kOutWarp0, q = cw & 3, ch = cw >> 2;
-        const int hf = NH == 2 ? q >> 1 : 0, h = h0 + hf;
-        const int p32 = NH == 2 ? 32 * (q & 1) : prow0 + 32 * q, p = p32 + lane;
+        const int hf = NH == 2 ? q >> 1 : 0;
         const uint32_t lq = (uint32_t)(32 * q) << 16;
-        if (NH == 2 || p32 < P) {
-            for (int c = 0; c < nc; ++c) {
-                const int s = c & 1;
+        int it = 0;
+        for (int kk = 0; kk < (2 * q < row_warps ? items : 0); ++kk) {
+            const Item m = get(kk);
+            const int64_t b = m.b;
+            const int h = m.h0 + hf, p32 = NH == 2 ? 32 * (q & 1) : m.prow0 + 32 * q, p = p32 + lane;
+            for (int c = m.c0; c < m.c1; ++c, ++it) {
+                const int s = it & 1;
                 const float *sc = scal + (s * NH + hf) * kScalDecay + 32 * ch;
                 uint16_t *vt = reinterpret_cast<uint16_t *>(sV + s * 16384 + q * 4096 + ch * 2048) + lane;
                 uint16_t *wt = reinterpret_cast<uint16_t *>(sW + q * 4096 + ch * 2048) + lane;
-                wait_on(&bars[BAR_B_DONE], c & 1, fail);
+                wait_on(&bars[BAR_B_DONE], it & 1, fail);
                 __syncwarp();
                 tc::tc_fence_after();
                 float qs[32], o[32];
@@ -442,7 +487,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars[BAR_O_READ]);
-                wait_on(&bars[BAR_T_FULL + s], (c >> 1) & 1, fail);
+                wait_on(&bars[BAR_T_FULL + s], (it >> 1) & 1, fail);
                 const uint64_t s2 = f2(a.scale, a.scale);
                 float4 eg[8];
 #pragma unroll
@@ -470,11 +515,11 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 }
                 __syncwarp();
             }
-            if (a.y && p < P)  // y is zero past the last chunk
-                for (int64_t t = (int64_t)nc * kC + ch; t < a.L; t += 2)
+            if (a.y && p < P && m.c0 == 0)  // y is zero past the last chunk
+                for (int64_t t = (int64_t)m.nc * kC + ch; t < a.L; t += 2)
                     ((__nv_bfloat16 *)a.y)[((b * a.L + t) * a.H + h) * P + p] = __float2bfloat16_rn(0.f);
-            if (lane == 0) tc::bulk_wait_all();
         }
+        if (lane == 0) tc::bulk_wait_all();
     }
     __syncthreads();
     if (tid == 0 && *fail) atomicCAS(a.status, SSD_OK, SSD_ERR_TIMEOUT);
@@ -486,7 +531,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
 
 template <int NH, bool SAVE> cudaError_t launch_form(ChainParams &p, cudaStream_t stream) {
     const DeltaArgs &a = p.a;
-    p.pblocks = (int)((a.P + 127) / 128);
+    p.pblocks = (int)row_blocks(a.P);
     p.units_per_b = (int)(NH == 2 ? a.H / 2 : a.H * p.pblocks);
     static DeviceOnce configured;
     int dev = 0;
@@ -499,8 +544,7 @@ template <int NH, bool SAVE> cudaError_t launch_form(ChainParams &p, cudaStream_
     } else if (e != cudaSuccess) {
         return e;
     }
-    return launch_programmatic(delta_chain_kernel<NH, SAVE>, dim3((unsigned)(a.B * p.units_per_b)), dim3(kThreads),
-                               smem_bytes(NH), stream, p);
+    return launch_chains(delta_chain_kernel<NH, SAVE>, p, a.B * p.units_per_b, p.nc, kThreads, smem_bytes(NH), stream);
 }
 
 }  // namespace
@@ -519,6 +563,8 @@ cudaError_t launch_chain(const PrepArgs &pr, __nv_bfloat16 *states, __nv_bfloat1
     p.scal = pr.scal;
     p.tile_bytes = pr.tile_bytes;
     p.states = states;
+    p.flags = pr.flags;
+    p.carry = pr.carry;
     p.nc = pr.nc;
     const bool pairs = pair_heads(a);
     if (states) return pairs ? launch_form<2, true>(p, stream) : launch_form<1, true>(p, stream);
@@ -537,9 +583,10 @@ bool delta_tc_supported(int io, int64_t B, int64_t L, int64_t H, int64_t P, int6
            device_cc_major_cached() == 10;
 }
 
-size_t delta_tc_workspace(int64_t B, int64_t L, int64_t H) {
-    const size_t items = (size_t)B * H * chunks(L);
-    return 256 + up256(items * delta::kTilesFwd) + up256(items * delta::kScal * 4);
+size_t delta_tc_workspace(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N) {
+    const size_t items = (size_t)(B * H) * chunks(L);
+    return 256 + items * delta::kTilesFwd + up256(items * delta::kScal * 4) + up256((size_t)(B * H * delta::row_blocks(P)) * 8) +
+           (size_t)(B * H * P * N) * 4;
 }
 
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
@@ -547,8 +594,13 @@ cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t st
     p.a = a;
     p.nc = (int64_t)chunks(a.L);
     p.tile_bytes = delta::kTilesFwd;
+    const size_t items = (size_t)(a.B * a.H * p.nc);
     p.tiles = static_cast<uint8_t *>(workspace) + 256;
-    p.scal = reinterpret_cast<float *>(p.tiles + up256((size_t)(a.B * a.H * p.nc) * delta::kTilesFwd));
+    uint8_t *o = p.tiles + items * delta::kTilesFwd;
+    p.scal = reinterpret_cast<float *>(o);
+    o += up256(items * delta::kScal * 4);
+    p.flags = reinterpret_cast<int *>(o);
+    p.carry = reinterpret_cast<float *>(o + up256((size_t)(a.B * a.H * delta::row_blocks(a.P)) * 8));
     cudaError_t e = delta::launch_prep(p, stream);
     return e != cudaSuccess ? e : delta::launch_chain(p, nullptr, nullptr, stream);
 }

@@ -44,11 +44,16 @@ constexpr int kScalEnd = SC_CHAIN * kC, kScalDecay = kScalEnd + 4;  // exp(c_63)
 constexpr uint32_t kScalBytes = kScalDecay * 4;                     // what the chains load
 constexpr int kScal = kScalDecay + 3 * kC;
 
+// Blocks of 128 state rows of a head.
+__host__ __device__ inline int64_t row_blocks(int64_t P) { return (P + 127) / 128; }
+
 struct PrepArgs {
     DeltaArgs a;
     int64_t nc;
     uint8_t *tiles;  // [B][H][nc][tile_bytes]
     float *scal;     // [B][H][nc][kScal]
+    int *flags;      // [2][B H row_blocks(P)]: cleared here, set where the forward or the reverse chain hands a state on
+    float *carry;    // [B][H][P][N]: that state
     uint32_t tile_bytes;
 };
 cudaError_t launch_prep(const PrepArgs &p, cudaStream_t stream);
@@ -113,6 +118,82 @@ static __device__ __noinline__ bool wait_long(uint32_t addr, uint32_t parity, vo
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *fail) {
     const uint32_t addr = tc::smem_u32(bar);
     return tc::mbar_try_wait(addr, parity) || wait_long(addr, parity, fail);
+}
+
+// The chains of chunks laid end to end, nc chunks each, cut into equal segments, one
+// per CTA (to one chunk). With at most one CTA per chain a segment is at least a chain
+// long, so a chain spans two CTAs at most. A CTA first runs the head of the chain it
+// ends in, then its whole chains, then the rest of the chain it begins in, which
+// waits for the state that the CTA before has left in its first item: every
+// head waits for nothing, so every wait ends, and is normally over before it begins.
+struct Segments {
+    int head, head_end, first, whole, rest, rest_start;  // chains (head and rest -1: none) and chunks
+    __device__ void set(int64_t chains, int64_t nc) {
+        const int64_t total = chains * nc, G = gridDim.x;
+        const int64_t start = blockIdx.x * total / G, end = (blockIdx.x + 1) * total / G;
+        const int64_t j0 = start / nc, j1 = (end - 1) / nc, cs = start % nc, ce = (end - 1) % nc + 1;
+        head = rest = -1;
+        head_end = rest_start = 0;
+        if (ce < nc) head = (int)j1, head_end = (int)ce;
+        const int64_t f0 = cs > 0 ? j0 + 1 : j0, f1 = ce < nc ? j1 - 1 : j1;
+        first = (int)f0;
+        whole = f1 >= f0 ? (int)(f1 - f0 + 1) : 0;
+        if (cs > 0) rest = (int)j0, rest_start = (int)cs;
+    }
+    __device__ __forceinline__ int items() const { return (head >= 0) + whole + (rest >= 0); }
+    // chain and chunks [c0, c1) of item k
+    __device__ __forceinline__ void item(int k, int nc, int &chain, int &c0, int &c1) const {
+        if (head >= 0) {
+            if (k == 0) {
+                chain = head, c0 = 0, c1 = head_end;
+                return;
+            }
+            --k;
+        }
+        if (k < whole)
+            chain = first + k, c0 = 0, c1 = nc;
+        else
+            chain = rest, c0 = rest_start, c1 = nc;
+    }
+};
+
+// The flag of a chain whose state is handed on: set by one thread after the others' stores, waited for (bounded).
+__device__ __forceinline__ void flag_set(int *f) { asm volatile("st.release.gpu.global.b32 [%0], 1;" ::"l"(f) : "memory"); }
+static __device__ __noinline__ void flag_wait(const int *f, volatile int *fail) {
+    const uint64_t t0 = tc::global_ns();
+    for (;;) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(f) : "memory");
+        if (v || *fail) return;
+        if (tc::global_ns() - t0 > kWaitNs) {
+            *fail = 1;
+            return;
+        }
+    }
+}
+
+// Launches a chain kernel: one CTA per chain, or one per SM where there are more
+// chains; those wait on one another, so the launch is cooperative then.
+template <typename Params>
+cudaError_t launch_chains(void (*kern)(Params), const Params &p, int64_t chains, int64_t nc, int threads, size_t smem,
+                          cudaStream_t stream) {
+    const int64_t grid = imin<int64_t>(chains, sm_count(1));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (chains * nc % grid == 0 && chains % grid == 0) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeCooperative;
+        attr[0].val.cooperative = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 // Byte offset of 16-byte piece `pc` of row `row` of a tile of 64 bf16 columns in the 128-byte swizzle.

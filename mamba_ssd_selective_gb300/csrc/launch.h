@@ -166,7 +166,7 @@ struct DeltaArgs {
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream);
 // The same in chunks of 64 tokens on the tensor cores.
 bool delta_tc_supported(int io, int64_t B, int64_t L, int64_t H, int64_t P, int64_t N);
-size_t delta_tc_workspace(int64_t B, int64_t L, int64_t H);
+size_t delta_tc_workspace(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N);
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
 
 // Its backward (layouts as in ssd_gated_delta_chunked_bwd).

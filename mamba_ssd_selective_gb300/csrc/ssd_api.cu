@@ -765,7 +765,8 @@ DeltaBwdWs delta_bwd_ws(const ssd_dims *d) {
 
 size_t ssd_gated_delta_workspace_size(const ssd_dims *dims) {
     if (check_delta(dims, true, 1.f) != SSD_OK) return 0;
-    return delta_on_tc(dims) ? ssd::delta_tc_workspace(dims->batch, dims->seqlen, dims->nheads) : 256;
+    return delta_on_tc(dims) ? ssd::delta_tc_workspace(dims->batch, dims->seqlen, dims->nheads, dims->headdim, dims->dstate)
+                             : 256;
 }
 
 ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const void *k, const void *v, const void *g,

@@ -332,3 +332,36 @@ def test_backward_where_beta_is_zero(ssd, io, P):
                                       dfinal_state=dev(df))
     for n in GRADS:
         near(got[n], want[n], io, n)
+
+
+# more chains than SMs: they are cut between CTAs, and the state is handed on between them
+MANY = [(1, 400, 160, 160, 64, 128), (5, 330, 64, 32, 64, 128), (1, 130, 100, 100, 200, 128), (2, 200, 80, 80, 128, 64)]
+
+
+@pytest.mark.parametrize("shape", MANY)
+@pytest.mark.parametrize("ragged", [False, True])
+def test_chains_cut_between_blocks(ssd, shape, ragged):
+    B, L, H, G, P, N = shape
+    lens = [[L, 0, 70, 1, L - 1][i % 5] for i in range(B)] if ragged else None
+    d = inputs.delta_inputs(B, L, H, G, P, N, "bf16", seed=31, init_state=True)
+    t, init = tokens(d, "bf16"), dev(d["init"])
+    for n, x in t.items():
+        for b, m in enumerate(lens or []):
+            x[b, m:] = float("nan")
+    y, S = ssd.gated_delta_chunked(**t, init_state=init, seqlens=lens_of(lens))
+    yr, Sr = delta.delta_seq(*(d[n] for n in NAMES), d["init"], lens)
+    near(y, yr, "bf16", "y")
+    near(S, Sr, "state", "final_state")
+    if P > 128:
+        return
+    r = np.random.default_rng(32)
+    dy = inputs.round_to(r.standard_normal(d["v"].shape), "bf16")
+    df = inputs.round_to(0.1 * r.standard_normal(d["init"].shape), "f32")
+    want = delta.delta_seq_bwd(*(d[n] for n in NAMES), dy, d["init"], df, lens)
+    dyt = dev(dy, torch.bfloat16)
+    for b, m in enumerate(lens or []):
+        dyt[b, m:] = float("nan")
+    got = ssd.gated_delta_chunked_bwd(**t, dy=dyt, init_state=init, dfinal_state=dev(df), seqlens=lens_of(lens))
+    for n in GRADS:
+        near(got[n], want[n], "bf16", n)
+    near(got["dinit"], want["dinit"], "state", "dinit")
