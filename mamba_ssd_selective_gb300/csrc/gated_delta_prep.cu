@@ -10,171 +10,266 @@
 // lost); the fragments of one product are the operands of the next, which
 // the tensor-memory path cannot give at this size.
 //
-// The sums c are taken in float64 and kept as a float32 and its remainder, so
-// that a steep decay does not blur the differences of the tokens after it.
+// The sums c are taken and kept as pairs of float32, value and remainder, so that
+// a steep decay does not blur the differences of the tokens after it (float64
+// would do, but its additions take a third of the block's time on this GPU).
 //
-// Bound by instruction issue (about 5 thousand warp instructions a block); several
-// blocks per SM cover the latencies of one.
+// Bound by instruction issue; five blocks per SM cover the latencies of one.
 #include "gated_delta_tc.cuh"
 
 namespace ssd {
 namespace delta {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kLo = 6;  // A's lo blocks begin at block 6
 // shared memory (bytes): K and Q, 64 rows in panels of 64 columns (128-byte swizzle), later the four tiles; then blocks
 // of A of 512 bytes (hi, then lo), the diagonal ones in float32; then the sums' factors
 constexpr uint32_t kOffBlk = 32768, kOffSc = kOffBlk + 12 * 512 + 4 * 1024;
-enum { S_HI, S_ROW, S_INV, S_N };  // c (base 2) rounded, 2^remainder, beta 2^-remainder
-constexpr uint32_t kSmem = kOffSc + S_N * kC * 4;
+// c (base 2) rounded, 2^remainder, beta 2^-remainder, and that times exp(c at the end of the block of 16 - c)
+enum { S_HI, S_ROW, S_INV, S_COL, S_N };
+constexpr uint32_t kOffBar = kOffSc + S_N * kC * 4, kSmem = kOffBar + 16;
 
 __device__ __forceinline__ int a_blk(int i, int j) { return (i * (i - 1)) / 2 + j; }
 // 16-byte half of a row of a 512-byte block: 32 bytes per row, the halves of rows 4-7 and 12-15 swapped
 __device__ __forceinline__ uint32_t in_blk(int row, int half) { return (uint32_t)(row * 32 + ((half ^ ((row >> 2) & 1)) << 4)); }
 
-// 16 bytes from global to shared memory without waiting; zeros where `on` is false
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
-                 : "memory");
+// a + b as a sum and its rounding error
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
+    const float v = __fadd_rn(a, b), t = __fsub_rn(v, a);
+    e = __fadd_rn(__fsub_rn(a, __fsub_rn(v, t)), __fsub_rn(b, t));
+    s = v;
+}
+// (h + l) log2(e), as a pair
+__device__ __forceinline__ void to_base2(float h, float l, float &ch, float &cl) {
+    constexpr float kHi = 1.44269504088896341f, kLo = (float)(1.44269504088896340736 - (double)1.44269504088896341f);
+    const float p = __fmul_rn(h, kHi);
+    two_sum(p, __fmaf_rn(h, kHi, -p) + (h * kLo + l * kHi), ch, cl);
 }
 
-__global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(PrepArgs p) {
+struct PrepParams {
+    PrepArgs p;
+    CUtensorMap mq, mk;
+};
+
+// Stores an accumulator block (r, k) of a tile as bf16 and, where lo is not null, its remainder.
+__device__ __forceinline__ void put_block(const float (&y)[8], uint8_t *hi, uint8_t *lo, int r, int k, int lane) {
+    const int g = lane >> 2;
+    const uint32_t o = (uint32_t)(g * 128 + (lane & 3) * 4 + ((g & 7) << 4)) ^ (uint32_t)(32 * k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t h, l;
+        split2(y[2 * e], y[2 * e + 1], h, l);
+        const uint32_t at = (o ^ (16u * (e >> 1))) + 2048 * r + 1024 * (e & 1);
+        *reinterpret_cast<uint32_t *>(hi + at) = h;
+        if (lo) *reinterpret_cast<uint32_t *>(lo + at) = l;
+    }
+}
+
+// Row W of the blocks of K K^T and Q K^T, scaled: A to shared memory, M to fragments. W is a template argument
+// because the row has W + 1 blocks, each in registers.
+template <int W>
+__device__ __forceinline__ void rows_of(const PrepArgs &p, uint8_t *smem, int lane, uint32_t (&mh)[4][4], uint32_t (&ml)[4][4]) {
+    uint8_t *sK = smem, *sQ = smem + 16384, *blk = smem + kOffBlk;
+    float *diag = reinterpret_cast<float *>(blk + 12 * 512);
+    const float *sc = reinterpret_cast<const float *>(smem + kOffSc);
+    const int g = lane >> 2, t2 = 2 * (lane & 3), NK = p.a.N <= 64 ? 64 : 128;
+    // lane parts of addresses: the row (lane & 15) and half lane >> 4 of a block for ldmatrix (the pieces of column
+    // block k are those of block 0 with 32 k in their place: xor); for the transposed operand of K K^T
+    const uint32_t lt = (uint32_t)((lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4));
+    const uint32_t ln = (uint32_t)(((lane & 7) + ((lane >> 4) << 3)) * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4));
+    float ak[W + 1][8] = {}, aq[W + 1][8] = {};
+    {
+        const uint32_t k0 = tc::smem_u32(sK), q0 = tc::smem_u32(sQ);
+#pragma unroll 2
+        for (int ks = 0; ks < NK / 16; ++ks) {
+            const uint32_t pan = (ks >> 2) * 8192, x = (ks & 3) << 5;
+            uint32_t fk[4], fq[4], fb[W + 1][4];
+            tc::ldm_x4(fk, k0 + pan + W * 2048 + (lt ^ x));
+            tc::ldm_x4(fq, q0 + pan + W * 2048 + (lt ^ x));
+#pragma unroll
+            for (int j = 0; j <= W; ++j) tc::ldm_x4(fb[j], k0 + pan + j * 2048 + (ln ^ x));
+#pragma unroll
+            for (int j = 0; j <= W; ++j) {
+                tc::mma_block(ak[j], fk, fb[j]);
+                tc::mma_block(aq[j], fq, fb[j]);
+            }
+        }
+    }
+    {
+        const int r0 = 16 * W + g;
+        const float hi0 = sc[S_HI * kC + r0], hi1 = sc[S_HI * kC + r0 + 8];
+        const float rf0 = sc[S_ROW * kC + r0], rf1 = sc[S_ROW * kC + r0 + 8];
+        const uint64_t s2 = f2(p.a.scale, p.a.scale);
+#pragma unroll
+        for (int j = 0; j <= W; ++j) {
+            // a block left of the diagonal: exp(c_t - c_j) = exp(c_t - c_e) exp(c_e - c_j), e the block's last token
+            const float he = sc[S_HI * kC + 16 * j + 15];
+            const float re0 = j < W ? rf0 * tc::ex2(hi0 - he) : rf0, re1 = j < W ? rf1 * tc::ex2(hi1 - he) : rf1;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int col = 16 * j + 8 * n + t2;
+                const float2 fc = *reinterpret_cast<const float2 *>(sc + S_INV * kC + col);
+                uint64_t d0, d1;
+                if (j < W) {
+                    const float2 cc = *reinterpret_cast<const float2 *>(sc + S_COL * kC + col);
+                    d0 = mul2(f2(re0, re0), f2(cc.x, cc.y)), d1 = mul2(f2(re1, re1), f2(cc.x, cc.y));
+                } else {  // nothing above the diagonal (where the exponent could overflow)
+                    const float2 hc = *reinterpret_cast<const float2 *>(sc + S_HI * kC + col);
+                    const float e00 = col <= r0 ? tc::ex2(hi0 - hc.x) : 0.f, e01 = col + 1 <= r0 ? tc::ex2(hi0 - hc.y) : 0.f;
+                    const float e10 = col <= r0 + 8 ? tc::ex2(hi1 - hc.x) : 0.f, e11 = col + 1 <= r0 + 8 ? tc::ex2(hi1 - hc.y) : 0.f;
+                    d0 = mul2(mul2(f2(re0, re0), f2(e00, e01)), f2(fc.x, fc.y));
+                    d1 = mul2(mul2(f2(re1, re1), f2(e10, e11)), f2(fc.x, fc.y));
+                }
+                split2(mul2(mul2(f2(aq[j][4 * n], aq[j][4 * n + 1]), s2), d0), mh[j][2 * n], ml[j][2 * n]);
+                split2(mul2(mul2(f2(aq[j][4 * n + 2], aq[j][4 * n + 3]), s2), d1), mh[j][2 * n + 1], ml[j][2 * n + 1]);
+                const uint64_t a0 = mul2(f2(ak[j][4 * n], ak[j][4 * n + 1]), d0), a1 = mul2(f2(ak[j][4 * n + 2], ak[j][4 * n + 3]), d1);
+                if (j == W) {  // what lies on and above the diagonal of A is not read
+                    float *o = diag + 256 * W + g * 16 + 8 * n + t2;
+                    *reinterpret_cast<uint64_t *>(o) = a0;
+                    *reinterpret_cast<uint64_t *>(o + 128) = a1;
+                } else {
+                    uint32_t hi, lo;
+                    uint8_t *o = blk + a_blk(W, j) * 512 + t2 * 2;
+                    split2(a0, hi, lo);
+                    *reinterpret_cast<uint32_t *>(o + in_blk(g, n)) = hi;
+                    *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g, n)) = lo;
+                    split2(a1, hi, lo);
+                    *reinterpret_cast<uint32_t *>(o + in_blk(g + 8, n)) = hi;
+                    *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g + 8, n)) = lo;
+                }
+            }
+        }
+    }
+}
+
+// Row W of M T.
+template <int W>
+__device__ __forceinline__ void m_times_t(const PrepArgs &p, uint8_t *smem, int lane, const uint32_t (&mh)[4][4],
+                                          const uint32_t (&ml)[4][4]) {
+    const uint32_t lt = (uint32_t)((lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4));
+    const uint32_t h0 = tc::smem_u32(smem) + lt, l0 = h0 + 2 * kTile;
+    uint8_t *mhi = smem + kTile, *mlo = p.tile_bytes > kTilesFwd ? smem + 3 * kTile : nullptr;
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+        float acc[8] = {};
+#pragma unroll
+        for (int k = j; k <= W; ++k) {
+            uint32_t yh[4], yl[4];
+            tc::ldm_x4_trans(yh, (h0 ^ (32 * j)) + 2048 * k);
+            tc::ldm_x4_trans(yl, (l0 ^ (32 * j)) + 2048 * k);
+            tc::mma_block(acc, mh[k], yh);
+            tc::mma_block(acc, mh[k], yl);
+            tc::mma_block(acc, ml[k], yh);
+        }
+        put_block(acc, mhi, mlo, W, j, lane);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(const __grid_constant__ PrepParams prm) {
     pdl_wait();
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sK = smem, *sQ = smem + 16384, *thi = smem, *mhi = smem + kTile, *tlo = smem + 2 * kTile, *mlo = smem + 3 * kTile;
-    uint8_t *blk = smem + kOffBlk;
-    constexpr int kLo = 6;
-    float *diag = reinterpret_cast<float *>(blk + 12 * 512);
-    float *sc = reinterpret_cast<float *>(smem + kOffSc);
+    uint64_t &bar = *reinterpret_cast<uint64_t *>(smem + kOffBar);
+    const PrepArgs &p = prm.p;
     const DeltaArgs &a = p.a;
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t2 = 2 * (lane & 3);
-    const int H = (int)a.H, N = (int)a.N;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int H = (int)a.H;
     const int h = (int)(blockIdx.x % H);
     const int64_t bc = blockIdx.x / H, c = bc % p.nc, b = bc / p.nc;
-    const int grp = h / (int)(a.H / a.G);
     const int64_t len = seq_len(a.seqlens, b, a.L), t0 = c * kC;
+    if (blockIdx.x == 0 && tid == 0) *a.status = SSD_OK;
     if (c == 0) {
         const int pb = (int)row_blocks(a.P);
         for (int x = tid; x < 2 * pb; x += kThreads) p.flags[((x / pb) * a.B * H + b * H + h) * pb + x % pb] = 0;
     }
     if (t0 >= len) return;
     const int64_t item = (b * H + h) * p.nc + c;
-    const int NK = N <= 64 ? 64 : 128;
 
-    // K and Q, zeros past the length and past N (N is a multiple of 8), all copies in flight at once
-    for (int x = tid; x < kC * (NK / 8); x += kThreads) {
-        const int row = x / (NK / 8), pc = x - row * (NK / 8);
-        const bool on = t0 + row < len && 8 * pc < N;
-        const int64_t at = on ? ((b * a.L + t0 + row) * a.G + grp) * N + 8 * pc : 0;
-        const uint32_t o = (pc >> 3) * 8192 + piece(row, pc & 7);
-        copy16(sK + o, (const __nv_bfloat16 *)a.k + at, on);
-        copy16(sQ + o, (const __nv_bfloat16 *)a.q + at, on);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (w == 0) {
-        float gv[2], bv[2];
+    float gv[2] = {0.f, 0.f}, bv[2] = {0.f, 0.f};
+    if (w == 1) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int64_t t = t0 + 2 * lane + e, at = (b * a.L + t) * H + h;
-            gv[e] = t < len ? to_f32(((const __nv_bfloat16 *)a.g)[at]) : 0.f;
-            bv[e] = t < len ? to_f32(((const __nv_bfloat16 *)a.beta)[at]) : 0.f;
+            if (t < len) {
+                gv[e] = to_f32(((const __nv_bfloat16 *)a.g)[at]);
+                bv[e] = to_f32(((const __nv_bfloat16 *)a.beta)[at]);
+            }
             // exp is 0 in float32 long before -256: the sums stay finite, the decays the same
             if (gv[e] < -256.f) gv[e] = -256.f;
         }
-        double sum = (double)gv[0] + (double)gv[1];
+    }
+    if (tid == 0) {
+        tc::mbar_init(&bar, 1);
+        tc::fence_mbar_init();
+        const int grp = h / (int)(a.H / a.G), panels = a.N <= 64 ? 1 : 2;
+        tc::mbar_arrive_expect_tx(&bar, panels * 2 * kTile);
+        for (int k = 0; k < panels; ++k) {
+            tc::tma_load_4d(smem + k * kTile, &prm.mk, &bar, 64 * k, grp, (int)t0, (int)b);
+            tc::tma_load_4d(smem + 16384 + k * kTile, &prm.mq, &bar, 64 * k, grp, (int)t0, (int)b);
+        }
+    }
+    if (w == 1) {
+        float *sc = reinterpret_cast<float *>(smem + kOffSc);
+        float sh, sl;  // the inclusive sum of the lane's two tokens and all before, as a pair
+        two_sum(gv[0], gv[1], sh, sl);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double u = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += u;
+            const float uh = __shfl_up_sync(0xffffffffu, sh, o), ul = __shfl_up_sync(0xffffffffu, sl, o);
+            float h2, l2;
+            two_sum(sh, uh, h2, l2);
+            if (lane >= o) two_sum(h2, l2 + (sl + ul), sh, sl);
         }
-        const double end = __shfl_sync(0xffffffffu, sum, 31) * (double)kLog2e;
+        float ch[2], cl[2], eh, el;  // c of the two tokens and at the end, in base-2 units
+        to_base2(sh, sl, ch[1], cl[1]);
+        two_sum(sh, -gv[1], eh, el);
+        to_base2(eh, el + sl, ch[0], cl[0]);
+        eh = __shfl_sync(0xffffffffu, ch[1], 31);
+        el = __shfl_sync(0xffffffffu, cl[1], 31);
+        const float he = __shfl_sync(0xffffffffu, ch[1], lane | 7);  // at the end of the block of 16
         float *o = p.scal + item * kScal + 2 * lane;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const double c2 = (e ? sum : sum - (double)gv[1]) * (double)kLog2e;  // base-2 units
-            const float hi = (float)c2, lo = (float)(c2 - (double)hi), eg = exp2f((float)c2);
-            const float row = exp2f(lo), inv = bv[e] * exp2f(-lo);
-            sc[S_HI * kC + 2 * lane + e] = hi;
+            const float row = tc::ex2(cl[e]), eg = tc::ex2(ch[e]) * row, inv = bv[e] * tc::ex2(-cl[e]);
+            sc[S_HI * kC + 2 * lane + e] = ch[e];
             sc[S_ROW * kC + 2 * lane + e] = row;
             sc[S_INV * kC + 2 * lane + e] = inv;
+            sc[S_COL * kC + 2 * lane + e] = inv * tc::ex2(he - ch[e]);
             o[SC_EG * kC + e] = eg;
             o[SC_NEG * kC + e] = -eg;
             o[SC_BETA * kC + e] = bv[e];
-            o[SC_BTAIL * kC + e] = bv[e] * exp2f((float)(end - c2));
-            o[kScalDecay + e] = hi;
+            o[SC_BTAIL * kC + e] = bv[e] * tc::ex2((eh - ch[e]) + (el - cl[e]));
+            o[kScalDecay + e] = ch[e];
             o[kScalDecay + kC + e] = row;
             o[kScalDecay + 2 * kC + e] = inv;
         }
-        if (lane == 0) p.scal[item * kScal + kScalEnd] = exp2f((float)end);
+        if (lane == 0) p.scal[item * kScal + kScalEnd] = tc::ex2(eh) * tc::ex2(el);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-
-    // row w of the blocks of K K^T and Q K^T
-    float ak[4][8] = {}, aq[4][8] = {};
-    const uint32_t arow = piece(16 * w + (lane & 15), 0), axor = (lane & 7) << 4, ah = (lane >> 4) << 4;
-    // for the other operand: rows (lane & 7) + 8 (lane >> 4), piece (lane >> 3) & 1
-    const uint32_t brow = piece((lane & 7) + ((lane >> 4) << 3), 0), bh = ((lane >> 3) & 1) << 4;
-    const uint32_t k0 = tc::smem_u32(sK), q0 = tc::smem_u32(sQ);
-#pragma unroll 1
-    for (int ks = 0; ks < NK / 16; ++ks) {
-        const uint32_t pan = (ks >> 2) * 8192, col = (ks & 3) << 5;
-        // a row's pieces are permuted by row & 7 = lane & 7; piece() above already holds that of piece 0
-        uint32_t fk[4], fq[4], fb[4];
-        tc::ldm_x4(fk, k0 + pan + ((arow ^ axor) + ((col + ah) ^ axor)));
-        tc::ldm_x4(fq, q0 + pan + ((arow ^ axor) + ((col + ah) ^ axor)));
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j <= w) {
-                tc::ldm_x4(fb, k0 + pan + j * 2048 + ((brow ^ axor) + ((col + bh) ^ axor)));
-                tc::mma_block(ak[j], fk, fb);
-                tc::mma_block(aq[j], fq, fb);
-            }
+    __syncthreads();  // the barrier is initialised, the sums are there
+    const bool ok = tc::mbar_wait(&bar, 0, kWaitNs);
+    if (t0 + kC > len && len < a.L) {  // tokens past the sequence's length
+        for (int x = (int)(len - t0) * 8 + tid; x < kC * 8; x += kThreads)
+            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4 *>(smem + k * kTile)[x] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
     }
-    // A to shared memory, M to fragments
+    uint8_t *thi = smem, *tlo = smem + 2 * kTile, *mlo = smem + 3 * kTile, *blk = smem + kOffBlk;
+    const float *diag = reinterpret_cast<const float *>(blk + 12 * 512);
     uint32_t mh[4][4], ml[4][4];
-    const int r0 = 16 * w + g;
-    const float hi0 = sc[S_HI * kC + r0], hi1 = sc[S_HI * kC + r0 + 8];
-    const float rf0 = sc[S_ROW * kC + r0], rf1 = sc[S_ROW * kC + r0 + 8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int cl = 16 * j + 8 * n + t2;
-                const float2 hc = *reinterpret_cast<const float2 *>(sc + S_HI * kC + cl);
-                const float2 fc = *reinterpret_cast<const float2 *>(sc + S_INV * kC + cl);
-                float d[4] = {rf0 * (tc::ex2(hi0 - hc.x) * fc.x), rf0 * (tc::ex2(hi0 - hc.y) * fc.y),
-                              rf1 * (tc::ex2(hi1 - hc.x) * fc.x), rf1 * (tc::ex2(hi1 - hc.y) * fc.y)};
-                float av[4], mv[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = r0 + 8 * (e >> 1), col = cl + (e & 1);
-                    if (col > row) d[e] = 0.f;
-                    av[e] = col < row ? ak[j][4 * n + e] * d[e] : 0.f;
-                    mv[e] = col <= row ? aq[j][4 * n + e] * d[e] * a.scale : 0.f;
-                }
-                split2(mv[0], mv[1], mh[j][2 * n], ml[j][2 * n]);
-                split2(mv[2], mv[3], mh[j][2 * n + 1], ml[j][2 * n + 1]);
-                if (j == w) {
-                    float *o = diag + 256 * w + g * 16 + 8 * n + t2;
-                    *reinterpret_cast<float2 *>(o) = make_float2(av[0], av[1]);
-                    *reinterpret_cast<float2 *>(o + 128) = make_float2(av[2], av[3]);
-                } else {
-                    uint32_t hi, lo;
-                    uint8_t *o = blk + a_blk(w, j) * 512 + t2 * 2;
-                    split2(av[0], av[1], hi, lo);
-                    *reinterpret_cast<uint32_t *>(o + in_blk(g, n)) = hi;
-                    *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g, n)) = lo;
-                    split2(av[2], av[3], hi, lo);
-                    *reinterpret_cast<uint32_t *>(o + in_blk(g + 8, n)) = hi;
-                    *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g + 8, n)) = lo;
-                }
-            }
-        }
+    if (w == 0)
+        rows_of<0>(p, smem, lane, mh, ml);
+    else if (w == 1)
+        rows_of<1>(p, smem, lane, mh, ml);
+    else if (w == 2)
+        rows_of<2>(p, smem, lane, mh, ml);
+    else
+        rows_of<3>(p, smem, lane, mh, ml);
     __syncthreads();
     // the tiles take the place of K and Q; zeros above the diagonal
-    for (int x = tid; x < 32768 / 16; x += kThreads) reinterpret_cast<uint4 *>(smem)[x] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int x = 0; x < (int)kTilesFwd / 16 / kThreads; ++x)
+        reinterpret_cast<uint4 *>(smem)[x * kThreads + tid] = make_uint4(0, 0, 0, 0);
+    if (p.tile_bytes > kTilesFwd)
+#pragma unroll
+        for (int x = 0; x < (int)kTile / 16 / kThreads; ++x)
+            reinterpret_cast<uint4 *>(mlo)[x * kThreads + tid] = make_uint4(0, 0, 0, 0);
     // column `lane & 15` of the inverse of diagonal block w, by substitution
     float x[16];
     {
@@ -206,22 +301,10 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(PrepArgs p) {
         }
     }
     __syncthreads();
-    // this lane's row address of a block for ldmatrix: of A, of a tile
-    const uint32_t blk_lane = tc::smem_u32(blk) + in_blk(lane & 15, lane >> 4);
-    auto tile_addr = [&](const uint8_t *tile, int r, int k) {
-        return tc::smem_u32(tile) + piece(16 * r + (lane & 15), 2 * k + (lane >> 4));
-    };
-    // stores an accumulator block as bf16 in a tile
-    auto put_block = [&](const uint32_t (&f)[4], uint8_t *tile, int r, int k) {
-        uint8_t *d = tile + (16 * r + g) * 128 + (lane & 3) * 4;
-        const int p0 = ((2 * k) ^ (g & 7)) << 4, p1 = ((2 * k + 1) ^ (g & 7)) << 4;
-        *reinterpret_cast<uint32_t *>(d + p0) = f[0];
-        *reinterpret_cast<uint32_t *>(d + 1024 + p0) = f[1];
-        *reinterpret_cast<uint32_t *>(d + p1) = f[2];
-        *reinterpret_cast<uint32_t *>(d + 1024 + p1) = f[3];
-    };
     // Off the diagonal, T_ij = -sum_k (sum_m T_im A_mk) T_kj: first within the blocks of 32 (warps 1 and 3: i = w,
     // j = w - 1, one k and m each), then the block of 32 below them (i = 2, 3, j = 0, 1, m from 2 to i, k from j to 1)
+    const uint32_t lt = (uint32_t)((lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4));
+    const uint32_t h0 = tc::smem_u32(thi) + lt, lb = tc::smem_u32(blk) + in_blk(lane & 15, lane >> 4);
 #pragma unroll 1
     for (int level = 0; level < 2; ++level) {
         const int i = level ? 2 + (w >> 1) : w, j = level ? w & 1 : w - 1;
@@ -233,55 +316,41 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(PrepArgs p) {
                 float acc[8] = {};
                 uint32_t xh[4], xl[4], yh[4], yl[4];
 #pragma unroll 1
-                for (int mm = m0; mm <= i; ++mm) {
-                    tc::ldm_x4(xh, tile_addr(thi, i, mm));
-                    tc::ldm_x4(xl, tile_addr(tlo, i, mm));
-                    tc::ldm_x4_trans(yh, blk_lane + a_blk(mm, k) * 512);
-                    tc::ldm_x4_trans(yl, blk_lane + (kLo + a_blk(mm, k)) * 512);
+                for (int m = m0; m <= i; ++m) {
+                    const uint32_t x = (h0 ^ (32 * m)) + 2048 * i, o = lb + a_blk(m, k) * 512;
+                    tc::ldm_x4(xh, x);
+                    tc::ldm_x4(xl, x + 2 * kTile);
+                    tc::ldm_x4_trans(yh, o);
+                    tc::ldm_x4_trans(yl, o + kLo * 512);
                     tc::mma_block(acc, xh, yh);
                     tc::mma_block(acc, xh, yl);
                     tc::mma_block(acc, xl, yh);
                 }
-                tc::ldm_x4_trans(yh, tile_addr(thi, k, j));
-                tc::ldm_x4_trans(yl, tile_addr(tlo, k, j));
+                const uint32_t x = (h0 ^ (32 * j)) + 2048 * k;
+                tc::ldm_x4_trans(yh, x);
+                tc::ldm_x4_trans(yl, x + 2 * kTile);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split2(-acc[2 * e], -acc[2 * e + 1], xh[e], xl[e]);
                 tc::mma_block(y, xh, yh);
                 tc::mma_block(y, xh, yl);
                 tc::mma_block(y, xl, yh);
             }
-            uint32_t yh[4], yl[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split2(y[2 * e], y[2 * e + 1], yh[e], yl[e]);
-            put_block(yh, thi, i, j);
-            put_block(yl, tlo, i, j);
+            put_block(y, thi, tlo, i, j, lane);
         }
         __syncthreads();
     }
-    // row w of M T
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-            float acc[8] = {};
-#pragma unroll
-            for (int k = j; k < 4; ++k)
-                if (k <= w) {
-                    uint32_t yh[4], yl[4];
-                    tc::ldm_x4_trans(yh, tile_addr(thi, k, j));
-                    tc::ldm_x4_trans(yl, tile_addr(tlo, k, j));
-                    tc::mma_block(acc, mh[k], yh);
-                    tc::mma_block(acc, mh[k], yl);
-                    tc::mma_block(acc, ml[k], yh);
-                }
-            uint32_t yh[4], yl[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split2(acc[2 * e], acc[2 * e + 1], yh[e], yl[e]);
-            put_block(yh, mhi, w, j);
-            put_block(yl, mlo, w, j);
-        }
+    if (w == 0)
+        m_times_t<0>(p, smem, lane, mh, ml);
+    else if (w == 1)
+        m_times_t<1>(p, smem, lane, mh, ml);
+    else if (w == 2)
+        m_times_t<2>(p, smem, lane, mh, ml);
+    else
+        m_times_t<3>(p, smem, lane, mh, ml);
     tc::fence_proxy_async_smem();
     __syncthreads();
     if (tid == 0) {
+        if (!ok) atomicCAS(a.status, SSD_OK, SSD_ERR_TIMEOUT);
         tc::bulk_store(p.tiles + item * p.tile_bytes, smem, p.tile_bytes);
         tc::bulk_commit();
         tc::bulk_wait_all();
@@ -291,8 +360,13 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(PrepArgs p) {
 }  // namespace
 
 cudaError_t launch_prep(const PrepArgs &p, cudaStream_t stream) {
+    PrepParams q;
+    q.p = p;
+    if (!tma_map_heads(&q.mq, p.a.q, p.a.N, p.a.G, p.a.L, p.a.B, 64, kC, true) ||
+        !tma_map_heads(&q.mk, p.a.k, p.a.N, p.a.G, p.a.L, p.a.B, 64, kC, true))
+        return cudaErrorInvalidValue;
     return launch_programmatic(delta_prep_kernel, dim3((unsigned)(p.a.B * p.nc * p.a.H)), dim3(kThreads), (size_t)kSmem,
-                               stream, p);
+                               stream, q);
 }
 
 }  // namespace delta

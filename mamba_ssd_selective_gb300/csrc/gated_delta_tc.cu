@@ -142,7 +142,6 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     const uint32_t tmem = *tmem_slot;
     const uint32_t tQS = tmem, tU = tmem + 64, tO = tmem + 128, tS = tmem + 256, tOp = tmem + 384;
     pdl_wait();
-    if (blockIdx.x == 0 && tid == 0) *a.status = SSD_OK;
     const int items = seg.items();
 
     if (warp == 0) {
