@@ -594,8 +594,8 @@ constexpr uint32_t kOffPan = kOffX + kTile; // per 64 state rows: S0 16 KB, E 16
 constexpr uint32_t kPan = 16384 * 3 + kTile;
 __host__ __device__ constexpr uint32_t off_scal(int NPAN) { return kOffPan + NPAN * kPan; }
 __host__ __device__ constexpr uint32_t off_red(int NPAN) { return off_scal(NPAN) + kScal * 4; }
-// sums: [4][64] of dc, [4][64] of dV.w, [64] the previous heads' dc, [64] dbeta where beta is zero, [8] <S1, E>, [8] scratch
-constexpr int kRed = 2 * 256 + 2 * kC + 16;
+// sums: [4][64] of dc, [2][64] of dV.w, [64] the previous heads' dc, [64] dbeta where beta is zero, [8] <S0, E>, [8] scratch
+constexpr int kRed = 256 + 4 * kC + 16;
 __host__ __device__ constexpr uint32_t columns(int NPAN) { return NPAN == 1 ? 256 : 512; }
 __host__ __device__ constexpr uint32_t off_bar(int NPAN) { return off_red(NPAN) + kRed * 4; }
 enum { BAR_FULL, BAR_READY, BAR_G_DONE, BAR_P_FULL, BAR_DONE, kBars };
@@ -604,9 +604,9 @@ __host__ __device__ constexpr size_t smem_bytes(int NPAN) { return off_bar(NPAN)
 
 struct GradParams {
     DeltaArgs a;
-    CUtensorMap mq, mk, ms, me, mdy, mdv, mw;
+    CUtensorMap mq, mk, ms, me, mdy, mdv, mw, mdq, mdk;
     const float *scal;
-    const __nv_bfloat16 *states, *cot, *dv, *w;
+    const __nv_bfloat16 *w;
     __nv_bfloat16 *dq, *dk, *dg, *dbeta;
     int64_t nc;
 };
@@ -621,6 +621,19 @@ template <int O> __device__ __forceinline__ void fold(float (&x)[32], int lane) 
         const float send = up ? x[k] : x[k + O], keep = up ? x[k + O] : x[k];
         x[k] = keep + __shfl_xor_sync(0xffffffffu, send, O);
     }
+}
+
+// 8 bf16 times f, rounded
+__device__ __forceinline__ uint4 scaled8(uint4 v, float f) {
+    uint32_t o[4] = {v.x, v.y, v.z, v.w};
+    const uint64_t f22 = f2(f, f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float x, y;
+        un2(mul2(f2(__uint_as_float(o[k] << 16), __uint_as_float(o[k] & 0xffff0000u)), f22), x, y);
+        o[k] = pack2(x, y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // sum of the products of 8 bf16 pairs
@@ -646,7 +659,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
     uint8_t *sKQ = smem + kOffKQ, *sG = smem + kOffG, *sX = smem + kOffX, *sPan = smem + kOffPan;
     float *sc = reinterpret_cast<float *>(smem + off_scal(NPAN));
     float *red = reinterpret_cast<float *>(smem + off_red(NPAN));
-    float *r_qk = red, *r_vw = red + 256, *prev = red + 512, *dbz = prev + kC, *r_se = dbz + kC;
+    float *r_qk = red, *r_vw = red + 256, *prev = r_vw + 2 * kC, *dbz = prev + kC, *r_se = dbz + kC;
     float *scratch = r_se + 8;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + off_bar(NPAN));
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
@@ -764,23 +777,6 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
         for (int i = 0; i < heads; ++i) {
             const int h = grp * r + i;
             const uint32_t ph = i & 1;
-            const int64_t bh = b * H + h, item = bh * prm.nc + c;
-            {  // <S0, E>, and dV . w of each token
-                const uint4 *s0 = reinterpret_cast<const uint4 *>(prm.states + (bh * (prm.nc + 1) + c) * P * N);
-                const uint4 *e = reinterpret_cast<const uint4 *>(prm.cot + item * P * N);
-                float acc = 0.f;
-                for (int x = tid; x < P * N / 8; x += kElem) acc = dot8(s0[x], e[x], acc);
-                acc = warp_sum(acc);
-                if (lane == 0) r_se[warp] = acc;
-                const int tt = tid & 63, qd = tid >> 6;
-                float vw = 0.f;
-                if (tt < valid) {
-                    const int64_t at = ((b * a.L + t0 + tt) * H + h) * P;
-                    const uint4 *pd = reinterpret_cast<const uint4 *>(prm.dv + at), *pw = reinterpret_cast<const uint4 *>(prm.w + at);
-                    for (int pc = qd; pc < P / 8; pc += 4) vw = dot8(pd[pc], pw[pc], vw);
-                }
-                r_vw[qd * kC + tt] = vw;
-            }
             wait_on(&bars[BAR_FULL], ph, fail);
             __syncwarp();
             if (valid < kC && a.seqlens) {  // dY past the length
@@ -792,16 +788,48 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                         for (int k = 0; k < 4; ++k)
                             reinterpret_cast<uint4 *>(sKQ + k * 8192 + valid * 128)[x] = make_uint4(0, 0, 0, 0);
                 tc::fence_proxy_async_smem();
+                elem_sync();
             }
             tc::mbar_arrive(&bars[BAR_READY]);
+            // under the product: half a row each of dY, or of dV and w, scaled in registers (to be stored over the
+            // tiles once the product has read them), dV . w, and <S0, E>, whose tiles have the same layout
+            uint4 r1[NPAN][4], r2[NPAN][4];
+            {
+                const float f1 = is_v ? sc[SC_NEG * kC + t] : sc[SC_EG * kC + t] * a.scale, f2s = sc[SC_BTAIL * kC + t];
+                float dot = 0.f;
+#pragma unroll
+                for (int pn = 0; pn < NPAN; ++pn) {
+                    const uint8_t *pan = sPan + pn * kPan;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t o = piece(t, 4 * half + k);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(pan + 32768 + (is_v ? kTile : 0) + o);
+                        r1[pn][k] = scaled8(v, f1);
+                        if (is_v) {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(pan + 49152 + o);
+                            dot = dot8(v, u, dot);
+                            r2[pn][k] = scaled8(u, f2s);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint8_t *at = pan + ((t + 64 * half) + 128 * (2 * k + e)) * 16;
+                                dot = dot8(*reinterpret_cast<const uint4 *>(at), *reinterpret_cast<const uint4 *>(at + 16384), dot);
+                            }
+                        }
+                    }
+                }
+                if (is_v) {
+                    r_vw[half * kC + t] = dot;
+                } else {
+                    dot = warp_sum(dot);
+                    if (lane == 0) r_se[(warp & 1) + 2 * half] = dot;
+                }
+            }
             wait_on(&bars[BAR_G_DONE], ph, fail);
             __syncwarp();
             tc::tc_fence_after();
             const float *hi = sc + kScalDecay, *rowf = hi + kC, *inv = rowf + kC;
             {
-                float x[32];
-                tc::tmem_ld32(tG + lq + 32 * half, x);
-                tc::tmem_ld_wait();
                 const float hi_t = hi[t];
                 // tokens whose beta is zero: dbeta_j = w_j . du_j with du formed anew
                 const uint32_t z0 = __ballot_sync(0xffffffffu, lane < valid && sc[SC_BETA * kC + lane] == 0.f);
@@ -811,7 +839,9 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                 while (zero) {
                     const int j = __ffsll((long long)zero) - 1;
                     zero &= zero - 1;
-                    float val = 0.f;
+                    float val = 0.f, y[8];
+                    tc::tmem_ld8(tG + lq + (j & 56), y);
+                    tc::tmem_ld_wait();
                     if ((j >> 5) == half && (is_v ? t > j : t >= j)) {
                         float kd = 0.f;  // q_t . k_j or k_t . k_j
                         for (int pc = 0; pc < 16; ++pc) {
@@ -821,7 +851,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                         }
                         float g = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) g = k == (j & 31) ? x[k] : g;
+                        for (int k = 0; k < 8; ++k) g = k == (j & 7) ? y[k] : g;
                         val = g * kd * tc::ex2(hi_t - hi[j]) * (is_v ? -1.f : a.scale);
                     }
                     // exp(c_63 - c_j) w_j . (E k_j): row tid & 63 of each panel, a quarter of the columns
@@ -846,9 +876,13 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                     }
                     elem_sync();
                 }
+                float x[32];
+                tc::tmem_ld32(tG + lq + 32 * half, x);
+                tc::tmem_ld_wait();
                 const float rf = rowf[t] * (is_v ? -1.f : a.scale);
                 const int last = (is_v ? t - 1 : t) - 32 * half;
                 uint8_t *d = is_v ? sX : sG;
+                const uint64_t rf2 = f2(rf, rf), ht2 = f2(hi_t, hi_t), m1 = f2(-1.f, -1.f);
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
                     uint32_t o[4];
@@ -856,42 +890,33 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                     for (int e = 0; e < 8; e += 4) {
                         const float4 h4 = *reinterpret_cast<const float4 *>(hi + 32 * half + k + e);
                         const float4 f4 = *reinterpret_cast<const float4 *>(inv + 32 * half + k + e);
-                        const float y0 = k + e <= last ? x[k + e] * rf * (tc::ex2(hi_t - h4.x) * f4.x) : 0.f;
-                        const float y1 = k + e + 1 <= last ? x[k + e + 1] * rf * (tc::ex2(hi_t - h4.y) * f4.y) : 0.f;
-                        const float y2 = k + e + 2 <= last ? x[k + e + 2] * rf * (tc::ex2(hi_t - h4.z) * f4.z) : 0.f;
-                        const float y3 = k + e + 3 <= last ? x[k + e + 3] * rf * (tc::ex2(hi_t - h4.w) * f4.w) : 0.f;
-                        o[e / 2] = pack2(y0, y1);
-                        o[e / 2 + 1] = pack2(y2, y3);
+                        float e0, e1, e2, e3;
+                        un2(fma2(f2(h4.x, h4.y), m1, ht2), e0, e1);
+                        un2(fma2(f2(h4.z, h4.w), m1, ht2), e2, e3);
+                        // above the diagonal the exponent could overflow
+                        e0 = k + e <= last ? tc::ex2(e0) : 0.f, e1 = k + e + 1 <= last ? tc::ex2(e1) : 0.f;
+                        e2 = k + e + 2 <= last ? tc::ex2(e2) : 0.f, e3 = k + e + 3 <= last ? tc::ex2(e3) : 0.f;
+                        un2(mul2(mul2(f2(x[k + e], x[k + e + 1]), rf2), mul2(f2(e0, e1), f2(f4.x, f4.y))), e0, e1);
+                        un2(mul2(mul2(f2(x[k + e + 2], x[k + e + 3]), rf2), mul2(f2(e2, e3), f2(f4.z, f4.w))), e2, e3);
+                        o[e / 2] = pack2(e0, e1);
+                        o[e / 2 + 1] = pack2(e2, e3);
                     }
                     *reinterpret_cast<uint4 *>(d + piece(t, 4 * half + k / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-            // dY, dV and w scaled in place (a row's pieces in any order)
-#pragma unroll 1
-            for (int x = tid; x < NPAN * 3 * 512; x += kElem) {
-                const int pn = x / 1536, y = x - pn * 1536, row = (y & 511) >> 3, which = y >> 9;
-                const float f = which == 0 ? sc[SC_EG * kC + row] * a.scale : which == 1 ? sc[SC_NEG * kC + row] : sc[SC_BTAIL * kC + row];
-                uint4 *pt = reinterpret_cast<uint4 *>(sPan + pn * kPan + 32768) + y;
-                uint4 v = *pt;
-                uint32_t o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    o[k] = pack2(__uint_as_float(o[k] << 16) * f, __uint_as_float(o[k] & 0xffff0000u) * f);
-                *pt = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+            for (int pn = 0; pn < NPAN; ++pn)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint8_t *pan = sPan + pn * kPan + piece(t, 4 * half + k);
+                    *reinterpret_cast<uint4 *>(pan + 32768 + (is_v ? kTile : 0)) = r1[pn][k];
+                    if (is_v) *reinterpret_cast<uint4 *>(pan + 49152) = r2[pn][k];
+                }
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
-            elem_sync();
             // dc over this and the previous heads: thread n, 32 tokens each
             float bl = 0.f, bh2 = 0.f, eq = 0.f;  // beta of this thread's tokens, exp(c_63), before the scalars are loaded anew
             if (warp == 0) bl = sc[SC_BETA * kC + 2 * lane], bh2 = sc[SC_BETA * kC + 2 * lane + 1], eq = sc[kScalEnd];
-            uint4 wr[NPAN][4];  // half of a row of beta exp(c_63 - c) w
-            if (is_v)
-#pragma unroll
-                for (int pn = 0; pn < NPAN; ++pn)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        wr[pn][k] = *reinterpret_cast<const uint4 *>(sPan + pn * kPan + 49152 + piece(t, 4 * half + k));
             tc::mbar_arrive(&bars[BAR_P_FULL]);
             wait_on(&bars[BAR_DONE], ph, fail);
             __syncwarp();
@@ -906,7 +931,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t u[4] = {wr[pn][k].x, wr[pn][k].y, wr[pn][k].z, wr[pn][k].w};
+                            const uint32_t u[4] = {r2[pn][k].x, r2[pn][k].y, r2[pn][k].z, r2[pn][k].w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 z = fmaf(__uint_as_float(u[e] << 16), y[8 * k + 2 * e], z);
@@ -955,11 +980,11 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                     const float cum = (r_qk[tt] + r_qk[kC + tt]) + (r_qk[2 * kC + tt] + r_qk[3 * kC + tt]);
                     d[e] = cum - prev[tt];
                     prev[tt] = cum;
-                    vw[e] = (r_vw[tt] + r_vw[kC + tt]) + (r_vw[2 * kC + tt] + r_vw[3 * kC + tt]);
+                    vw[e] = r_vw[tt] + r_vw[kC + tt];
                 }
                 float se = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) se += r_se[k];
+                for (int k = 0; k < 4; ++k) se += r_se[k];
                 se *= eq;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) se += scratch[k];
@@ -983,27 +1008,38 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
             elem_sync();  // the sums' space is free again
         }
         if (heads > 0) {
+            // [64 tokens][64 columns] tiles in the panels' space, stored by TMA
             const int n = 32 * wq + lane;
 #pragma unroll 1
             for (int which = 0; which < 2; ++which) {
                 float x[32];
                 tc::tmem_ld32((which ? tK : tQ) + lq + 32 * half, x);
                 if (which) {
-                    float y[32];
-                    tc::tmem_ld32(tR + lq + 32 * half, y);
-                    tc::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] += y[k];
+                    for (int k0 = 0; k0 < 32; k0 += 16) {
+                        float y[16];
+                        tc::tmem_ld16(tR + lq + 32 * half + k0, y);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x[k0 + k] += y[k];
+                    }
                 }
                 tc::tmem_ld_wait();
-                __nv_bfloat16 *o = which ? prm.dk : prm.dq;
+                __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(sPan + which * 16384 + (n >> 6) * 8192) + (n & 63);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const int tt = 32 * half + k;
-                    if (n < N && tt < rows) o[((b * a.L + t0 + tt) * G + grp) * N + n] = __float2bfloat16_rn(tt < valid ? x[k] : 0.f);
-                }
+                for (int k = 0; k < 32; ++k) o[(32 * half + k) * 64] = __float2bfloat16_rn(32 * half + k < valid ? x[k] : 0.f);
             }
             tc::tc_fence_before();
+            tc::fence_proxy_async_smem();
+            elem_sync();
+            if (tid == 0) {
+                for (int k = 0; k < (N > 64 ? 2 : 1); ++k) {
+                    tc::tma_store_4d(&prm.mdq, sPan + k * 8192, 64 * k, grp, (int)t0, (int)b);
+                    tc::tma_store_4d(&prm.mdk, sPan + 16384 + k * 8192, 64 * k, grp, (int)t0, (int)b);
+                }
+                tc::bulk_commit();
+                tc::bulk_wait_all();
+            }
         } else {  // no token here
             for (int x = tid; x < rows * N; x += kElem) {
                 const int64_t at = ((b * a.L + t0 + x / N) * G + grp) * N + x % N;
@@ -1133,11 +1169,10 @@ cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &args, void *workspace, cudaS
     ok = ok && tma_map_heads(&gp.mdy, args.dy, a.P, a.H, a.L, a.B, 64, kC, true);
     ok = ok && tma_map_heads(&gp.mdv, args.dv, a.P, a.H, a.L, a.B, 64, kC, true);
     ok = ok && tma_map_heads(&gp.mw, bf(s.w), a.P, a.H, a.L, a.B, 64, kC, true);
+    ok = ok && tma_map_heads(&gp.mdq, args.dq, a.N, a.G, a.L, a.B, 64, kC, false);
+    ok = ok && tma_map_heads(&gp.mdk, args.dk, a.N, a.G, a.L, a.B, 64, kC, false);
     if (!ok) return cudaErrorInvalidValue;
     gp.scal = p.scal;
-    gp.states = bf(s.states);
-    gp.cot = bf(s.cot);
-    gp.dv = rp.dv;
     gp.w = bf(s.w);
     gp.dq = static_cast<__nv_bfloat16 *>(args.dq);
     gp.dk = static_cast<__nv_bfloat16 *>(args.dk);
