@@ -2,9 +2,13 @@
 // next, per row, in one pass over the data:
 //     u = y silu(z)      n = u rsqrt(mean u^2 + eps) w_post     (no w_post: n = u)
 //     r = res + s n      out = r rsqrt(mean r^2 + eps) w_pre
-// and its backward. Rows are held in registers in float32 (thread t owns the
-// vectors t, t + threads, ... of the row), statistics are float32 sums over a
-// fixed tree, and each result is rounded once.
+// and its backward. Thread t owns the vectors t, t + threads, ... of a row, in
+// registers in float32; statistics are float32 sums over a fixed tree, and each
+// result is rounded once.
+//
+// Bound by HBM. A block walks rows (row i, i + blocks, ...): the next row is on its
+// way to shared memory (cp.async, each thread copies and reads its own vectors, so
+// nothing but the sums crosses threads) while this one is reduced and written.
 #include "common.cuh"
 #include "launch.h"
 
@@ -13,10 +17,15 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 
-// V consecutive elements as float32, V * sizeof(T) aligned (at most 16 bytes at once).
+// V elements of type T as float32.
 template <typename T, int V> __device__ __forceinline__ void ld(float (&f)[V], const T *p) {
     if constexpr (V == 1) {
         f[0] = to_f32(p[0]);
+    } else if constexpr (V == 8 && sizeof(T) == 2) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[2 * k] = __uint_as_float(w[k] << 16), f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     } else {
 #pragma unroll
         for (int k = 0; k < V; k += 4) {
@@ -33,111 +42,121 @@ template <typename T, int V> __device__ __forceinline__ void st(T *p, const floa
         for (int k = 0; k < V; k += 4)
             *reinterpret_cast<float4 *>(p + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
     } else {
-        T v[V];
+        uint32_t v[V / 2];
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = from_f32<T>(f[k]);
-#pragma unroll
-        for (int k = 0; k < V; k += 4)
-            *reinterpret_cast<uint2 *>(p + k) = *reinterpret_cast<const uint2 *>(v + k);
+        for (int k = 0; k < V / 2; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            v[k] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        if constexpr (V == 8)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+        else
+            *reinterpret_cast<uint2 *>(p) = make_uint2(v[0], v[1]);
     }
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + __expf(-z)); }
+// 1 / (1 + exp(-z)) with the approximate exponential and reciprocal, each within 2 units in the last place
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-// Sum over the block, the same in every thread; `part` is not used by another
-// reduction until a __syncthreads() later.
-__device__ __forceinline__ float block_sum(float v, float *part) {
-    v = warp_sum(v);
+// V weights, or ones where there are none.
+template <int V> __device__ __forceinline__ void weights(float (&w)[V], const float *p, int v) {
+    if (p) {
+        ld<float, V>(w, p + v * V);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[e] = 1.f;
+    }
+}
+
+// Sum over the block, and of two values at once, the same in every thread. `part`
+// is not written again before two more __syncthreads().
+__device__ __forceinline__ float block_sum(float a, float *part) {
+    a = warp_sum(a);
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (lane == 0) part[threadIdx.x >> 5] = v;
+    if (lane == 0) part[threadIdx.x >> 5] = a;
     __syncthreads();
     return warp_sum(lane < nw ? part[lane] : 0.f);
 }
-
-template <typename T, typename TR, int V, int RV>
-__global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs a) {
-    pdl_enter();
-    __shared__ float part[2][kMaxWarps];
-    const int64_t base = (int64_t)blockIdx.x * a.dim;
-    const T *y = (const T *)a.y + base, *z = a.z ? (const T *)a.z + base : nullptr;
-    const TR *res = (const TR *)a.res + base;
-    const int nv = (int)(a.dim / V);
-    const float inv = 1.f / (float)a.dim;
-    float u[RV][V], r[RV][V], ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < RV; ++k) {
-        const int v = threadIdx.x + k * blockDim.x;
-        if (v < nv) {
-            ld<T, V>(u[k], y + (int64_t)v * V);
-            ld<TR, V>(r[k], res + (int64_t)v * V);
-            if (z) {
-                float zz[V];
-                ld<T, V>(zz, z + (int64_t)v * V);
-#pragma unroll
-                for (int e = 0; e < V; ++e) u[k][e] *= zz[e] * sigmoid_f(zz[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(u[k][e], u[k][e], ss);
-        }
-    }
-    float tau = 1.f;
-    if (a.post_w) tau = rsqrtf(block_sum(ss, part[0]) * inv + a.eps);
-    ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < RV; ++k) {
-        const int v = threadIdx.x + k * blockDim.x;
-        if (v < nv) {
-            float w[V], s[V];
-            if (a.post_w) ld<float, V>(w, a.post_w + v * V);
-            if (a.scale) ld<float, V>(s, a.scale + v * V);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float n = u[k][e] * tau;
-                if (a.post_w) n *= w[e];
-                r[k][e] += a.scale ? s[e] * n : n;
-                ss = fmaf(r[k][e], r[k][e], ss);
-            }
-            st<TR, V>((TR *)a.res_out + base + (int64_t)v * V, r[k]);
-        }
-    }
-    const float rho = rsqrtf(block_sum(ss, part[1]) * inv + a.eps);
-#pragma unroll
-    for (int k = 0; k < RV; ++k) {
-        const int v = threadIdx.x + k * blockDim.x;
-        if (v < nv) {
-            float w[V];
-            ld<float, V>(w, a.pre_w + v * V);
-#pragma unroll
-            for (int e = 0; e < V; ++e) w[e] *= r[k][e] * rho;
-            st<T, V>((T *)a.out + base + (int64_t)v * V, w);
-        }
-    }
+__device__ __forceinline__ float2 block_sum(float a, float b, float *part) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) part[threadIdx.x >> 5] = a, part[kMaxWarps + (threadIdx.x >> 5)] = b;
+    __syncthreads();
+    a = lane < nw ? part[lane] : 0.f;
+    b = lane < nw ? part[kMaxWarps + lane] : 0.f;
+    return make_float2(warp_sum(a), warp_sum(b));
 }
 
-// Backward: r is formed again from the inputs (no saved statistics). Block i
-// walks the rows i, i + blocks, ... and keeps its sums of the weights'
-// gradients in registers; block_norm_reduce_kernel adds the blocks' sums.
+// A thread's vectors of one array of a row, copied ahead into shared memory. Vectors
+// of two bytes (V = 1, bf16) cannot be and are read where they lie.
+template <typename T, int V, int RV, bool STAGED = true> struct Ahead {
+    static constexpr int kBytes = V * sizeof(T);
+    static constexpr bool kCopy = STAGED && kBytes >= 4;
+    __host__ __device__ static constexpr size_t bytes(int threads) { return kCopy ? (size_t)RV * threads * kBytes : 0; }
+    __device__ static __forceinline__ void fetch(uint8_t *buf, const T *row, int nv) {
+        if constexpr (kCopy) {
+#pragma unroll
+            for (int k = 0; k < RV; ++k) {
+                const int v = threadIdx.x + k * blockDim.x;
+                if (v >= nv) continue;
+                const uint32_t d = (uint32_t)__cvta_generic_to_shared(buf + (size_t)v * kBytes);
+                const char *s = reinterpret_cast<const char *>(row + (int64_t)v * V);
+                if constexpr (kBytes >= 16) {
+#pragma unroll
+                    for (int e = 0; e < kBytes; e += 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + e), "l"(s + e) : "memory");
+                } else if constexpr (kBytes == 8) {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(s) : "memory");
+                } else {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(s) : "memory");
+                }
+            }
+        }
+    }
+    __device__ static __forceinline__ void get(float (&f)[V], const uint8_t *buf, const T *row, int v) {
+        if constexpr (kCopy)
+            ld<T, V>(f, reinterpret_cast<const T *>(buf) + (size_t)v * V);
+        else
+            ld<T, V>(f, row + (int64_t)v * V);
+    }
+};
+__device__ __forceinline__ void ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void ahead_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
 template <typename T, typename TR, int V, int RV>
-__global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormArgs a) {
+__global__ void __launch_bounds__(256) block_norm_kernel(BlockNormArgs a) {
     pdl_enter();
-    __shared__ float part[4][kMaxWarps];
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float part[2][2][kMaxWarps];
+    using A = Ahead<T, V, RV>;
+    using AR = Ahead<TR, V, RV>;
+    uint8_t *by = smem, *bz = by + A::bytes(blockDim.x), *br = bz + A::bytes(blockDim.x);
+    const T *y = (const T *)a.y, *z = (const T *)a.z;
+    const TR *res = (const TR *)a.res;
     const int nv = (int)(a.dim / V);
     const float inv = 1.f / (float)a.dim;
-    float gpre[RV][V] = {}, gpost[RV][V] = {}, gscale[RV][V] = {};
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    auto fetch = [&](int64_t row) {
+        A::fetch(by, y + row * a.dim, nv);
+        if (z) A::fetch(bz, z + row * a.dim, nv);
+        AR::fetch(br, res + row * a.dim, nv);
+        ahead_commit();
+    };
+    fetch(blockIdx.x);
+    int ph = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ph ^= 1) {
         const int64_t base = row * a.dim;
-        float u[RV][V], r[RV][V], d[RV][V], ss = 0.f;
+        float u[RV][V], r[RV][V], ss = 0.f;
+        ahead_wait<0>();
 #pragma unroll
         for (int k = 0; k < RV; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v < nv) {
-                const int64_t at = base + (int64_t)v * V;
-                ld<T, V>(u[k], (const T *)a.y + at);
-                ld<TR, V>(r[k], (const TR *)a.res + at);
-                ld<T, V>(d[k], (const T *)a.dout + at);
-                if (a.z) {
+                A::get(u[k], by, y + base, v);
+                AR::get(r[k], br, res + base, v);
+                if (z) {
                     float zz[V];
-                    ld<T, V>(zz, (const T *)a.z + at);
+                    A::get(zz, bz, z + base, v);
 #pragma unroll
                     for (int e = 0; e < V; ++e) u[k][e] *= zz[e] * sigmoid_f(zz[e]);
                 }
@@ -145,91 +164,181 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormArgs a) {
                 for (int e = 0; e < V; ++e) ss = fmaf(u[k][e], u[k][e], ss);
             }
         }
+        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
         float tau = 1.f;
-        if (a.post_w) tau = rsqrtf(block_sum(ss, part[0]) * inv + a.eps);
+        if (a.post_w) tau = rsqrtf(block_sum(ss, part[ph][0]) * inv + a.eps);
         ss = 0.f;
-        float ar = 0.f;
+#pragma unroll
+        for (int k = 0; k < RV; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            if (v < nv) {
+                float w[V], s[V];
+                weights(w, a.post_w, v);
+                weights(s, a.scale, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    r[k][e] = fmaf(s[e], u[k][e] * tau * w[e], r[k][e]);
+                    ss = fmaf(r[k][e], r[k][e], ss);
+                }
+                st<TR, V>((TR *)a.res_out + base + (int64_t)v * V, r[k]);
+            }
+        }
+        const float rho = rsqrtf(block_sum(ss, part[ph][1]) * inv + a.eps);
+#pragma unroll
+        for (int k = 0; k < RV; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            if (v < nv) {
+                float w[V];
+                ld<float, V>(w, a.pre_w + v * V);
+#pragma unroll
+                for (int e = 0; e < V; ++e) w[e] *= r[k][e] * rho;
+                st<T, V>((T *)a.out + base + (int64_t)v * V, w);
+            }
+        }
+    }
+}
+
+// Backward: r is formed again from the inputs (no saved statistics), which stay in
+// shared memory while their row is worked on (with two stages the next row's are on
+// their way meanwhile); where a row is too long for that they are read from
+// memory each time (STAGED false). A block keeps its sums of the weights' gradients
+// in registers; block_norm_reduce_kernel adds the blocks' sums.
+// MOST threads at most: 320 (two blocks per SM with one vector per thread: 16384 x
+// 2560 bf16 takes 187 us, 267 us where 122 registers leave one block) or 512.
+template <typename T, typename TR, int V, int RV, bool STAGED, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 320 && RV == 1 ? 2 : 1) block_norm_bwd_kernel(BlockNormArgs a, int stages) {
+    pdl_enter();
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float part[2][4][kMaxWarps];
+    using A = Ahead<T, V, RV, STAGED>;
+    using AR = Ahead<TR, V, RV, STAGED>;
+    const size_t na = A::bytes(blockDim.x), nr = AR::bytes(blockDim.x), stage = 3 * na + 2 * nr;
+    const T *y = (const T *)a.y, *z = (const T *)a.z, *dout = (const T *)a.dout;
+    const TR *res = (const TR *)a.res, *dres_out = (const TR *)a.dres_out;
+    const int nv = (int)(a.dim / V);
+    const float inv = 1.f / (float)a.dim;
+    auto fetch = [&](int64_t row, uint8_t *buf) {
+        const int64_t at = row * a.dim;
+        A::fetch(buf, y + at, nv);
+        if (z) A::fetch(buf + na, z + at, nv);
+        A::fetch(buf + 2 * na, dout + at, nv);
+        AR::fetch(buf + 3 * na, res + at, nv);
+        if (dres_out) AR::fetch(buf + 3 * na + nr, dres_out + at, nv);
+        ahead_commit();
+    };
+    float gpre[RV][V] = {}, gpost[RV][V] = {}, gscale[RV][V] = {};
+    fetch(blockIdx.x, smem);
+    int ph = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ph ^= 1) {
+        const int64_t base = row * a.dim;
+        uint8_t *buf = smem + (stages == 2 && ph ? stage : 0);
+        if (stages == 2 && row + gridDim.x < a.rows) {
+            fetch(row + gridDim.x, smem + (ph ? 0 : stage));
+            ahead_wait<1>();
+        } else {
+            ahead_wait<0>();
+        }
+        float u[RV][V], r[RV][V], d[RV][V], ss = 0.f, ar = 0.f, bu = 0.f;
+#pragma unroll
+        for (int k = 0; k < RV; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            if (v < nv) {
+                A::get(u[k], buf, y + base, v);
+                if (z) {
+                    float zv[V];
+                    A::get(zv, buf + na, z + base, v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) u[k][e] *= zv[e] * sigmoid_f(zv[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) ss = fmaf(u[k][e], u[k][e], ss);
+            }
+        }
+        float tau = 1.f;
+        if (a.post_w) tau = rsqrtf(block_sum(ss, part[ph][0]) * inv + a.eps);
+        ss = 0.f;
 #pragma unroll
         for (int k = 0; k < RV; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v < nv) {
                 float w[V], s[V], p[V];
-                if (a.post_w) ld<float, V>(w, a.post_w + v * V);
-                if (a.scale) ld<float, V>(s, a.scale + v * V);
+                weights(w, a.post_w, v);
+                weights(s, a.scale, v);
                 ld<float, V>(p, a.pre_w + v * V);
+                AR::get(r[k], buf + 3 * na, res + base, v);
+                A::get(d[k], buf + 2 * na, dout + base, v);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    float n = u[k][e] * tau;
-                    if (a.post_w) n *= w[e];
-                    r[k][e] += a.scale ? s[e] * n : n;
+                    u[k][e] *= tau;
+                    r[k][e] = fmaf(s[e], u[k][e] * w[e], r[k][e]);
                     ss = fmaf(r[k][e], r[k][e], ss);
                     ar = fmaf(d[k][e] * p[e], r[k][e], ar);
                 }
             }
         }
-        const float rho = rsqrtf(block_sum(ss, part[1]) * inv + a.eps);
-        const float c = block_sum(ar, part[2]) * inv * rho * rho;
-        float bu = 0.f;
+        const float2 sums = block_sum(ss, ar, part[ph][1]);
+        const float rho = rsqrtf(sums.x * inv + a.eps), c = sums.y * inv * rho * rho;
 #pragma unroll
         for (int k = 0; k < RV; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v < nv) {
-                const int64_t at = base + (int64_t)v * V;
-                float w[V], s[V], p[V], dr[V];
-                if (a.post_w) ld<float, V>(w, a.post_w + v * V);
-                if (a.scale) ld<float, V>(s, a.scale + v * V);
+                float w[V], s[V], p[V], o[V];
+                weights(w, a.post_w, v);
+                weights(s, a.scale, v);
                 ld<float, V>(p, a.pre_w + v * V);
-                if (a.dres_out) ld<TR, V>(dr, (const TR *)a.dres_out + at);
+                if (dres_out) {
+                    AR::get(o, buf + 3 * na + nr, dres_out + base, v);
+                } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
+                    for (int e = 0; e < V; ++e) o[e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {  // u holds u tau
                     gpre[k][e] = fmaf(d[k][e], r[k][e] * rho, gpre[k][e]);
-                    const float x = rho * (d[k][e] * p[e] - r[k][e] * c);
-                    dr[e] = a.dres_out ? dr[e] + x : x;
-                    float n = u[k][e] * tau;
-                    if (a.post_w) n *= w[e];
-                    gscale[k][e] = fmaf(dr[e], n, gscale[k][e]);
-                    const float dn = a.scale ? dr[e] * s[e] : dr[e];
-                    gpost[k][e] = fmaf(dn, u[k][e] * tau, gpost[k][e]);
-                    d[k][e] = a.post_w ? dn * w[e] : dn;
+                    o[e] = fmaf(rho, d[k][e] * p[e] - r[k][e] * c, o[e]);
+                    gscale[k][e] = fmaf(o[e], u[k][e] * w[e], gscale[k][e]);
+                    const float dn = o[e] * s[e];
+                    gpost[k][e] = fmaf(dn, u[k][e], gpost[k][e]);
+                    d[k][e] = dn * w[e];
                     bu = fmaf(d[k][e], u[k][e], bu);
                 }
-                st<TR, V>((TR *)a.dres + at, dr);
+                st<TR, V>((TR *)a.dres + base + (int64_t)v * V, o);
             }
         }
-        float m = 0.f;
-        if (a.post_w) m = block_sum(bu, part[3]) * inv * tau * tau;
+        float m = 0.f;  // mean of (cotangent of the normed u) . (u tau)
+        if (a.post_w) m = block_sum(bu, part[ph][3]) * inv;
 #pragma unroll
         for (int k = 0; k < RV; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v < nv) {
                 const int64_t at = base + (int64_t)v * V;
 #pragma unroll
-                for (int e = 0; e < V; ++e) d[k][e] = tau * (d[k][e] - u[k][e] * m);
-                if (a.z) {
-                    float zz[V], yy[V];
-                    ld<T, V>(zz, (const T *)a.z + at);
-                    ld<T, V>(yy, (const T *)a.y + at);
+                for (int e = 0; e < V; ++e) d[k][e] = tau * fmaf(-u[k][e], m, d[k][e]);
+                if (z) {
+                    float yv[V], zv[V];
+                    A::get(yv, buf, y + base, v);
+                    A::get(zv, buf + na, z + base, v);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const float sg = sigmoid_f(zz[e]), x = d[k][e];
-                        d[k][e] = x * zz[e] * sg;
-                        zz[e] = x * yy[e] * sg * (1.f + zz[e] * (1.f - sg));
+                        const float sg = sigmoid_f(zv[e]), t = zv[e] * sg;
+                        yv[e] *= d[k][e] * fmaf(t, 1.f - sg, sg);
+                        d[k][e] *= t;
                     }
-                    st<T, V>((T *)a.dz + at, zz);
+                    st<T, V>((T *)a.dz + at, yv);
                 }
                 st<T, V>((T *)a.dy + at, d[k]);
             }
         }
-        __syncthreads();  // part is free again
+        if (stages == 1 && row + gridDim.x < a.rows) fetch(row + gridDim.x, smem);
     }
-    float *o = a.part + (int64_t)blockIdx.x * 3 * a.dim;
+    float *out = a.part + (int64_t)blockIdx.x * 3 * a.dim;
 #pragma unroll
     for (int k = 0; k < RV; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
         if (v < nv) {
-            st<float, V>(o + (int64_t)v * V, gpre[k]);
-            st<float, V>(o + a.dim + (int64_t)v * V, gpost[k]);
-            st<float, V>(o + 2 * a.dim + (int64_t)v * V, gscale[k]);
+            st<float, V>(out + (int64_t)v * V, gpre[k]);
+            st<float, V>(out + a.dim + (int64_t)v * V, gpost[k]);
+            st<float, V>(out + 2 * a.dim + (int64_t)v * V, gscale[k]);
         }
     }
 }
@@ -243,8 +352,10 @@ __global__ void __launch_bounds__(256) block_norm_reduce_kernel(BlockNormArgs a,
     float *dst = which == 0 ? a.dpre_w : which == 1 ? a.dpost_w : a.dscale;
     if (!dst) return;
     float v = 0.f;
-    if (col < a.dim)
+    if (col < a.dim) {
+#pragma unroll 4
         for (int i = warp; i < parts; i += 8) v += a.part[((int64_t)i * 3 + which) * a.dim + col];
+    }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && col < a.dim) {
@@ -256,19 +367,22 @@ __global__ void __launch_bounds__(256) block_norm_reduce_kernel(BlockNormArgs a,
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-// Vectors of four elements where the row length allows them (the pointers are
-// 16-byte aligned), else single elements; vectors per thread so that a block
-// of at most 1024 threads holds a row.
-template <typename F> cudaError_t for_row(int64_t dim, F f) {
-    auto pick = [&](auto v) {
-        const int64_t nv = dim / v.value;
-        auto threads = [&](int rv) { return (int)(((nv + rv - 1) / rv + 31) / 32 * 32); };
-        if (nv <= 1024) return f(v, Int<1>{}, threads(1));
-        if (nv <= 2048) return f(v, Int<2>{}, threads(2));
-        if (decltype(v)::value == 4 || nv <= 4096) return f(v, Int<4>{}, threads(4));
-        if constexpr (decltype(v)::value == 1) return f(v, Int<16>{}, threads(16));
-    };
-    return dim % 4 == 0 ? pick(Int<4>{}) : pick(Int<1>{});
+// Vectors of eight or four elements where the row length allows them (the
+// pointers are 16-byte aligned), else single ones; RV of them per thread, the least
+// of the given numbers with which a block of at most `most` threads holds a row.
+template <typename F, int... RVs> cudaError_t with_rv(int64_t nv, int most, F f, std::integer_sequence<int, RVs...>) {
+    cudaError_t e = cudaErrorInvalidValue;
+    bool done = false;
+    ((done || (nv + RVs - 1) / RVs > most ? void() : (done = true, e = f(Int<RVs>{}, (int)(((nv + RVs - 1) / RVs + 31) / 32 * 32)), void())),
+     ...);
+    return e;
+}
+template <typename F> cudaError_t for_row(int64_t dim, int most, F f) {
+    if (dim % 8 == 0)
+        return with_rv(dim / 8, most, [&](auto rv, int t) { return f(Int<8>{}, rv, t); }, std::integer_sequence<int, 1, 2, 4, 8>{});
+    if (dim % 4 == 0)
+        return with_rv(dim / 4, most, [&](auto rv, int t) { return f(Int<4>{}, rv, t); }, std::integer_sequence<int, 1, 2, 4, 8>{});
+    return with_rv(dim, most, [&](auto rv, int t) { return f(Int<1>{}, rv, t); }, std::integer_sequence<int, 1, 4, 8, 32, 64>{});
 }
 
 template <typename F> cudaError_t for_types(int io, int res_io, F f) {
@@ -276,31 +390,73 @@ template <typename F> cudaError_t for_types(int io, int res_io, F f) {
     return f(0.f, 0.f);
 }
 
+// Blocks for `rows` rows: all that are resident at once, and no more.
+template <typename K> cudaError_t resident(K kern, int threads, size_t smem, int64_t rows, int64_t *grid) {
+    if (smem > 40 * 1024) {  // with the static part past the 48 KB that need no asking
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    *grid = imin<int64_t>(rows, sm_count(1));
+    if (rows > *grid) {
+        int per_sm = 0;
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+        if (e != cudaSuccess) return e;
+        *grid = imin<int64_t>(rows, (int64_t)sm_count(1) * imax(1, per_sm));
+    }
+    return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_block_norm(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream) {
     return for_types(io, res_io, [&](auto t, auto tr) {
-        return for_row(a.dim, [&](auto v, auto rv, int threads) {
-            return launch_programmatic(block_norm_kernel<decltype(t), decltype(tr), decltype(v)::value, decltype(rv)::value>,
-                                       dim3((unsigned)a.rows), dim3(threads), 0, stream, a);
+        return for_row(a.dim, 256, [&](auto v, auto rv, int threads) {
+            using T = decltype(t);
+            using TR = decltype(tr);
+            constexpr int V = decltype(v)::value, RV = decltype(rv)::value;
+            auto kern = block_norm_kernel<T, TR, V, RV>;
+            const size_t smem = 2 * Ahead<T, V, RV>::bytes(threads) + Ahead<TR, V, RV>::bytes(threads);
+            int64_t grid = 0;
+            cudaError_t e = resident(kern, threads, smem, a.rows, &grid);
+            return e != cudaSuccess ? e : launch_programmatic(kern, dim3((unsigned)grid), dim3(threads), smem, stream, a);
         });
     });
 }
 
-int block_norm_bwd_parts(int64_t rows, int64_t) { return (int)imin<int64_t>(rows, 2 * (int64_t)sm_count(152)); }
+// The workspace holds the parts of this many blocks (three of 320 threads are resident per SM).
+int block_norm_bwd_parts(int64_t rows, int64_t) { return (int)imin<int64_t>(rows, 4 * (int64_t)sm_count(152)); }
 
 cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream) {
-    const int parts = block_norm_bwd_parts(a.rows, a.dim);
-    cudaError_t e = a.rows == 0 ? cudaSuccess : for_types(io, res_io, [&](auto t, auto tr) {
-        return for_row(a.dim, [&](auto v, auto rv, int threads) {
-            return launch_programmatic(
-                block_norm_bwd_kernel<decltype(t), decltype(tr), decltype(v)::value, decltype(rv)::value>,
-                dim3((unsigned)parts), dim3(threads), 0, stream, a);
+    int64_t parts = 0;
+    if (a.rows > 0) {
+        cudaError_t e = for_types(io, res_io, [&](auto t, auto tr) {
+            return for_row(a.dim, 512, [&](auto v, auto rv, int threads) {
+                using T = decltype(t);
+                using TR = decltype(tr);
+                constexpr int V = decltype(v)::value, RV = decltype(rv)::value;
+                constexpr size_t kMost = 220 * 1024;
+                const size_t stage = 3 * Ahead<T, V, RV>::bytes(threads) + 2 * Ahead<TR, V, RV>::bytes(threads);
+                auto go = [&](auto kern, int stages) {
+                    const size_t smem = stages * stage;
+                    cudaError_t r = resident(kern, threads, smem, a.rows, &parts);
+                    if (r != cudaSuccess) return r;
+                    parts = imin<int64_t>(parts, block_norm_bwd_parts(a.rows, a.dim));
+                    return launch_programmatic(kern, dim3((unsigned)parts), dim3(threads), smem, stream, a, stages);
+                };
+                const int stages = 2 * stage <= kMost ? 2 : 1;
+                if (stage > kMost) {
+                    if constexpr (RV * V >= 16) return go(block_norm_bwd_kernel<T, TR, V, RV, false, 512>, 0);
+                    return cudaErrorInvalidValue;
+                }
+                if constexpr (RV <= 2)
+                    if (threads <= 320) return go(block_norm_bwd_kernel<T, TR, V, RV, true, 320>, stages);
+                return go(block_norm_bwd_kernel<T, TR, V, RV, true, 512>, stages);
+            });
         });
-    });
-    if (e != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
+    }
     return launch_programmatic(block_norm_reduce_kernel, dim3((unsigned)((a.dim + 31) / 32), 3), dim3(256), 0, stream, a,
-                               parts);
+                               (int)parts);
 }
 
 }  // namespace ssd
