@@ -56,6 +56,7 @@ struct ReverseParams {
     __nv_bfloat16 *dv;
     int *flags;             // per chain
     float *carry;           // [B][H][P][N]
+    Pieces pieces;
     int64_t nc;
     int units_per_b, pblocks;
 };
@@ -93,7 +94,7 @@ enum {
 __host__ __device__ constexpr size_t smem_bytes(int NH) { return off_bar(NH) + kBars * 8 + 16 + 1024; }
 }  // namespace rev
 
-template <int NH> __global__ void __launch_bounds__(rev::kThreads, 1)
+template <int NH, int PASS> __global__ void __launch_bounds__(rev::kThreads, 1)
 delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
     using namespace rev;
     static_assert(smem_bytes(NH) <= 232448, "shared memory of one CTA");
@@ -110,20 +111,34 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const int row_warps = NH == 2 || P >= 128 ? 8 : 2 * ((P + 31) / 32);
+    // as in the forward chain; Phi starts from the identity with dY = 0
+    const int cut = PASS == FIND ? find_units(prm.pieces.n, prm.pblocks) : prm.pieces.n * prm.pblocks;
+    int piece = (blockIdx.x % cut) / prm.pblocks, kind = (blockIdx.x % cut) % prm.pblocks;
+    if (PASS == FIND) find_unit(blockIdx.x % cut, prm.pblocks, piece, kind);
+    const bool phi = PASS == FIND && kind == prm.pblocks;
+    const int R = phi ? N : P, row_warps = NH == 2 || R >= 128 ? 8 : 2 * ((R + 31) / 32);
     __shared__ Segments seg;
     // item k: its steps [c0, c1), step i being chunk nc - 1 - i, and where its rows are
     struct Item {
         int64_t b, len;
-        int unit, h0, prow0, grp, c0, c1, nc;
+        int unit, piece, h0, prow0, grp, c0, c1, nc;
     };
     auto get = [&](int k) {
         Item m;
-        seg.item(k, (int)prm.nc, m.unit, m.c0, m.c1);
-        m.b = m.unit / prm.units_per_b;
-        const int un = m.unit % prm.units_per_b;
-        m.h0 = NH == 2 ? 2 * un : un / prm.pblocks;
-        m.prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;
+        if (PASS == WHOLE) {
+            seg.item(k, (int)prm.nc, m.unit, m.c0, m.c1);
+            m.b = m.unit / prm.units_per_b;
+            const int un = m.unit % prm.units_per_b;
+            m.h0 = NH == 2 ? 2 * un : un / prm.pblocks;
+            m.prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;
+        } else {
+            m.piece = piece;
+            m.b = blockIdx.x / cut / a.H;
+            m.h0 = (int)(blockIdx.x / cut % a.H);
+            m.prow0 = phi ? 0 : kind * 128;
+            m.c0 = m.piece * prm.pieces.chunks;
+            m.c1 = m.c0 + prm.pieces.chunks;
+        }
         m.grp = m.h0 / (int)(a.H / a.G);
         m.len = seq_len(a.seqlens, m.b, a.L);
         m.nc = (int)((m.len + kC - 1) / kC);
@@ -141,7 +156,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
         }
         tc::fence_mbar_init();
         *fail = 0;
-        seg.set(a.B * prm.units_per_b, prm.nc);
+        if (PASS == WHOLE) seg.set(a.B * prm.units_per_b, prm.nc);
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, 512);
@@ -152,7 +167,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
     const uint32_t tmem = *tmem_slot;
     const uint32_t tX = tmem, tD = tmem + 64, tE = tmem + 128, tOp = tmem + 256, tY = tmem + 384, tYe = tmem + 448;
     pdl_wait();
-    const int items = seg.items();
+    const int items = PASS == WHOLE ? seg.items() : 1;
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
@@ -184,7 +199,8 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                 bar = &bars[BAR_DY_FULL + s];
                 tc::mbar_arrive_expect_tx(bar, 16384u);
                 for (int k = 0; k < 4; ++k) {
-                    const int hh = NH == 2 ? h0 + (k >> 1) : h0, p = NH == 2 ? 32 * (k & 1) : m.prow0 + 32 * k;
+                    const int hh = NH == 2 ? h0 + (k >> 1) : h0;
+                    const int p = NH == 2 ? 32 * (k & 1) : (phi ? 128 * prm.pblocks : m.prow0) + 32 * k;  // Phi: past P, zeros
                     tc::tma_load_4d(sDY + s * 16384 + k * 4096, &prm.mdy, bar, p, hh, c * kC, (int)b);
                 }
                 n[2] = it + 1;
@@ -314,7 +330,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
             const Item m = get(kk);
             const int64_t b = m.b;
             const int h = m.h0 + hf, p = (NH == 2 ? 32 * (q & 1) : m.prow0 + 32 * q) + lane;
-            const int64_t srow = ((b * a.H + h) * a.P + p) * a.N;
+            const int64_t bh = b * a.H + h, srow = (bh * a.P + p) * a.N;
             // 16 columns of E of chunk c: operands, scaled for the next accumulation, and kept for the gradients
             auto put_state = [&](const float (&v)[16], int c0, float eq, int c) {
                 uint32_t hi[8], lo[8], sc[16];
@@ -330,37 +346,45 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                 tc::tmem_st8(tOp + lq + c0 / 2, hi);
                 tc::tmem_st8(tOp + 64 + lq + c0 / 2, lo);
                 tc::tmem_st16(tE + lq + c0, sc);
-                if (p < P) {
+                if (PASS != FIND && p < P) {
                     uint4 *o = reinterpret_cast<uint4 *>(prm.cot + (((b * a.H + h) * prm.nc + c) * P + p) * N + c0);
                     if (c0 < N) o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     if (c0 + 8 < N) o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
                 }
             };
-            auto get_state = [&](float (&v)[16], const float *from, int c0) {
+            auto get_state = [&](float (&v)[16], const float *row, int c0) {
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (from && p < P && c0 + k < N) x = __ldcg(reinterpret_cast<const float4 *>(from + srow + c0 + k));
+                    if (row && p < R && c0 + k < N) x = __ldcg(reinterpret_cast<const float4 *>(row + c0 + k));
                     v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
                 }
+                if (phi)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = c0 + k == p ? 1.f : 0.f;
             };
-            auto out_state = [&](const float (&v)[16], float *to, int c0) {
-                if (p >= P || !to) return;
+            auto out_state = [&](const float (&v)[16], float *row, int c0) {
+                if (p >= R || !row) return;
 #pragma unroll
                 for (int k = 0; k < 16; k += 4)
-                    if (c0 + k < N)
-                        *reinterpret_cast<float4 *>(to + srow + c0 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    if (c0 + k < N) *reinterpret_cast<float4 *>(row + c0 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
             };
+            auto row_of = [&](auto *states) { return states ? states + srow : nullptr; };
             if (m.c0 >= m.c1) {  // no token, or none left
-                if (m.nc == 0 && m.c0 == 0)
+                if (PASS != FIND && m.nc == 0 && m.c0 == 0)
                     for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
                         float v[16];
-                        get_state(v, prm.dfinal, c0);
-                        out_state(v, prm.dinit, c0);
+                        get_state(v, row_of(prm.dfinal), c0);
+                        out_state(v, row_of(prm.dinit), c0);
                     }
                 continue;
             }
-            if (m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
+            if (PASS == WHOLE && m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
+            const float *from = row_of(prm.dfinal);
+            if (m.c0 > 0)
+                from = PASS == WHOLE ? row_of(prm.carry)
+                       : PASS == FIND ? nullptr
+                                      : prm.pieces.in + ((bh * prm.pieces.n + m.piece) * P + p) * N;
             wait_on(&bars[BAR_SC_FULL + (it & 1)], (it >> 1) & 1, fail);
             const float eq0 = scal[((it & 1) * NH + hf) * kScalDecay + kScalEnd];
             __syncwarp();
@@ -368,7 +392,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
             for (int k4 = 0; k4 < 4; ++k4) {
                 const int c0 = 64 * ch + 16 * k4;
                 float v[16];
-                get_state(v, m.c0 > 0 ? prm.carry : prm.dfinal, c0);
+                get_state(v, from, c0);
                 put_state(v, c0, eq0, m.nc - 1 - m.c0);
             }
             tc::tmem_st_wait();
@@ -457,16 +481,20 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                         tc::mbar_arrive(&bars[BAR_E_FULL + half]);
                     }
                 } else {
-                    const bool last = m.c1 == m.nc;
+                    const bool last = PASS != FIND && m.c1 == m.nc;
+                    float *to = PASS == FIND ? (phi ? prm.pieces.phi + ((bh * (prm.pieces.n - 1) + m.piece) * N + p) * N
+                                                    : prm.pieces.psi + ((bh * (prm.pieces.n - 1) + m.piece) * P + p) * N)
+                                : last       ? row_of(prm.dinit)
+                                             : (PASS == WHOLE ? row_of(prm.carry) : nullptr);
 #pragma unroll 1
                     for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
                         float v0[16];
                         tc::tmem_ld16(tE + lq + c0, v0);
                         tc::tmem_ld_wait();
-                        out_state(v0, last ? prm.dinit : prm.carry, c0);
+                        out_state(v0, to, c0);
                     }
                     tc::tc_fence_before();
-                    if (!last) {  // handed on to the next CTA
+                    if (PASS == WHOLE && !last) {  // handed on to the next CTA
                         __threadfence();
                         asm volatile("bar.sync 1, %0;" ::"r"(32 * row_warps) : "memory");
                         if (cw == 0 && lane == 0) flag_set(prm.flags + m.unit);
@@ -539,6 +567,11 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                     wait_on(&bars[BAR_B_DONE], it & 1, fail);
                     __syncwarp();
                     tc::tc_fence_after();
+                    if constexpr (PASS == FIND) {
+                        if (lane == 0) tc::mbar_arrive(&bars[BAR_D_READ]);
+                        __syncwarp();
+                        continue;
+                    }
                     float x[32];
                     tc::tmem_ld32(tD + lq + 32 * ch, x);
                     tc::tmem_ld_wait();
@@ -562,7 +595,7 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                         tc::bulk_commit();
                     }
                 }
-                if (p < P && m.c0 == 0)  // zero past the last chunk
+                if (PASS != FIND && p < P && m.c0 == 0)  // zero past the last chunk
                     for (int64_t t = (int64_t)m.nc * kC + ch; t < a.L; t += 2)
                         prm.dv[((m.b * a.L + t) * a.H + h) * P + p] = __float2bfloat16_rn(0.f);
             }
@@ -1059,7 +1092,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
     }
 }
 
-template <int NH> cudaError_t launch_reverse(ReverseParams &p, cudaStream_t stream) {
+template <int NH, int PASS> cudaError_t launch_reverse(ReverseParams &p, cudaStream_t stream) {
     const DeltaArgs &a = p.a;
     p.pblocks = (int)row_blocks(a.P);
     p.units_per_b = (int)(NH == 2 ? a.H / 2 : a.H * p.pblocks);
@@ -1067,14 +1100,19 @@ template <int NH> cudaError_t launch_reverse(ReverseParams &p, cudaStream_t stre
     int dev = 0;
     cudaError_t e = cudaSuccess;
     if (configured.pending(&dev, &e)) {
-        e = cudaFuncSetAttribute(delta_reverse_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(delta_reverse_kernel<NH, PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)rev::smem_bytes(NH));
         if (e != cudaSuccess) return e;
         configured.done(dev);
     } else if (e != cudaSuccess) {
         return e;
     }
-    return launch_chains(delta_reverse_kernel<NH>, p, a.B * p.units_per_b, p.nc, rev::kThreads, rev::smem_bytes(NH), stream);
+    if (PASS != WHOLE) {
+        const int64_t grid = a.B * a.H * (PASS == FIND ? find_units(p.pieces.n, p.pblocks) : p.pieces.n * p.pblocks);
+        return launch_programmatic(delta_reverse_kernel<NH, PASS>, dim3((unsigned)grid), dim3(rev::kThreads),
+                                   rev::smem_bytes(NH), stream, p);
+    }
+    return launch_chains(delta_reverse_kernel<NH, PASS>, p, a.B * p.units_per_b, p.nc, rev::kThreads, rev::smem_bytes(NH), stream);
 }
 
 template <int NPAN> cudaError_t launch_grad(const GradParams &p, cudaStream_t stream) {
@@ -1096,7 +1134,7 @@ template <int NPAN> cudaError_t launch_grad(const GradParams &p, cudaStream_t st
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct BwdWs {
-    size_t tiles, scal, flags, carry, states, cot, w, total;
+    size_t tiles, scal, flags, carry, pieces, states, cot, w, total;
 };
 BwdWs bwd_ws(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N) {
     const size_t nc = (size_t)((L + kC - 1) / kC), items = (size_t)(B * H) * nc;
@@ -1105,7 +1143,8 @@ BwdWs bwd_ws(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N) {
     s.scal = s.tiles + items * kTilesBwd;
     s.flags = s.scal + up256(items * kScal * 4);
     s.carry = s.flags + up256((size_t)(B * H * row_blocks(P)) * 8);
-    s.states = s.carry + up256((size_t)(B * H * P * N) * 4);
+    s.pieces = s.carry + up256((size_t)(B * H * P * N) * 4);
+    s.states = s.pieces + up256(plan_pieces(B, H, P, (int64_t)nc, true).bytes(B * H, P, N));
     s.cot = s.states + up256((items + (size_t)(B * H)) * P * N * 2);
     s.w = s.cot + up256(items * P * N * 2);
     s.total = s.w + up256((size_t)(B * L * H * P) * 2);
@@ -1137,6 +1176,8 @@ cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &args, void *workspace, cudaS
     p.tile_bytes = kTilesBwd;
     p.flags = reinterpret_cast<int *>(base + s.flags);
     p.carry = reinterpret_cast<float *>(base + s.carry);
+    p.pieces = plan_pieces(a.B, a.H, a.P, p.nc, true);
+    p.pieces.carve(base + s.pieces, a.B * a.H, a.P, a.N);
     cudaError_t e = launch_prep(p, stream);
     if (e == cudaSuccess) e = launch_chain(p, bf(s.states), bf(s.w), stream);
     if (e != cudaSuccess) return e;
@@ -1157,7 +1198,14 @@ cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &args, void *workspace, cudaS
     rp.flags = p.flags + a.B * a.H * row_blocks(a.P);
     rp.carry = p.carry;
     rp.nc = p.nc;
-    e = pair_heads(a) ? launch_reverse<2>(rp, stream) : launch_reverse<1>(rp, stream);
+    rp.pieces = p.pieces;
+    if (p.pieces.n > 1) {
+        e = launch_reverse<1, FIND>(rp, stream);
+        if (e == cudaSuccess) e = launch_combine(p.pieces, a.B * a.H, a.P, a.N, stream);
+        if (e == cudaSuccess) e = launch_reverse<1, PIECES>(rp, stream);
+    } else {
+        e = pair_heads(a) ? launch_reverse<2, WHOLE>(rp, stream) : launch_reverse<1, WHOLE>(rp, stream);
+    }
     if (e != cudaSuccess) return e;
 
     GradParams gp;

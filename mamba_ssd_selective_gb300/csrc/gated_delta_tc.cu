@@ -27,7 +27,8 @@
 // Warps: 0 loads; 1 products; 4-11 the chain's elementwise steps (two warps per
 // 32 rows, half of the tokens or columns each); 12-19 y (and w for the backward).
 //
-// Where there are more chains than SMs they are cut into equal segments (Segments).
+// Where there are more chains than SMs they are cut into equal segments (Segments),
+// where there are few into pieces that run at once (Pieces).
 //
 // Bound by the latency of the chain. A product of 16 columns of K takes 64
 // cycles whatever N, 36 of them a chunk (NH = 1); the rest is the elementwise steps
@@ -53,6 +54,7 @@ struct ChainParams {
     __nv_bfloat16 *states;  // SAVE: [B][H][nc + 1][P][N] states entering each chunk, then the final one
     int *flags;             // per chain
     float *carry;           // [B][H][P][N]
+    Pieces pieces;
     int64_t nc;
     int units_per_b;  // NH = 2: head pairs; NH = 1: heads times blocks of 128 rows
     int pblocks;      // NH = 1: ceil(P / 128)
@@ -84,7 +86,7 @@ enum {
 };
 __host__ __device__ constexpr size_t smem_bytes(int NH) { return off_bar(NH) + kBars * 8 + 16 + 1024; }
 
-template <int NH, bool SAVE> __global__ void __launch_bounds__(kThreads, 1)
+template <int NH, bool SAVE, int PASS> __global__ void __launch_bounds__(kThreads, 1)
 delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     static_assert(smem_bytes(NH) <= 232448, "shared memory of one CTA");
     const DeltaArgs &a = prm.a;
@@ -99,21 +101,36 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    // warps with rows of the state; those whose rows lie past P take no part
-    const int row_warps = NH == 2 || P >= 128 ? 8 : 2 * ((P + 31) / 32);
+    // a piece's CTA: of its chain's `cut`, the piece and the block of rows, or Phi
+    const int cut = PASS == FIND ? find_units(prm.pieces.n, prm.pblocks) : prm.pieces.n * prm.pblocks;
+    int piece = (blockIdx.x % cut) / prm.pblocks, kind = (blockIdx.x % cut) % prm.pblocks;
+    if (PASS == FIND) find_unit(blockIdx.x % cut, prm.pblocks, piece, kind);
+    const bool phi = PASS == FIND && kind == prm.pblocks;
+    const int R = phi ? N : P;  // rows of the state
+    // warps with rows of the state; those whose rows lie past R take no part
+    const int row_warps = NH == 2 || R >= 128 ? 8 : 2 * ((R + 31) / 32);
     __shared__ Segments seg;
-    // item k: its chunks [c0, c1) that hold tokens, and where its rows are; false: no chunk
+    // item k: its chunks [c0, c1) that hold tokens, and where its rows are
     struct Item {
         int64_t b, len;
-        int unit, h0, prow0, grp, c0, c1, nc;
+        int unit, piece, h0, prow0, grp, c0, c1, nc;
     };
     auto get = [&](int k) {
         Item m;
-        seg.item(k, (int)prm.nc, m.unit, m.c0, m.c1);
-        m.b = m.unit / prm.units_per_b;
-        const int un = m.unit % prm.units_per_b;
-        m.h0 = NH == 2 ? 2 * un : un / prm.pblocks;
-        m.prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;  // state row of lane 0
+        if (PASS == WHOLE) {
+            seg.item(k, (int)prm.nc, m.unit, m.c0, m.c1);
+            m.b = m.unit / prm.units_per_b;
+            const int un = m.unit % prm.units_per_b;
+            m.h0 = NH == 2 ? 2 * un : un / prm.pblocks;
+            m.prow0 = NH == 2 ? 0 : (un % prm.pblocks) * 128;  // state row of lane 0
+        } else {
+            m.piece = piece;
+            m.b = blockIdx.x / cut / a.H;
+            m.h0 = (int)(blockIdx.x / cut % a.H);
+            m.prow0 = phi ? 0 : kind * 128;
+            m.c0 = m.piece * prm.pieces.chunks;
+            m.c1 = m.c0 + prm.pieces.chunks;
+        }
         m.grp = m.h0 / (int)(a.H / a.G);
         m.len = seq_len(a.seqlens, m.b, a.L);
         m.nc = (int)((m.len + kC - 1) / kC);
@@ -131,7 +148,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
         }
         tc::fence_mbar_init();
         *fail = 0;
-        seg.set(a.B * prm.units_per_b, prm.nc);
+        if (PASS == WHOLE) seg.set(a.B * prm.units_per_b, prm.nc);
     }
     if (warp == 1) {
         tc::tmem_alloc(tmem_slot, 512);
@@ -142,7 +159,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     const uint32_t tmem = *tmem_slot;
     const uint32_t tQS = tmem, tU = tmem + 64, tO = tmem + 128, tS = tmem + 256, tOp = tmem + 384;
     pdl_wait();
-    const int items = seg.items();
+    const int items = PASS == WHOLE ? seg.items() : 1;
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
@@ -173,7 +190,8 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                     bar = &bars[BAR_V_FULL + s];
                     tc::mbar_arrive_expect_tx(bar, 16384u);
                     for (int e = 0; e < 4; ++e) {
-                        const int hh = NH == 2 ? m.h0 + (e >> 1) : m.h0, p = NH == 2 ? 32 * (e & 1) : m.prow0 + 32 * e;
+                        const int hh = NH == 2 ? m.h0 + (e >> 1) : m.h0;
+                        const int p = NH == 2 ? 32 * (e & 1) : (phi ? 128 * prm.pblocks : m.prow0) + 32 * e;  // Phi: past P, zeros
                         tc::tma_load_4d(sV + s * 16384 + e * 4096, &prm.mv, bar, p, hh, c * kC, (int)m.b);
                     }
                     v_done = it + 1;
@@ -273,7 +291,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
             const Item m = get(kk);
             const int64_t b = m.b, len = m.len;
             const int h = m.h0 + hf, p = (NH == 2 ? 32 * (q & 1) : m.prow0 + 32 * q) + lane;  // this thread's row
-            const int64_t srow = ((b * a.H + h) * a.P + p) * a.N;
+            const int64_t bh = b * a.H + h, srow = (bh * a.P + p) * a.N;  // this thread's row of [B][H][P][N]
             // 16 columns of the state as hi + lo operands, and scaled for the next accumulation
             auto put_state = [&](const float (&v)[16], int c0, float eq, int c) {
                 uint32_t hi[8], lo[8], sc[16];
@@ -295,23 +313,26 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                     if (c0 + 8 < N) o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
                 }
             };
-            // 16 columns of the state from float32 rows, which may be null (zero)
-            auto get_state = [&](float (&v)[16], const float *from, int c0) {
+            // 16 columns of the state from this thread's float32 row, which may be null (zero; Phi: the identity)
+            auto get_state = [&](float (&v)[16], const float *row, int c0) {
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (from && p < P && c0 + k < N) x = __ldcg(reinterpret_cast<const float4 *>(from + srow + c0 + k));
+                    if (row && p < R && c0 + k < N) x = __ldcg(reinterpret_cast<const float4 *>(row + c0 + k));
                     v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
                 }
+                if (phi)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = c0 + k == p ? 1.f : 0.f;
             };
             // and to them; with SAVE the final state in bf16 as well
-            auto out_state = [&](const float (&v)[16], float *to, int c0, bool last) {
-                if (p >= P) return;
-                if (to)
+            auto out_state = [&](const float (&v)[16], float *row, int c0, bool last) {
+                if (p >= R) return;
+                if (row)
 #pragma unroll
                     for (int k = 0; k < 16; k += 4)
                         if (c0 + k < N)
-                            *reinterpret_cast<float4 *>(to + srow + c0 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                            *reinterpret_cast<float4 *>(row + c0 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                 if (SAVE && last) {
                     uint4 *o = reinterpret_cast<uint4 *>(prm.states + (((b * a.H + h) * (prm.nc + 1) + m.nc) * P + p) * N + c0);
                     if (c0 < N) o[0] = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
@@ -319,16 +340,22 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                         o[1] = make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]), pack2(v[14], v[15]));
                 }
             };
+            auto row_of = [&](auto *states) { return states ? states + srow : nullptr; };
             if (m.c0 >= m.c1) {  // no token, or none left
-                if (m.nc == 0 && m.c0 == 0)
+                if (PASS != FIND && m.nc == 0 && m.c0 == 0)
                     for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
                         float v[16];
-                        get_state(v, a.init, c0);
-                        out_state(v, a.final_state, c0, true);
+                        get_state(v, row_of(a.init), c0);
+                        out_state(v, row_of(a.final_state), c0, true);
                     }
                 continue;
             }
-            if (m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
+            if (PASS == WHOLE && m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
+            const float *from = row_of(a.init);
+            if (m.c0 > 0)
+                from = PASS == WHOLE ? row_of(prm.carry)
+                       : PASS == FIND ? nullptr
+                                      : prm.pieces.in + ((bh * prm.pieces.n + m.piece) * P + p) * N;
             wait_on(&bars[BAR_T_FULL + (it & 1)], (it >> 1) & 1, fail);
             const float eq0 = scal[((it & 1) * NH + hf) * kScalDecay + kScalEnd];
             __syncwarp();
@@ -336,7 +363,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
             for (int k4 = 0; k4 < 4; ++k4) {
                 const int c0 = 64 * ch + 16 * k4;
                 float v[16];
-                get_state(v, m.c0 > 0 ? prm.carry : a.init, c0);
+                get_state(v, from, c0);
                 put_state(v, c0, eq0, m.c0);
             }
             tc::tmem_st_wait();
@@ -433,8 +460,11 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                         tc::mbar_arrive(&bars[BAR_S_FULL + half]);
                     }
                 } else {
-                    const bool last = m.c1 == m.nc;
-                    float *to = last ? a.final_state : prm.carry;
+                    const bool last = PASS != FIND && m.c1 == m.nc;
+                    float *to = PASS == FIND ? (phi ? prm.pieces.phi + ((bh * (prm.pieces.n - 1) + m.piece) * N + p) * N
+                                                    : prm.pieces.psi + ((bh * (prm.pieces.n - 1) + m.piece) * P + p) * N)
+                                : last       ? row_of(a.final_state)
+                                             : (PASS == WHOLE ? row_of(prm.carry) : nullptr);
 #pragma unroll 1
                     for (int c0 = 64 * ch; c0 < 64 * ch + 64; c0 += 16) {
                         float v0[16];
@@ -443,7 +473,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                         out_state(v0, to, c0, last);
                     }
                     tc::tc_fence_before();
-                    if (!last) {  // handed on to the next CTA
+                    if (PASS == WHOLE && !last) {  // handed on to the next CTA
                         __threadfence();
                         asm volatile("bar.sync 1, %0;" ::"r"(32 * row_warps) : "memory");
                         if (cw == 0 && lane == 0) flag_set(prm.flags + m.unit);
@@ -469,6 +499,15 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 wait_on(&bars[BAR_B_DONE], it & 1, fail);
                 __syncwarp();
                 tc::tc_fence_after();
+                if constexpr (PASS == FIND) {  // no outputs: the buffers are free at once
+                    if (lane == 0) {
+                        tc::mbar_arrive(&bars[BAR_O_READ]);
+                        tc::mbar_arrive(&bars[BAR_T_EMPTY + s]);
+                        tc::mbar_arrive(&bars[BAR_V_EMPTY + s]);
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 float qs[32], o[32];
                 if (SAVE) {
                     tc::tmem_ld32(tU + lq + 32 * ch, qs);
@@ -514,7 +553,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 }
                 __syncwarp();
             }
-            if (a.y && p < P && m.c0 == 0)  // y is zero past the last chunk
+            if (PASS != FIND && a.y && p < P && m.c0 == 0)  // y is zero past the last chunk
                 for (int64_t t = (int64_t)m.nc * kC + ch; t < a.L; t += 2)
                     ((__nv_bfloat16 *)a.y)[((b * a.L + t) * a.H + h) * P + p] = __float2bfloat16_rn(0.f);
         }
@@ -528,7 +567,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     }
 }
 
-template <int NH, bool SAVE> cudaError_t launch_form(ChainParams &p, cudaStream_t stream) {
+template <int NH, bool SAVE, int PASS> cudaError_t launch_form(ChainParams &p, cudaStream_t stream) {
     const DeltaArgs &a = p.a;
     p.pblocks = (int)row_blocks(a.P);
     p.units_per_b = (int)(NH == 2 ? a.H / 2 : a.H * p.pblocks);
@@ -536,14 +575,19 @@ template <int NH, bool SAVE> cudaError_t launch_form(ChainParams &p, cudaStream_
     int dev = 0;
     cudaError_t e = cudaSuccess;
     if (configured.pending(&dev, &e)) {
-        e = cudaFuncSetAttribute(delta_chain_kernel<NH, SAVE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(delta_chain_kernel<NH, SAVE, PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem_bytes(NH));
         if (e != cudaSuccess) return e;
         configured.done(dev);
     } else if (e != cudaSuccess) {
         return e;
     }
-    return launch_chains(delta_chain_kernel<NH, SAVE>, p, a.B * p.units_per_b, p.nc, kThreads, smem_bytes(NH), stream);
+    if (PASS != WHOLE) {
+        const int64_t grid = a.B * a.H * (PASS == FIND ? find_units(p.pieces.n, p.pblocks) : p.pieces.n * p.pblocks);
+        return launch_programmatic(delta_chain_kernel<NH, SAVE, PASS>, dim3((unsigned)grid), dim3(kThreads), smem_bytes(NH),
+                                   stream, p);
+    }
+    return launch_chains(delta_chain_kernel<NH, SAVE, PASS>, p, a.B * p.units_per_b, p.nc, kThreads, smem_bytes(NH), stream);
 }
 
 }  // namespace
@@ -565,9 +609,89 @@ cudaError_t launch_chain(const PrepArgs &pr, __nv_bfloat16 *states, __nv_bfloat1
     p.flags = pr.flags;
     p.carry = pr.carry;
     p.nc = pr.nc;
+    p.pieces = pr.pieces;
+    if (p.pieces.n > 1) {
+        cudaError_t e = launch_form<1, false, FIND>(p, stream);
+        if (e == cudaSuccess) e = launch_combine(p.pieces, a.B * a.H, a.P, a.N, stream);
+        if (e != cudaSuccess) return e;
+        return states ? launch_form<1, true, PIECES>(p, stream) : launch_form<1, false, PIECES>(p, stream);
+    }
     const bool pairs = pair_heads(a);
-    if (states) return pairs ? launch_form<2, true>(p, stream) : launch_form<1, true>(p, stream);
-    return pairs ? launch_form<2, false>(p, stream) : launch_form<1, false>(p, stream);
+    if (states) return pairs ? launch_form<2, true, WHOLE>(p, stream) : launch_form<1, true, WHOLE>(p, stream);
+    return pairs ? launch_form<2, false, WHOLE>(p, stream) : launch_form<1, false, WHOLE>(p, stream);
+}
+
+Pieces plan_pieces(int64_t B, int64_t H, int64_t P, int64_t nc, bool backward) {
+    Pieces q{1, (int)nc, nullptr, nullptr, nullptr};
+    const int64_t pb = row_blocks(P), sms = sm_count(152) / imax<int64_t>(1, B * H);
+    const int64_t most = imin<int64_t>(1 + (sms + 1) / (pb + 1), sms / pb);
+    double best = (backward ? 5.9 : 2.45) * (double)nc;
+    for (int64_t n = 2; n <= imin<int64_t>(most, nc); ++n) {
+        const int64_t chunks = (nc + n - 1) / n;
+        const double t = (backward ? 11.5 : 5.3) * (double)chunks + (backward ? 1.4 : 0.7) * (double)(n - 1) + (backward ? 30. : 20.);
+        if (t < best && (n - 1) * chunks < nc) best = t, q.n = (int)n, q.chunks = (int)chunks;
+    }
+    return q;
+}
+
+namespace {
+
+// The state carried over the pieces, S Phi + Psi in float32. A CTA has kCarryRows rows;
+// thread (n, j) adds up the j-th quarter of the products of column n, and the
+// quarters are then added in a fixed order. Its column of the next Phi is in flight
+// meanwhile, so that a piece costs its 128 x kCarryRows products a column and two barriers.
+constexpr int kCarryRows = 4, kCarryPart = 32;
+__global__ void __launch_bounds__(512, 1) combine_kernel(Pieces q, int P, int N) {
+    pdl_wait();
+    __shared__ float4 s[128];  // [column], kCarryRows rows
+    __shared__ float part[4][kCarryRows][128];
+    const int n = threadIdx.x & 127, j = threadIdx.x >> 7, m0 = j * kCarryPart;
+    const int64_t bh = blockIdx.x, p = (int64_t)blockIdx.y * kCarryRows + j;  // the row that this thread adds up
+    const bool mine = n < N && p < P;
+    const float *phi = q.phi + bh * (q.n - 1) * N * N + n, *psi = q.psi + (bh * (q.n - 1) * P + p) * N + n;
+    float *in = q.in + (bh * q.n * P + p) * N + n;
+    float f[2][kCarryPart], add[2];
+    auto fetch = [&](int k, float (&to)[kCarryPart], float &plus) {
+        const bool some = k < q.n - 1;
+        plus = some && mine ? psi[(int64_t)k * P * N] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kCarryPart; ++i) to[i] = some && n < N && m0 + i < N ? phi[((int64_t)k * N + m0 + i) * N] : 0.f;
+    };
+    auto leave = [&](int k, float v) {
+        if (mine) in[(int64_t)k * P * N] = v;
+        reinterpret_cast<float *>(&s[n])[j] = v;
+    };
+    auto step = [&](int k, const float (&now)[kCarryPart], float plus) {
+        float v[kCarryRows] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kCarryPart; ++i) {
+            const float4 x = s[m0 + i];
+            v[0] = fmaf(x.x, now[i], v[0]), v[1] = fmaf(x.y, now[i], v[1]);
+            v[2] = fmaf(x.z, now[i], v[2]), v[3] = fmaf(x.w, now[i], v[3]);
+        }
+#pragma unroll
+        for (int r = 0; r < kCarryRows; ++r) part[j][r][n] = v[r];
+        __syncthreads();
+        leave(k + 1, ((part[0][j][n] + part[1][j][n]) + (part[2][j][n] + part[3][j][n])) + plus);
+        __syncthreads();
+    };
+    fetch(1, f[1], add[1]);
+    leave(1, mine ? psi[0] : 0.f);
+    __syncthreads();
+    for (int k = 1; k < q.n - 1; k += 2) {
+        fetch(k + 1, f[0], add[0]);
+        step(k, f[1], add[1]);
+        if (k + 1 == q.n - 1) break;
+        fetch(k + 2, f[1], add[1]);
+        step(k + 1, f[0], add[0]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const Pieces &q, int64_t BH, int64_t P, int64_t N, cudaStream_t stream) {
+    return launch_programmatic(combine_kernel, dim3((unsigned)BH, (unsigned)((P + kCarryRows - 1) / kCarryRows)), dim3(512), 0,
+                               stream, q, (int)P, (int)N);
 }
 
 }  // namespace delta
@@ -585,7 +709,7 @@ bool delta_tc_supported(int io, int64_t B, int64_t L, int64_t H, int64_t P, int6
 size_t delta_tc_workspace(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N) {
     const size_t items = (size_t)(B * H) * chunks(L);
     return 256 + items * delta::kTilesFwd + up256(items * delta::kScal * 4) + up256((size_t)(B * H * delta::row_blocks(P)) * 8) +
-           (size_t)(B * H * P * N) * 4;
+           up256((size_t)(B * H * P * N) * 4) + delta::plan_pieces(B, H, P, (int64_t)chunks(L), false).bytes(B * H, P, N);
 }
 
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
@@ -599,7 +723,10 @@ cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t st
     p.scal = reinterpret_cast<float *>(o);
     o += up256(items * delta::kScal * 4);
     p.flags = reinterpret_cast<int *>(o);
-    p.carry = reinterpret_cast<float *>(o + up256((size_t)(a.B * a.H * delta::row_blocks(a.P)) * 8));
+    o += up256((size_t)(a.B * a.H * delta::row_blocks(a.P)) * 8);
+    p.carry = reinterpret_cast<float *>(o);
+    p.pieces = delta::plan_pieces(a.B, a.H, a.P, p.nc, false);
+    p.pieces.carve(o + up256((size_t)(a.B * a.H * a.P * a.N) * 4), a.B * a.H, a.P, a.N);
     cudaError_t e = delta::launch_prep(p, stream);
     return e != cudaSuccess ? e : delta::launch_chain(p, nullptr, nullptr, stream);
 }

@@ -47,6 +47,46 @@ constexpr int kScal = kScalDecay + 3 * kC;
 // Blocks of 128 state rows of a head.
 __host__ __device__ inline int64_t row_blocks(int64_t P) { return (P + 127) / 128; }
 
+// Few chains leave most of the GPU idle, and a chain's chunks cannot overlap. What a
+// stretch of chunks does to a state is linear, S -> S Phi + Psi with Phi [N, N]
+// and Psi [P, N], and the chain kernels find both: Psi is the state they leave
+// when they start from zero, Phi the one that they leave on N rows when they start from
+// the identity with v = 0. So a chain of nc chunks is cut into n pieces; Phi
+// and Psi of all but the last are found at once (of the first only what it makes of the
+// chain's first state), combine_kernel carries the state over the pieces, and a second
+// run of all pieces at once forms the outputs. All of it in float32, Phi and Psi from
+// the same hi + lo products as the states.
+struct Pieces {
+    int n, chunks;          // n = 1: the chain whole
+    float *phi, *psi, *in;  // [B H][n - 1][N][N], [B H][n - 1][P][N], [B H][n][P][N] states entering the pieces; no [0]
+    size_t bytes(int64_t BH, int64_t P, int64_t N) const {
+        return n == 1 ? 0 : sizeof(float) * (size_t)BH * (size_t)((n - 1) * N * (N + P) + n * P * N);
+    }
+    void carve(void *base, int64_t BH, int64_t P, int64_t N) {
+        phi = static_cast<float *>(base);
+        psi = phi + BH * (n - 1) * N * N;
+        in = psi + BH * (n - 1) * P * N;
+    }
+};
+// How the chains are run: whole (handed on between CTAs where they are cut), the
+// pieces' Phi and Psi, or the pieces from their entering states.
+enum { WHOLE, FIND, PIECES };
+// The number of pieces, from times on GB300: whole, a chunk takes 2.45 us (5.9 with the
+// backward's two chains); in pieces 5.3 (11.5), and 0.7 (1.4) for each piece that the
+// state is carried over and 20 (30) for the launches more. Every CTA has an SM of its
+// own. Whole against pieces, whole calls, N 128, P 64: B1 L4096 H24 187 and 132 us (backward
+// 466 and 305), B1 L8192 H4 322 and 88 (767 and 189), B1 L2048 H24 100 and 85 (247 and 188);
+// and where this rule leaves them whole: B1 L1024 H24 55 and 58, B1 L768 H4 44 and 46 (B1 L1024 H48 160 and 182).
+Pieces plan_pieces(int64_t B, int64_t H, int64_t P, int64_t nc, bool backward);
+// The CTAs of a chain in the first run, and what CTA i of it does: `kind` a block of rows of Psi or, past them, Phi.
+__host__ __device__ inline int find_units(int n, int pblocks) { return (n - 1) * (pblocks + 1) - 1; }
+__device__ __forceinline__ void find_unit(int i, int pblocks, int &piece, int &kind) {
+    i += i >= pblocks;  // the first piece has no Phi
+    piece = i / (pblocks + 1), kind = i % (pblocks + 1);
+}
+// in[piece] from phi and psi
+cudaError_t launch_combine(const Pieces &q, int64_t BH, int64_t P, int64_t N, cudaStream_t stream);
+
 struct PrepArgs {
     DeltaArgs a;
     int64_t nc;
@@ -54,6 +94,7 @@ struct PrepArgs {
     float *scal;     // [B][H][nc][kScal]
     int *flags;      // [2][B H row_blocks(P)]: cleared here, set where the forward or the reverse chain hands a state on
     float *carry;    // [B][H][P][N]: that state
+    Pieces pieces;
     uint32_t tile_bytes;
 };
 cudaError_t launch_prep(const PrepArgs &p, cudaStream_t stream);

@@ -336,14 +336,17 @@ def test_backward_where_beta_is_zero(ssd, io, P):
 
 # more chains than SMs: they are cut between CTAs, and the state is handed on between them
 MANY = [(1, 400, 160, 160, 64, 128), (5, 330, 64, 32, 64, 128), (1, 130, 100, 100, 200, 128), (2, 200, 80, 80, 128, 64)]
+# and few chains of many chunks, which are cut into pieces that run at once
+FEW = [(1, 1500, 2, 1, 64, 128), (2, 1100, 2, 2, 128, 128), (1, 1281, 3, 1, 48, 64), (5, 1300, 1, 1, 64, 128), (1, 1024, 4, 1, 200, 40)]
 
 
-@pytest.mark.parametrize("shape", MANY)
+# with the slow decay the state of one piece is still felt in the next
+@pytest.mark.parametrize("shape,rate", [(s, 1.0) for s in MANY + FEW] + [(s, 0.01) for s in FEW])
 @pytest.mark.parametrize("ragged", [False, True])
-def test_chains_cut_between_blocks(ssd, shape, ragged):
+def test_chains_cut_between_blocks(ssd, shape, rate, ragged):
     B, L, H, G, P, N = shape
     lens = [[L, 0, 70, 1, L - 1][i % 5] for i in range(B)] if ragged else None
-    d = inputs.delta_inputs(B, L, H, G, P, N, "bf16", seed=31, init_state=True)
+    d = inputs.delta_inputs(B, L, H, G, P, N, "bf16", seed=31, init_state=True, rate=rate)
     t, init = tokens(d, "bf16"), dev(d["init"])
     for n, x in t.items():
         for b, m in enumerate(lens or []):
