@@ -15,7 +15,6 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 128, kRowsPass = kThreads / 8;  // rows a block handles at once
-constexpr int kTile = 32;                                // tokens staged at once
 
 __device__ __forceinline__ float group_sum(float v) {
     v += __shfl_xor_sync(0xffffffffu, v, 1);
@@ -111,15 +110,21 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepArgs a, i
 
 // --------------------------------------------------- recurrent forward
 // One block per (b, h, 16 rows): the state stays in registers over the whole
-// sequence, tokens are staged in shared memory 32 at a time. With `ckpt` the
-// states entering every ckpt_len-th token are stored for the backward.
+// sequence. What bounds it is the latency of a token, from the old state over
+// the sums of 8 lanes to the new state; so everything else is off that way: 16
+// tokens are staged in shared memory while the next 16 are on their way to
+// registers, a token's k and q are read while the one before it is done, k . q is
+// formed at staging, and the dots are taken of S_{t-1}, the decay coming after.
+// With `ckpt` the states entering every ckpt_len-th token are stored for the backward.
+constexpr int kStage = kRowsPass;  // tokens staged at once; group t of lanes forms k . q of token t
+
 template <typename T, int VW, int NE>
 __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaArgs a, float *ckpt, int ckpt_len) {
     pdl_enter();
     extern __shared__ float sm[];
     const int N = (int)a.N, P = (int)a.P;
-    float *sk = sm, *sq = sk + kTile * N, *sv = sq + kTile * N;
-    float *sa = sv + kTile * kRowsPass, *sb = sa + kTile, *skq = sb + kTile;
+    float *sk = sm, *sq = sk + kStage * N;
+    __shared__ float sv[kStage * kRowsPass], sa[kStage], sb[kStage], skq[kStage];
     const int64_t bh = blockIdx.x;
     const int h = (int)(bh % a.H);
     const int64_t b = bh / a.H;
@@ -137,54 +142,85 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaArgs a, 
 #pragma unroll
         for (int e = 0; e < NE; ++e) s[e] = 0.f;
     }
-    for (int64_t t0 = 0; t0 < len; t0 += kTile) {
-        const int nt = (int)imin<int64_t>(kTile, len - t0);
-        __syncthreads();
-        for (int x = threadIdx.x; x < nt * N; x += kThreads) {
-            const int t = x / N, n = x - t * N;
-            const int64_t at = ((b * a.L + t0 + t) * a.G + i) * N + n;
-            sk[x] = to_f32(((const T *)a.k)[at]);
-            sq[x] = a.q ? to_f32(((const T *)a.q)[at]) : 0.f;
+    // Staged element x = e kThreads + thread of [kStage][N] (NE kThreads >= kStage N), of v [kStage][rows].
+    T rk[NE], rq[NE], rv[2], rg, rb;
+    static_assert(kStage * 8 == kThreads && kStage * kRowsPass == 2 * kThreads, "the shares of a thread");
+    auto fetch = [&](int64_t t0) {
+        const int nt = (int)imin<int64_t>(kStage, len - t0);
+        if (nt <= 0) return;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int x = e * kThreads + threadIdx.x, t = x / N;
+            const int64_t at = ((b * a.L + t0 + t) * a.G + i) * N + (x - t * N);
+            rk[e] = t < nt ? ((const T *)a.k)[at] : from_f32<T>(0.f);
+            rq[e] = t < nt && a.q ? ((const T *)a.q)[at] : from_f32<T>(0.f);
         }
-        for (int x = threadIdx.x; x < nt * kRowsPass; x += kThreads) {
-            const int t = x / kRowsPass, r = x - t * kRowsPass;
-            sv[x] = p0 + r < P ? to_f32(((const T *)a.v)[((b * a.L + t0 + t) * a.H + h) * P + p0 + r]) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int x = e * kThreads + threadIdx.x, t = x / kRowsPass, r = x % kRowsPass;
+            rv[e] = t < nt && p0 + r < P ? ((const T *)a.v)[((b * a.L + t0 + t) * a.H + h) * P + p0 + r] : from_f32<T>(0.f);
         }
         if ((int)threadIdx.x < nt) {
             const int64_t at = (b * a.L + t0 + threadIdx.x) * a.H + h;
-            sa[threadIdx.x] = expf(to_f32(((const T *)a.g)[at]));
-            sb[threadIdx.x] = to_f32(((const T *)a.beta)[at]);
+            rg = ((const T *)a.g)[at];
+            rb = ((const T *)a.beta)[at];
+        }
+    };
+    fetch(0);
+    for (int64_t t0 = 0; t0 < len; t0 += kStage) {
+        const int nt = (int)imin<int64_t>(kStage, len - t0);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int x = e * kThreads + threadIdx.x;
+            if (x < kStage * N) sk[x] = to_f32(rk[e]), sq[x] = to_f32(rq[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sv[e * kThreads + threadIdx.x] = to_f32(rv[e]);
+        if ((int)threadIdx.x < nt) {
+            sa[threadIdx.x] = expf(to_f32(rg));
+            sb[threadIdx.x] = to_f32(rb);
         }
         __syncthreads();
-        for (int t = row; t < nt + row; t += kRowsPass) {  // k . q of each staged token
+        fetch(t0 + kStage);
+        float kv[NE], qv[NE];
+        {
             float d = 0.f;
-            if (t < nt)
-                for (int n = j; n < N; n += 8) d = fmaf(sk[t * N + n], sq[t * N + n], d);
+            load_row<VW, NE>(kv, sk + row * N, N, j);
+            load_row<VW, NE>(qv, sq + row * N, N, j);
+#pragma unroll
+            for (int e = 0; e < NE; ++e) d = fmaf(kv[e], qv[e], d);
             d = group_sum(d);
-            if (t < nt && j == 0) skq[t] = d;
+            if (j == 0) skq[row] = d;
         }
         __syncthreads();
+        load_row<VW, NE>(kv, sk, N, j);
+        load_row<VW, NE>(qv, sq, N, j);
+#pragma unroll 2
         for (int t = 0; t < nt; ++t) {
             if (ckpt && (t0 + t) % ckpt_len == 0 && on)
                 store_row<VW, NE>(s, ckpt + (((bh * nck + (t0 + t) / ckpt_len) * P) + p) * N, N, j);
-            float d = 0.f, o = 0.f, kv[NE];
-            const float alpha = sa[t];
-            load_row<VW, NE>(kv, sk + t * N, N, j);
-            float qv[NE];
-            load_row<VW, NE>(qv, sq + t * N, N, j);
+            const int next = imin(t + 1, kStage - 1);
+            float nk[NE], nq[NE];
+            load_row<VW, NE>(nk, sk + next * N, N, j);
+            load_row<VW, NE>(nq, sq + next * N, N, j);
+            const float alpha = sa[t], beta = sb[t], v = sv[t * kRowsPass + row], kq = skq[t];
+            float d[4] = {}, o[4] = {};
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
+                d[e & 3] = fmaf(s[e], kv[e], d[e & 3]);
+                o[e & 3] = fmaf(s[e], qv[e], o[e & 3]);
                 s[e] *= alpha;
-                d = fmaf(s[e], kv[e], d);
-                o = fmaf(s[e], qv[e], o);
             }
-            d = group_sum(d);
-            o = group_sum(o);
-            const float u = sb[t] * (sv[t * kRowsPass + row] - d);
+            const float sd = group_sum((d[0] + d[1]) + (d[2] + d[3])), so = group_sum((o[0] + o[1]) + (o[2] + o[3]));
+            const float u = beta * fmaf(-alpha, sd, v);
 #pragma unroll
-            for (int e = 0; e < NE; ++e) s[e] = fmaf(u, kv[e], s[e]);
+            for (int e = 0; e < NE; ++e) {
+                s[e] = fmaf(u, kv[e], s[e]);
+                kv[e] = nk[e], qv[e] = nq[e];
+            }
             if (a.y && on && j == 0)
-                ((T *)a.y)[((b * a.L + t0 + t) * a.H + h) * P + p] = from_f32<T>(a.scale * fmaf(u, skq[t], o));
+                ((T *)a.y)[((b * a.L + t0 + t) * a.H + h) * P + p] = from_f32<T>(a.scale * fmaf(u, kq, alpha * so));
         }
     }
     if (a.final_state && on) store_row<VW, NE>(s, a.final_state + (bh * P + p) * N, N, j);
@@ -413,7 +449,7 @@ template <typename T>
 cudaError_t forward_t(const DeltaArgs &a, float *ckpt, int ckpt_len, cudaStream_t stream) {
     return for_width(a.N, [&](auto vw, auto ne) {
         auto kern = delta_recurrent_kernel<T, vw.value, ne.value>;
-        const size_t smem = sizeof(float) * (kTile * (2 * a.N + kRowsPass + 3));
+        const size_t smem = sizeof(float) * kStage * 2 * a.N;
         cudaError_t e = with_smem(kern, smem);
         if (e != cudaSuccess) return e;
         const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.P + kRowsPass - 1) / kRowsPass));

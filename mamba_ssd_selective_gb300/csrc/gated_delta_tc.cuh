@@ -44,6 +44,10 @@ constexpr int kScalEnd = SC_CHAIN * kC, kScalDecay = kScalEnd + 4;  // exp(c_63)
 constexpr uint32_t kScalBytes = kScalDecay * 4;                     // what the chains load
 constexpr int kScal = kScalDecay + 3 * kC;
 
+// Whether these kernels take a call: its sizes fit, and it isn't so short (tokens x blocks of 16 rows at most `few`,
+// and at most 16 tokens) that the recurrent kernels are faster.
+bool tc_takes(int io, int64_t B, int64_t L, int64_t H, int64_t P, int64_t N, int64_t few);
+
 // Blocks of 128 state rows of a head.
 __host__ __device__ inline int64_t row_blocks(int64_t P) { return (P + 127) / 128; }
 
