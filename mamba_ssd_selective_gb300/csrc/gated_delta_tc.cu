@@ -636,62 +636,75 @@ Pieces plan_pieces(int64_t B, int64_t H, int64_t P, int64_t nc, bool backward) {
 
 namespace {
 
-// The state carried over the pieces, S Phi + Psi in float32. A CTA has kCarryRows rows;
+// The state carried over the pieces, S Phi + Psi in float32. A CTA has ROWS rows;
 // thread (n, j) adds up the j-th quarter of the products of column n, and the
-// quarters are then added in a fixed order. Its column of the next Phi is in flight
-// meanwhile, so that a piece costs its 128 x kCarryRows products a column and two barriers.
-constexpr int kCarryRows = 4, kCarryPart = 32;
-__global__ void __launch_bounds__(512, 1) combine_kernel(Pieces q, int P, int N) {
+// quarters are then added in a fixed order. A value of Phi is replaced by the next
+// piece's as soon as it has been used, so that a piece costs its products and two barriers.
+// 4 rows where these CTAs have an SM each, else 8, so that fewer read all of Phi: a whole call
+// of B1 L8192 H4 takes 88 us with 4 and 97 with 8, the backward of B1 L2048 H24 184 and 180.
+constexpr int kCarryPart = 32;
+template <int ROWS> __global__ void __launch_bounds__(512, 2) combine_kernel(Pieces q, int P, int N) {
     pdl_wait();
-    __shared__ float4 s[128];  // [column], kCarryRows rows
-    __shared__ float part[4][kCarryRows][128];
+    __shared__ float4 s[128][ROWS / 4];  // [column][row]
+    __shared__ float part[4][ROWS][128];
     const int n = threadIdx.x & 127, j = threadIdx.x >> 7, m0 = j * kCarryPart;
-    const int64_t bh = blockIdx.x, p = (int64_t)blockIdx.y * kCarryRows + j;  // the row that this thread adds up
-    const bool mine = n < N && p < P;
-    const float *phi = q.phi + bh * (q.n - 1) * N * N + n, *psi = q.psi + (bh * (q.n - 1) * P + p) * N + n;
-    float *in = q.in + (bh * q.n * P + p) * N + n;
-    float f[2][kCarryPart], add[2];
-    auto fetch = [&](int k, float (&to)[kCarryPart], float &plus) {
-        const bool some = k < q.n - 1;
-        plus = some && mine ? psi[(int64_t)k * P * N] : 0.f;
+    const int64_t bh = blockIdx.x, p0 = (int64_t)blockIdx.y * ROWS + j;  // this thread adds up rows p0, p0 + 4
+    // column n (past N the last one, whose sums are not kept) of Phi's rows m0, m0 + 1, ... (past N the last one, times 0)
+    const int last = imin(n, N - 1), steps = imin(kCarryPart, imax(1, N - m0));
+    const float *phi = q.phi + (bh * (q.n - 1) * N + imin(m0, N - 1)) * N + last;
+    const float *psi = q.psi + (bh * (q.n - 1) * P + p0) * N + last;
+    float *in = q.in + (bh * q.n * P + p0) * N + n;
+    float f[kCarryPart], add[ROWS / 4];
+    auto psi_at = [&](int k, int r) { return k < q.n - 1 && p0 + 4 * r < P ? psi[((int64_t)k * P + 4 * r) * N] : 0.f; };
+    auto leave = [&](int k, int r, float v) {
+        if (n < N && p0 + 4 * r < P) in[((int64_t)k * P + 4 * r) * N] = v;
+        reinterpret_cast<float *>(&s[n][r])[j] = n < N ? v : 0.f;
+    };
+    const float *at = phi + (q.n > 2 ? (int64_t)N * N : 0);
 #pragma unroll
-        for (int i = 0; i < kCarryPart; ++i) to[i] = some && n < N && m0 + i < N ? phi[((int64_t)k * N + m0 + i) * N] : 0.f;
-    };
-    auto leave = [&](int k, float v) {
-        if (mine) in[(int64_t)k * P * N] = v;
-        reinterpret_cast<float *>(&s[n])[j] = v;
-    };
-    auto step = [&](int k, const float (&now)[kCarryPart], float plus) {
-        float v[kCarryRows] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kCarryPart; ++i) {
+        f[i] = *at;
+        at += i + 1 < steps ? N : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS / 4; ++r) {
+        leave(1, r, psi_at(0, r));
+        add[r] = psi_at(1, r);
+    }
+    __syncthreads();
+    for (int k = 1; k < q.n - 1; ++k) {
+        float v[ROWS] = {};
+        at = phi + (int64_t)imin(k + 1, q.n - 2) * N * N;
 #pragma unroll
         for (int i = 0; i < kCarryPart; ++i) {
-            const float4 x = s[m0 + i];
-            v[0] = fmaf(x.x, now[i], v[0]), v[1] = fmaf(x.y, now[i], v[1]);
-            v[2] = fmaf(x.z, now[i], v[2]), v[3] = fmaf(x.w, now[i], v[3]);
+#pragma unroll
+            for (int r = 0; r < ROWS; r += 4) {
+                const float4 x = s[m0 + i][r / 4];
+                v[r] = fmaf(x.x, f[i], v[r]), v[r + 1] = fmaf(x.y, f[i], v[r + 1]);
+                v[r + 2] = fmaf(x.z, f[i], v[r + 2]), v[r + 3] = fmaf(x.w, f[i], v[r + 3]);
+            }
+            f[i] = *at;
+            at += i + 1 < steps ? N : 0;
         }
 #pragma unroll
-        for (int r = 0; r < kCarryRows; ++r) part[j][r][n] = v[r];
+        for (int r = 0; r < ROWS; ++r) part[j][r][n] = v[r];
         __syncthreads();
-        leave(k + 1, ((part[0][j][n] + part[1][j][n]) + (part[2][j][n] + part[3][j][n])) + plus);
+#pragma unroll
+        for (int r = 0; r < ROWS / 4; ++r) {
+            const int w = 4 * r + j;
+            leave(k + 1, r, ((part[0][w][n] + part[1][w][n]) + (part[2][w][n] + part[3][w][n])) + add[r]);
+            add[r] = psi_at(k + 1, r);
+        }
         __syncthreads();
-    };
-    fetch(1, f[1], add[1]);
-    leave(1, mine ? psi[0] : 0.f);
-    __syncthreads();
-    for (int k = 1; k < q.n - 1; k += 2) {
-        fetch(k + 1, f[0], add[0]);
-        step(k, f[1], add[1]);
-        if (k + 1 == q.n - 1) break;
-        fetch(k + 2, f[1], add[1]);
-        step(k + 1, f[0], add[0]);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_combine(const Pieces &q, int64_t BH, int64_t P, int64_t N, cudaStream_t stream) {
-    return launch_programmatic(combine_kernel, dim3((unsigned)BH, (unsigned)((P + kCarryRows - 1) / kCarryRows)), dim3(512), 0,
-                               stream, q, (int)P, (int)N);
+    const int rows = BH * ((P + 3) / 4) <= sm_count(152) ? 4 : 8;
+    return launch_programmatic(rows == 4 ? combine_kernel<4> : combine_kernel<8>, dim3((unsigned)BH, (unsigned)((P + rows - 1) / rows)),
+                               dim3(512), 0, stream, q, (int)P, (int)N);
 }
 
 }  // namespace delta
