@@ -204,7 +204,11 @@ __global__ void __launch_bounds__(256) block_norm_kernel(BlockNormArgs a) {
 // memory each time (STAGED false). A block keeps its sums of the weights' gradients
 // in registers; block_norm_reduce_kernel adds the blocks' sums.
 // MOST threads at most: 320 (two blocks per SM with one vector per thread: 16384 x
-// 2560 bf16 takes 187 us, 267 us where 122 registers leave one block) or 512.
+// 2560 bf16 took 187 us, 267 us where 122 registers leave one block), 640 where that
+// leaves a thread one vector of eight (8192 x 5120 bf16: 148 us, 203 us with 320 threads and two
+// vectors), else 512.
+// 8192 x 2560 bf16 with a float32 residual: 84 us, 5.5 TB/s (110 us with the weights
+// read anew for each row and three sums for the three weights).
 template <typename T, typename TR, int V, int RV, bool STAGED, int MOST>
 __global__ void __launch_bounds__(MOST, MOST == 320 && RV == 1 ? 2 : 1) block_norm_bwd_kernel(BlockNormArgs a, int stages) {
     pdl_enter();
@@ -226,7 +230,23 @@ __global__ void __launch_bounds__(MOST, MOST == 320 && RV == 1 ? 2 : 1) block_no
         if (dres_out) AR::fetch(buf + 3 * na + nr, dres_out + at, nv);
         ahead_commit();
     };
-    float gpre[RV][V] = {}, gpost[RV][V] = {}, gscale[RV][V] = {};
+    // sums of dout r rho and, with o = dL/dr, of o u tau: that sum times scale is post_w's gradient, times post_w scale's
+    float gpre[RV][V] = {}, gsum[RV][V] = {};
+    // pre_w, and scale post_w: kept for all rows where there are registers for it
+    constexpr bool KEEP = RV * V <= 8;
+    float wp[KEEP ? RV : 1][V], ws[KEEP ? RV : 1][V];
+    auto read_weights = [&](float (&p)[V], float (&sw)[V], int v) {
+        float w[V];
+        ld<float, V>(p, a.pre_w + v * V);
+        weights(sw, a.scale, v);
+        weights(w, a.post_w, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sw[e] *= w[e];
+    };
+    if constexpr (KEEP)
+#pragma unroll
+        for (int k = 0; k < RV; ++k)
+            if ((int)(threadIdx.x + k * blockDim.x) < nv) read_weights(wp[k], ws[k], threadIdx.x + k * blockDim.x);
     fetch(blockIdx.x, smem);
     int ph = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ph ^= 1) {
@@ -261,16 +281,14 @@ __global__ void __launch_bounds__(MOST, MOST == 320 && RV == 1 ? 2 : 1) block_no
         for (int k = 0; k < RV; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v < nv) {
-                float w[V], s[V], p[V];
-                weights(w, a.post_w, v);
-                weights(s, a.scale, v);
-                ld<float, V>(p, a.pre_w + v * V);
+                float (&p)[V] = wp[KEEP ? k : 0], (&sw)[V] = ws[KEEP ? k : 0];
+                if constexpr (!KEEP) read_weights(p, sw, v);
                 AR::get(r[k], buf + 3 * na, res + base, v);
                 A::get(d[k], buf + 2 * na, dout + base, v);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     u[k][e] *= tau;
-                    r[k][e] = fmaf(s[e], u[k][e] * w[e], r[k][e]);
+                    r[k][e] = fmaf(sw[e], u[k][e], r[k][e]);
                     ss = fmaf(r[k][e], r[k][e], ss);
                     ar = fmaf(d[k][e] * p[e], r[k][e], ar);
                 }
@@ -282,10 +300,8 @@ __global__ void __launch_bounds__(MOST, MOST == 320 && RV == 1 ? 2 : 1) block_no
         for (int k = 0; k < RV; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v < nv) {
-                float w[V], s[V], p[V], o[V];
-                weights(w, a.post_w, v);
-                weights(s, a.scale, v);
-                ld<float, V>(p, a.pre_w + v * V);
+                float (&p)[V] = wp[KEEP ? k : 0], (&sw)[V] = ws[KEEP ? k : 0], o[V];
+                if constexpr (!KEEP) read_weights(p, sw, v);
                 if (dres_out) {
                     AR::get(o, buf + 3 * na + nr, dres_out + base, v);
                 } else {
@@ -296,10 +312,8 @@ __global__ void __launch_bounds__(MOST, MOST == 320 && RV == 1 ? 2 : 1) block_no
                 for (int e = 0; e < V; ++e) {  // u holds u tau
                     gpre[k][e] = fmaf(d[k][e], r[k][e] * rho, gpre[k][e]);
                     o[e] = fmaf(rho, d[k][e] * p[e] - r[k][e] * c, o[e]);
-                    gscale[k][e] = fmaf(o[e], u[k][e] * w[e], gscale[k][e]);
-                    const float dn = o[e] * s[e];
-                    gpost[k][e] = fmaf(dn, u[k][e], gpost[k][e]);
-                    d[k][e] = dn * w[e];
+                    gsum[k][e] = fmaf(o[e], u[k][e], gsum[k][e]);
+                    d[k][e] = o[e] * sw[e];
                     bu = fmaf(d[k][e], u[k][e], bu);
                 }
                 st<TR, V>((TR *)a.dres + base + (int64_t)v * V, o);
@@ -331,37 +345,40 @@ __global__ void __launch_bounds__(MOST, MOST == 320 && RV == 1 ? 2 : 1) block_no
         }
         if (stages == 1 && row + gridDim.x < a.rows) fetch(row + gridDim.x, smem);
     }
-    float *out = a.part + (int64_t)blockIdx.x * 3 * a.dim;
+    float *out = a.part + (int64_t)blockIdx.x * 2 * a.dim;
 #pragma unroll
     for (int k = 0; k < RV; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
         if (v < nv) {
             st<float, V>(out + (int64_t)v * V, gpre[k]);
-            st<float, V>(out + a.dim + (int64_t)v * V, gpost[k]);
-            st<float, V>(out + 2 * a.dim + (int64_t)v * V, gscale[k]);
+            st<float, V>(out + a.dim + (int64_t)v * V, gsum[k]);
         }
     }
 }
 
-// One warp per 32 columns of one of the three sums; eight warps split the blocks' parts.
-__global__ void __launch_bounds__(256) block_norm_reduce_kernel(BlockNormArgs a, int parts) {
+// 32 columns of one of the two sums; sixteen warps split the blocks' parts, few loads after one another.
+constexpr int kReduceWarps = 16;
+__global__ void __launch_bounds__(32 * kReduceWarps) block_norm_reduce_kernel(BlockNormArgs a, int parts) {
     pdl_enter();
-    __shared__ float s[8][32];
+    __shared__ float s[kReduceWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y;
     const int64_t col = (int64_t)blockIdx.x * 32 + lane;
-    float *dst = which == 0 ? a.dpre_w : which == 1 ? a.dpost_w : a.dscale;
-    if (!dst) return;
     float v = 0.f;
     if (col < a.dim) {
-#pragma unroll 4
-        for (int i = warp; i < parts; i += 8) v += a.part[((int64_t)i * 3 + which) * a.dim + col];
+#pragma unroll 10
+        for (int i = warp; i < parts; i += kReduceWarps) v += a.part[((int64_t)i * 2 + which) * a.dim + col];
     }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && col < a.dim) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) v += s[w][lane];
-        dst[col] = v;
+        for (int w = 1; w < kReduceWarps; ++w) v += s[w][lane];
+        if (which == 0) {
+            a.dpre_w[col] = v;
+        } else {
+            if (a.dpost_w) a.dpost_w[col] = a.scale ? v * a.scale[col] : v;
+            if (a.dscale) a.dscale[col] = a.post_w ? v * a.post_w[col] : v;
+        }
     }
 }
 
@@ -423,14 +440,17 @@ cudaError_t launch_block_norm(int io, int res_io, const BlockNormArgs &a, cudaSt
     });
 }
 
-// The workspace holds the parts of this many blocks (three of 320 threads are resident per SM).
-int block_norm_bwd_parts(int64_t rows, int64_t) { return (int)imin<int64_t>(rows, 4 * (int64_t)sm_count(152)); }
+// The workspace holds the parts of this many blocks: an SM's registers hold about 640 threads of 8 elements
+// (16384 x 768 bf16: 53 us, 57 us with 4 blocks per SM).
+int block_norm_bwd_parts(int64_t rows, int64_t dim) {
+    return (int)imin<int64_t>(rows, sm_count(152) * imax<int64_t>(4, imin<int64_t>(16, 5120 / imax<int64_t>(1, dim) + 1)));
+}
 
 cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream) {
     int64_t parts = 0;
     if (a.rows > 0) {
         cudaError_t e = for_types(io, res_io, [&](auto t, auto tr) {
-            return for_row(a.dim, 512, [&](auto v, auto rv, int threads) {
+            return for_row(a.dim, a.dim % 8 == 0 && a.dim <= 8 * 640 ? 640 : 512, [&](auto v, auto rv, int threads) {
                 using T = decltype(t);
                 using TR = decltype(tr);
                 constexpr int V = decltype(v)::value, RV = decltype(rv)::value;
@@ -448,6 +468,8 @@ cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cu
                     if constexpr (RV * V >= 16) return go(block_norm_bwd_kernel<T, TR, V, RV, false, 512>, 0);
                     return cudaErrorInvalidValue;
                 }
+                if constexpr (RV == 1 && V == 8)
+                    if (threads > 512) return go(block_norm_bwd_kernel<T, TR, V, RV, true, 640>, stages);
                 if constexpr (RV <= 2)
                     if (threads <= 320) return go(block_norm_bwd_kernel<T, TR, V, RV, true, 320>, stages);
                 return go(block_norm_bwd_kernel<T, TR, V, RV, true, 512>, stages);
@@ -455,8 +477,8 @@ cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cu
         });
         if (e != cudaSuccess) return e;
     }
-    return launch_programmatic(block_norm_reduce_kernel, dim3((unsigned)((a.dim + 31) / 32), 3), dim3(256), 0, stream, a,
-                               (int)parts);
+    return launch_programmatic(block_norm_reduce_kernel, dim3((unsigned)((a.dim + 31) / 32), 2), dim3(32 * kReduceWarps), 0,
+                               stream, a, (int)parts);
 }
 
 }  // namespace ssd

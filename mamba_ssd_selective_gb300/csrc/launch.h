@@ -199,7 +199,7 @@ struct BlockNormArgs {
     const void *dout, *dres_out;                // dres_out may be null
     void *dy, *dz, *dres;
     float *dpre_w, *dpost_w, *dscale;
-    float *part;                                // [block_norm_bwd_parts][3][dim]
+    float *part;                                // [block_norm_bwd_parts][2][dim]
 };
 cudaError_t launch_block_norm(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream);
 int block_norm_bwd_parts(int64_t rows, int64_t dim);

@@ -898,7 +898,7 @@ ssd_status ssd_block_norm(int64_t rows, int64_t dim, int32_t io_dtype, int32_t r
 
 size_t ssd_block_norm_bwd_workspace_size(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype) {
     if (check_norm(rows, dim, io_dtype, res_dtype, 0.f) != SSD_OK) return 0;
-    return 256 + round256((size_t)ssd::block_norm_bwd_parts(rows, dim) * 3 * dim * sizeof(float));
+    return 256 + round256((size_t)ssd::block_norm_bwd_parts(rows, dim) * 2 * dim * sizeof(float));
 }
 
 ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32_t res_dtype, const void *y,
