@@ -28,16 +28,16 @@ template <int VW> __device__ __forceinline__ int col_of(int e, int j) {
     return ((e / VW) * 8 + j) * VW + e % VW;
 }
 
-template <int VW, int NE>
-__device__ __forceinline__ void load_row(float (&s)[NE], const float *row, int N, int j) {
+template <int VW, int NE, typename T>
+__device__ __forceinline__ void load_row(float (&s)[NE], const T *row, int N, int j) {
 #pragma unroll
     for (int e = 0; e < NE; e += VW) {
         const int n = col_of<VW>(e, j);
         if constexpr (VW == 4) {
-            const float4 v = n < N ? *reinterpret_cast<const float4 *>(row + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = n < N ? ld4(row + n) : make_float4(0.f, 0.f, 0.f, 0.f);
             s[e] = v.x, s[e + 1] = v.y, s[e + 2] = v.z, s[e + 3] = v.w;
         } else {
-            s[e] = n < N ? row[n] : 0.f;
+            s[e] = n < N ? to_f32(row[n]) : 0.f;
         }
     }
 }
@@ -73,23 +73,28 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepArgs a, i
         return;
     }
     const int j = threadIdx.x & 7, row = threadIdx.x >> 3;
-    const T *kp = (const T *)a.k + (b * a.G + i) * N, *qp = (const T *)a.q + (b * a.G + i) * N;
+    const int64_t base = (slot * a.H + h) * (int64_t)P * N;
+    const T *v = (const T *)a.v + bh * P;
+    float next[NE], next_v;  // the next row of this thread, on its way while one is worked on
+    auto fetch = [&](int p) {
+        load_row<VW, NE>(next, a.state + base + (int64_t)p * N, N, j);
+        next_v = to_f32(v[p]);
+    };
+    fetch(imin(p0 + row, p1 - 1));
     float kv[NE], qv[NE], kq = 0.f;
+    load_row<VW, NE>(kv, (const T *)a.k + (b * a.G + i) * N, N, j);
+    load_row<VW, NE>(qv, (const T *)a.q + (b * a.G + i) * N, N, j);
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-        const int n = col_of<VW>(e, j);
-        kv[e] = n < N ? to_f32(kp[n]) : 0.f;
-        qv[e] = n < N ? to_f32(qp[n]) : 0.f;
-        kq = fmaf(kv[e], qv[e], kq);
-    }
+    for (int e = 0; e < NE; ++e) kq = fmaf(kv[e], qv[e], kq);
     kq = group_sum(kq);
     const float alpha = expf(to_f32(((const T *)a.g)[bh])), beta = to_f32(((const T *)a.beta)[bh]);
-    const T *v = (const T *)a.v + bh * P;
-    const int64_t base = (slot * a.H + h) * (int64_t)P * N;
     for (int p = p0 + row; p < p1 + row; p += kRowsPass) {  // whole warps stay in for the shuffles
         const bool on = p < p1;
         float s[NE];
-        load_row<VW, NE>(s, a.state + base + (int64_t)(on ? p : p0) * N, N, j);
+#pragma unroll
+        for (int e = 0; e < NE; ++e) s[e] = next[e];
+        const float vp = next_v;
+        if (p + kRowsPass < p1) fetch(p + kRowsPass);
         float sk = 0.f, sq = 0.f;
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepArgs a, i
         sk = group_sum(sk);
         sq = group_sum(sq);
         if (!on) continue;
-        const float u = beta * (to_f32(v[p]) - sk);
+        const float u = beta * (vp - sk);
 #pragma unroll
         for (int e = 0; e < NE; ++e) s[e] = fmaf(u, kv[e], s[e]);
         store_row<VW, NE>(s, a.new_state + base + (int64_t)p * N, N, j);
