@@ -9,10 +9,13 @@
 // n = (i 8 + j) VW .. + VW (VW = 4 where N allows 16-byte rows, else 1), and the
 // two dots S k and S q are taken in one pass, three shuffles each.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "launch.h"
 
 namespace ssd {
 namespace {
+
+using namespace delta;
 
 constexpr int kThreads = 128, kRowsPass = kThreads / 8;  // rows a block handles at once
 
@@ -55,9 +58,32 @@ __device__ __forceinline__ void store_row(const float (&s)[NE], float *row, int 
     }
 }
 
+// The same as pairs of float32.
+template <int VW, int NE>
+__device__ __forceinline__ void load_pairs(uint64_t (&s)[NE / 2], const float *row, int N, int j) {
+    float x[NE];
+    load_row<VW, NE>(x, row, N, j);
+#pragma unroll
+    for (int e = 0; e < NE; e += 2) s[e / 2] = f2(x[e], x[e + 1]);
+}
+template <int VW, int NE>
+__device__ __forceinline__ void store_pairs(const uint64_t (&s)[NE / 2], float *row, int N, int j) {
+    float x[NE];
+#pragma unroll
+    for (int e = 0; e < NE; e += 2) un2(s[e / 2], x[e], x[e + 1]);
+    store_row<VW, NE>(x, row, N, j);
+}
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+    float x, y;
+    un2(v, x, y);
+    return x + y;
+}
+
 // ------------------------------------------------------------------- the step
-// Memory-bound: the state is read and written once. A block covers
-// rows [p0, p0 + rows_per_block) of one (b, h).
+// Bound by HBM: the state is read and written once. A block covers
+// rows [p0, p0 + rows_per_block) of one (b, h). With N 128, P 64: 54 us for 64
+// rows of 80 heads, 6.2 TB/s (58 us where a row is requested when the one before is
+// done); a state of 24 heads takes 2.4 us, the latency of a launch.
 template <typename T, int VW, int NE>
 __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepArgs a, int rows_per_block) {
     pdl_enter();
@@ -119,7 +145,10 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(DeltaStepArgs a, i
 // the sums of 8 lanes to the new state; so everything else is off that way: 16
 // tokens are staged in shared memory while the next 16 are on their way to
 // registers, a token's k and q are read while the one before it is done, k . q is
-// formed at staging, and the dots are taken of S_{t-1}, the decay coming after.
+// formed at staging, the dots are taken of S_{t-1}, the decay coming after, and y
+// leaves once per 16 tokens. float32, 12 heads of P 64, N 64, 777 tokens: 147 us,
+// 360 cycles a token, a third of it the three dependent shuffles (310 us with loads of
+// each 32 tokens waited for and the decay first).
 // With `ckpt` the states entering every ckpt_len-th token are stored for the backward.
 constexpr int kStage = kRowsPass;  // tokens staged at once; group t of lanes forms k . q of token t
 
@@ -129,7 +158,8 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaArgs a, 
     extern __shared__ float sm[];
     const int N = (int)a.N, P = (int)a.P;
     float *sk = sm, *sq = sk + kStage * N;
-    __shared__ float sv[kStage * kRowsPass], sa[kStage], sb[kStage], skq[kStage];
+    __shared__ float sv[kStage * kRowsPass], sy[kStage * kRowsPass];
+    __shared__ float4 sx[kStage];
     const int64_t bh = blockIdx.x;
     const int h = (int)(bh % a.H);
     const int64_t b = bh / a.H;
@@ -140,13 +170,8 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaArgs a, 
     const int64_t len = seq_len(a.seqlens, b, a.L);
     if (a.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
     const int64_t nck = ckpt ? (a.L + ckpt_len - 1) / ckpt_len : 0;
-    float s[NE];
-    if (a.init && on) {
-        load_row<VW, NE>(s, a.init + (bh * P + p) * N, N, j);
-    } else {
-#pragma unroll
-        for (int e = 0; e < NE; ++e) s[e] = 0.f;
-    }
+    uint64_t s[NE / 2] = {};
+    if (a.init && on) load_pairs<VW, NE>(s, a.init + (bh * P + p) * N, N, j);
     // Staged element x = e kThreads + thread of [kStage][N] (NE kThreads >= kStage N), of v [kStage][rows].
     T rk[NE], rq[NE], rv[2], rg, rb;
     static_assert(kStage * 8 == kThreads && kStage * kRowsPass == 2 * kThreads, "the shares of a thread");
@@ -182,53 +207,70 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaArgs a, 
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) sv[e * kThreads + threadIdx.x] = to_f32(rv[e]);
-        if ((int)threadIdx.x < nt) {
-            sa[threadIdx.x] = expf(to_f32(rg));
-            sb[threadIdx.x] = to_f32(rb);
-        }
+        if ((int)threadIdx.x < nt) sx[threadIdx.x] = make_float4(expf(to_f32(rg)), to_f32(rb), 0.f, 0.f);
         __syncthreads();
         fetch(t0 + kStage);
-        float kv[NE], qv[NE];
+        uint64_t kv[NE / 2], qv[NE / 2];
         {
-            float d = 0.f;
-            load_row<VW, NE>(kv, sk + row * N, N, j);
-            load_row<VW, NE>(qv, sq + row * N, N, j);
+            uint64_t d = 0;
+            load_pairs<VW, NE>(kv, sk + row * N, N, j);
+            load_pairs<VW, NE>(qv, sq + row * N, N, j);
 #pragma unroll
-            for (int e = 0; e < NE; ++e) d = fmaf(kv[e], qv[e], d);
-            d = group_sum(d);
-            if (j == 0) skq[row] = d;
+            for (int e = 0; e < NE / 2; ++e) d = fma2(kv[e], qv[e], d);
+            const float kq = group_sum(pair_sum(d));
+            if (j == 0) sx[row].z = kq;
         }
         __syncthreads();
-        load_row<VW, NE>(kv, sk, N, j);
-        load_row<VW, NE>(qv, sq, N, j);
-#pragma unroll 2
-        for (int t = 0; t < nt; ++t) {
-            if (ckpt && (t0 + t) % ckpt_len == 0 && on)
-                store_row<VW, NE>(s, ckpt + (((bh * nck + (t0 + t) / ckpt_len) * P) + p) * N, N, j);
-            const int next = imin(t + 1, kStage - 1);
-            float nk[NE], nq[NE];
-            load_row<VW, NE>(nk, sk + next * N, N, j);
-            load_row<VW, NE>(nq, sq + next * N, N, j);
-            const float alpha = sa[t], beta = sb[t], v = sv[t * kRowsPass + row], kq = skq[t];
-            float d[4] = {}, o[4] = {};
-#pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                d[e & 3] = fmaf(s[e], kv[e], d[e & 3]);
-                o[e & 3] = fmaf(s[e], qv[e], o[e & 3]);
-                s[e] *= alpha;
-            }
-            const float sd = group_sum((d[0] + d[1]) + (d[2] + d[3])), so = group_sum((o[0] + o[1]) + (o[2] + o[3]));
-            const float u = beta * fmaf(-alpha, sd, v);
-#pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                s[e] = fmaf(u, kv[e], s[e]);
-                kv[e] = nk[e], qv[e] = nq[e];
-            }
-            if (a.y && on && j == 0)
-                ((T *)a.y)[((b * a.L + t0 + t) * a.H + h) * P + p] = from_f32<T>(a.scale * fmaf(u, kq, alpha * so));
+        constexpr bool AHEAD = NE <= 16;  // registers for two tokens' k and q
+        if (AHEAD) {
+            load_pairs<VW, NE>(kv, sk, N, j);
+            load_pairs<VW, NE>(qv, sq, N, j);
         }
+#pragma unroll 1
+        for (int half = 0; half < 16; half += 8) {
+            if (ckpt && half < nt && on && (half == 0 || ckpt_len == 8))
+                store_pairs<VW, NE>(s, ckpt + (((bh * nck + (t0 + half) / ckpt_len) * P) + p) * N, N, j);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int t = half + x;
+                if (t >= nt) break;
+                uint64_t nk[NE / 2], nq[NE / 2];
+                const int at = AHEAD ? imin(t + 1, kStage - 1) : t;
+                load_pairs<VW, NE>(nk, sk + at * N, N, j);
+                load_pairs<VW, NE>(nq, sq + at * N, N, j);
+                if (!AHEAD)
+#pragma unroll
+                    for (int e = 0; e < NE / 2; ++e) kv[e] = nk[e], qv[e] = nq[e];
+                const float4 f = sx[t];  // exp(g), beta, k . q
+                const float v = sv[t * kRowsPass + row];
+                const uint64_t alpha = f2(f.x, f.x);
+                uint64_t d[2] = {}, o[2] = {};
+#pragma unroll
+                for (int e = 0; e < NE / 2; ++e) {
+                    d[e & 1] = fma2(s[e], kv[e], d[e & 1]);
+                    o[e & 1] = fma2(s[e], qv[e], o[e & 1]);
+                    s[e] = mul2(s[e], alpha);
+                }
+                const float sd = group_sum(pair_sum(d[0]) + pair_sum(d[1])), so = group_sum(pair_sum(o[0]) + pair_sum(o[1]));
+                const float u = f.y * fmaf(-f.x, sd, v);
+                const uint64_t u2 = f2(u, u);
+#pragma unroll
+                for (int e = 0; e < NE / 2; ++e) {
+                    s[e] = fma2(u2, kv[e], s[e]);
+                    if (AHEAD) kv[e] = nk[e], qv[e] = nq[e];
+                }
+                if (j == 0) sy[t * kRowsPass + row] = a.scale * fmaf(u, f.z, f.x * so);
+            }
+        }
+        __syncthreads();
+        if (a.y)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int x = e * kThreads + threadIdx.x, t = x / kRowsPass, r = x % kRowsPass;
+                if (t < nt && p0 + r < P) ((T *)a.y)[((b * a.L + t0 + t) * a.H + h) * P + p0 + r] = from_f32<T>(sy[x]);
+            }
     }
-    if (a.final_state && on) store_row<VW, NE>(s, a.final_state + (bh * P + p) * N, N, j);
+    if (a.final_state && on) store_pairs<VW, NE>(s, a.final_state + (bh * P + p) * N, N, j);
     if (a.y)  // tokens past the sequence's length
         for (int64_t x = threadIdx.x; x < (a.L - len) * kRowsPass; x += kThreads) {
             const int64_t t = len + x / kRowsPass;
@@ -244,6 +286,8 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaArgs a, 
 //     dq_t += scale dy_t S_t     E += scale dy_t q_t^T     du = E k_t
 //     dv_t = beta du             dbeta_t += du . w         dk_t += u E - beta du F
 //     E -= beta du k_t^T         dg_t += <E, F>            E *= exp(g_t)
+// Bound by instruction issue: every row's share of dq and dk is summed over the rows of
+// a block for every token. float32, 12 heads of P 64, N 64, 777 tokens: 835 us.
 // The sums over rows are taken per warp by shuffles and over the four warps in
 // shared memory; sums over row blocks and over the heads of a group are left
 // to delta_reduce_kernel, in a fixed order.
@@ -441,7 +485,8 @@ template <typename K> cudaError_t with_smem(K kern, size_t bytes) {
 
 template <typename T> cudaError_t step_t(const DeltaStepArgs &a, cudaStream_t stream) {
     return for_width(a.N, [&](auto vw, auto ne) {
-        // rows a block walks: as many passes of 16 as leave the GPU two blocks per SM
+        // rows a block walks: as many passes of 16 as leave the GPU two blocks per SM (64 rows of 80 heads: 69 us
+        // with 16 rows a block, 58 with 64; one row of 24 heads: 2.6 us with 16, 4.4 with 64)
         int rows = kRowsPass;
         const int64_t want = 2 * (int64_t)sm_count(1);
         while (rows < a.P && a.B * a.H * ((a.P + 2 * rows - 1) / (2 * rows)) >= want) rows *= 2;

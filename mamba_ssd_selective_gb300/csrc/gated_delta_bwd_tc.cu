@@ -41,6 +41,8 @@ namespace {
 //
 // Warps: 0 loads; 1 products; 4-11 the chain's elementwise steps; 12-19 the
 // operands of dY, and dv.
+//
+// Bound as the forward chain is; 107 us for the 2560 chunks of B2 L2048 H80.
 namespace rev {
 constexpr int kChainWarp0 = 4, kOutWarp0 = 12, kThreads = 640;
 }  // namespace rev
@@ -618,7 +620,13 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
 // and w scaled in place; G and X written by the threads.
 //
 // 104 KB of shared memory and 256 TMEM columns ([dY; dV] w^T, dQ^T, dk"^T, dk'^T): two
-// blocks per SM (P <= 64), one computing while the other loads.
+// blocks per SM (P <= 64), one computing while the other loads. G, X, dY, dV and w enter
+// the products in bf16, as they are written to memory in bf16 (each error is below the
+// results' own rounding); their sums are float32.
+//
+// Bound by shared memory, which the operands of 40 products (6 KB each) and the element
+// steps of a head both go through: 8 thousand cycles a head and chunk, 160 us for the
+// 5120 of B2 L2048 H80, HBM 36 %, tensor pipe 15 % busy.
 namespace grad {
 constexpr int kThreads = 288, kElem = 256;  // warps 0-7 elementwise, warp 8 loads and products
 constexpr uint32_t kOffKQ = 0;              // 32 KB: two panels of 64 columns, each 64 rows of Q, then 64 of K

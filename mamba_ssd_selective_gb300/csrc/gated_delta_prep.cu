@@ -14,7 +14,9 @@
 // a steep decay does not blur the differences of the tokens after it (float64
 // would do, but its additions take a third of the block's time on this GPU).
 //
-// Bound by instruction issue; five blocks per SM cover the latencies of one.
+// Bound by its latencies and shared memory: 12 to 14 thousand cycles a block, five
+// blocks per SM (with four B8 L2048 H80 takes 4 % longer), issue slots 39 % and shared
+// memory 53 % used; 69 us for the 5120 items of B2 L2048 H80.
 #include "gated_delta_tc.cuh"
 
 namespace ssd {

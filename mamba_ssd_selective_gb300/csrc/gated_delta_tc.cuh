@@ -13,6 +13,7 @@
 // (b, head, chunk) at once, and the chains of chunks, forward and backward, read them.
 #pragma once
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "launch.h"
 #include "ssd_scan.h"
 #include "tc_host.h"
@@ -106,7 +107,8 @@ cudaError_t launch_prep(const PrepArgs &p, cudaStream_t stream);
 // states entering each chunk [B][H][nc + 1][P][N] (the final one last) and w [B, L, H, P], in bf16.
 cudaError_t launch_chain(const PrepArgs &p, __nv_bfloat16 *states, __nv_bfloat16 *w, cudaStream_t stream);
 
-// Whether a CTA takes two heads of a group.
+// Whether a CTA takes two heads of a group: where pairs alone fill the SMs (B8 L2048 H80 G40: 477 us in pairs, 599 one by
+// one; the backward of B4 785 and 877); with fewer, one by one (B2 L2048 H80 would leave half of the SMs idle in pairs).
 inline bool pair_heads(const DeltaArgs &a) {
     return a.P <= 64 && (a.H / a.G) % 2 == 0 && a.B * (a.H / 2) >= (int64_t)sm_count(152);
 }
@@ -114,25 +116,6 @@ inline bool pair_heads(const DeltaArgs &a) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
-}
-// Two float32 in one 64-bit register pair, and the packed operations on them.
-__device__ __forceinline__ uint64_t f2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void un2(uint64_t v, float &x, float &y) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 // A pair as bf16 pairs hi and lo, hi + lo within 2^-17 of each.
 __device__ __forceinline__ void split2(uint64_t v, uint32_t &hi, uint32_t &lo) {
@@ -166,7 +149,7 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile
 }
 
 // The chains of chunks laid end to end, nc chunks each, cut into equal segments, one
-// per CTA (to one chunk). With at most one CTA per chain a segment is at least a chain
+// per CTA (to one chunk): B2 L2048 H80 took 179 us so and 245 with whole chains, B8 528 and 591. With at most one CTA per chain a segment is at least a chain
 // long, so a chain spans two CTAs at most. A CTA first runs the head of the chain it
 // ends in, then its whole chains, then the rest of the chain it begins in, which
 // waits for the state that the CTA before has left in its first item: every
