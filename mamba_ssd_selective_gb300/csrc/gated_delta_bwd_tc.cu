@@ -621,8 +621,9 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
 //
 // 104 KB of shared memory and 256 TMEM columns ([dY; dV] w^T, dQ^T, dk"^T, dk'^T): two
 // blocks per SM (P <= 64), one computing while the other loads. G, X, dY, dV and w enter
-// the products in bf16, as they are written to memory in bf16 (each error is below the
-// results' own rounding); their sums are float32.
+// the products in bf16 and S0 and E come from memory in bf16; the sums are float32. Together
+// these roundings take the error of dq and dk from 1.7e-3 (2-norm), which rounding them to
+// bf16 makes alone, to 3.0e-3.
 //
 // Bound by shared memory, which the operands of 40 products (6 KB each) and the element
 // steps of a head both go through: 8 thousand cycles a head and chunk, 160 us for the
