@@ -24,9 +24,10 @@ namespace delta {
 namespace {
 
 constexpr int kThreads = 128, kLo = 6;  // A's lo blocks begin at block 6
-// shared memory (bytes): K and Q, 64 rows in panels of 64 columns (128-byte swizzle), later the four tiles; then blocks
-// of A of 512 bytes (hi, then lo), the diagonal ones in float32; then the sums' factors
-constexpr uint32_t kOffBlk = 32768, kOffSc = kOffBlk + 12 * 512 + 4 * 1024;
+// shared memory (bytes): K and Q, 64 rows in panels of 64 columns (128-byte swizzle), whose place the tiles take once
+// their products are formed, and where M T lo will be, and behind it, blocks of A of 512 bytes (hi, then lo) and the
+// diagonal ones in float32; then the sums' factors
+constexpr uint32_t kOffBlk = 3 * kTile, kOffSc = kOffBlk + 12 * 512 + 4 * 1024;
 // c (base 2) rounded, 2^remainder, beta 2^-remainder, and that times exp(c at the end of the block of 16 - c)
 enum { S_HI, S_ROW, S_INV, S_COL, S_N };
 constexpr uint32_t kOffBar = kOffSc + S_N * kC * 4, kSmem = kOffBar + 16;
@@ -67,10 +68,13 @@ __device__ __forceinline__ void put_block(const float (&y)[8], uint8_t *hi, uint
     }
 }
 
-// Row W of the blocks of K K^T and Q K^T, scaled: A to shared memory, M to fragments. W is a template argument
-// because the row has W + 1 blocks, each in registers.
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+// Row W of the blocks of Q K^T and row 3 - W of K K^T, five blocks together, scaled: M to fragments, A to shared memory.
+// W is a template argument because the blocks are in registers.
 template <int W>
 __device__ __forceinline__ void rows_of(const PrepArgs &p, uint8_t *smem, int lane, uint32_t (&mh)[4][4], uint32_t (&ml)[4][4]) {
+    constexpr int R = 3 - W;
     uint8_t *sK = smem, *sQ = smem + 16384, *blk = smem + kOffBlk;
     float *diag = reinterpret_cast<float *>(blk + 12 * 512);
     const float *sc = reinterpret_cast<const float *>(smem + kOffSc);
@@ -79,69 +83,75 @@ __device__ __forceinline__ void rows_of(const PrepArgs &p, uint8_t *smem, int la
     // block k are those of block 0 with 32 k in their place: xor); for the transposed operand of K K^T
     const uint32_t lt = (uint32_t)((lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4));
     const uint32_t ln = (uint32_t)(((lane & 7) + ((lane >> 4) << 3)) * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4));
-    float ak[W + 1][8] = {}, aq[W + 1][8] = {};
+    float ak[R + 1][8] = {}, aq[W + 1][8] = {};
     {
         const uint32_t k0 = tc::smem_u32(sK), q0 = tc::smem_u32(sQ);
 #pragma unroll 2
         for (int ks = 0; ks < NK / 16; ++ks) {
             const uint32_t pan = (ks >> 2) * 8192, x = (ks & 3) << 5;
-            uint32_t fk[4], fq[4], fb[W + 1][4];
-            tc::ldm_x4(fk, k0 + pan + W * 2048 + (lt ^ x));
+            uint32_t fk[4], fq[4];
+            tc::ldm_x4(fk, k0 + pan + R * 2048 + (lt ^ x));
             tc::ldm_x4(fq, q0 + pan + W * 2048 + (lt ^ x));
 #pragma unroll
-            for (int j = 0; j <= W; ++j) tc::ldm_x4(fb[j], k0 + pan + j * 2048 + (ln ^ x));
-#pragma unroll
-            for (int j = 0; j <= W; ++j) {
-                tc::mma_block(ak[j], fk, fb[j]);
-                tc::mma_block(aq[j], fq, fb[j]);
+            for (int j = 0; j <= (W > R ? W : R); ++j) {
+                uint32_t fb[4];
+                tc::ldm_x4(fb, k0 + pan + j * 2048 + (ln ^ x));
+                if (j <= R) tc::mma_block(ak[j <= R ? j : 0], fk, fb);
+                if (j <= W) tc::mma_block(aq[j <= W ? j : 0], fq, fb);
             }
         }
     }
-    {
-        const int r0 = 16 * W + g;
+    block_sync();  // the sums of g are there, and K and Q have been read
+    // D beta of half n of block (row, j): rows g and g + 8
+    auto factors = [&](int row, int j, int n, uint64_t &d0, uint64_t &d1) {
+        const int r0 = 16 * row + g, col = 16 * j + 8 * n + t2;
         const float hi0 = sc[S_HI * kC + r0], hi1 = sc[S_HI * kC + r0 + 8];
         const float rf0 = sc[S_ROW * kC + r0], rf1 = sc[S_ROW * kC + r0 + 8];
-        const uint64_t s2 = f2(p.a.scale, p.a.scale);
+        if (j < row) {  // exp(c_t - c_j) = exp(c_t - c_e) exp(c_e - c_j), e the block's last token
+            const float he = sc[S_HI * kC + 16 * j + 15], re0 = rf0 * tc::ex2(hi0 - he), re1 = rf1 * tc::ex2(hi1 - he);
+            const float2 cc = *reinterpret_cast<const float2 *>(sc + S_COL * kC + col);
+            d0 = mul2(f2(re0, re0), f2(cc.x, cc.y)), d1 = mul2(f2(re1, re1), f2(cc.x, cc.y));
+        } else {  // nothing above the diagonal (where the exponent could overflow)
+            const float2 fc = *reinterpret_cast<const float2 *>(sc + S_INV * kC + col);
+            const float2 hc = *reinterpret_cast<const float2 *>(sc + S_HI * kC + col);
+            const float e00 = col <= r0 ? tc::ex2(hi0 - hc.x) : 0.f, e01 = col + 1 <= r0 ? tc::ex2(hi0 - hc.y) : 0.f;
+            const float e10 = col <= r0 + 8 ? tc::ex2(hi1 - hc.x) : 0.f, e11 = col + 1 <= r0 + 8 ? tc::ex2(hi1 - hc.y) : 0.f;
+            d0 = mul2(mul2(f2(rf0, rf0), f2(e00, e01)), f2(fc.x, fc.y));
+            d1 = mul2(mul2(f2(rf1, rf1), f2(e10, e11)), f2(fc.x, fc.y));
+        }
+    };
 #pragma unroll
-        for (int j = 0; j <= W; ++j) {
-            // a block left of the diagonal: exp(c_t - c_j) = exp(c_t - c_e) exp(c_e - c_j), e the block's last token
-            const float he = sc[S_HI * kC + 16 * j + 15];
-            const float re0 = j < W ? rf0 * tc::ex2(hi0 - he) : rf0, re1 = j < W ? rf1 * tc::ex2(hi1 - he) : rf1;
+    for (int j = 0; j <= R; ++j)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int col = 16 * j + 8 * n + t2;
-                const float2 fc = *reinterpret_cast<const float2 *>(sc + S_INV * kC + col);
-                uint64_t d0, d1;
-                if (j < W) {
-                    const float2 cc = *reinterpret_cast<const float2 *>(sc + S_COL * kC + col);
-                    d0 = mul2(f2(re0, re0), f2(cc.x, cc.y)), d1 = mul2(f2(re1, re1), f2(cc.x, cc.y));
-                } else {  // nothing above the diagonal (where the exponent could overflow)
-                    const float2 hc = *reinterpret_cast<const float2 *>(sc + S_HI * kC + col);
-                    const float e00 = col <= r0 ? tc::ex2(hi0 - hc.x) : 0.f, e01 = col + 1 <= r0 ? tc::ex2(hi0 - hc.y) : 0.f;
-                    const float e10 = col <= r0 + 8 ? tc::ex2(hi1 - hc.x) : 0.f, e11 = col + 1 <= r0 + 8 ? tc::ex2(hi1 - hc.y) : 0.f;
-                    d0 = mul2(mul2(f2(re0, re0), f2(e00, e01)), f2(fc.x, fc.y));
-                    d1 = mul2(mul2(f2(re1, re1), f2(e10, e11)), f2(fc.x, fc.y));
-                }
-                split2(mul2(mul2(f2(aq[j][4 * n], aq[j][4 * n + 1]), s2), d0), mh[j][2 * n], ml[j][2 * n]);
-                split2(mul2(mul2(f2(aq[j][4 * n + 2], aq[j][4 * n + 3]), s2), d1), mh[j][2 * n + 1], ml[j][2 * n + 1]);
-                const uint64_t a0 = mul2(f2(ak[j][4 * n], ak[j][4 * n + 1]), d0), a1 = mul2(f2(ak[j][4 * n + 2], ak[j][4 * n + 3]), d1);
-                if (j == W) {  // what lies on and above the diagonal of A is not read
-                    float *o = diag + 256 * W + g * 16 + 8 * n + t2;
-                    *reinterpret_cast<uint64_t *>(o) = a0;
-                    *reinterpret_cast<uint64_t *>(o + 128) = a1;
-                } else {
-                    uint32_t hi, lo;
-                    uint8_t *o = blk + a_blk(W, j) * 512 + t2 * 2;
-                    split2(a0, hi, lo);
-                    *reinterpret_cast<uint32_t *>(o + in_blk(g, n)) = hi;
-                    *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g, n)) = lo;
-                    split2(a1, hi, lo);
-                    *reinterpret_cast<uint32_t *>(o + in_blk(g + 8, n)) = hi;
-                    *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g + 8, n)) = lo;
-                }
+        for (int n = 0; n < 2; ++n) {
+            uint64_t d0, d1;
+            factors(R, j, n, d0, d1);
+            const uint64_t a0 = mul2(f2(ak[j][4 * n], ak[j][4 * n + 1]), d0), a1 = mul2(f2(ak[j][4 * n + 2], ak[j][4 * n + 3]), d1);
+            if (j == R) {  // what lies on and above the diagonal of A is not read
+                float *o = diag + 256 * R + g * 16 + 8 * n + t2;
+                *reinterpret_cast<uint64_t *>(o) = a0;
+                *reinterpret_cast<uint64_t *>(o + 128) = a1;
+            } else {
+                uint32_t hi, lo;
+                uint8_t *o = blk + a_blk(R, j) * 512 + t2 * 2;
+                split2(a0, hi, lo);
+                *reinterpret_cast<uint32_t *>(o + in_blk(g, n)) = hi;
+                *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g, n)) = lo;
+                split2(a1, hi, lo);
+                *reinterpret_cast<uint32_t *>(o + in_blk(g + 8, n)) = hi;
+                *reinterpret_cast<uint32_t *>(o + kLo * 512 + in_blk(g + 8, n)) = lo;
             }
         }
-    }
+    const uint64_t s2 = f2(p.a.scale, p.a.scale);
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint64_t d0, d1;
+            factors(W, j, n, d0, d1);
+            split2(mul2(mul2(f2(aq[j][4 * n], aq[j][4 * n + 1]), s2), d0), mh[j][2 * n], ml[j][2 * n]);
+            split2(mul2(mul2(f2(aq[j][4 * n + 2], aq[j][4 * n + 3]), s2), d1), mh[j][2 * n + 1], ml[j][2 * n + 1]);
+        }
 }
 
 // Row W of M T.
@@ -165,9 +175,14 @@ __device__ __forceinline__ void m_times_t(const PrepArgs &p, uint8_t *smem, int 
         }
         put_block(acc, mhi, mlo, W, j, lane);
     }
+    if (mlo) {  // above the diagonal, where A was
+        const float zero[8] = {};
+#pragma unroll
+        for (int j = W + 1; j < 4; ++j) put_block(zero, mlo, nullptr, W, j, lane);
+    }
 }
 
-__global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(const __grid_constant__ PrepParams prm) {
+__global__ void __launch_bounds__(kThreads, 6) delta_prep_kernel(const __grid_constant__ PrepParams prm) {
     pdl_wait();
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t &bar = *reinterpret_cast<uint64_t *>(smem + kOffBar);
@@ -209,7 +224,8 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(const __grid_co
             tc::tma_load_4d(smem + 16384 + k * kTile, &prm.mq, &bar, 64 * k, grp, (int)t0, (int)b);
         }
     }
-    if (w == 1) {
+    __syncthreads();  // the barrier is initialised
+    if (w == 1) {  // the sums, while the other warps' products run
         float *sc = reinterpret_cast<float *>(smem + kOffSc);
         float sh, sl;  // the inclusive sum of the lane's two tokens and all before, as a pair
         two_sum(gv[0], gv[1], sh, sl);
@@ -245,14 +261,13 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(const __grid_co
         }
         if (lane == 0) p.scal[item * kScal + kScalEnd] = tc::ex2(eh) * tc::ex2(el);
     }
-    __syncthreads();  // the barrier is initialised, the sums are there
     const bool ok = tc::mbar_wait(&bar, 0, kWaitNs);
     if (t0 + kC > len && len < a.L) {  // tokens past the sequence's length
         for (int x = (int)(len - t0) * 8 + tid; x < kC * 8; x += kThreads)
             for (int k = 0; k < 4; ++k) reinterpret_cast<uint4 *>(smem + k * kTile)[x] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
-    uint8_t *thi = smem, *tlo = smem + 2 * kTile, *mlo = smem + 3 * kTile, *blk = smem + kOffBlk;
+    uint8_t *thi = smem, *tlo = smem + 2 * kTile, *blk = smem + kOffBlk;
     const float *diag = reinterpret_cast<const float *>(blk + 12 * 512);
     uint32_t mh[4][4], ml[4][4];
     if (w == 0)
@@ -265,13 +280,11 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(const __grid_co
         rows_of<3>(p, smem, lane, mh, ml);
     __syncthreads();
     // the tiles take the place of K and Q; zeros above the diagonal
-#pragma unroll
-    for (int x = 0; x < (int)kTilesFwd / 16 / kThreads; ++x)
-        reinterpret_cast<uint4 *>(smem)[x * kThreads + tid] = make_uint4(0, 0, 0, 0);
-    if (p.tile_bytes > kTilesFwd)
-#pragma unroll
-        for (int x = 0; x < (int)kTile / 16 / kThreads; ++x)
-            reinterpret_cast<uint4 *>(mlo)[x * kThreads + tid] = make_uint4(0, 0, 0, 0);
+    for (int j = w + 1; j < 4; ++j) {
+        const float zero[8] = {};
+        put_block(zero, thi, tlo, w, j, lane);
+        put_block(zero, smem + kTile, nullptr, w, j, lane);
+    }
     // column `lane & 15` of the inverse of diagonal block w, by substitution
     float x[16];
     {
@@ -355,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 5) delta_prep_kernel(const __grid_co
         if (!ok) atomicCAS(a.status, SSD_OK, SSD_ERR_TIMEOUT);
         tc::bulk_store(p.tiles + item * p.tile_bytes, smem, p.tile_bytes);
         tc::bulk_commit();
-        tc::bulk_wait_all();
+        tc::bulk_wait_read_all();
     }
 }
 
