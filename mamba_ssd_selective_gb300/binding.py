@@ -552,17 +552,23 @@ def _delta_sizes(q, k, v, g, beta, lead):
     dev, io = v.device, v.dtype
     G, N = q.shape[-2:]
     H, P = v.shape[-2:]
-    _need(q, "q", (*lead, G, N), io, dev)
+    heads = (*lead, H)
+    if (isinstance(k, torch.Tensor) and isinstance(g, torch.Tensor) and isinstance(beta, torch.Tensor)
+            and q.shape == k.shape == (*lead, G, N) and v.shape == (*heads, P) and g.shape == beta.shape == heads
+            and q.dtype == k.dtype == g.dtype == beta.dtype == io and q.device == k.device == g.device == beta.device == dev
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()):
+        return H, G, P, N
+    _need(q, "q", (*lead, G, N), io, dev)  # one of these says what is wrong
     _need(k, "k", (*lead, G, N), io, dev)
-    _need(v, "v", (*lead, H, P), io, dev)
-    _need(g, "g", (*lead, H), io, dev)
-    _need(beta, "beta", (*lead, H), io, dev)
+    _need(v, "v", (*heads, P), io, dev)
+    _need(g, "g", heads, io, dev)
+    _need(beta, "beta", heads, io, dev)
     return H, G, P, N
 
 
 def _workspace(workspace, need, device):
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device)
     _need(workspace, "workspace", (workspace.numel(),), torch.uint8, device)
     return workspace
 
@@ -584,10 +590,12 @@ def gated_delta_chunked(q, k, v, g, beta, init_state=None, seqlens=None, scale=N
     d = _dims(Bsz, L, H, P, N, G, _io_code(io), SSD_FLAG_SIMT if simt else 0)
     if y is None:
         y = torch.empty_like(v)
-    _need(y, "y", (Bsz, L, H, P), io, dev)
+    else:
+        _need(y, "y", (Bsz, L, H, P), io, dev)
     if final_state is None and want_final_state:
         final_state = torch.empty((Bsz, H, P, N), dtype=torch.float32, device=dev)
-    _need(final_state, "final_state", (Bsz, H, P, N), torch.float32, dev)
+    else:
+        _need(final_state, "final_state", (Bsz, H, P, N), torch.float32, dev)
     lib = load()
     workspace = _workspace(workspace, int(lib.ssd_gated_delta_workspace_size(ctypes.byref(d))), dev)
     _check(lib.ssd_gated_delta_chunked(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -639,10 +647,12 @@ def gated_delta_step(state, q, k, v, g, beta, slots=None, new_state=None, scale=
         raise ValueError(f"state holds {S} states for {Bsz} rows")
     if new_state is None:
         new_state = state
-    _need(new_state, "new_state", (S, H, P, N), torch.float32, dev)
+    else:
+        _need(new_state, "new_state", (S, H, P, N), torch.float32, dev)
     if y is None:
         y = torch.empty_like(v)
-    _need(y, "y", (Bsz, H, P), io, dev)
+    else:
+        _need(y, "y", (Bsz, H, P), io, dev)
     d = _dims(Bsz, 1, H, P, N, G, _io_code(io))
     _check(load().ssd_gated_delta_step(ctypes.byref(d), S, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                        _ptr(slots), 1.0 / math.sqrt(N) if scale is None else scale, _ptr(new_state),
@@ -677,10 +687,12 @@ def block_norm(y, res, pre_weight, post_weight=None, z=None, scale=None, eps=1e-
     R, D, io, rio = _norm_args(y, res, pre_weight, post_weight, z, scale)
     if out is None:
         out = torch.empty_like(y)
+    else:
+        _need(out, "out", (R, D), y.dtype, y.device)
     if res_out is None:
         res_out = torch.empty_like(res)
-    _need(out, "out", (R, D), y.dtype, y.device)
-    _need(res_out, "res_out", (R, D), res.dtype, y.device)
+    else:
+        _need(res_out, "res_out", (R, D), res.dtype, y.device)
     _check(load().ssd_block_norm(R, D, io, rio, _ptr(y), _ptr(res), _ptr(z), _ptr(post_weight), _ptr(scale),
                                  _ptr(pre_weight), float(eps), _ptr(out), _ptr(res_out), _stream(stream, y.device)))
     return out, res_out
@@ -695,7 +707,7 @@ def block_norm_bwd(y, res, dout, pre_weight, dres_out=None, post_weight=None, z=
     dev = y.device
     _need(dout, "dout", (R, D), y.dtype, dev)
     _need(dres_out, "dres_out", (R, D), res.dtype, dev)
-    w = lambda on: torch.empty(D, dtype=torch.float32, device=dev) if on is not None else None  # noqa: E731
+    w = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
     g = dict(dy=torch.empty_like(y), dz=None if z is None else torch.empty_like(y), dres=torch.empty_like(res),
              dpre_weight=w(pre_weight), dpost_weight=w(post_weight), dscale=w(scale))
     lib = load()
