@@ -1043,7 +1043,9 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                     if (tt >= rows) continue;
                     const int64_t at = (b * a.L + t0 + tt) * H + h;
                     const float dg = (e ? sum - d[0] : sum) + se, db = be[e] == 0.f ? dbz[tt] : vw[e] / be[e];
-                    prm.dg[at] = __float2bfloat16_rn(tt < valid ? dg : 0.f);
+                    // the first decay scales a zero state where there is no other: the sums leave only their rounding there
+                    const bool felt = tt < valid && (t0 + tt > 0 || a.init);
+                    prm.dg[at] = __float2bfloat16_rn(felt ? dg : 0.f);
                     prm.dbeta[at] = __float2bfloat16_rn(tt < valid ? db : 0.f);
                 }
             }

@@ -334,6 +334,18 @@ def test_backward_where_beta_is_zero(ssd, io, P):
         near(got[n], want[n], io, n)
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 2, 1, 64, 128), (4, 1, 40, 10, 64, 128), (2, 20, 40, 20, 128, 64), (1, 130, 2, 1, 64, 128)])
+@pytest.mark.parametrize("simt", [False, True])
+def test_first_decay_has_no_gradient_without_a_state(ssd, shape, simt):
+    d = inputs.delta_inputs(*shape, "bf16", seed=41)
+    t = tokens(d, "bf16")
+    dy = torch.ones_like(t["v"])
+    got = ssd.gated_delta_chunked_bwd(**t, dy=dy, simt=simt)
+    assert (got["dg"][:, 0] == 0).all()
+    got = ssd.gated_delta_chunked_bwd(**t, dy=dy, init_state=torch.ones(shape[0], shape[2], shape[4], shape[5], device="cuda"), simt=simt)
+    assert (got["dg"][:, 0] != 0).any()
+
+
 # more chains than SMs: they are cut between CTAs, and the state is handed on between them
 MANY = [(1, 400, 160, 160, 64, 128), (5, 330, 64, 32, 64, 128), (1, 130, 100, 100, 200, 128), (2, 200, 80, 80, 128, 64)]
 # and few chains of many chunks, which are cut into pieces that run at once
