@@ -1,9 +1,9 @@
 // T and M T of every chunk of the gated delta rule (gated_delta_tc.cuh), and its
 // decays: one block of four warps per (b, chunk, head), bf16 inputs, N <= 128.
 //
-// Everything is blocks of 16 x 16. Warp w forms row w of the blocks of K K^T and
-// Q K^T (mma.sync, K and Q exact, float32 sums) and scales them to A and M in
-// registers. The diagonal blocks of I + A are inverted by substitution in
+// Everything is blocks of 16 x 16. Warp w forms row 3 - w of the blocks of K K^T and
+// row w of Q K^T (mma.sync, K and Q exact, float32 sums), five blocks each, while warp 1
+// first takes the sums of g, and scales them to A and M in registers. The diagonal blocks of I + A are inverted by substitution in
 // float32, one warp each; the rest of T follows from
 // [[Ta, 0], [-Tb A Ta, Tb]], first for the blocks of 32, then of 64, and M T row
 // by row. Operands that were rounded go in as pairs hi + lo of bf16 (2^-17 is
@@ -14,9 +14,11 @@
 // a steep decay does not blur the differences of the tokens after it (float64
 // would do, but its additions take a third of the block's time on this GPU).
 //
-// Bound by its latencies and shared memory: 12 to 14 thousand cycles a block, five
-// blocks per SM (with four B8 L2048 H80 takes 4 % longer), issue slots 39 % and shared
-// memory 53 % used; 69 us for the 5120 items of B2 L2048 H80.
+// Bound by nothing alone: 18 thousand cycles a block of loads, products and
+// barriers, six blocks per SM (B1 L4096 H24: 124 us, 125 with five, 127 with four), issue
+// slots 41 % and shared memory 59 % used; 69 us for the 5120 items of B2 L2048 H80. Of the 470 us of
+// B8 L2048 H80 storing the tiles costs 30, the products 29, loading K and Q 18,
+// T from the diagonal blocks 10 and M T 5 (each left out in turn).
 #include "gated_delta_tc.cuh"
 
 namespace ssd {
