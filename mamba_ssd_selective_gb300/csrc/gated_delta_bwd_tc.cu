@@ -655,13 +655,14 @@ struct GradParams {
 
 __device__ __forceinline__ void elem_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// One step of a sum over a warp's lanes that leaves value `lane` to each: lanes O apart exchange half of their 2 O values.
-template <int O> __device__ __forceinline__ void fold(float (&x)[32], int lane) {
-    const bool up = lane & O;
+// One step of a sum over the lanes of equal lane % 4 that leaves value lane / 4 of eight to each: lanes 4 O apart
+// exchange half of their 2 O values.
+template <int O> __device__ __forceinline__ void fold(float (&x)[8], int lane) {
+    const bool up = lane & (4 * O);
 #pragma unroll
     for (int k = 0; k < O; ++k) {
         const float send = up ? x[k] : x[k + O], keep = up ? x[k + O] : x[k];
-        x[k] = keep + __shfl_xor_sync(0xffffffffu, send, O);
+        x[k] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * O);
     }
 }
 
@@ -956,7 +957,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                 }
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
-            // dc over this and the previous heads: thread n, 32 tokens each
+            // dc over this and the previous heads
             float bl = 0.f, bh2 = 0.f, eq = 0.f;  // beta of this thread's tokens, exp(c_63), before the scalars are loaded anew
             if (warp == 0) bl = sc[SC_BETA * kC + 2 * lane], bh2 = sc[SC_BETA * kC + 2 * lane + 1], eq = sc[kScalEnd];
             tc::mbar_arrive(&bars[BAR_P_FULL]);
@@ -986,32 +987,38 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                 if (lane == 0) scratch[warp] = z;
             }
             {
-                float x[32];
-                const int n = 32 * wq + lane;
-                const uint8_t *pan = sKQ + (n >> 6) * 16384 + (n & 7) * 2;
+                // As fragments: Q and K transposed by ldmatrix give every thread the values that its own stand beside.
+                // Lanes 0-15 hold the addresses of the two blocks of 8 columns of Q, 16-31 of K.
+                float x[8] = {};  // tokens 8 (v / 2) + 2 (lane % 4) + v % 2 of this half
+                const uint32_t at = tc::smem_u32(sKQ) + (wq >> 1) * 16384 + (lane >> 4) * 8192;
 #pragma unroll
-                for (int k0 = 0; k0 < 32; k0 += 16) {
-                    float y[16], z[16], v[16];
-                    tc::tmem_ld16(tQ + lq + 32 * half + k0, v);
-                    tc::tmem_ld16(tK + lq + 32 * half + k0, y);
-                    tc::tmem_ld16(tR + lq + 32 * half + k0, z);
+                for (int m = 0; m < 2; ++m) {
+                    float v[16], y[16], z[16];
+                    const uint32_t lm = lq + (16u << 16) * m + 32 * half;
+                    tc::tmem_ld_frag32(tQ + lm, v);
+                    tc::tmem_ld_frag32(tK + lm, y);
+                    tc::tmem_ld_frag32(tR + lm, z);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const uint32_t o = piece(32 * half + k0 + k, (n & 63) >> 3);
-                        const float qv = to_f32(*reinterpret_cast<const __nv_bfloat16 *>(pan + o));
-                        const float kv = to_f32(*reinterpret_cast<const __nv_bfloat16 *>(pan + 8192 + o));
-                        x[k0 + k] = qv * v[k] + kv * (z[k] - y[k]);
+                    for (int tb = 0; tb < 4; ++tb) {
+                        uint32_t qk[4];
+                        tc::ldm_x4_trans(qk, at + piece(32 * half + 8 * tb + (lane & 7), 4 * (wq & 1) + 2 * m + ((lane >> 3) & 1)));
+#pragma unroll
+                        for (int r8 = 0; r8 < 2; ++r8)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int i4 = 4 * tb + 2 * r8 + e;
+                                const float qv = __uint_as_float(e ? qk[r8] & 0xffff0000u : qk[r8] << 16);
+                                const float kv = __uint_as_float(e ? qk[2 + r8] & 0xffff0000u : qk[2 + r8] << 16);
+                                x[2 * tb + e] = fmaf(qv, v[i4], fmaf(kv, z[i4] - y[i4], x[2 * tb + e]));
+                            }
                     }
                 }
                 tc::tc_fence_before();
-                // sums over the lanes, token `lane` left to each: halves of the values change places
-                fold<16>(x, lane);
-                fold<8>(x, lane);
                 fold<4>(x, lane);
                 fold<2>(x, lane);
                 fold<1>(x, lane);
-                r_qk[wq * kC + 32 * half + lane] = x[0];
+                r_qk[wq * kC + 32 * half + 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1)] = x[0];
             }
             elem_sync();
             if (warp == 0) {
