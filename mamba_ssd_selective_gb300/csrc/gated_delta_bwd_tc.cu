@@ -1059,26 +1059,36 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
             elem_sync();  // the sums' space is free again
         }
         if (heads > 0) {
-            // [64 tokens][64 columns] tiles in the panels' space, stored by TMA
-            const int n = 32 * wq + lane;
+            // [64 tokens][64 columns] tiles (128-byte swizzle) in the panels' space, stored by TMA: the sums as fragments,
+            // transposed by stmatrix
 #pragma unroll 1
             for (int which = 0; which < 2; ++which) {
-                float x[32];
-                tc::tmem_ld32((which ? tK : tQ) + lq + 32 * half, x);
-                if (which) {
+                const uint32_t tile = tc::smem_u32(sPan) + which * 16384 + (wq >> 1) * 8192;
 #pragma unroll
-                    for (int k0 = 0; k0 < 32; k0 += 16) {
+                for (int m = 0; m < 2; ++m) {
+                    float x[16];
+                    const uint32_t lm = lq + (16u << 16) * m + 32 * half;
+                    tc::tmem_ld_frag32((which ? tK : tQ) + lm, x);
+                    if (which) {
                         float y[16];
-                        tc::tmem_ld16(tR + lq + 32 * half + k0, y);
+                        tc::tmem_ld_frag32(tR + lm, y);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k0 + k] += y[k];
+                        for (int k = 0; k < 16; ++k) x[k] += y[k];
+                    }
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int tb = 0; tb < 4; tb += 2) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t8 = 32 * half + 8 * (tb + (k >> 1)) + 2 * (lane & 3), i4 = 4 * tb + 2 * k;
+                            o[k] = pack2(t8 < valid ? x[i4] : 0.f, t8 + 1 < valid ? x[i4 + 1] : 0.f);
+                        }
+                        tc::stm_x4_trans(tile + piece(32 * half + 8 * (tb + (lane >> 4)) + (lane & 7),
+                                                      4 * (wq & 1) + 2 * m + ((lane >> 3) & 1)), o);
                     }
                 }
-                tc::tmem_ld_wait();
-                __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(sPan + which * 16384 + (n >> 6) * 8192) + (n & 63);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[(32 * half + k) * 64] = __float2bfloat16_rn(32 * half + k < valid ? x[k] : 0.f);
             }
             tc::tc_fence_before();
             tc::fence_proxy_async_smem();
@@ -1237,8 +1247,8 @@ cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &args, void *workspace, cudaS
     ok = ok && tma_map_heads(&gp.mdy, args.dy, a.P, a.H, a.L, a.B, 64, kC, true);
     ok = ok && tma_map_heads(&gp.mdv, args.dv, a.P, a.H, a.L, a.B, 64, kC, true);
     ok = ok && tma_map_heads(&gp.mw, bf(s.w), a.P, a.H, a.L, a.B, 64, kC, true);
-    ok = ok && tma_map_heads(&gp.mdq, args.dq, a.N, a.G, a.L, a.B, 64, kC, false);
-    ok = ok && tma_map_heads(&gp.mdk, args.dk, a.N, a.G, a.L, a.B, 64, kC, false);
+    ok = ok && tma_map_heads(&gp.mdq, args.dq, a.N, a.G, a.L, a.B, 64, kC, true);
+    ok = ok && tma_map_heads(&gp.mdk, args.dk, a.N, a.G, a.L, a.B, 64, kC, true);
     if (!ok) return cudaErrorInvalidValue;
     gp.scal = p.scal;
     gp.w = bf(s.w);

@@ -369,6 +369,12 @@ __device__ __forceinline__ void ldm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
+// The reverse: four 8x8 blocks transposed to rows of 16 bytes at the lanes' addresses.
+__device__ __forceinline__ void stm_x4_trans(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
 // c (16x16: columns 0-7 in c[0..3], 8-15 in c[4..7]) += a b; a from ldm_x4 of a
 // row-major 16x16 block, b from ldm_x4_trans of a row-major [k][n] block.
 __device__ __forceinline__ void mma_block(float (&c)[8], const uint32_t (&a)[4], const uint32_t (&b)[4]) {
