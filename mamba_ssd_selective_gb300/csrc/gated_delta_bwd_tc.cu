@@ -625,9 +625,10 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
 // these roundings take the error of dq and dk from 1.7e-3 (2-norm), which rounding them to
 // bf16 makes alone, to 3.0e-3.
 //
-// Bound by shared memory, which the operands of 40 products (6 KB each) and the element
-// steps of a head both go through: 8 thousand cycles a head and chunk, 160 us for the
-// 5120 of B2 L2048 H80, HBM 36 %, tensor pipe 15 % busy.
+// Bound by shared memory and issue slots, which the operands of 40 products (6 KB each) and the
+// element steps of a head both want: the sums with q and k and the stores of dq and dk
+// as fragments instead of one lane a column took B4 L2048 H80 from 788 to 757 us; products
+// issued earlier, under G and X, changed nothing.
 namespace grad {
 constexpr int kThreads = 288, kElem = 256;  // warps 0-7 elementwise, warp 8 loads and products
 constexpr uint32_t kOffKQ = 0;              // 32 KB: two panels of 64 columns, each 64 rows of Q, then 64 of K
@@ -1099,7 +1100,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                     tc::tma_store_4d(&prm.mdk, sPan + 16384 + k * 8192, 64 * k, grp, (int)t0, (int)b);
                 }
                 tc::bulk_commit();
-                tc::bulk_wait_all();
+                tc::bulk_wait_read_all();
             }
         } else {  // no token here
             for (int x = tid; x < rows * N; x += kElem) {

@@ -108,7 +108,7 @@ cudaError_t launch_prep(const PrepArgs &p, cudaStream_t stream);
 cudaError_t launch_chain(const PrepArgs &p, __nv_bfloat16 *states, __nv_bfloat16 *w, cudaStream_t stream);
 
 // Whether a CTA takes two heads of a group: where pairs alone fill the SMs (B8 L2048 H80 G40: 477 us in pairs, 599 one by
-// one; the backward of B4 785 and 877); with fewer, one by one (B2 L2048 H80 would leave half of the SMs idle in pairs).
+// one; the backward of B4 takes 92 us longer one by one); with fewer, one by one (B2 L2048 H80 would leave half of the SMs idle in pairs).
 inline bool pair_heads(const DeltaArgs &a) {
     return a.P <= 64 && (a.H / a.G) % 2 == 0 && a.B * (a.H / 2) >= (int64_t)sm_count(152);
 }
