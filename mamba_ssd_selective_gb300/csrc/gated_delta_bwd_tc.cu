@@ -35,9 +35,9 @@ namespace {
 // dY^T Q under that of z. All of E's terms keep hi + lo, so that its gradient of
 // the initial state is as exact as the forward's state.
 //
-// TMEM (512 columns): X [0,64) | D [64,128) | E float32 [128,256) | operands [256,384):
+// TMEM (512 columns, gated_delta_columns.h): X 64 | D 64 | E float32 128 | operands 128:
 // E hi 64, lo 64; z of each head hi 32, lo 32; exp(c) dR hi 32, lo 32 | dY^T of each
-// head 32 [384,448) | s exp(c) dY^T hi 32, lo 32 [448,512).
+// head 32 | s exp(c) dY^T hi 32, lo 32.
 //
 // Warps: 0 loads; 1 products; 4-11 the chain's elementwise steps; 12-19 the
 // operands of dY, and dv.
@@ -167,7 +167,8 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tX = tmem, tD = tmem + 64, tE = tmem + 128, tOp = tmem + 256, tY = tmem + 384, tYe = tmem + 448;
+    const uint32_t tX = tmem + rev_col::kX, tD = tmem + rev_col::kD, tE = tmem + rev_col::kE;
+    const uint32_t tOp = tmem + rev_col::kOp, tY = tmem + rev_col::kY, tYe = tmem + rev_col::kYe;
     pdl_wait();
     const int items = PASS == WHOLE ? seg.items() : 1;
 

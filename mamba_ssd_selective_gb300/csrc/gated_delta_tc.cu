@@ -21,9 +21,10 @@
 // exact; M T, which only reaches y, is bf16: y's error is 2.3e-3, 1.7e-3 of it from
 // rounding y itself.
 //
-// TMEM (448 of 512 columns): QS [0,64) | KS, then w [64,128) | M w [128,192) |
-// S float32 [256,384) | operands [384,512): S hi 64, lo 64; R of each head hi 32,
-// lo 32; the update hi 32, lo 32, one after the other.
+// TMEM (512 columns, gated_delta_columns.h): Q S0^T | K S0^T | w | M w, 64 each; S float32 128;
+// operands 128: S hi 64, lo 64; R of each head hi 32, lo 32; the update hi 32, lo 32, one after
+// the other. w has columns of its own: its product begins when the first half of R is written, while
+// the chain's warps still read the second half of K S0^T.
 //
 // Warps: 0 loads; 1 products; 4-11 the chain's elementwise steps (two warps per
 // 32 rows, half of the tokens or columns each); 12-19 y (and w for the backward).
@@ -159,7 +160,8 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tQS = tmem, tU = tmem + 64, tO = tmem + 128, tS = tmem + 256, tOp = tmem + 384;
+    const uint32_t tQS = tmem + col::kQS, tKS = tmem + col::kKS, tW = tmem + col::kW, tMW = tmem + col::kMW;
+    const uint32_t tS = tmem + col::kS, tOp = tmem + col::kOp;
     pdl_wait();
     const int items = PASS == WHOLE ? seg.items() : 1;
 
@@ -261,9 +263,9 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                     const uint64_t dt = dT + (uint64_t)((s * NH + hf) * (kTilesFwd / 16)), dl = dt + 1024;
 #pragma unroll
                     for (int k = half; k < 8; k += 2)  // R hi, R lo with [T hi; M T]
-                        tc::mma_bf16_ts_if(one, tU, r0 + 8 * k, dt + 2 * (k & 3), id128, half > 0 || hf > 0 || k > 0);
+                        tc::mma_bf16_ts_if(one, tW, r0 + 8 * k, dt + 2 * (k & 3), id128, half > 0 || hf > 0 || k > 0);
 #pragma unroll
-                    for (int k = half; k < 4; k += 2) tc::mma_bf16_ts_if(one, tU, r0 + 8 * k, dl + 2 * k, id64, 1);
+                    for (int k = half; k < 4; k += 2) tc::mma_bf16_ts_if(one, tW, r0 + 8 * k, dl + 2 * k, id64, 1);
                 }
             }
             tc::mma_commit_if(one, &bars[BAR_B_DONE]);
@@ -390,7 +392,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
 #pragma unroll
                 for (int t0 = 0; t0 < 32; t0 += 16) {
                     float ks[16];
-                    tc::tmem_ld16(tU + lq + 32 * ch + t0, ks);
+                    tc::tmem_ld16(tKS + lq + 32 * ch + t0, ks);
                     float4 ng[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) ng[k] = *reinterpret_cast<const float4 *>(sc + SC_NEG * kC + t0 + 4 * k);
@@ -424,7 +426,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
 #pragma unroll
                 for (int t0 = 0; t0 < 32; t0 += 16) {
                     float u[16];
-                    tc::tmem_ld16(tU + lq + 32 * ch + t0, u);
+                    tc::tmem_ld16(tW + lq + 32 * ch + t0, u);
                     tc::tmem_ld_wait();
                     uint32_t hi[8], lo[8];
 #pragma unroll
@@ -512,7 +514,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 }
                 float qs[32], o[32];
                 if (SAVE) {
-                    tc::tmem_ld32(tU + lq + 32 * ch, qs);
+                    tc::tmem_ld32(tW + lq + 32 * ch, qs);
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
@@ -522,7 +524,7 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                     }
                 }
                 tc::tmem_ld32(tQS + lq + 32 * ch, qs);
-                tc::tmem_ld32(tO + lq + 32 * ch, o);
+                tc::tmem_ld32(tMW + lq + 32 * ch, o);
                 tc::tmem_ld_wait();
                 tc::tc_fence_before();
                 __syncwarp();

@@ -14,6 +14,7 @@
 #pragma once
 #include "common.cuh"
 #include "f32x2.cuh"
+#include "gated_delta_columns.h"
 #include "launch.h"
 #include "ssd_scan.h"
 #include "tc_host.h"
