@@ -383,11 +383,8 @@ delta_reverse_kernel(const __grid_constant__ ReverseParams prm) {
                 continue;
             }
             if (PASS == WHOLE && m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
-            const float *from = row_of(prm.dfinal);
-            if (m.c0 > 0)
-                from = PASS == WHOLE ? row_of(prm.carry)
-                       : PASS == FIND ? nullptr
-                                      : prm.pieces.in + ((bh * prm.pieces.n + m.piece) * P + p) * N;
+            const float *from = m.c0 == 0 ? row_of(prm.dfinal) : PASS == WHOLE ? row_of(prm.carry) : nullptr;
+            if (PASS == PIECES) from = prm.pieces.in + ((bh * prm.pieces.n + m.piece) * P + p) * N;
             wait_on(&bars[BAR_SC_FULL + (it & 1)], (it >> 1) & 1, fail);
             const float eq0 = scal[((it & 1) * NH + hf) * kScalDecay + kScalEnd];
             __syncwarp();
@@ -1233,7 +1230,7 @@ cudaError_t launch_delta_bwd_tc(const DeltaBwdArgs &args, void *workspace, cudaS
     rp.pieces = p.pieces;
     if (p.pieces.n > 1) {
         e = launch_reverse<1, FIND>(rp, stream);
-        if (e == cudaSuccess) e = launch_combine(p.pieces, a.B * a.H, a.P, a.N, stream);
+        if (e == cudaSuccess) e = launch_combine(p.pieces, args.dfinal, a.B * a.H, a.P, a.N, stream);
         if (e == cudaSuccess) e = launch_reverse<1, PIECES>(rp, stream);
     } else {
         e = pair_heads(a) ? launch_reverse<2, WHOLE>(rp, stream) : launch_reverse<1, WHOLE>(rp, stream);

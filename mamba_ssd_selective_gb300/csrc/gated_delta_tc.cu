@@ -355,11 +355,8 @@ delta_chain_kernel(const __grid_constant__ ChainParams prm) {
                 continue;
             }
             if (PASS == WHOLE && m.c0 > 0) flag_wait(prm.flags + m.unit, fail);
-            const float *from = row_of(a.init);
-            if (m.c0 > 0)
-                from = PASS == WHOLE ? row_of(prm.carry)
-                       : PASS == FIND ? nullptr
-                                      : prm.pieces.in + ((bh * prm.pieces.n + m.piece) * P + p) * N;
+            const float *from = m.c0 == 0 ? row_of(a.init) : PASS == WHOLE ? row_of(prm.carry) : nullptr;
+            if (PASS == PIECES) from = prm.pieces.in + ((bh * prm.pieces.n + m.piece) * P + p) * N;
             wait_on(&bars[BAR_T_FULL + (it & 1)], (it >> 1) & 1, fail);
             const float eq0 = scal[((it & 1) * NH + hf) * kScalDecay + kScalEnd];
             __syncwarp();
@@ -616,7 +613,7 @@ cudaError_t launch_chain(const PrepArgs &pr, __nv_bfloat16 *states, __nv_bfloat1
     p.pieces = pr.pieces;
     if (p.pieces.n > 1) {
         cudaError_t e = launch_form<1, false, FIND>(p, stream);
-        if (e == cudaSuccess) e = launch_combine(p.pieces, a.B * a.H, a.P, a.N, stream);
+        if (e == cudaSuccess) e = launch_combine(p.pieces, a.init, a.B * a.H, a.P, a.N, stream);
         if (e != cudaSuccess) return e;
         return states ? launch_form<1, true, PIECES>(p, stream) : launch_form<1, false, PIECES>(p, stream);
     }
@@ -644,10 +641,12 @@ namespace {
 // thread (n, j) adds up the j-th quarter of the products of column n, and the
 // quarters are then added in a fixed order. A value of Phi is replaced by the next
 // piece's as soon as it has been used, so that a piece costs its products and two barriers.
+// in[0] is a copy of the chains' first states (zero without them): the pieces then run at once without
+// reading them, and the last piece may write its final state over them.
 // 4 rows where these CTAs have an SM each, else 8, so that fewer read all of Phi: a whole call
 // of B1 L8192 H4 takes 88 us with 4 and 97 with 8, the backward of B1 L2048 H24 184 and 180.
 constexpr int kCarryPart = 32;
-template <int ROWS> __global__ void __launch_bounds__(512, 2) combine_kernel(Pieces q, int P, int N) {
+template <int ROWS> __global__ void __launch_bounds__(512, 2) combine_kernel(Pieces q, const float *first, int P, int N) {
     pdl_wait();
     __shared__ float4 s[128][ROWS / 4];  // [column][row]
     __shared__ float part[4][ROWS][128];
@@ -664,6 +663,10 @@ template <int ROWS> __global__ void __launch_bounds__(512, 2) combine_kernel(Pie
         if (n < N && p0 + 4 * r < P) in[((int64_t)k * P + 4 * r) * N] = v;
         reinterpret_cast<float *>(&s[n][r])[j] = n < N ? v : 0.f;
     };
+#pragma unroll
+    for (int r = 0; r < ROWS / 4; ++r)
+        if (n < N && p0 + 4 * r < P)
+            in[(int64_t)4 * r * N] = first ? first[(bh * P + p0 + 4 * r) * N + n] : 0.f;
     const float *at = phi + (q.n > 2 ? (int64_t)N * N : 0);
 #pragma unroll
     for (int i = 0; i < kCarryPart; ++i) {
@@ -705,10 +708,10 @@ template <int ROWS> __global__ void __launch_bounds__(512, 2) combine_kernel(Pie
 
 }  // namespace
 
-cudaError_t launch_combine(const Pieces &q, int64_t BH, int64_t P, int64_t N, cudaStream_t stream) {
+cudaError_t launch_combine(const Pieces &q, const float *first, int64_t BH, int64_t P, int64_t N, cudaStream_t stream) {
     const int rows = BH * ((P + 3) / 4) <= sm_count(152) ? 4 : 8;
     return launch_programmatic(rows == 4 ? combine_kernel<4> : combine_kernel<8>, dim3((unsigned)BH, (unsigned)((P + rows - 1) / rows)),
-                               dim3(512), 0, stream, q, (int)P, (int)N);
+                               dim3(512), 0, stream, q, first, (int)P, (int)N);
 }
 
 }  // namespace delta

@@ -64,7 +64,7 @@ __host__ __device__ inline int64_t row_blocks(int64_t P) { return (P + 127) / 12
 // the same hi + lo products as the states.
 struct Pieces {
     int n, chunks;          // n = 1: the chain whole
-    float *phi, *psi, *in;  // [B H][n - 1][N][N], [B H][n - 1][P][N], [B H][n][P][N] states entering the pieces; no [0]
+    float *phi, *psi, *in;  // [B H][n - 1][N][N], [B H][n - 1][P][N], [B H][n][P][N] states entering the pieces
     size_t bytes(int64_t BH, int64_t P, int64_t N) const {
         return n == 1 ? 0 : sizeof(float) * (size_t)BH * (size_t)((n - 1) * N * (N + P) + n * P * N);
     }
@@ -90,8 +90,8 @@ __device__ __forceinline__ void find_unit(int i, int pblocks, int &piece, int &k
     i += i >= pblocks;  // the first piece has no Phi
     piece = i / (pblocks + 1), kind = i % (pblocks + 1);
 }
-// in[piece] from phi and psi
-cudaError_t launch_combine(const Pieces &q, int64_t BH, int64_t P, int64_t N, cudaStream_t stream);
+// in[piece] from phi and psi; in[0] from the chains' first states [B H][P][N], which may be null (zero)
+cudaError_t launch_combine(const Pieces &q, const float *first, int64_t BH, int64_t P, int64_t N, cudaStream_t stream);
 
 struct PrepArgs {
     DeltaArgs a;

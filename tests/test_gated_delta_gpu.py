@@ -380,3 +380,20 @@ def test_chains_cut_between_blocks(ssd, shape, rate, ragged):
     for n in GRADS:
         near(got[n], want[n], "bf16", n)
     near(got["dinit"], want["dinit"], "state", "dinit")
+
+
+@pytest.mark.parametrize("shape", FEW + [(1, 1301, 8, 8, 128, 128)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_state_in_place_where_chains_are_cut(ssd, shape, ragged):
+    """A pool updated in place: the pieces of a chain run at once, and only the last one may write the state."""
+    B, L, H, G, P, N = shape
+    lens = lens_of([[L - 130, L, 0, 70, 1][i % 5] for i in range(B)]) if ragged else None
+    d = inputs.delta_inputs(B, L, H, G, P, N, "bf16", seed=33, init_state=True, rate=0.01)
+    t, init = tokens(d, "bf16"), dev(d["init"])
+    y, S = ssd.gated_delta_chunked(**t, init_state=init, seqlens=lens)
+    state = init.clone()
+    y2, S2 = ssd.gated_delta_chunked(**t, init_state=state, final_state=state, seqlens=lens)
+    assert S2 is state and torch.equal(y, y2) and torch.equal(S, S2)
+    y, S = ssd.gated_delta_chunked(**t, seqlens=lens)
+    y2, S2 = ssd.gated_delta_chunked(**t, init_state=torch.zeros_like(init), seqlens=lens)
+    assert torch.equal(y, y2) and torch.equal(S, S2)
