@@ -396,11 +396,12 @@ template <typename F, int... RVs> cudaError_t with_rv(int64_t nv, int most, F f,
      ...);
     return e;
 }
-template <typename F> cudaError_t for_row(int64_t dim, int most, F f) {
+// `RV4` lists the numbers for vectors of four: 16 is for the forward's 256 threads and rows above 8192.
+template <typename RV4, typename F> cudaError_t for_row(int64_t dim, int most, F f) {
     if (dim % 8 == 0)
         return with_rv(dim / 8, most, [&](auto rv, int t) { return f(Int<8>{}, rv, t); }, std::integer_sequence<int, 1, 2, 4, 8>{});
     if (dim % 4 == 0)
-        return with_rv(dim / 4, most, [&](auto rv, int t) { return f(Int<4>{}, rv, t); }, std::integer_sequence<int, 1, 2, 4, 8>{});
+        return with_rv(dim / 4, most, [&](auto rv, int t) { return f(Int<4>{}, rv, t); }, RV4{});
     return with_rv(dim, most, [&](auto rv, int t) { return f(Int<1>{}, rv, t); }, std::integer_sequence<int, 1, 4, 8, 32, 64>{});
 }
 
@@ -429,7 +430,7 @@ template <typename K> cudaError_t resident(K kern, int threads, size_t smem, int
 
 cudaError_t launch_block_norm(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream) {
     return for_types(io, res_io, [&](auto t, auto tr) {
-        return for_row(a.dim, 256, [&](auto v, auto rv, int threads) {
+        return for_row<std::integer_sequence<int, 1, 2, 4, 8, 16>>(a.dim, 256, [&](auto v, auto rv, int threads) {
             using T = decltype(t);
             using TR = decltype(tr);
             constexpr int V = decltype(v)::value, RV = decltype(rv)::value;
@@ -452,7 +453,8 @@ cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cu
     int64_t parts = 0;
     if (a.rows > 0) {
         cudaError_t e = for_types(io, res_io, [&](auto t, auto tr) {
-            return for_row(a.dim, a.dim % 8 == 0 && a.dim <= 8 * 640 ? 640 : 512, [&](auto v, auto rv, int threads) {
+            const int most = a.dim % 8 == 0 && a.dim <= 8 * 640 ? 640 : 512;
+            return for_row<std::integer_sequence<int, 1, 2, 4, 8>>(a.dim, most, [&](auto v, auto rv, int threads) {
                 using T = decltype(t);
                 using TR = decltype(tr);
                 constexpr int V = decltype(v)::value, RV = decltype(rv)::value;

@@ -102,3 +102,18 @@ def test_block_norm_rows_of_zeros(ssd):
     assert torch.allclose(out[0], torch.full((64,), (1 + 1e-5) ** -0.5, device="cuda"), rtol=1e-6)
     g = ssd.block_norm_bwd(y, res, torch.ones_like(y), w, post_weight=w, z=y, scale=w)
     assert all(torch.isfinite(x).all() for x in g.values())
+
+
+@pytest.mark.parametrize("size", [(3, 8196), (2, 10004), (2, 16380)])
+@pytest.mark.parametrize("io,rio", TYPES)
+def test_block_norm_wide_rows_of_vectors_of_four(ssd, size, io, rio):
+    """Rows above 8192 channels that are a multiple of four and not of eight, both directions."""
+    x, t = case(*size, io, rio, size[1], (1, 1, 1))
+    kw = dict(post_weight=t["post"], z=t["z"], scale=t["scale"])
+    out, r = ssd.block_norm(t["y"], t["res"], t["pre"], **kw)
+    for got, want, n in zip((out, r), delta.block_norm(x["y"], x["res"], x["pre"], x["post"], x["z"], x["scale"]), ("out", "res_out")):
+        near(got, want, n)
+    got = ssd.block_norm_bwd(t["y"], t["res"], t["dout"], t["pre"], dres_out=t["dres"], **kw)
+    want = delta.block_norm_bwd(x["y"], x["res"], x["dout"], x["pre"], x["dres"], x["post"], x["z"], x["scale"])
+    for n, w in want.items():
+        near(got[n], w, n)

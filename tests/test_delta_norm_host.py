@@ -2,12 +2,16 @@
 bad calls before any CUDA call, and the binding turns down tensors of another
 shape, type or layout. No GPU needed."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from mamba_ssd_selective_gb300 import binding
 from mamba_ssd_selective_gb300 import build as nvbuild
+from tests.conftest import ROOT
 
 OK, INVALID, UNSUPPORTED = 0, 1, 2
 P = ctypes.c_void_p(1 << 20)  # an aligned address that no refused call may touch
@@ -162,3 +166,24 @@ def test_binding_refuses_other_tensors():
         binding.block_norm(y[:, ::2], y[:, ::2], torch.ones(4))
     with pytest.raises(TypeError):
         binding.block_norm_bwd(y, y, y.float(), torch.ones(8))
+
+
+WIDTHS = """
+import ctypes
+from mamba_ssd_selective_gb300 import binding
+lib, P = binding.load(), ctypes.c_void_p(1 << 20)
+for io, rio in ((0, 0), (1, 1), (1, 0)):
+    for dim in range(1, 16385):
+        for f in (lambda: lib.ssd_block_norm(3, dim, io, rio, *[P] * 6, 1e-5, P, P, None),
+                  lambda: lib.ssd_block_norm_bwd(3, dim, io, rio, *[P] * 6, 1e-5, *[P] * 9, 1 << 40, None)):
+            assert f() == binding.SSD_ERR_CUDA, (dim, io, rio)
+            assert b"invalid argument" not in lib.ssd_last_error(), (dim, io, rio, lib.ssd_last_error())
+"""
+
+
+def test_block_norm_has_a_kernel_for_every_width(lib):
+    """In a process that sees no GPU the calls end at the first CUDA call, with the driver's error; a width without a
+    kernel is turned down before it as an invalid argument."""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="", PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", WIDTHS], env=env, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
