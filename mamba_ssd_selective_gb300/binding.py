@@ -6,6 +6,10 @@ allocates outputs and the workspace with torch when the caller passes none,
 and forwards pointers plus the current CUDA stream. Every step of the scan
 runs in the library's CUDA kernels; there is no fallback. If the library has
 not been built, or does not load, the first call raises.
+
+A `stream` argument runs the call on that stream instead: the caller orders
+it behind what writes the inputs and before what reads the outputs, and may
+drop any tensor as soon as the call has returned.
 """
 from __future__ import annotations
 
@@ -152,6 +156,29 @@ def _stream(stream, device):
     return stream.cuda_stream
 
 
+def _elsewhere(stream, device) -> bool:
+    """Whether `stream` is another stream than torch's current one."""
+    return stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _run_on(stream, call, args):
+    """call(**args) with `stream` as torch's current stream. What the call allocates then belongs to `stream`, where its
+    kernels run, so that its memory is handed out again only behind them; and what the caller gave, or is given, is kept
+    by the allocator until the work on both streams is done, whenever the caller lets go of it."""
+    given = [t for t in args.values() if isinstance(t, torch.Tensor)]
+    here = torch.cuda.current_stream(given[0].device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=given[0].device)
+    with torch.cuda.stream(stream):
+        out = call(**{**args, "stream": None})
+    for t in given:
+        t.record_stream(stream)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
 def _need(t, name, shape, dtype, device):
     if t is None:
         return
@@ -202,6 +229,8 @@ def ssd_scan_chunked(x, dt, A, B, C, D=None, init_state=None, chunk_size=None, y
     for bf16 inputs: "fused" (single pass, chunk 128), "staged" (three
     tensor-core kernels), "simt" (CUDA cores); None lets the library choose.
     Returns (y, final_state)."""
+    if _elsewhere(stream, x.device):
+        return _run_on(stream, ssd_scan_chunked, locals())
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError("x must be [B,L,H,P] and B, C [B,L,G,N]")
     Bsz, L, H, P = x.shape
@@ -246,6 +275,8 @@ def ssd_scan_chunked_bwd(x, dt, A, B, C, dy, D=None, init_state=None, dfinal_sta
     inputs. Returns a dict of float32 tensors dx, ddt, dA, dB, dC, dD (None when
     D is None) and dinit (None unless want_dinit). simt=True keeps the
     per-chunk gradients on the CUDA cores where the tensor cores would take them."""
+    if _elsewhere(stream, x.device):
+        return _run_on(stream, ssd_scan_chunked_bwd, locals())
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError("x must be [B,L,H,P] and B, C [B,L,G,N]")
     Bsz, L, H, P = x.shape
@@ -289,6 +320,8 @@ def ssd_scan_chunked_noalloc(x, dt, A, B, C, D=None, init_state=None, chunk_size
     and `final_state`; this wrapper allocates them only when they are None.
     The scan runs on x's device, which must be the current CUDA device: the
     library looks the scratch up on the current device. Returns (y, final_state)."""
+    if _elsewhere(stream, x.device):
+        return _run_on(stream, ssd_scan_chunked_noalloc, locals())
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError("x must be [B,L,H,P] and B, C [B,L,G,N]")
     Bsz, L, H, P = x.shape
@@ -329,6 +362,8 @@ def ssd_scan_chunked_noalloc_status(stream=None):
 
 def ssd_decode_step(state, x, dt, A, B, C, D=None, y=None, stream=None):
     """One decode token; `state` [B,H,P,N] float32 is updated in place. Returns y[B,H,P]."""
+    if _elsewhere(stream, x.device):
+        return _run_on(stream, ssd_decode_step, locals())
     Bsz, H, P, N = state.shape
     G = B.shape[1]
     dev, io = x.device, x.dtype
@@ -364,6 +399,8 @@ def selective_scan_diag(x, dt, A, B, C, D=None, init_state=None, chunk_size=2048
     from `workspace` (uint8, at least selective_scan_diag_workspace_size
     bytes) or allocated here; segmented=False runs one pass per sequence.
     Returns (y, final_state)."""
+    if _elsewhere(stream, x.device):
+        return _run_on(stream, selective_scan_diag, locals())
     Bsz, L, Dm = x.shape
     N = A.shape[1]
     dev, io = x.device, x.dtype
@@ -432,6 +469,8 @@ def ssd_selftest_bounded_wait(workspace, spin_limit, stream=None) -> None:
 def conv1d_step(x, conv_state, weight, bias=None, silu=True, out=None, stream=None):
     """Causal depthwise convolution step: x[B,C] shifts into the window
     conv_state[B,C,W] (float32, in place); returns act(weight . window + bias)."""
+    if _elsewhere(stream, x.device):
+        return _run_on(stream, conv1d_step, locals())
     Bsz, C = x.shape
     W = conv_state.shape[2]
     dev, io = x.device, x.dtype
@@ -448,6 +487,8 @@ def conv1d_step(x, conv_state, weight, bias=None, silu=True, out=None, stream=No
 
 def gated_rmsnorm(y, z, weight, group=None, eps=1e-5, out=None, stream=None):
     """out = g / sqrt(mean over each group of g^2 + eps) * weight, g = y * silu(z)."""
+    if _elsewhere(stream, y.device):
+        return _run_on(stream, gated_rmsnorm, locals())
     Bsz, D = y.shape
     dev, io = y.device, y.dtype
     _need(z, "z", (Bsz, D), io, dev)
@@ -497,6 +538,8 @@ def decode_layer_step(xBC, conv_state, conv_weight, conv_bias, dt, A, D, ssm_sta
     """One token of the decode layer body (conv step + silu, SSD decode step,
     gated RMS norm), states updated in place. xBC[B, H*P + 2*G*N], conv_state
     [B, Cc, W], ssm_state[B,H,P,N] float32, dt[B,H], z[B, H*P]. Returns out[B, H*P]."""
+    if _elsewhere(stream, xBC.device):
+        return _run_on(stream, decode_layer_step, locals())
     d, W, group, out, workspace = _layer_args(xBC, conv_state, conv_weight, conv_bias, dt, A, D, ssm_state, z,
                                               norm_weight, norm_group, out, workspace)
     _check(load().ssd_decode_layer_step(ctypes.byref(d), W, _ptr(xBC), _ptr(conv_state), _ptr(conv_weight),
@@ -582,6 +625,8 @@ def gated_delta_chunked(q, k, v, g, beta, init_state=None, seqlens=None, scale=N
     the device) are the tokens of right-padded sequences; y is zero past them.
     scale defaults to 1/sqrt(N). simt=True keeps bf16 inputs on the CUDA cores.
     Returns (y[B,L,H,P], final_state[B,H,P,N])."""
+    if _elsewhere(stream, v.device):
+        return _run_on(stream, gated_delta_chunked, locals())
     Bsz, L = v.shape[:2]
     H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz, L))
     dev, io = v.device, v.dtype
@@ -610,6 +655,8 @@ def gated_delta_chunked_bwd(q, k, v, g, beta, dy, init_state=None, dfinal_state=
     """Gradients of <dy, y> + <dfinal_state, final_state> for the inputs of
     gated_delta_chunked. Returns a dict of dq, dk, dv, dg, dbeta (the inputs'
     type) and dinit (float32; None unless want_dinit)."""
+    if _elsewhere(stream, v.device):
+        return _run_on(stream, gated_delta_chunked_bwd, locals())
     Bsz, L = v.shape[:2]
     H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz, L))
     dev, io = v.device, v.dtype
@@ -637,6 +684,8 @@ def gated_delta_step(state, q, k, v, g, beta, slots=None, new_state=None, scale=
     g/beta[B,H]. Row b uses state slots[b] (int32, on the device; a value
     outside the pool marks an idle row: y is zero, no state is touched), or
     state b without slots. Returns y[B,H,P]."""
+    if _elsewhere(stream, v.device):
+        return _run_on(stream, gated_delta_step, locals())
     Bsz = v.shape[0]
     H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz,))
     dev, io = v.device, v.dtype
@@ -684,6 +733,8 @@ def block_norm(y, res, pre_weight, post_weight=None, z=None, scale=None, eps=1e-
     res_out^2 + eps) pre_weight; without z, post_weight or scale that factor (and
     its norm) is left out. y/z[rows, dim] float32 or bfloat16, res of the same
     type or float32, weights and scale [dim] float32. Returns (out, res_out)."""
+    if _elsewhere(stream, y.device):
+        return _run_on(stream, block_norm, locals())
     R, D, io, rio = _norm_args(y, res, pre_weight, post_weight, z, scale)
     if out is None:
         out = torch.empty_like(y)
@@ -703,6 +754,8 @@ def block_norm_bwd(y, res, dout, pre_weight, dres_out=None, post_weight=None, z=
     """Gradients of <dout, out> + <dres_out, res_out> for block_norm's inputs.
     Returns a dict of dy, dz (y's type), dres (res's type), dpre_weight,
     dpost_weight and dscale (float32); None for an input that was not given."""
+    if _elsewhere(stream, y.device):
+        return _run_on(stream, block_norm_bwd, locals())
     R, D, io, rio = _norm_args(y, res, pre_weight, post_weight, z, scale)
     dev = y.device
     _need(dout, "dout", (R, D), y.dtype, dev)
