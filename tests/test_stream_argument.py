@@ -79,6 +79,19 @@ def test_what_a_call_makes_belongs_to_its_stream(monkeypatch, name):
     assert out and all(any(u is t and s is here for u, s in used) for t in out)
 
 
+@pytest.mark.parametrize("stream", [None, FakeStream()])
+@pytest.mark.parametrize("name", sorted(calls(torch.zeros)))
+def test_tensors_in_host_memory_are_refused(monkeypatch, name, stream):
+    """By their device, whatever the stream, before the library gets a pointer."""
+    class Library:
+        def __getattr__(self, f):
+            return lambda *a: 4096 if f.endswith("_size") else pytest.fail(f"{f} was called")
+
+    monkeypatch.setattr(binding, "load", Library)
+    with pytest.raises(ValueError, match="CUDA device"):
+        getattr(binding, name)(**calls(torch.zeros)[name], stream=stream)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("what", ["chunked", "backward", "norm_bwd", "scan"])
 def test_memory_let_go_of_while_the_call_waits(ssd, what):
