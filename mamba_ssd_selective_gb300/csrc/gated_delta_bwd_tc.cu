@@ -635,10 +635,13 @@ constexpr uint32_t kOffPan = kOffX + kTile; // per 64 state rows: S0 16 KB, E 16
 constexpr uint32_t kPan = 16384 * 3 + kTile;
 __host__ __device__ constexpr uint32_t off_scal(int NPAN) { return kOffPan + NPAN * kPan; }
 __host__ __device__ constexpr uint32_t off_red(int NPAN) { return off_scal(NPAN) + kScal * 4; }
-// sums: [4][64] of dc, [2][64] of dV.w, [64] the previous heads' dc, [64] dbeta where beta is zero, [8] <S0, E>, [8] scratch
+// sums: [4][64] of dc, [2][64] of dV.w, [64] the previous heads' dc, [64] dbeta where beta is tiny, [8] <S0, E>, [8] scratch
 constexpr int kRed = 256 + 4 * kC + 16;
 __host__ __device__ constexpr uint32_t columns(int NPAN) { return NPAN == 1 ? 256 : 512; }
 __host__ __device__ constexpr uint32_t off_bar(int NPAN) { return off_red(NPAN) + kRed * 4; }
+// dbeta is (dV . w) / beta, but dV = beta du is a bf16 operand: where beta is below this, du is formed without it, so that
+// du of 1e-18 still keeps dV from falling below the normal numbers (at beta = 2^-120 dbeta was off by 1.3e-2, at 2^-126 by half)
+constexpr float kTinyBeta = 0x1p-64f;
 enum { BAR_FULL, BAR_READY, BAR_G_DONE, BAR_P_FULL, BAR_DONE, kBars };
 __host__ __device__ constexpr size_t smem_bytes(int NPAN) { return off_bar(NPAN) + kBars * 8 + 16 + 1024; }
 }  // namespace grad
@@ -873,9 +876,9 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
             const float *hi = sc + kScalDecay, *rowf = hi + kC, *inv = rowf + kC;
             {
                 const float hi_t = hi[t];
-                // tokens whose beta is zero: dbeta_j = w_j . du_j with du formed anew
-                const uint32_t z0 = __ballot_sync(0xffffffffu, lane < valid && sc[SC_BETA * kC + lane] == 0.f);
-                const uint32_t z1 = __ballot_sync(0xffffffffu, lane + 32 < valid && sc[SC_BETA * kC + 32 + lane] == 0.f);
+                // tokens whose beta is too small to divide by: dbeta_j = w_j . du_j with du formed anew
+                const uint32_t z0 = __ballot_sync(0xffffffffu, lane < valid && fabsf(sc[SC_BETA * kC + lane]) < kTinyBeta);
+                const uint32_t z1 = __ballot_sync(0xffffffffu, lane + 32 < valid && fabsf(sc[SC_BETA * kC + 32 + lane]) < kTinyBeta);
                 uint64_t zero = (uint64_t)z1 << 32 | z0;
 #pragma unroll 1
                 while (zero) {
@@ -1048,7 +1051,7 @@ delta_grad_kernel(const __grid_constant__ GradParams prm) {
                     const int tt = 2 * lane + e;
                     if (tt >= rows) continue;
                     const int64_t at = (b * a.L + t0 + tt) * H + h;
-                    const float dg = (e ? sum - d[0] : sum) + se, db = be[e] == 0.f ? dbz[tt] : vw[e] / be[e];
+                    const float dg = (e ? sum - d[0] : sum) + se, db = fabsf(be[e]) < kTinyBeta ? dbz[tt] : vw[e] / be[e];
                     // the first decay scales a zero state where there is no other: the sums leave only their rounding there
                     const bool felt = tt < valid && (t0 + tt > 0 || a.init);
                     prm.dg[at] = __float2bfloat16_rn(felt ? dg : 0.f);

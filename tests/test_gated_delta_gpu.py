@@ -397,3 +397,19 @@ def test_state_in_place_where_chains_are_cut(ssd, shape, ragged):
     y, S = ssd.gated_delta_chunked(**t, seqlens=lens)
     y2, S2 = ssd.gated_delta_chunked(**t, init_state=torch.zeros_like(init), seqlens=lens)
     assert torch.equal(y, y2) and torch.equal(S, S2)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("beta", [2.0 ** -40, 2.0 ** -70, 2.0 ** -120, 2.0 ** -126, 2.0 ** -133, -2.0 ** -120])
+def test_backward_where_beta_is_tiny(ssd, io, beta):
+    """Tokens that write next to nothing, down to the least bf16: their dbeta has the size of the others'. (Their dv is
+    beta times that, below the normal numbers, and is not asked for.)"""
+    d = inputs.delta_inputs(1, 100, 4, 2, 64, 128, io, seed=19, init_state=True)
+    d["beta"][:, ::3] = beta
+    r = np.random.default_rng(20)
+    dy = inputs.round_to(r.standard_normal(d["v"].shape), io)
+    want = delta.delta_seq_bwd(*(d[n] for n in NAMES), dy, d["init"])
+    got = ssd.gated_delta_chunked_bwd(**tokens(d, io), dy=dev(dy, IO_TORCH[io]), init_state=dev(d["init"]))
+    for n in GRADS:
+        near(got[n], want[n], io, n)
+    near(got["dbeta"][:, ::3], want["dbeta"][:, ::3], io, "dbeta of those tokens")
