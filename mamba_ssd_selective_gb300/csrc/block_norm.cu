@@ -410,16 +410,16 @@ template <typename F> cudaError_t for_types(int io, int res_io, F f) {
     return f(0.f, 0.f);
 }
 
-// Blocks for `rows` rows: all that are resident at once, and no more.
-template <typename K> cudaError_t resident(K kern, int threads, size_t smem, int64_t rows, int64_t *grid) {
-    if (smem > 40 * 1024) {  // with the static part past the 48 KB that need no asking
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Blocks for `rows` rows: all that are resident at once, and no more. `most` is the largest smem of any call of KERN.
+template <auto KERN> cudaError_t resident(int threads, size_t smem, size_t most, int64_t rows, int64_t *grid) {
+    if (most > 40 * 1024) {  // with the static part past the 48 KB that need no asking
+        cudaError_t e = allow_shared<KERN>(most);
         if (e != cudaSuccess) return e;
     }
     *grid = imin<int64_t>(rows, sm_count(1));
     if (rows > *grid) {
         int per_sm = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERN, threads, smem);
         if (e != cudaSuccess) return e;
         *grid = imin<int64_t>(rows, (int64_t)sm_count(1) * imax(1, per_sm));
     }
@@ -430,14 +430,16 @@ template <typename K> cudaError_t resident(K kern, int threads, size_t smem, int
 
 cudaError_t launch_block_norm(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream) {
     return for_types(io, res_io, [&](auto t, auto tr) {
-        return for_row<std::integer_sequence<int, 1, 2, 4, 8, 16>>(a.dim, 256, [&](auto v, auto rv, int threads) {
+        constexpr int kMost = 256;
+        return for_row<std::integer_sequence<int, 1, 2, 4, 8, 16>>(a.dim, kMost, [&](auto v, auto rv, int threads) {
             using T = decltype(t);
             using TR = decltype(tr);
             constexpr int V = decltype(v)::value, RV = decltype(rv)::value;
-            auto kern = block_norm_kernel<T, TR, V, RV>;
-            const size_t smem = 2 * Ahead<T, V, RV>::bytes(threads) + Ahead<TR, V, RV>::bytes(threads);
+            constexpr auto kern = block_norm_kernel<T, TR, V, RV>;
+            auto smem_of = [](int n) { return 2 * Ahead<T, V, RV>::bytes(n) + Ahead<TR, V, RV>::bytes(n); };
+            const size_t smem = smem_of(threads);
             int64_t grid = 0;
-            cudaError_t e = resident(kern, threads, smem, a.rows, &grid);
+            cudaError_t e = resident<kern>(threads, smem, smem_of(kMost), a.rows, &grid);
             return e != cudaSuccess ? e : launch_programmatic(kern, dim3((unsigned)grid), dim3(threads), smem, stream, a);
         });
     });
@@ -460,23 +462,24 @@ cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cu
                 constexpr int V = decltype(v)::value, RV = decltype(rv)::value;
                 constexpr size_t kMost = 220 * 1024;
                 const size_t stage = 3 * Ahead<T, V, RV>::bytes(threads) + 2 * Ahead<TR, V, RV>::bytes(threads);
-                auto go = [&](auto kern, int stages) {
+                auto go = [&](auto staged, auto most, int stages) {
+                    constexpr auto kern = block_norm_bwd_kernel<T, TR, V, RV, decltype(staged)::value, decltype(most)::value>;
                     const size_t smem = stages * stage;
-                    cudaError_t r = resident(kern, threads, smem, a.rows, &parts);
+                    cudaError_t r = resident<kern>(threads, smem, decltype(staged)::value ? kMost : 0, a.rows, &parts);
                     if (r != cudaSuccess) return r;
                     parts = imin<int64_t>(parts, block_norm_bwd_parts(a.rows, a.dim));
                     return launch_programmatic(kern, dim3((unsigned)parts), dim3(threads), smem, stream, a, stages);
                 };
                 const int stages = 2 * stage <= kMost ? 2 : 1;
                 if (stage > kMost) {
-                    if constexpr (RV * V >= 16) return go(block_norm_bwd_kernel<T, TR, V, RV, false, 512>, 0);
+                    if constexpr (RV * V >= 16) return go(std::false_type{}, Int<512>{}, 0);
                     return cudaErrorInvalidValue;
                 }
                 if constexpr (RV == 1 && V == 8)
-                    if (threads > 512) return go(block_norm_bwd_kernel<T, TR, V, RV, true, 640>, stages);
+                    if (threads > 512) return go(std::true_type{}, Int<640>{}, stages);
                 if constexpr (RV <= 2)
-                    if (threads <= 320) return go(block_norm_bwd_kernel<T, TR, V, RV, true, 320>, stages);
-                return go(block_norm_bwd_kernel<T, TR, V, RV, true, 512>, stages);
+                    if (threads <= 320) return go(std::true_type{}, Int<320>{}, stages);
+                return go(std::true_type{}, Int<512>{}, stages);
             });
         });
         if (e != cudaSuccess) return e;

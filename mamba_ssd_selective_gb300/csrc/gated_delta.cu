@@ -478,11 +478,6 @@ template <typename F> cudaError_t for_width(int64_t N, F f) {
     return f(Int<1>{}, Int<32>{});
 }
 
-template <typename K> cudaError_t with_smem(K kern, size_t bytes) {
-    return bytes <= 48 * 1024 ? cudaSuccess
-                              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <typename T> cudaError_t step_t(const DeltaStepArgs &a, cudaStream_t stream) {
     return for_width(a.N, [&](auto vw, auto ne) {
         // rows a block walks: as many passes of 16 as leave the GPU two blocks per SM (64 rows of 80 heads: 69 us
@@ -499,9 +494,7 @@ template <typename T>
 cudaError_t forward_t(const DeltaArgs &a, float *ckpt, int ckpt_len, cudaStream_t stream) {
     return for_width(a.N, [&](auto vw, auto ne) {
         auto kern = delta_recurrent_kernel<T, vw.value, ne.value>;
-        const size_t smem = sizeof(float) * kStage * 2 * a.N;
-        cudaError_t e = with_smem(kern, smem);
-        if (e != cudaSuccess) return e;
+        const size_t smem = sizeof(float) * kStage * 2 * a.N;  // at most 32 KB
         const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.P + kRowsPass - 1) / kRowsPass));
         return launch_programmatic(kern, grid, dim3(kThreads), smem, stream, a, ckpt, ckpt_len);
     });
@@ -517,10 +510,12 @@ template <typename T> cudaError_t backward_t(const DeltaBwdArgs &a, cudaStream_t
     if (e != cudaSuccess) return e;
     e = for_width(a.f.N, [&](auto vw, auto ne) {
         constexpr int NE = decltype(ne)::value, CK = NE > 16 ? 8 : 16;
-        auto kern = delta_recurrent_bwd_kernel<T, vw.value, NE, CK>;
-        const size_t smem = sizeof(float) * (CK * NE * kThreads +
-                                             CK * (2 * a.f.N + 2 * kRowsPass + 2 * 4 * a.f.N + 2 * 4 + 2));
-        cudaError_t r = with_smem(kern, smem);
+        constexpr auto kern = delta_recurrent_bwd_kernel<T, decltype(vw)::value, NE, CK>;
+        auto smem_of = [](int64_t N) {
+            return sizeof(float) * (CK * NE * kThreads + CK * (2 * N + 2 * kRowsPass + 2 * 4 * N + 2 * 4 + 2));
+        };
+        const size_t smem = smem_of(a.f.N);
+        cudaError_t r = allow_shared<kern>(smem_of(8 * NE));  // 8 NE columns at most
         if (r != cudaSuccess) return r;
         return launch_programmatic(kern, dim3((unsigned)(a.f.B * a.f.H), (unsigned)nrb), dim3(kThreads), smem, stream,
                                    a);

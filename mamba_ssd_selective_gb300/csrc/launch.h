@@ -29,6 +29,18 @@ class DeviceOnce {
     std::atomic<unsigned long long> bits_{0};
 };
 
+// Lets kernel KERN take up to `most` bytes of dynamic shared memory, the most that any of its launches asks for: set
+// once per device and never lowered, so that calls of other sizes in other host threads can't take it back.
+template <auto KERN> cudaError_t allow_shared(size_t most) {
+    static DeviceOnce configured;
+    int dev = 0;
+    cudaError_t e = cudaSuccess;
+    if (!configured.pending(&dev, &e)) return e;
+    e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess) configured.done(dev);
+    return e;
+}
+
 // Streaming multiprocessors of the current device, queried once per device
 // ordinal (below 64). Returns `fallback` when no device can be queried (host
 // code on a machine without a GPU, e.g. a workspace-size query).

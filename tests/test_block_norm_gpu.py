@@ -5,6 +5,8 @@ below 1e-6 in the 2-norm; weights' gradients add up to a thousand rows. 1e-5 (2-
 largest result). bf16 results are rounded once: half a unit in the last of 8 bits is at most 2^-8 of each value, so of
 the 2-norm too (over many values 1.7e-3): 2^-8 for both, and a little for the float32 value's own error.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -117,3 +119,27 @@ def test_block_norm_wide_rows_of_vectors_of_four(ssd, size, io, rio):
     want = delta.block_norm_bwd(x["y"], x["res"], x["dout"], x["pre"], x["dres"], x["post"], x["z"], x["scale"])
     for n, w in want.items():
         near(got[n], w, n)
+
+
+def test_block_norm_from_two_threads(ssd):
+    """Widths that share a kernel and differ in the shared memory they ask for, at once: a call must not take back what
+    another has been allowed."""
+    said = []
+
+    def work(dim):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                y, w = torch.randn(4, dim, device="cuda"), torch.ones(dim, device="cuda")
+                for _ in range(1000):
+                    ssd.block_norm(y, y, w, z=y)
+                    ssd.block_norm_bwd(y, y, y, w, z=y)
+        except Exception as e:
+            said.append(e)
+
+    threads = [threading.Thread(target=work, args=(d,)) for d in (4096, 3400, 4096, 3400)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not said
