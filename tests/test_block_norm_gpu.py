@@ -143,3 +143,15 @@ def test_block_norm_from_two_threads(ssd):
         t.join()
     torch.cuda.synchronize()
     assert not said
+
+
+def test_block_norm_gate_of_any_size(ssd):
+    """silu of gates from -80 to 80 in float32, element by element: expf within 1 unit in the last place (2^-23), the sum
+    2^-24, the quotient 2 units, two products 2^-24 each: 4.5 units of 2^-23."""
+    z = torch.linspace(-80, 80, 16000, device="cuda").reshape(1, -1)
+    y, w = torch.ones_like(z), torch.ones(16000, device="cuda")
+    _, r = ssd.block_norm(y, torch.zeros_like(z), w, z=z)
+    want = z.double() / (1 + torch.exp(-z.double()))
+    assert ((r.double() - want).abs() <= 4.5 * 2.0 ** -23 * want.abs()).all()
+    g = ssd.block_norm_bwd(y, torch.zeros_like(z), torch.zeros_like(z), w, dres_out=y, z=z)  # dy = silu(z)
+    assert ((g["dy"].double() - want).abs() <= 4.5 * 2.0 ** -23 * want.abs()).all()
