@@ -452,6 +452,16 @@ ssd_status ssd_decode_graph_destroy(ssd_decode_graph *graph);
  * g is the logarithm of the decay (normally <= 0) and beta the step towards v
  * (normally in [0, 1]); q and k are used as given (rows of norm 1 keep the
  * update a contraction). States and all sums are float32.
+ *
+ * bf16 sequences with dstate <= 128 and both headdim and dstate multiples of 8
+ * go to the tensor cores in chunks of 64 tokens (the gradients with headdim <=
+ * 128), all others and those of a few tokens to recurrent kernels. Which form
+ * runs, and how long chains are cut, goes by the sizes, the batch among them:
+ * a call repeats itself bitwise, but a sequence alone can differ in the last
+ * bits from the same sequence in a batch. On the tensor cores a NaN or an
+ * infinity in a token can reach the tokens before it in its chunk, and, in k,
+ * g or beta, the heads that share its keys; other sequences and other groups
+ * never see it.
  * ------------------------------------------------------------------------- */
 
 /*
@@ -489,8 +499,11 @@ ssd_status ssd_gated_delta_chunked(const ssd_dims *dims, const void *q, const vo
  *   dv           [B, L, H, P]  io_dtype     dg, dbeta    [B, L, H]    io_dtype
  *   dinit_state  [B, H, P, N]  float32, may be NULL (not written)
  *   workspace    ssd_gated_delta_chunked_bwd_workspace_size(dims) bytes, 256-byte aligned
- * Gradients past a sequence's length are zero. The other arguments and limits
- * as for ssd_gated_delta_chunked.
+ * Gradients past a sequence's length are zero. On the tensor cores a head's dg
+ * is the difference that the head makes to sums over its group: beside its own
+ * rounding it is off by up to 2e-6 of the largest dg of the group's earlier heads
+ * (below the rounding to bf16 unless that is a thousand times its own), and NaN
+ * where theirs is. The other arguments and limits as for ssd_gated_delta_chunked.
  */
 size_t ssd_gated_delta_chunked_bwd_workspace_size(const ssd_dims *dims);
 ssd_status ssd_gated_delta_chunked_bwd(const ssd_dims *dims, const void *q, const void *k, const void *v,

@@ -413,3 +413,21 @@ def test_backward_where_beta_is_tiny(ssd, io, beta):
     for n in GRADS:
         near(got[n], want[n], io, n)
     near(got["dbeta"][:, ::3], want["dbeta"][:, ::3], io, "dbeta of those tokens")
+
+
+@pytest.mark.parametrize("how", ["small", "fast"])
+def test_backward_head_by_head(ssd, how):
+    """Heads of one group whose gradients or decays lie far apart, each head's dg and dbeta against its own size: dg of
+    the last four is what is left of sums with the first four, whose gradients are a thousand times theirs."""
+    d = inputs.delta_inputs(2, 300, 8, 1, 64, 128, "bf16", seed=61, init_state=True)
+    dy = np.random.default_rng(62).standard_normal(d["v"].shape)
+    if how == "small":
+        dy[:, :, 4:] *= 1e-3
+    else:
+        d["g"][:, :, 4:] = inputs.round_to(100 * d["g"][:, :, 4:], "bf16")
+    dy = inputs.round_to(dy, "bf16")
+    want = delta.delta_seq_bwd(*(d[n] for n in NAMES), dy, d["init"])
+    got = ssd.gated_delta_chunked_bwd(**tokens(d, "bf16"), dy=dev(dy, torch.bfloat16), init_state=dev(d["init"]))
+    for n in ("dv", "dg", "dbeta"):
+        for h in range(8):
+            near(got[n][:, :, h], want[n][:, :, h], "bf16", f"{n} of head {h}")
