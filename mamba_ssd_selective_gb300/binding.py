@@ -628,7 +628,8 @@ def gated_delta_chunked(q, k, v, g, beta, init_state=None, seqlens=None, scale=N
     q/k[B,L,G,N], v[B,L,H,P], g/beta[B,L,H] (float32 or bfloat16; head h reads
     group h // (H // G)), init_state[B,H,P,N] (float32). seqlens[B] (int32, on
     the device) are the tokens of right-padded sequences; y is zero past them.
-    scale defaults to 1/sqrt(N). simt=True keeps bf16 inputs on the CUDA cores.
+    scale defaults to 1/sqrt(N). simt=True keeps bf16 inputs on the CUDA cores:
+    float32 throughout, each result rounded once, and 3 to 50 times the time.
     Returns (y[B,L,H,P], final_state[B,H,P,N])."""
     if _elsewhere(stream, v.device):
         return _run_on(stream, gated_delta_chunked, locals())
@@ -658,8 +659,8 @@ def gated_delta_chunked(q, k, v, g, beta, init_state=None, seqlens=None, scale=N
 def gated_delta_chunked_bwd(q, k, v, g, beta, dy, init_state=None, dfinal_state=None, seqlens=None, scale=None,
                             workspace=None, stream=None, want_dinit=True, simt=False):
     """Gradients of <dy, y> + <dfinal_state, final_state> for the inputs of
-    gated_delta_chunked. Returns a dict of dq, dk, dv, dg, dbeta (the inputs'
-    type) and dinit (float32; None unless want_dinit)."""
+    gated_delta_chunked (simt as there). Returns a dict of dq, dk, dv, dg, dbeta
+    (the inputs' type) and dinit (float32; None unless want_dinit)."""
     if _elsewhere(stream, v.device):
         return _run_on(stream, gated_delta_chunked_bwd, locals())
     Bsz, L = v.shape[:2]

@@ -10,7 +10,7 @@
 // way to shared memory (cp.async, each thread copies and reads its own vectors, so
 // nothing but the sums crosses threads) while this one is reduced and written.
 // 16384 x 2560 bf16: 70 us, 6.0 TB/s; rows that are no multiple of four elements go
-// one by one (4096 x 1537 bf16: 49 us, 1.3 TB/s).
+// one by one (4096 x 1537 bf16 from cold caches: 83 us, 0.8 TB/s; 38 without a gate).
 #include "common.cuh"
 #include "launch.h"
 
@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(256) block_norm_kernel(BlockNormArgs a) {
 // MOST threads at most: 320 (two blocks per SM with one vector per thread: 16384 x
 // 2560 bf16 took 187 us, 267 us where 122 registers leave one block), 640 where that
 // leaves a thread one vector of eight (8192 x 5120 bf16: 148 us, 203 us with 320 threads and two
-// vectors), else 512.
+// vectors), else 512. 320 and 640 threads are rows of 2560 and 5120; the limits were measured there, and shorter rows take
+// the same forms with fewer threads (float32 residual, gate, cold: 16384 x 1024 65 us, 8192 x 2048 72, 4096 x 5120 91).
 // 8192 x 2560 bf16 with a float32 residual: 84 us, 5.5 TB/s (110 us with the weights
 // read anew for each row and three sums for the three weights).
 template <typename T, typename TR, int V, int RV, bool STAGED, int MOST>

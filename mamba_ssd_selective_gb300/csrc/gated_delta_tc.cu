@@ -35,7 +35,7 @@
 // Bound by the latency of the chain. A product of 16 columns of K takes 64
 // cycles whatever N, 36 of them a chunk (NH = 1); the rest is the elementwise steps
 // between them: 4700 cycles a chunk, 5600 for two heads (NH = 2). Tensor pipe 40 % busy, HBM
-// 38 %; 98 us for the 2560 chunks of B2 L2048 H80, 477 us the whole call of B8 L2048 H80.
+// 38 %; 98 us for the 2560 chunks of B2 L2048 H80, 469 us the whole call of B8 L2048 H80.
 //
 // Every wait is bounded (2 s): a timeout raises a flag, after which no wait
 // waits; the copies and products in flight are waited for (bounded too), and the

@@ -83,6 +83,8 @@ enum { WHOLE, FIND, PIECES };
 // own. Whole against pieces, whole calls, N 128, P 64: B1 L4096 H24 187 and 132 us (backward
 // 466 and 305), B1 L8192 H4 322 and 88 (767 and 189), B1 L2048 H24 100 and 85 (247 and 188);
 // and where this rule leaves them whole: B1 L1024 H24 55 and 58, B1 L768 H4 44 and 46 (B1 L1024 H48 160 and 182).
+// The costs are those of N 128, P 64 for every size. With P or N of 64 and 128 the cuts it makes paid as well: B1 L2048 H24
+// whole and cut 88 and 66 (N 64), 98 and 82 (P 128), 90 and 73 (both), backward 211 and 154, 310 and 220, 262 and 194.
 Pieces plan_pieces(int64_t B, int64_t H, int64_t P, int64_t nc, bool backward);
 // The CTAs of a chain in the first run, and what CTA i of it does: `kind` a block of rows of Psi or, past them, Phi.
 __host__ __device__ inline int find_units(int n, int pblocks) { return (n - 1) * (pblocks + 1) - 1; }
