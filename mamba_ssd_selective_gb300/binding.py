@@ -150,20 +150,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _current(device):
-    """The handle of torch's current stream on a tensor's device (a Stream object costs 2 us more)."""
-    if device.type != "cuda":
-        raise ValueError(f"expected tensors on a CUDA device, got {device}")
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _stream(stream, device):
-    return _current(device) if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    index = device.index  # none where a tensor is in host memory
+    if index is None:
+        raise ValueError(f"expected tensors on a CUDA device, got {device}")
+    return torch._C._cuda_getCurrentRawStream(index)  # the handle alone: a Stream object costs 2 us
 
 
 def _elsewhere(stream, device) -> bool:
     """Whether `stream` is another stream than torch's current one."""
-    return stream is not None and stream.cuda_stream != _current(device)
+    return stream.cuda_stream != _stream(None, device)
 
 
 def _run_on(stream, call, args):
@@ -234,7 +232,7 @@ def ssd_scan_chunked(x, dt, A, B, C, D=None, init_state=None, chunk_size=None, y
     for bf16 inputs: "fused" (single pass, chunk 128), "staged" (three
     tensor-core kernels), "simt" (CUDA cores); None lets the library choose.
     Returns (y, final_state)."""
-    if _elsewhere(stream, x.device):
+    if stream is not None and _elsewhere(stream, x.device):
         return _run_on(stream, ssd_scan_chunked, locals())
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError("x must be [B,L,H,P] and B, C [B,L,G,N]")
@@ -280,7 +278,7 @@ def ssd_scan_chunked_bwd(x, dt, A, B, C, dy, D=None, init_state=None, dfinal_sta
     inputs. Returns a dict of float32 tensors dx, ddt, dA, dB, dC, dD (None when
     D is None) and dinit (None unless want_dinit). simt=True keeps the
     per-chunk gradients on the CUDA cores where the tensor cores would take them."""
-    if _elsewhere(stream, x.device):
+    if stream is not None and _elsewhere(stream, x.device):
         return _run_on(stream, ssd_scan_chunked_bwd, locals())
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError("x must be [B,L,H,P] and B, C [B,L,G,N]")
@@ -325,7 +323,7 @@ def ssd_scan_chunked_noalloc(x, dt, A, B, C, D=None, init_state=None, chunk_size
     and `final_state`; this wrapper allocates them only when they are None.
     The scan runs on x's device, which must be the current CUDA device: the
     library looks the scratch up on the current device. Returns (y, final_state)."""
-    if _elsewhere(stream, x.device):
+    if stream is not None and _elsewhere(stream, x.device):
         return _run_on(stream, ssd_scan_chunked_noalloc, locals())
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError("x must be [B,L,H,P] and B, C [B,L,G,N]")
@@ -367,7 +365,7 @@ def ssd_scan_chunked_noalloc_status(stream=None):
 
 def ssd_decode_step(state, x, dt, A, B, C, D=None, y=None, stream=None):
     """One decode token; `state` [B,H,P,N] float32 is updated in place. Returns y[B,H,P]."""
-    if _elsewhere(stream, x.device):
+    if stream is not None and _elsewhere(stream, x.device):
         return _run_on(stream, ssd_decode_step, locals())
     Bsz, H, P, N = state.shape
     G = B.shape[1]
@@ -404,7 +402,7 @@ def selective_scan_diag(x, dt, A, B, C, D=None, init_state=None, chunk_size=2048
     from `workspace` (uint8, at least selective_scan_diag_workspace_size
     bytes) or allocated here; segmented=False runs one pass per sequence.
     Returns (y, final_state)."""
-    if _elsewhere(stream, x.device):
+    if stream is not None and _elsewhere(stream, x.device):
         return _run_on(stream, selective_scan_diag, locals())
     Bsz, L, Dm = x.shape
     N = A.shape[1]
@@ -474,7 +472,7 @@ def ssd_selftest_bounded_wait(workspace, spin_limit, stream=None) -> None:
 def conv1d_step(x, conv_state, weight, bias=None, silu=True, out=None, stream=None):
     """Causal depthwise convolution step: x[B,C] shifts into the window
     conv_state[B,C,W] (float32, in place); returns act(weight . window + bias)."""
-    if _elsewhere(stream, x.device):
+    if stream is not None and _elsewhere(stream, x.device):
         return _run_on(stream, conv1d_step, locals())
     Bsz, C = x.shape
     W = conv_state.shape[2]
@@ -492,7 +490,7 @@ def conv1d_step(x, conv_state, weight, bias=None, silu=True, out=None, stream=No
 
 def gated_rmsnorm(y, z, weight, group=None, eps=1e-5, out=None, stream=None):
     """out = g / sqrt(mean over each group of g^2 + eps) * weight, g = y * silu(z)."""
-    if _elsewhere(stream, y.device):
+    if stream is not None and _elsewhere(stream, y.device):
         return _run_on(stream, gated_rmsnorm, locals())
     Bsz, D = y.shape
     dev, io = y.device, y.dtype
@@ -543,7 +541,7 @@ def decode_layer_step(xBC, conv_state, conv_weight, conv_bias, dt, A, D, ssm_sta
     """One token of the decode layer body (conv step + silu, SSD decode step,
     gated RMS norm), states updated in place. xBC[B, H*P + 2*G*N], conv_state
     [B, Cc, W], ssm_state[B,H,P,N] float32, dt[B,H], z[B, H*P]. Returns out[B, H*P]."""
-    if _elsewhere(stream, xBC.device):
+    if stream is not None and _elsewhere(stream, xBC.device):
         return _run_on(stream, decode_layer_step, locals())
     d, W, group, out, workspace = _layer_args(xBC, conv_state, conv_weight, conv_bias, dt, A, D, ssm_state, z,
                                               norm_weight, norm_group, out, workspace)
@@ -631,7 +629,7 @@ def gated_delta_chunked(q, k, v, g, beta, init_state=None, seqlens=None, scale=N
     scale defaults to 1/sqrt(N). simt=True keeps bf16 inputs on the CUDA cores:
     float32 throughout, each result rounded once, and 3 to 50 times the time.
     Returns (y[B,L,H,P], final_state[B,H,P,N])."""
-    if _elsewhere(stream, v.device):
+    if stream is not None and _elsewhere(stream, v.device):
         return _run_on(stream, gated_delta_chunked, locals())
     Bsz, L = v.shape[:2]
     H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz, L))
@@ -661,7 +659,7 @@ def gated_delta_chunked_bwd(q, k, v, g, beta, dy, init_state=None, dfinal_state=
     """Gradients of <dy, y> + <dfinal_state, final_state> for the inputs of
     gated_delta_chunked (simt as there). Returns a dict of dq, dk, dv, dg, dbeta
     (the inputs' type) and dinit (float32; None unless want_dinit)."""
-    if _elsewhere(stream, v.device):
+    if stream is not None and _elsewhere(stream, v.device):
         return _run_on(stream, gated_delta_chunked_bwd, locals())
     Bsz, L = v.shape[:2]
     H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz, L))
@@ -690,7 +688,7 @@ def gated_delta_step(state, q, k, v, g, beta, slots=None, new_state=None, scale=
     g/beta[B,H]. Row b uses state slots[b] (int32, on the device; a value
     outside the pool marks an idle row: y is zero, no state is touched), or
     state b without slots. Returns y[B,H,P]."""
-    if _elsewhere(stream, v.device):
+    if stream is not None and _elsewhere(stream, v.device):
         return _run_on(stream, gated_delta_step, locals())
     Bsz = v.shape[0]
     H, G, P, N = _delta_sizes(q, k, v, g, beta, (Bsz,))
@@ -739,7 +737,7 @@ def block_norm(y, res, pre_weight, post_weight=None, z=None, scale=None, eps=1e-
     res_out^2 + eps) pre_weight; without z, post_weight or scale that factor (and
     its norm) is left out. y/z[rows, dim] float32 or bfloat16, res of the same
     type or float32, weights and scale [dim] float32. Returns (out, res_out)."""
-    if _elsewhere(stream, y.device):
+    if stream is not None and _elsewhere(stream, y.device):
         return _run_on(stream, block_norm, locals())
     R, D, io, rio = _norm_args(y, res, pre_weight, post_weight, z, scale)
     if out is None:
@@ -760,7 +758,7 @@ def block_norm_bwd(y, res, dout, pre_weight, dres_out=None, post_weight=None, z=
     """Gradients of <dout, out> + <dres_out, res_out> for block_norm's inputs.
     Returns a dict of dy, dz (y's type), dres (res's type), dpre_weight,
     dpost_weight and dscale (float32); None for an input that was not given."""
-    if _elsewhere(stream, y.device):
+    if stream is not None and _elsewhere(stream, y.device):
         return _run_on(stream, block_norm_bwd, locals())
     R, D, io, rio = _norm_args(y, res, pre_weight, post_weight, z, scale)
     dev = y.device
