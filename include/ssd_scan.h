@@ -569,6 +569,114 @@ ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32
                               void *dz, void *dres, float *dpre_weight, float *dpost_weight, float *dscale,
                               void *workspace, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated linear recurrence: a scan of single channels whose decay is a gate of
+ * the token. Per sequence and channel d, with sigmoids of the gates r and i and
+ * a weight lam per channel:
+ *
+ *     w_t = c softplus(lam) sigmoid(r_t)      a_t = exp(-w_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t      y_t = h_t
+ *
+ * States, decays and sums are float32. A sequence gives bitwise the same y and
+ * states alone as in a batch, and every call repeats itself bitwise. A NaN or
+ * an infinity in a token reaches the later tokens of its channel (in the
+ * backward the earlier ones too, and the channel's dlam) and no other.
+ * ------------------------------------------------------------------------- */
+
+#define SSD_GATED_LINEAR_CHUNK 64 /* tokens between two saved states */
+#define SSD_PACK8_GROUP 16        /* tokens of a channel that share a scale in 8 bits */
+
+/*
+ * The recurrence over a whole sequence.
+ *   x, r, i    [B, L, D]  io_dtype
+ *   lam        [D]        float32
+ *   c          positive and finite
+ *   init_state [B, D]     float32, may be NULL (zero)
+ *   seqlens    [B]        int32 on the device, may be NULL (L for every b):
+ *              sequence b is its first seqlens[b] tokens (values outside
+ *              [0, L] are brought into it). What x, r and i hold past them is
+ *              not used, y is zero there.
+ *   y          [B, L, D]  io_dtype, written
+ *   final_state[B, D]     float32, the state after the last token of each
+ *              sequence; may be NULL, may be the same buffer as init_state
+ * For a backward pass, each may be NULL:
+ *   states     [B, ceil(L/64), D]     float32: the state before token 0, 64, ...
+ *              (past a sequence's end its final state)
+ *   values     [3, B, L, D]           int8 and
+ *   scales     [3, B, ceil(L/16), D]  uint8, with values: x, r and i as
+ *              ssd_pack8 keeps them
+ * Outputs may not alias x, r or i. Limits here and below: batch <= 65535,
+ * dim <= 2097120, seqlen < 2^31.
+ */
+ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
+                                    const void *r, const void *i, const float *lam, float c, const float *init_state,
+                                    const int32_t *seqlens, void *y, float *final_state, float *states, int8_t *values,
+                                    uint8_t *scales, cudaStream_t stream);
+
+/*
+ * Backward of ssd_gated_linear_chunked: the gradients of
+ *     <dy, y> + <dfinal_state, final_state>
+ * with respect to every input. Deterministic (fixed-order sums, no atomics).
+ *   states       as the forward wrote them, or NULL: they are formed again, in
+ *                the workspace, from x, r, i and init_state (which is read then
+ *                only, and may be NULL)
+ *   dy           [B, L, D] io_dtype      dfinal_state [B, D] float32, may be NULL (0)
+ *   dx, dr, di   [B, L, D] io_dtype, zero past a sequence's length
+ *   dlam         [D] float32             dinit_state [B, D] float32, may be NULL
+ *   workspace    ssd_gated_linear_chunked_bwd_workspace_size(..., states given?)
+ *                bytes, 256-byte aligned
+ * Outputs may not alias inputs. The _packed form takes x, r and i in 8 bits as
+ * the forward (or ssd_pack8, three times) wrote them, with the states: the
+ * gradients are those at the values that the 8 bits stand for, h going on from
+ * the given state every 64 tokens.
+ */
+size_t ssd_gated_linear_chunked_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype,
+                                                   int32_t have_states);
+ssd_status ssd_gated_linear_chunked_bwd(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
+                                        const void *r, const void *i, const float *lam, float c,
+                                        const float *init_state, const float *states, const int32_t *seqlens,
+                                        const void *dy, const float *dfinal_state, void *dx, void *dr, void *di,
+                                        float *dlam, float *dinit_state, void *workspace, size_t ws_bytes,
+                                        cudaStream_t stream);
+ssd_status ssd_gated_linear_chunked_bwd_packed(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype,
+                                               const int8_t *values, const uint8_t *scales, const float *lam, float c,
+                                               const float *states, const int32_t *seqlens, const void *dy,
+                                               const float *dfinal_state, void *dx, void *dr, void *di, float *dlam,
+                                               float *dinit_state, void *workspace, size_t ws_bytes,
+                                               cudaStream_t stream);
+
+/*
+ * One token of the recurrence for a batch of sequences whose states lie in a pool.
+ *   state      [nslots, D] float32
+ *   x, r, i, y [B, D]      io_dtype (y may be the same buffer as one of the others)
+ *   slots      [B] int32 on the device, may be NULL (row b uses state b, and
+ *              nslots >= batch): row b uses state slots[b]. A value outside
+ *              [0, nslots) marks an idle row: its y is zero and no state is
+ *              touched. Two rows of one call must not name the same state.
+ *   new_state  [nslots, D] float32, the new states, written at the same slots;
+ *              may be the same buffer as state (update in place)
+ */
+ssd_status ssd_gated_linear_step(int64_t batch, int64_t dim, int32_t io_dtype, int64_t nslots, const float *state,
+                                 const void *x, const void *r, const void *i, const float *lam, float c,
+                                 const int32_t *slots, float *new_state, void *y, cudaStream_t stream);
+
+/*
+ * Activations in 8 bits, for what a backward pass reads again: tokens 16 j to
+ * 16 j + 15 of a sequence and channel share a scale 2^e, e the least whole
+ * number with max |x| <= 127 2^e and e >= -127; each value is the whole number
+ * nearest to x / 2^e, ties to even (off by 2^e / 2 at most, 1/127 of the
+ * group's largest).
+ *   x       [B, L, D] io_dtype         seqlens as above: zeros are kept past them
+ *   values  [B, L, D] int8, written    scales [B, ceil(L/16), D] uint8: e + 127
+ * A group with a NaN or an infinity is kept as NaN (scale 255, values 0).
+ * ssd_unpack8 gives back values * 2^e, which either io_dtype holds exactly (from
+ * inputs above 127 2^121, 3.38e38, it can be an infinity).
+ */
+ssd_status ssd_pack8(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
+                     const int32_t *seqlens, int8_t *values, uint8_t *scales, cudaStream_t stream);
+ssd_status ssd_unpack8(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const int8_t *values,
+                       const uint8_t *scales, void *out, cudaStream_t stream);
+
 /* Thread-local description of the last error returned on this thread. */
 const char *ssd_last_error(void);
 

@@ -1,7 +1,8 @@
 """GB300 (sm_103a) implementation of the Mamba-2 SSD selective scan, its
 decode step and the Mamba-1 diagonal scan; of the gated delta rule (over
-sequences, its gradients, one token over a pool of states); and of the block
-norm with its gradients.
+sequences, its gradients, one token over a pool of states); of the gated linear
+recurrence likewise, and activations in 8 bits for its backward; and of the
+block norm with its gradients.
 
 The compute path is the C-ABI library ``libssdscan.so`` (hand-written CUDA,
 declared in ``include/ssd_scan.h``); :mod:`.binding` is the thin Python layer

@@ -105,6 +105,20 @@ def load() -> ctypes.CDLL:
             for f in (lib.ssd_gated_delta_chunked, lib.ssd_gated_delta_chunked_bwd, lib.ssd_gated_delta_step,
                       lib.ssd_block_norm, lib.ssd_block_norm_bwd):
                 f.restype = ctypes.c_int
+            lib.ssd_gated_linear_chunked.argtypes = [i64, i64, i64, i32] + [vp] * 4 + [f32] + [vp] * 8
+            lib.ssd_gated_linear_chunked_bwd_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+            lib.ssd_gated_linear_chunked_bwd_workspace_size.restype = sz
+            lib.ssd_gated_linear_chunked_bwd.argtypes = ([i64, i64, i64, i32] + [vp] * 4 + [f32] + [vp] * 10
+                                                         + [vp, sz, vp])
+            lib.ssd_gated_linear_chunked_bwd_packed.argtypes = ([i64, i64, i64, i32] + [vp] * 3 + [f32] + [vp] * 9
+                                                                + [vp, sz, vp])
+            lib.ssd_gated_linear_step.argtypes = [i64, i64, i32, i64] + [vp] * 5 + [f32] + [vp] * 4
+            lib.ssd_pack8.argtypes = [i64, i64, i64, i32] + [vp] * 5
+            lib.ssd_unpack8.argtypes = [i64, i64, i64, i32] + [vp] * 4
+            for f in (lib.ssd_gated_linear_chunked, lib.ssd_gated_linear_chunked_bwd,
+                      lib.ssd_gated_linear_chunked_bwd_packed, lib.ssd_gated_linear_step, lib.ssd_pack8,
+                      lib.ssd_unpack8):
+                f.restype = ctypes.c_int
             lib.ssd_scan_chunked.argtypes = [dp] + [vp] * 7 + [ctypes.c_int, vp, vp, vp, sz, vp]
             lib.ssd_scan_chunked_noalloc.argtypes = [dp] + [vp] * 7 + [ctypes.c_int, vp, vp, vp]
             lib.ssd_scan_chunked_noalloc.restype = ctypes.c_int
@@ -774,3 +788,212 @@ def block_norm_bwd(y, res, dout, pre_weight, dres_out=None, post_weight=None, z=
                                   _ptr(g["dz"]), _ptr(g["dres"]), _ptr(g["dpre_weight"]), _ptr(g["dpost_weight"]),
                                   _ptr(g["dscale"]), _ptr(workspace), workspace.numel(), _stream(stream, dev)))
     return g
+
+
+# ------------------------------- gated linear recurrence, activations in 8 bits
+
+def _given(**tensors):
+    for n, t in tensors.items():
+        if t is None:
+            raise TypeError(f"{n} must be a torch.Tensor")
+
+
+def _linear_tokens(x, r, i, lam):
+    """Checks the token tensors and weights of a gated-linear call; returns x's shape."""
+    _given(r=r, i=i, lam=lam)
+    _need(x, "x", x.shape, x.dtype, x.device)
+    _need(r, "r", x.shape, x.dtype, x.device)
+    _need(i, "i", x.shape, x.dtype, x.device)
+    _need(lam, "lam", x.shape[-1:], torch.float32, x.device)
+    return x.shape
+
+
+def gated_linear_checkpoint(x, packed=True):
+    """Room for what gated_linear_chunked keeps for a backward pass over x[B,L,D], as the keyword arguments that it
+    and gated_linear_chunked_bwd_packed take: states[B,ceil(L/64),D] (float32), and with packed values[3,B,L,D]
+    (int8) and scales[3,B,ceil(L/16),D] (uint8), 3.2 bytes a token and channel for x, r and i."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, L, D]")
+    Bsz, L, D = x.shape
+    kept = dict(states=torch.empty((Bsz, -(-L // 64), D), dtype=torch.float32, device=x.device))
+    if packed:
+        kept["values"] = torch.empty((3, Bsz, L, D), dtype=torch.int8, device=x.device)
+        kept["scales"] = torch.empty((3, Bsz, -(-L // 16), D), dtype=torch.uint8, device=x.device)
+    return kept
+
+
+def gated_linear_chunked(x, r, i, lam, c=8.0, init_state=None, seqlens=None, y=None, final_state=None, states=None,
+                         values=None, scales=None, stream=None, want_final_state=True):
+    """The gated linear recurrence over a sequence, per channel: with a_t =
+    exp(-c softplus(lam) sigmoid(r_t)), h_t = a_t h_{t-1} + sqrt(1 - a_t^2)
+    sigmoid(i_t) x_t and y_t = h_t. x/r/i[B,L,D] (float32 or bfloat16), lam[D],
+    init_state[B,D] (float32). seqlens[B] (int32, on the device) are the tokens
+    of right-padded sequences; y is zero past them. states, and values with
+    scales, are written for a backward pass if given (gated_linear_checkpoint
+    makes them). Returns (y[B,L,D], final_state[B,D])."""
+    if stream is not None and _elsewhere(stream, x.device):
+        return _run_on(stream, gated_linear_chunked, locals())
+    if x.dim() != 3:
+        raise ValueError("x must be [B, L, D]")
+    Bsz, L, D = _linear_tokens(x, r, i, lam)
+    dev, io = x.device, x.dtype
+    if init_state is not None:
+        _need(init_state, "init_state", (Bsz, D), torch.float32, dev)
+    if seqlens is not None:
+        _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
+    if states is not None:
+        _need(states, "states", (Bsz, -(-L // 64), D), torch.float32, dev)
+    if (values is None) != (scales is None):
+        raise ValueError("values and scales must be given together")
+    if values is not None:
+        _need(values, "values", (3, Bsz, L, D), torch.int8, dev)
+        _need(scales, "scales", (3, Bsz, -(-L // 16), D), torch.uint8, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", (Bsz, L, D), io, dev)
+    if final_state is None and want_final_state:
+        final_state = torch.empty((Bsz, D), dtype=torch.float32, device=dev)
+    else:
+        _need(final_state, "final_state", (Bsz, D), torch.float32, dev)
+    _check(load().ssd_gated_linear_chunked(Bsz, L, D, _io_code(io), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), c,
+                                           _ptr(init_state), _ptr(seqlens), _ptr(y), _ptr(final_state), _ptr(states),
+                                           _ptr(values), _ptr(scales), _stream(stream, dev)))
+    return y, final_state
+
+
+def _linear_grads(dy, lam, dfinal_state, states, seqlens, want_dinit):
+    """Checks what both backward calls take; returns their outputs."""
+    if dy.dim() != 3:
+        raise ValueError("dy must be [B, L, D]")
+    Bsz, L, D = dy.shape
+    dev = dy.device
+    _given(lam=lam)
+    _need(lam, "lam", (D,), torch.float32, dev)
+    _need(dfinal_state, "dfinal_state", (Bsz, D), torch.float32, dev)
+    _need(states, "states", (Bsz, -(-L // 64), D), torch.float32, dev)
+    _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
+    return dict(dx=torch.empty_like(dy), dr=torch.empty_like(dy), di=torch.empty_like(dy), dlam=torch.empty_like(lam),
+                dinit=torch.empty((Bsz, D), dtype=torch.float32, device=dev) if want_dinit else None)
+
+
+def gated_linear_chunked_bwd(x, r, i, lam, dy, c=8.0, init_state=None, states=None, dfinal_state=None, seqlens=None,
+                             workspace=None, stream=None, want_dinit=True):
+    """Gradients of <dy, y> + <dfinal_state, final_state> for the inputs of
+    gated_linear_chunked. With the states that it wrote the sequence is not gone
+    over a second time (init_state is not read then). Returns a dict of dx, dr,
+    di (the inputs' type), dlam and dinit (float32; None unless want_dinit)."""
+    if stream is not None and _elsewhere(stream, dy.device):
+        return _run_on(stream, gated_linear_chunked_bwd, locals())
+    if x.dim() != 3:
+        raise ValueError("x must be [B, L, D]")
+    Bsz, L, D = _linear_tokens(x, r, i, lam)
+    _need(dy, "dy", (Bsz, L, D), x.dtype, x.device)
+    _need(init_state, "init_state", (Bsz, D), torch.float32, x.device)
+    g = _linear_grads(dy, lam, dfinal_state, states, seqlens, want_dinit)
+    lib, io = load(), _io_code(x.dtype)
+    need = int(lib.ssd_gated_linear_chunked_bwd_workspace_size(Bsz, L, D, io, int(states is not None)))
+    workspace = _workspace(workspace, need, x.device)
+    _check(lib.ssd_gated_linear_chunked_bwd(
+        Bsz, L, D, io, _ptr(x), _ptr(r), _ptr(i), _ptr(lam), c, _ptr(init_state), _ptr(states), _ptr(seqlens), _ptr(dy),
+        _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dlam"]), _ptr(g["dinit"]),
+        _ptr(workspace), workspace.numel(), _stream(stream, x.device)))
+    return g
+
+
+def gated_linear_chunked_bwd_packed(values, scales, states, lam, dy, c=8.0, dfinal_state=None, seqlens=None,
+                                    workspace=None, stream=None, want_dinit=True):
+    """gated_linear_chunked_bwd from the checkpoint that gated_linear_chunked
+    wrote (values, scales, states) instead of x, r and i: the gradients at the
+    values that the 8 bits stand for, in dy's type."""
+    if stream is not None and _elsewhere(stream, dy.device):
+        return _run_on(stream, gated_linear_chunked_bwd_packed, locals())
+    _given(values=values, scales=scales, states=states)
+    g = _linear_grads(dy, lam, dfinal_state, states, seqlens, want_dinit)
+    Bsz, L, D = dy.shape
+    dev = dy.device
+    _need(dy, "dy", (Bsz, L, D), dy.dtype, dev)
+    _need(values, "values", (3, Bsz, L, D), torch.int8, dev)
+    _need(scales, "scales", (3, Bsz, -(-L // 16), D), torch.uint8, dev)
+    lib, io = load(), _io_code(dy.dtype)
+    workspace = _workspace(workspace, int(lib.ssd_gated_linear_chunked_bwd_workspace_size(Bsz, L, D, io, 1)), dev)
+    _check(lib.ssd_gated_linear_chunked_bwd_packed(
+        Bsz, L, D, io, _ptr(values), _ptr(scales), _ptr(lam), c, _ptr(states), _ptr(seqlens), _ptr(dy),
+        _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dlam"]), _ptr(g["dinit"]),
+        _ptr(workspace), workspace.numel(), _stream(stream, dev)))
+    return g
+
+
+def gated_linear_step(state, x, r, i, lam, c=8.0, slots=None, new_state=None, y=None, stream=None):
+    """One token of the gated linear recurrence. state[S,D] (float32) is a pool
+    of states, updated in place or written to new_state; x/r/i[B,D]. Row b uses
+    state slots[b] (int32, on the device; a value outside the pool marks an idle
+    row: y is zero, no state is touched), or state b without slots. Returns y[B,D]."""
+    if stream is not None and _elsewhere(stream, x.device):
+        return _run_on(stream, gated_linear_step, locals())
+    if x.dim() != 2:
+        raise ValueError("x must be [B, D]")
+    Bsz, D = _linear_tokens(x, r, i, lam)
+    dev, io, S = x.device, x.dtype, state.shape[0]
+    _need(state, "state", (S, D), torch.float32, dev)
+    if slots is not None:
+        _need(slots, "slots", (Bsz,), torch.int32, dev)
+    elif S < Bsz:
+        raise ValueError(f"state holds {S} states for {Bsz} rows")
+    if new_state is None:
+        new_state = state
+    else:
+        _need(new_state, "new_state", (S, D), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", (Bsz, D), io, dev)
+    _check(load().ssd_gated_linear_step(Bsz, D, _io_code(io), S, _ptr(state), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), c,
+                                        _ptr(slots), _ptr(new_state), _ptr(y), _stream(stream, dev)))
+    return y
+
+
+def pack8(x, seqlens=None, values=None, scales=None, stream=None):
+    """x[B,L,...] (float32 or bfloat16) in 8 bits, for what a backward pass reads
+    again: 16 tokens of a channel share a power of two, values are whole numbers
+    from -127 to 127, zero past seqlens[b]; a group with a NaN or an infinity
+    reads back as NaN. Returns (values[B,L,...] int8, scales[B,ceil(L/16),...] uint8)."""
+    if stream is not None and _elsewhere(stream, x.device):
+        return _run_on(stream, pack8, locals())
+    if x.dim() < 3:
+        raise ValueError("x must be [B, L, ...]")
+    Bsz, L = x.shape[:2]
+    rest, dev = tuple(x.shape[2:]), x.device
+    _need(x, "x", tuple(x.shape), x.dtype, dev)
+    _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
+    if values is None:
+        values = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    else:
+        _need(values, "values", tuple(x.shape), torch.int8, dev)
+    if scales is None:
+        scales = torch.empty((Bsz, -(-L // 16), *rest), dtype=torch.uint8, device=dev)
+    else:
+        _need(scales, "scales", (Bsz, -(-L // 16), *rest), torch.uint8, dev)
+    _check(load().ssd_pack8(Bsz, L, math.prod(rest), _io_code(x.dtype), _ptr(x), _ptr(seqlens), _ptr(values),
+                            _ptr(scales), _stream(stream, dev)))
+    return values, scales
+
+
+def unpack8(values, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """What pack8's values[B,L,...] and scales stand for, in dtype (float32 or bfloat16)."""
+    if stream is not None and _elsewhere(stream, values.device):
+        return _run_on(stream, unpack8, locals())
+    if values.dim() < 3:
+        raise ValueError("values must be [B, L, ...]")
+    Bsz, L = values.shape[:2]
+    rest, dev = tuple(values.shape[2:]), values.device
+    _given(scales=scales)
+    _need(values, "values", tuple(values.shape), torch.int8, dev)
+    _need(scales, "scales", (Bsz, -(-L // 16), *rest), torch.uint8, dev)
+    if out is None:
+        out = torch.empty(values.shape, dtype=dtype, device=dev)
+    else:
+        _need(out, "out", tuple(values.shape), dtype, dev)
+    _check(load().ssd_unpack8(Bsz, L, math.prod(rest), _io_code(dtype), _ptr(values), _ptr(scales), _ptr(out),
+                              _stream(stream, dev)))
+    return out

@@ -217,6 +217,51 @@ cudaError_t launch_block_norm(int io, int res_io, const BlockNormArgs &a, cudaSt
 int block_norm_bwd_parts(int64_t rows, int64_t dim);
 cudaError_t launch_block_norm_bwd(int io, int res_io, const BlockNormArgs &a, cudaStream_t stream);
 
+// Gated linear recurrence (layouts as in ssd_gated_linear_chunked, _bwd, _step) and values in 8 bits (ssd_pack8).
+struct LinearArgs {
+    int64_t B, L, D;
+    const void *x, *r, *i;   // null in a backward from 8 bits
+    const float *lam, *init; // init may be null
+    float c;
+    const int32_t *seqlens;  // may be null
+    void *y;                 // null in the backward's forward pass
+    float *final_state;      // may be null
+    float *states;           // [B, ceil(L / 64), D], may be null in the forward
+    int8_t *values;          // [3, B, L, D] and
+    uint8_t *scales;         // [3, B, ceil(L / 16), D]: x, r and i in 8 bits, or null
+};
+struct LinearBwdArgs {
+    LinearArgs f;            // states, and either x, r, i or values and scales
+    const void *dy;
+    const float *dfinal;     // may be null
+    void *dx, *dr, *di;
+    float *dlam, *dinit;     // dinit may be null
+    float *part;             // [linear_bwd_parts(B)][D]
+};
+struct LinearStepArgs {
+    int64_t B, D, nslots;
+    const float *state;
+    float *new_state;
+    const void *x, *r, *i;
+    const float *lam;
+    float c;
+    const int32_t *slots;    // may be null
+    void *y;
+};
+struct Pack8Args {
+    int64_t B, L, D;
+    const void *x;           // packing
+    const int32_t *seqlens;  // packing, may be null
+    int8_t *values;
+    uint8_t *scales;
+    void *out;               // unpacking, else null
+};
+cudaError_t launch_linear(int io, const LinearArgs &a, cudaStream_t stream);
+int64_t linear_bwd_parts(int64_t B);
+cudaError_t launch_linear_bwd(int io, const LinearBwdArgs &a, cudaStream_t stream);
+cudaError_t launch_linear_step(int io, const LinearStepArgs &a, cudaStream_t stream);
+cudaError_t launch_pack8(int io, const Pack8Args &a, cudaStream_t stream);
+
 // Forward chunk states and entering states only (CUDA-core chunk state, then
 // the float32 state pass in place): a.states holds h_in(c), a.chunk_sum the
 // chunk decays. Used by the backward to recompute the forward.

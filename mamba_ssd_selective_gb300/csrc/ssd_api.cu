@@ -931,6 +931,178 @@ ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32
     return ok();
 }
 
+// ---- gated linear recurrence, values in 8 bits ----
+
+namespace {
+// Sizes of a call over [batch, seqlen, dim]: a block per sequence and 32 channels or more.
+ssd_status check_linear(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype) {
+    if (batch < 0 || seqlen < 0 || dim < 1)
+        return fail(SSD_ERR_INVALID_ARG, "batch and seqlen must be >= 0 and dim >= 1 (got %lld, %lld, %lld)",
+                    (long long)batch, (long long)seqlen, (long long)dim);
+    if (io_dtype != SSD_F32 && io_dtype != SSD_BF16)
+        return fail(SSD_ERR_INVALID_ARG, "io_dtype must be SSD_F32 or SSD_BF16 (got %d)", io_dtype);
+    if (batch > 65535) return fail(SSD_ERR_UNSUPPORTED, "batch must be <= 65535");
+    if (dim > 32 * 65535) return fail(SSD_ERR_UNSUPPORTED, "dim must be <= %d", 32 * 65535);
+    if (seqlen > 0x7fffffffLL) return fail(SSD_ERR_UNSUPPORTED, "seqlen must be below 2^31");
+    return SSD_OK;
+}
+ssd_status check_rate(float c) {
+    if (!(c > 0.f) || !std::isfinite(c)) return fail(SSD_ERR_INVALID_ARG, "c must be positive and finite");
+    return SSD_OK;
+}
+size_t linear_states_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
+    return round256((size_t)batch * (size_t)((seqlen + SSD_GATED_LINEAR_CHUNK - 1) / SSD_GATED_LINEAR_CHUNK) * (size_t)dim *
+                    sizeof(float));
+}
+size_t linear_part_bytes(int64_t batch, int64_t dim) {
+    return round256((size_t)ssd::linear_bwd_parts(batch) * (size_t)dim * sizeof(float));
+}
+ssd_status linear_bwd(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const ssd::LinearBwdArgs &given,
+                      void *workspace, size_t ws_bytes, cudaStream_t stream, const char *name) {
+    ssd::LinearBwdArgs a = given;
+    const bool some = batch > 0 && seqlen > 0;
+    if (!a.f.lam || !a.dlam || (some && (!a.dy || !a.dx || !a.dr || !a.di)))
+        return fail(SSD_ERR_INVALID_ARG, "lam, dy, dx, dr, di and dlam must be non-NULL");
+    ssd_status s = check_rate(a.f.c);
+    if (s != SSD_OK) return s;
+    s = check_aligned({{a.f.x, "x"}, {a.f.r, "r"}, {a.f.i, "i"}, {a.f.values, "values"}, {a.f.scales, "scales"},
+                       {a.f.lam, "lam"}, {a.f.init, "init_state"}, {a.f.states, "states"}, {a.f.seqlens, "seqlens"},
+                       {a.dy, "dy"}, {a.dfinal, "dfinal_state"}, {a.dx, "dx"}, {a.dr, "dr"}, {a.di, "di"},
+                       {a.dlam, "dlam"}, {a.dinit, "dinit_state"}});
+    if (s != SSD_OK) return s;
+    const size_t states = a.f.states ? 0 : linear_states_bytes(batch, seqlen, dim);
+    if ((s = check_ws(workspace, ws_bytes, 256 + states + linear_part_bytes(batch, dim))) != SSD_OK) return s;
+    char *ws = static_cast<char *>(workspace) + 256;
+    a.f.B = batch, a.f.L = seqlen, a.f.D = dim;
+    a.part = reinterpret_cast<float *>(ws + states);
+    cudaError_t e = cudaSuccess;
+    if (!a.f.states) {
+        a.f.states = reinterpret_cast<float *>(ws);
+        if (some) e = ssd::launch_linear(io_of(io_dtype), a.f, stream);
+    }
+    if (e == cudaSuccess) e = ssd::launch_linear_bwd(io_of(io_dtype), a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    return ok();
+}
+}  // namespace
+
+ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
+                                    const void *r, const void *i, const float *lam, float c, const float *init_state,
+                                    const int32_t *seqlens, void *y, float *final_state, float *states, int8_t *values,
+                                    uint8_t *scales, cudaStream_t stream) {
+    ssd_status s = check_linear(batch, seqlen, dim, io_dtype);
+    if (s == SSD_OK) s = check_rate(c);
+    if (s != SSD_OK) return s;
+    if (batch == 0) return ok();
+    if (!lam || (seqlen > 0 && (!x || !r || !i || !y)))
+        return fail(SSD_ERR_INVALID_ARG, "x, r, i, lam and y must be non-NULL");
+    if (!values != !scales) return fail(SSD_ERR_INVALID_ARG, "values and scales must be given together");
+    s = check_aligned({{x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}, {init_state, "init_state"}, {seqlens, "seqlens"},
+                       {y, "y"}, {final_state, "final_state"}, {states, "states"}, {values, "values"},
+                       {scales, "scales"}});
+    if (s != SSD_OK) return s;
+    ssd::LinearArgs a{};
+    a.B = batch, a.L = seqlen, a.D = dim;
+    a.x = x, a.r = r, a.i = i, a.lam = lam, a.c = c, a.init = init_state, a.seqlens = seqlens;
+    a.y = y, a.final_state = final_state, a.states = states, a.values = values, a.scales = scales;
+    cudaError_t e = ssd::launch_linear(io_of(io_dtype), a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_linear_chunked");
+    return ok();
+}
+
+size_t ssd_gated_linear_chunked_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype,
+                                                   int32_t have_states) {
+    if (check_linear(batch, seqlen, dim, io_dtype) != SSD_OK) return 0;
+    return 256 + (have_states ? 0 : linear_states_bytes(batch, seqlen, dim)) + linear_part_bytes(batch, dim);
+}
+
+ssd_status ssd_gated_linear_chunked_bwd(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
+                                        const void *r, const void *i, const float *lam, float c,
+                                        const float *init_state, const float *states, const int32_t *seqlens,
+                                        const void *dy, const float *dfinal_state, void *dx, void *dr, void *di,
+                                        float *dlam, float *dinit_state, void *workspace, size_t ws_bytes,
+                                        cudaStream_t stream) {
+    ssd_status s = check_linear(batch, seqlen, dim, io_dtype);
+    if (s != SSD_OK) return s;
+    if (batch > 0 && seqlen > 0 && (!x || !r || !i)) return fail(SSD_ERR_INVALID_ARG, "x, r and i must be non-NULL");
+    ssd::LinearBwdArgs a{};
+    a.f.x = x, a.f.r = r, a.f.i = i, a.f.lam = lam, a.f.c = c, a.f.init = init_state;
+    a.f.states = const_cast<float *>(states), a.f.seqlens = seqlens;
+    a.dy = dy, a.dfinal = dfinal_state, a.dx = dx, a.dr = dr, a.di = di, a.dlam = dlam, a.dinit = dinit_state;
+    return linear_bwd(batch, seqlen, dim, io_dtype, a, workspace, ws_bytes, stream, "ssd_gated_linear_chunked_bwd");
+}
+
+ssd_status ssd_gated_linear_chunked_bwd_packed(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype,
+                                               const int8_t *values, const uint8_t *scales, const float *lam, float c,
+                                               const float *states, const int32_t *seqlens, const void *dy,
+                                               const float *dfinal_state, void *dx, void *dr, void *di, float *dlam,
+                                               float *dinit_state, void *workspace, size_t ws_bytes,
+                                               cudaStream_t stream) {
+    ssd_status s = check_linear(batch, seqlen, dim, io_dtype);
+    if (s != SSD_OK) return s;
+    if (batch > 0 && seqlen > 0 && (!values || !scales || !states))
+        return fail(SSD_ERR_INVALID_ARG, "values, scales and states must be non-NULL");
+    ssd::LinearBwdArgs a{};
+    a.f.values = const_cast<int8_t *>(values), a.f.scales = const_cast<uint8_t *>(scales), a.f.lam = lam, a.f.c = c;
+    a.f.states = const_cast<float *>(states), a.f.seqlens = seqlens;
+    a.dy = dy, a.dfinal = dfinal_state, a.dx = dx, a.dr = dr, a.di = di, a.dlam = dlam, a.dinit = dinit_state;
+    return linear_bwd(batch, seqlen, dim, io_dtype, a, workspace, ws_bytes, stream, "ssd_gated_linear_chunked_bwd_packed");
+}
+
+ssd_status ssd_gated_linear_step(int64_t batch, int64_t dim, int32_t io_dtype, int64_t nslots, const float *state,
+                                 const void *x, const void *r, const void *i, const float *lam, float c,
+                                 const int32_t *slots, float *new_state, void *y, cudaStream_t stream) {
+    ssd_status s = check_linear(batch, 1, dim, io_dtype);
+    if (s == SSD_OK) s = check_rate(c);
+    if (s != SSD_OK) return s;
+    if (nslots < 0 || (!slots && nslots < batch))
+        return fail(SSD_ERR_INVALID_ARG, "nslots (%lld) must hold a state for each row without slots",
+                    (long long)nslots);
+    if (batch == 0) return ok();
+    if (!x || !r || !i || !lam || !y || (nslots > 0 && (!state || !new_state)))
+        return fail(SSD_ERR_INVALID_ARG, "state, x, r, i, lam, new_state and y must be non-NULL");
+    s = check_aligned({{state, "state"}, {x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}, {slots, "slots"},
+                       {new_state, "new_state"}, {y, "y"}});
+    if (s != SSD_OK) return s;
+    ssd::LinearStepArgs a{};
+    a.B = batch, a.D = dim, a.nslots = nslots, a.state = state, a.new_state = new_state;
+    a.x = x, a.r = r, a.i = i, a.lam = lam, a.c = c, a.slots = slots, a.y = y;
+    cudaError_t e = ssd::launch_linear_step(io_of(io_dtype), a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_linear_step");
+    return ok();
+}
+
+ssd_status ssd_pack8(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
+                     const int32_t *seqlens, int8_t *values, uint8_t *scales, cudaStream_t stream) {
+    ssd_status s = check_linear(batch, seqlen, dim, io_dtype);
+    if (s != SSD_OK) return s;
+    if (batch == 0 || seqlen == 0) return ok();
+    if (!x || !values || !scales) return fail(SSD_ERR_INVALID_ARG, "x, values and scales must be non-NULL");
+    s = check_aligned({{x, "x"}, {seqlens, "seqlens"}, {values, "values"}, {scales, "scales"}});
+    if (s != SSD_OK) return s;
+    ssd::Pack8Args a{};
+    a.B = batch, a.L = seqlen, a.D = dim, a.x = x, a.seqlens = seqlens, a.values = values, a.scales = scales;
+    cudaError_t e = ssd::launch_pack8(io_of(io_dtype), a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_pack8");
+    return ok();
+}
+
+ssd_status ssd_unpack8(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const int8_t *values,
+                       const uint8_t *scales, void *out, cudaStream_t stream) {
+    ssd_status s = check_linear(batch, seqlen, dim, io_dtype);
+    if (s != SSD_OK) return s;
+    if (batch == 0 || seqlen == 0) return ok();
+    if (!values || !scales || !out) return fail(SSD_ERR_INVALID_ARG, "values, scales and out must be non-NULL");
+    s = check_aligned({{values, "values"}, {scales, "scales"}, {out, "out"}});
+    if (s != SSD_OK) return s;
+    ssd::Pack8Args a{};
+    a.B = batch, a.L = seqlen, a.D = dim, a.out = out;
+    a.values = const_cast<int8_t *>(values), a.scales = const_cast<uint8_t *>(scales);
+    cudaError_t e = ssd::launch_pack8(io_of(io_dtype), a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_unpack8");
+    return ok();
+}
+
 ssd_status ssd_record_stage_events(cudaEvent_t *events, int count) {
     if (!events) {
         for (int i = 0; i < 4; ++i) g_stage_ev[i] = nullptr;

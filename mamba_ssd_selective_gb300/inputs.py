@@ -261,3 +261,16 @@ def block_norm_inputs(rows, dim, io_dtype="bf16", res_dtype="bf16", seed=0) -> d
     for n, m in (("pre", 1.0), ("post", 1.0), ("scale", 0.5)):
         x[n] = round_to(m + 0.1 * r.standard_normal(dim), "f32")
     return x
+
+
+# -------------------------------------------------- gated linear recurrence
+
+def linear_inputs(batch, seqlen, dim, io_dtype="bf16", seed=0, rate=1.0) -> dict:
+    """x, r, i, dy [B,L,D] ~ N(0, 1) (r and i before their sigmoids), lam with
+    exp(-8 softplus(lam)) = u^rate, u uniform in [0.9, 0.999], init and dfinal
+    [B,D]; float64 arrays exact in their types. A larger rate forgets faster."""
+    r = _rng(seed, 42)
+    d = {n: round_to(r.standard_normal((batch, seqlen, dim)), io_dtype) for n in ("x", "r", "i", "dy")}
+    d["lam"] = round_to(np.log(np.expm1(-rate * np.log(r.uniform(0.9, 0.999, dim)) / 8)), "f32")
+    d["init"], d["dfinal"] = (round_to(0.5 * r.standard_normal((batch, dim)), "f32") for _ in range(2))
+    return d
