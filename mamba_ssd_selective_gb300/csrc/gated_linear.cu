@@ -4,9 +4,14 @@
 // its backward, and one token of it over a pool of states.
 //
 // A run of tokens acts on the state as h -> A h + H, A the product of its a and H its result from zero, so runs are formed
-// apart and joined in order. A warp holds 32 V channels of a run of tokens in registers: it forms a and b, and its (A, H);
-// the warps of a block lie one behind the other in time and exchange (A, H) in shared memory; then each goes over its
-// run again from the state that enters it. Tokens past a sequence's end act as a = 1, b = 0 and are not read.
+// apart and joined in order. A lane has two channels; a warp holds 64 channels of a run in registers, the warps of a block lie
+// one behind the other in time, and so do the blocks of a cluster. A warp forms a, b and its (A, H), the warps of a block
+// join theirs in shared memory, each block sends its own to the others of its cluster, and every warp goes over its run again
+// from the state that enters it. The cluster then takes the next tokens of the sequence, the state kept by all of its threads.
+// Blocks of kBlock tokens are always joined one after the other, so the result depends neither on the cluster's size nor on
+// the batch. Tokens past a sequence's end act as a = 1, b = 0 and are not read.
+#include <cooperative_groups.h>
+
 #include "gated_linear.cuh"
 #include "launch.h"
 
@@ -14,113 +19,275 @@ namespace ssd {
 namespace linear {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kFwdRun = kGroup;          // tokens of a warp in the forward: a group of the 8-bit values
+constexpr int kTile = 64;                 // channels of a block, two a lane
+constexpr int kFwdRun = kGroup;           // tokens of a warp in the forward: a group of the 8-bit values
 constexpr int kBwdRun = kState / kWarps;  // and in the backward, whose block takes the tokens between two saved states
+constexpr int kMaxCluster = 8;
+
+// ------------------------------------------------------- copies to shared memory
+// A warp fetches the rows of its own runs, two steps ahead, and only it reads them: no barrier but its own. WIDE: 16 bytes a
+// lane, for rows that begin at a multiple of 16 bytes. Otherwise 4 bytes: the aligned words around each row, of those at the
+// tensor's end and the tile's only the bytes that belong to the tensor; a row then begins up to 3 bytes into its first word.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void *from, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T, bool WIDE> struct Row {  // in shared memory
+    static constexpr int kPitch = kTile * (int)sizeof(T) + (WIDE || sizeof(T) == 4 ? 0 : 4);
+};
+
+// Rows 0..n-1 of a tile: channels c0..min(c0 + 64, D) of the rows of `base` ([.., D]) from row `row` on.
+template <typename T, bool WIDE, int R>
+__device__ __forceinline__ void fetch_rows(unsigned char *to, const T *base, int64_t row, int n, int64_t c0, int64_t D, int lane) {
+    constexpr int PITCH = Row<T, WIDE>::kPitch;
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (WIDE) {
+        constexpr int PER = kTile * (int)sizeof(T) / 16, ROWS = 32 / PER > R ? R : 32 / PER;  // lanes a row, rows at once
+        const int piece = lane % PER, first = lane / PER;
+        const int64_t c = c0 + piece * (16 / (int)sizeof(T));
+        if (c < D && first < ROWS) {
+            const T *from = base + (row + first) * D + c;
+#pragma unroll
+            for (int j = 0; j < R / ROWS; ++j)
+                if (j * ROWS + first < n) copy16(dst + (j * ROWS + first) * PITCH + piece * 16, from + (int64_t)j * ROWS * D);
+        }
+    } else {
+        const int64_t have = imin<int64_t>(kTile, D - c0) * (int64_t)sizeof(T);  // bytes of the tile's row
+        for (int t = 0; t < n; ++t) {
+            const unsigned char *from = reinterpret_cast<const unsigned char *>(base + (row + t) * D + c0);
+            const int off = (int)(reinterpret_cast<uintptr_t>(from) & 3);
+            for (int w = lane; w * 4 < off + have; w += 32)
+                copy4(dst + t * PITCH + w * 4, from - off + w * 4, (int)imin<int64_t>(4, off + have - w * 4));
+        }
+    }
+}
+// The two channels of a lane in a row fetched so; `off` the bytes that the row begins into its first word.
+template <typename T, bool WIDE> __device__ __forceinline__ Raw<T, 2> row_pair(const unsigned char *row, int off, int lane, bool both) {
+    Raw<T, 2> r;
+    const T *p = reinterpret_cast<const T *>(row + off) + 2 * lane;
+    if constexpr (WIDE) {
+        r.word = *reinterpret_cast<const decltype(r.word) *>(p);
+    } else {
+        r.v[0] = p[0], r.v[1] = both ? p[1] : p[0];
+    }
+    return r;
+}
+// The same two channels in global memory; `both` and `one`: whether they exist.
+template <typename T, bool WIDE> __device__ __forceinline__ void store_pair(T *p, const Raw<T, 2> &r, bool one, bool both) {
+    if constexpr (WIDE) {
+        if (one) store<T, 2>(p, r);
+    } else {
+        if (one) p[0] = r.v[0];
+        if (both) p[1] = r.v[1];
+    }
+}
+template <typename T, bool WIDE> __device__ __forceinline__ void store_pair(T *p, float a, float b, bool one, bool both) {
+    Raw<T, 2> r;
+    r.v[0] = from_f32<T>(a), r.v[1] = from_f32<T>(b);
+    store_pair<T, WIDE>(p, r, one, both);
+}
+
+// ------------------------------------------------------------ runs, joined in order
+// (A, H) of a lane's two channels: h -> A h + H.
+struct Run2 {
+    float a0, h0, a1, h1;
+};
+__device__ __forceinline__ Run2 after(const Run2 &x, const Run2 &y) {  // x, then y
+    return {x.a0 * y.a0, fmaf(y.a0, x.h0, y.h0), x.a1 * y.a1, fmaf(y.a1, x.h1, y.h1)};
+}
 
 // ------------------------------------------------------------------ forward
+// Bound by HBM (8 bytes a token and channel in bf16) with the special function unit and the issue slots close behind it.
+template <typename T, bool WIDE> struct FwdShared {
+    static constexpr int kPitch = Row<T, WIDE>::kPitch;
+    struct Stage {
+        alignas(16) unsigned char row[3][kFwdRun][kPitch];
+    };
+    Stage stage[2][kWarps];
+    Run2 run[kWarps][32];
+    Run2 block[2][kMaxCluster][32];
+};
 
-template <typename T, int V, bool PACK> __global__ void __launch_bounds__(kThreads) linear_fwd_kernel(LinearArgs p) {
+template <typename T, bool WIDE, bool PACK>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_fwd_kernel(LinearArgs p) {
+    namespace cg = cooperative_groups;
     pdl_enter();
     constexpr int R = kFwdRun;
-    __shared__ float2 run[kWarps][32 * V];
+    extern __shared__ __align__(16) unsigned char raw_smem[];
+    FwdShared<T, WIDE> &sh = *reinterpret_cast<FwdShared<T, WIDE> *>(raw_smem);
+    const cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t c0 = ((int64_t)blockIdx.y * 32 + lane) * V, b = blockIdx.z, D = p.D;
-    const bool on = c0 < D;
-    const int64_t len = seq_len(p.seqlens, b, p.L);
-    float k[V], carry[V];
+    const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
+    const int64_t D = p.D, L = p.L;
+    const uint32_t tiles = (uint32_t)((D + kTile - 1) / kTile), items = (uint32_t)p.B * tiles;  // below 2^31
+    const uint32_t clusters = gridDim.x / blocks;
+    const int64_t tokens = (int64_t)warps * R, span = tokens * blocks;
+    const int64_t mine = rank * tokens + warp * R;  // of this warp's run, from the step's first token
+    const int64_t n = p.B * L * D;
+
+    auto fetch = [&](uint32_t item, int64_t s0, int stage) {
+        if (item < items) {
+            const uint32_t b = item / tiles;
+            const int64_t c0 = (int64_t)(item - b * tiles) * kTile, t0 = s0 + mine;
+            const int live = (int)imax<int64_t>(0, imin<int64_t>(R, seq_len(p.seqlens, b, L) - t0));
+            auto &to = sh.stage[stage][warp];
+            fetch_rows<T, WIDE, R>(to.row[0][0], (const T *)p.x, b * L + t0, live, c0, D, lane);
+            fetch_rows<T, WIDE, R>(to.row[1][0], (const T *)p.r, b * L + t0, live, c0, D, lane);
+            fetch_rows<T, WIDE, R>(to.row[2][0], (const T *)p.i, b * L + t0, live, c0, D, lane);
+        }
+        copy_commit();
+    };
+    // the step after (item, s0)
+    auto advance = [&](uint32_t &item, int64_t &s0) {
+        s0 += span;
+        if (s0 >= L) s0 = 0, item += clusters;
+    };
+
+    uint32_t item = blockIdx.x / blocks, next_item = item;
+    int64_t s0 = 0, next_s0 = 0;
+    fetch(next_item, next_s0, 0);
+    advance(next_item, next_s0);
+    fetch(next_item, next_s0, 1);
+    float carry[2] = {0.f, 0.f};
+    uint64_t rate2 = 0, rate_log2 = 0;
+    for (int step = 0; item < items; ++step) {
+        const int64_t b = item / tiles, c = (int64_t)(item - (uint32_t)b * tiles) * kTile + 2 * lane, t0 = s0 + mine;
+        const int64_t at = (b * L + t0) * D + c;
+        const bool one = c < D, both = c + 1 < D;
+        const int live = (int)imax<int64_t>(0, imin<int64_t>(R, seq_len(p.seqlens, b, L) - t0));  // tokens of the run that count
+        const int rows = (int)imax<int64_t>(0, imin<int64_t>(R, L - t0));                         // and that exist
+        auto &in = sh.stage[step & 1][warp];
+        float k[2];
+        if (s0 == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        k[v] = on ? p.c * softplus(p.lam[c0 + v]) : 0.f;
-        carry[v] = on && p.init ? p.init[b * D + c0 + v] : 0.f;
-    }
-    const int64_t n = p.B * p.L * D;
-    for (int64_t s0 = 0; s0 < p.L; s0 += (int64_t)warps * R) {
-        const int64_t t0 = s0 + warp * R, at = (b * p.L + t0) * D + c0;
-        const int live = on ? (int)imax<int64_t>(0, imin<int64_t>(R, len - t0)) : 0;  // tokens of the run that count
-        const int rows = on ? (int)imax<int64_t>(0, imin<int64_t>(R, p.L - t0)) : 0;  // and that exist
-        Raw<T, V> x[R], r[R], i[R];
-#pragma unroll
-        for (int t = 0; t < R; ++t)
-            if (t < live) {
-                x[t] = load<T, V>((const T *)p.x + at + t * D);
-                r[t] = load<T, V>((const T *)p.r + at + t * D);
-                i[t] = load<T, V>((const T *)p.i + at + t * D);
+            for (int v = 0; v < 2; ++v) {
+                k[v] = c + v < D ? p.lam[c + v] : 0.f;
+                carry[v] = c + v < D && p.init ? p.init[b * D + c + v] : 0.f;
             }
+        }
+        copy_wait<1>();
+        __syncwarp();
+        if (s0 == 0) {
+            k[0] = p.c * softplus(k[0]), k[1] = p.c * softplus(k[1]);
+            rate2 = f2(2.f * k[0], 2.f * k[1]), rate_log2 = f2(kLog2e * k[0], kLog2e * k[1]);
+        }
+        auto offset = [&](const void *base, int t) {  // of a row in its first word
+            return WIDE || sizeof(T) == 4 ? 0 : (int)((reinterpret_cast<uintptr_t>(base) + (uintptr_t)(at - 2 * lane + t * D) * sizeof(T)) & 3);
+        };
         if constexpr (PACK) {
             if (rows > 0) {
-                const int64_t groups = (p.L + kGroup - 1) / kGroup;
-                const Raw<T, V> *src[3] = {x, r, i};
+                const int64_t groups = (L + kGroup - 1) / kGroup;
+                const void *base[3] = {p.x, p.r, p.i};
 #pragma unroll
                 for (int z = 0; z < 3; ++z) {
-                    To8 to8[V];
-                    Raw<uint8_t, V> code;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int t = 0; t < R; ++t) top = max(top, abs_bits(to_f32(src[z][t].v[v])));
-                        code.v[v] = (uint8_t)scale_code(top);
-                        to8[v] = To8(code.v[v]);
-                    }
-                    store<uint8_t, V>(p.scales + ((z * p.B + b) * groups + t0 / kGroup) * D + c0, code);
+                    uint32_t top[2] = {0, 0};
 #pragma unroll
                     for (int t = 0; t < R; ++t) {
-                        Raw<int8_t, V> q;
+                        const Raw<T, 2> v = row_pair<T, WIDE>(in.row[z][t], offset(base[z], t), lane, both);
+                        if (t < live) {
+                            top[0] = max(top[0], abs_bits(to_f32(v.v[0])));
+                            top[1] = max(top[1], abs_bits(to_f32(v.v[1])));
+                        }
+                    }
+                    Raw<uint8_t, 2> code;
+                    code.v[0] = (uint8_t)scale_code(top[0]), code.v[1] = (uint8_t)scale_code(top[1]);
+                    const To8 to0(code.v[0]), to1(code.v[1]);
+                    store_pair<uint8_t, WIDE>(p.scales + ((z * p.B + b) * groups + t0 / kGroup) * D + c, code, one, both);
 #pragma unroll
-                        for (int v = 0; v < V; ++v) q.v[v] = to8[v](to_f32(src[z][t].v[v]));
-                        if (t < rows) store<int8_t, V>(p.values + z * n + at + t * D, q);
+                    for (int t = 0; t < R; ++t) {
+                        const Raw<T, 2> v = row_pair<T, WIDE>(in.row[z][t], offset(base[z], t), lane, both);
+                        Raw<int8_t, 2> q;
+                        q.v[0] = t < live ? to0(to_f32(v.v[0])) : (int8_t)0;
+                        q.v[1] = t < live ? to1(to_f32(v.v[1])) : (int8_t)0;
+                        if (t < rows) store_pair<int8_t, WIDE>(p.values + z * n + at + t * D, q, one, both);
                     }
                 }
             }
         }
-        float a[R][V], h[R][V], A[V], H[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
-#pragma unroll
-        for (int t = 0; t < R; ++t)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Gates g = gates<T>(to_f32(r[t].v[v]), to_f32(i[t].v[v]), k[v]);
-                a[t][v] = t < live ? g.a : 1.f;
-                h[t][v] = t < live ? g.beta2 * g.rbeta * g.iota * to_f32(x[t].v[v]) : 0.f;
-                A[v] *= a[t][v];
-                H[v] = fmaf(a[t][v], H[v], h[t][v]);
-            }
-        __syncthreads();  // the runs of the step before have been read
-#pragma unroll
-        for (int v = 0; v < V; ++v) run[warp][lane * V + v] = make_float2(A[v], H[v]);
-        __syncthreads();
-        float e[V];  // the state that enters this run
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            e[v] = carry[v];
-            for (int w = 0; w < warps; ++w) {
-                const float2 m = run[w][lane * V + v];
-                carry[v] = fmaf(m.x, carry[v], m.y);
-                if (w + 1 == warp) e[v] = carry[v];
-            }
-        }
-        if (rows > 0 && p.states && t0 % kState == 0) {
-            float *to = p.states + (b * ((p.L + kState - 1) / kState) + t0 / kState) * D + c0;
-#pragma unroll
-            for (int v = 0; v < V; ++v) to[v] = e[v];
-        }
-        if (p.y) {
+        uint64_t a[R], h[R];
+        uint64_t A = f2(1.f), H = f2(0.f);
+        const bool full = live == R;
+        Raw<T, 2> low = row_pair<T, WIDE>(in.row[1][0], offset(p.r, 0), lane, both);
+        if (full) {
 #pragma unroll
             for (int t = 0; t < R; ++t) {
-                float y[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    e[v] = fmaf(a[t][v], e[v], h[t][v]);
-                    y[v] = t < live ? e[v] : 0.f;
-                }
-                if (t < rows) store_f32<T, V>((T *)p.y + at + t * D, y);
+                if (t > 0) lower(low, row_pair<T, WIDE>(in.row[1][t], offset(p.r, t), lane, both));
+                lower(low, row_pair<T, WIDE>(in.row[2][t], offset(p.i, t), lane, both));
             }
         }
-    }
-    if (on && warp == 0 && p.final_state)
+        auto tokens_of = [&](auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.final_state[b * D + c0 + v] = carry[v];
+            for (int t = 0; t < R; ++t) {
+                const Gates2 g = gates2<T, FAST>(pair_of(row_pair<T, WIDE>(in.row[1][t], offset(p.r, t), lane, both)),
+                                                 pair_of(row_pair<T, WIDE>(in.row[2][t], offset(p.i, t), lane, both)), rate2, rate_log2);
+                a[t] = g.a;
+                h[t] = mul2(mul2(mul2(g.beta2, g.rbeta), g.iota), pair_of(row_pair<T, WIDE>(in.row[0][t], offset(p.x, t), lane, both)));
+                if (!FAST && t >= live) a[t] = f2(1.f), h[t] = f2(0.f);
+                A = mul2(A, a[t]);
+                H = fma2(a[t], H, h[t]);
+            }
+        };
+        if (full && !__any_sync(0xffffffffu, one && is_low(low)))
+            tokens_of(std::true_type{});
+        else
+            tokens_of(std::false_type{});
+        Run2 own;
+        un2(A, own.a0, own.a1);
+        un2(H, own.h0, own.h1);
+        sh.run[warp][lane] = own;
+        __syncthreads();
+        Run2 before{1.f, 0.f, 1.f, 0.f};  // the block's runs before this one
+        for (int w = 0; w < warp; ++w) before = after(before, sh.run[w][lane]);
+        if (warp == warps - 1) {
+            const Run2 all = after(before, own);
+            for (int j = 0; j < blocks; ++j) *cluster.map_shared_rank(&sh.block[step & 1][rank][lane], j) = all;
+        }
+        // the stage has been read (by this warp alone): its rows of the step after the next are on their way while the cluster meets
+        if (warp == warps - 1)
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        else  // has written nothing for the others: its stores of y need not arrive first
+            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        advance(next_item, next_s0);
+        fetch(next_item, next_s0, step & 1);
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        float e[2] = {carry[0], carry[1]};
+        for (int j = 0; j < blocks; ++j) {
+            if (j == rank) e[0] = carry[0], e[1] = carry[1];
+            const Run2 m = sh.block[step & 1][j][lane];
+            carry[0] = fmaf(m.a0, carry[0], m.h0), carry[1] = fmaf(m.a1, carry[1], m.h1);
+        }
+        e[0] = fmaf(before.a0, e[0], before.h0), e[1] = fmaf(before.a1, e[1], before.h1);
+        if (rows > 0 && p.states && t0 % kState == 0)
+            store_pair<float, WIDE>(p.states + (b * ((L + kState - 1) / kState) + t0 / kState) * D + c, e[0], e[1], one, both);
+        if (p.y) {
+            uint64_t y = f2(e[0], e[1]);
+            T *to = (T *)p.y + at;
+#pragma unroll
+            for (int t = 0; t < R; ++t, to += D) {
+                y = fma2(a[t], y, h[t]);
+                un2(y, e[0], e[1]);
+                if (full || t < rows)
+                    store_pair<T, WIDE>(to, full || t < live ? e[0] : 0.f, full || t < live ? e[1] : 0.f, one, both);
+            }
+        }
+        advance(item, s0);
+        if (s0 == 0 && rank == 0 && warp == 0 && p.final_state)
+            store_pair<float, WIDE>(p.final_state + b * D + c, carry[0], carry[1], one, both);
+    }
+    copy_wait<0>();
+}
+
+// A sequence of no tokens: its state goes through.
+__global__ void __launch_bounds__(256) linear_keep_kernel(const float *init, float *final_state, int64_t n) {
+    pdl_enter();
+    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (j < n) final_state[j] = init ? init[j] : 0.f;
 }
 
 // ----------------------------------------------------------------- backward
@@ -130,6 +297,14 @@ template <typename T, int V, bool PACK> __global__ void __launch_bounds__(kThrea
 //     dlam = sigmoid(lam) / softplus(lam) sum psi
 // (psi rather than dL/dw, which has 1 / beta: w / beta goes to zero with w.) h_{t-1} is formed again from the state that
 // enters each kState tokens. A block goes over its sequence from the end, kState tokens at a time.
+__device__ __forceinline__ float one_minus_a2(float w, float a) {
+    const float t = 2.f * w;
+    float p = fmaf(t, 0.0067828623577952385f, -0.0410132110118866f);
+    p = fmaf(t, p, 0.16655193269252777f);
+    p = fmaf(t, p, -0.49999287724494934f);
+    p = fmaf(t, p, 0.9999999403953552f);
+    return t < 0.5f ? t * p : fmaf(-a, a, 1.f);
+}
 template <typename T, int V, bool PACK> __global__ void __launch_bounds__(kThreads) linear_bwd_kernel(LinearBwdArgs p) {
     pdl_enter();
     constexpr int R = kBwdRun;
@@ -377,13 +552,70 @@ unsigned tiles(int64_t D, int V) { return (unsigned)((D + 32 * V - 1) / (32 * V)
 // Warps of a block for a sequence of L tokens in runs of R: no more than have a token.
 int warps_for(int64_t L, int R) { return (int)imax<int64_t>(1, imin<int64_t>(kWarps, (L + R - 1) / R)); }
 
+// Clusters of `blocks` blocks of KERN that the device holds at once; asked of the driver once per device and size.
+template <auto KERN> cudaError_t clusters_at_once(int blocks, int threads, size_t smem, int *count) {
+    static std::atomic<int> known[64][kMaxCluster + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int> *slot = dev < 64 ? &known[dev][blocks] : nullptr;
+    if (slot && (*count = slot->load(std::memory_order_acquire)) > 0) return cudaSuccess;
+    e = allow_shared<KERN>(smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)blocks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)blocks), cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr, cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(count, KERN, &cfg);
+    if (e == cudaSuccess && slot) slot->store(*count, std::memory_order_release);
+    return e;
+}
+
+// Launches KERN over `items` sequences and tiles of `L` tokens in blocks of `tokens`. The cluster's size: the one whose waves
+// times steps are fewest, a step of a cluster counted a tenth dearer than one of a single block for the meeting.
+template <auto KERN, typename Args> cudaError_t launch_clusters(const Args &a, int64_t items, int64_t L, int warps, int run, size_t smem, cudaStream_t stream) {
+    const int64_t tokens = (int64_t)warps * run, need = (L + tokens - 1) / tokens;
+    int best = 1, held = 1;
+    double cost = 0;
+    for (int blocks = 1; blocks <= kMaxCluster && blocks <= need; ++blocks) {
+        int count = 0;
+        cudaError_t e = clusters_at_once<KERN>(blocks, kThreads, smem, &count);
+        if (e != cudaSuccess) return e;
+        if (count < 1) continue;
+        const double c = (double)((items + count - 1) / count) * (double)((need + blocks - 1) / blocks) * (blocks > 1 ? 1.1 : 1.0);
+        if (blocks == 1 || c < cost) best = blocks, held = count, cost = c;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)best, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(imin<int64_t>(items, held) * best)), cfg.blockDim = dim3((unsigned)(32 * warps));
+    cfg.dynamicSmemBytes = smem, cfg.stream = stream, cfg.attrs = attr, cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, KERN, a);
+}
+
+// Whether every row of `t`-byte elements begins at a multiple of 16 bytes.
+bool wide_rows(int64_t D, size_t t) { return D * (int64_t)t % 16 == 0; }
+
+template <typename T, bool WIDE> cudaError_t forward_w(const LinearArgs &a, cudaStream_t stream) {
+    const int64_t items = a.B * ((a.D + kTile - 1) / kTile);
+    const int warps = warps_for(a.L, kFwdRun);
+    const size_t smem = sizeof(FwdShared<T, WIDE>);
+    return a.values ? launch_clusters<linear_fwd_kernel<T, WIDE, true>>(a, items, a.L, warps, kFwdRun, smem, stream)
+                    : launch_clusters<linear_fwd_kernel<T, WIDE, false>>(a, items, a.L, warps, kFwdRun, smem, stream);
+}
 template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t stream) {
-    return for_width(a.D, [&](auto vw) {
-        constexpr int V = decltype(vw)::value;
-        const dim3 grid(1, tiles(a.D, V), (unsigned)a.B), block(32 * warps_for(a.L, kFwdRun));
-        return a.values ? launch_programmatic(linear_fwd_kernel<T, V, true>, grid, block, 0, stream, a)
-                        : launch_programmatic(linear_fwd_kernel<T, V, false>, grid, block, 0, stream, a);
-    });
+    if (a.L == 0) {
+        if (!a.final_state || a.final_state == a.init) return cudaSuccess;
+        return launch_programmatic(linear_keep_kernel, dim3((unsigned)((a.B * a.D + 255) / 256)), dim3(256), 0, stream, a.init,
+                                   a.final_state, a.B * a.D);
+    }
+    return wide_rows(a.D, sizeof(T)) ? forward_w<T, true>(a, stream) : forward_w<T, false>(a, stream);
 }
 
 template <typename T> cudaError_t backward_t(const LinearBwdArgs &a, cudaStream_t stream) {

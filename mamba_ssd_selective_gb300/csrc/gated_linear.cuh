@@ -2,6 +2,7 @@
 // vectors of V channels, the gates of a token, and the conversion to 8 bits.
 #pragma once
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace ssd {
 namespace linear {
@@ -46,50 +47,126 @@ __device__ __forceinline__ float softplus_ratio(float lam) {
     return lam < -16.f ? 1.f : 1.f / ((1.f + expf(-lam)) * softplus(lam));
 }
 
-// float32 inputs take expf; bf16 inputs, whose results are rounded to 8 bits, the exponential of the special function unit (2 units
-// in the last place, and that of its argument: 1e-6 relative at |x| = 8).
-template <typename T> __device__ __forceinline__ float exp_of(float x) {
-    if constexpr (sizeof(T) == 4) return expf(x);
-    return __expf(x);
+__device__ __forceinline__ float ex2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-
 __device__ __forceinline__ float rsqrt_approx(float x) {
     float r;
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float rcp_approx(float x) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-// 1 - exp(-2 w), a = exp(-w). Where 1 - a^2 would cancel (2 w < 1/2) by its series to the seventh term (the next is below
-// 2e-7 of it); above, the difference of 1 and a^2 <= 0.61 costs 5e-7 at most.
-__device__ __forceinline__ float one_minus_a2(float w, float a) {
-    const float t = 2.f * w;
-    float p = fmaf(t, 1.f / 5040.f, -1.f / 720.f);
-    p = fmaf(t, p, 1.f / 120.f);
-    p = fmaf(t, p, -1.f / 24.f);
-    p = fmaf(t, p, 1.f / 6.f);
-    p = fmaf(t, p, -0.5f);
-    p = fmaf(t, p, 1.f);
-    return t < 0.5f ? t * p : fmaf(-a, a, 1.f);
+using delta::add2;
+using delta::f2;
+using delta::fma2;
+using delta::mul2;
+using delta::un2;
+__device__ __forceinline__ uint64_t f2(float x) { return f2(x, x); }
+__device__ __forceinline__ uint64_t pair_of(const Raw<float, 2> &r) { return f2(r.v[0], r.v[1]); }
+__device__ __forceinline__ uint64_t pair_of(const Raw<__nv_bfloat16, 2> &r) {
+    return f2(__uint_as_float(r.word << 16), __uint_as_float(r.word & 0xffff0000u));
 }
 
-// The gates of one token and channel: rho and iota the sigmoids, w = k rho, a = exp(-w), beta = sqrt(1 - a^2).
+constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.9259629911e-8f, kLn2 = 0.6931471805599453f;
+
+// exp(-x) for two numbers: within 2 units in the last place, and that of its argument (|x| 1e-7 relative). float32 inputs get
+// the argument's rest too; the results of bf16 inputs are rounded to 8 bits.
+template <typename T> __device__ __forceinline__ uint64_t exp_minus(uint64_t x) {
+    const uint64_t y = mul2(x, f2(kLog2e));
+    float y0, y1;
+    un2(y, y0, y1);
+    uint64_t e = f2(ex2_approx(-y0), ex2_approx(-y1));
+    if constexpr (sizeof(T) == 4) {
+        const uint64_t rest = fma2(x, f2(-kLog2eRest), fma2(x, f2(-kLog2e), y));
+        // an exponential that is 0 or infinite stays so: its rest is finite, and with x infinite not a number
+        const uint64_t f = fma2(e, mul2(rest, f2(kLn2)), e);
+        float f0, f1, e0, e1;
+        un2(f, f0, f1);
+        un2(e, e0, e1);
+        e = f2(fabsf(y0) < 126.f ? f0 : e0, fabsf(y1) < 126.f ? f1 : e1);
+    }
+    return e;
+}
+
+// The gates of one token, for two channels: rho and iota the sigmoids, t = 2 w = 2 k rho, a = exp(-w), beta2 = 1 - a^2 and
+// rbeta = 1 / sqrt(beta2), finite where w is 0, so that beta2 rbeta is 0 there (SHARED: 3e-19). rate2 is 2 k, rate_log2 is
+// k log2(e).
+// SHARED: both sigmoids from one reciprocal, 1 / (1 + e^-r)(1 + e^-i): the special function unit takes twice the time of an
+// exponential for one, and it is what the issue slots wait for next. The product is finite for r, i > kLowGate.
+// beta2 where 1 - a^2 would cancel (t < 1/2) is t times the polynomial of degree 4 through (1 - e^-t) / t at its Chebyshev
+// points on [0, 1/2] (1.1e-7 off at most); above, the difference of 1 and a^2 <= 0.61 costs 5e-7 at most.
+constexpr float kLowGate = -43.f;
+struct Gates2 {
+    uint64_t rho, iota, t, a, beta2, rbeta;
+};
+template <typename T, bool SHARED>
+__device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, uint64_t rate2, uint64_t rate_log2) {
+    Gates2 g;
+    const uint64_t one = f2(1.f), u = add2(exp_minus<T>(r), one), v = add2(exp_minus<T>(i), one);
+    if constexpr (SHARED) {
+        float d0, d1;
+        un2(mul2(u, v), d0, d1);
+        const uint64_t q = f2(rcp_approx(d0), rcp_approx(d1));
+        g.rho = mul2(q, v), g.iota = mul2(q, u);
+    } else {
+        float u0, u1, v0, v1;
+        un2(u, u0, u1);
+        un2(v, v0, v1);
+        g.rho = f2(rcp_approx(u0), rcp_approx(u1)), g.iota = f2(rcp_approx(v0), rcp_approx(v1));
+    }
+    float w0, w1, t0, t1, s0, s1, b0, b1;
+    un2(mul2(g.rho, rate_log2), w0, w1);
+    const float a0 = ex2_approx(-w0), a1 = ex2_approx(-w1);
+    g.a = f2(a0, a1);
+    g.t = mul2(g.rho, rate2);
+    uint64_t s = fma2(g.t, f2(0.0067828623577952385f), f2(-0.0410132110118866f));
+    s = fma2(g.t, s, f2(0.16655193269252777f));
+    s = fma2(g.t, s, f2(-0.49999287724494934f));
+    s = fma2(g.t, s, f2(0.9999999403953552f));
+    un2(fma2(g.t, s, f2(SHARED ? 1e-37f : 0.f)), s0, s1);
+    un2(g.t, t0, t1);
+    b0 = t0 < 0.5f ? s0 : fmaf(-a0, a0, 1.f);
+    b1 = t1 < 0.5f ? s1 : fmaf(-a1, a1, 1.f);
+    g.beta2 = f2(b0, b1);
+    g.rbeta = SHARED ? f2(rsqrt_approx(b0), rsqrt_approx(b1)) : f2(rsqrt_approx(fmaxf(b0, 1e-37f)), rsqrt_approx(fmaxf(b1, 1e-37f)));
+    return g;
+}
+// The lesser of the gates seen, to tell whether they are all above kLowGate.
+__device__ __forceinline__ void lower(Raw<float, 2> &m, const Raw<float, 2> &g) {
+    m.v[0] = fminf(m.v[0], g.v[0]), m.v[1] = fminf(m.v[1], g.v[1]);
+}
+__device__ __forceinline__ void lower(Raw<__nv_bfloat16, 2> &m, const Raw<__nv_bfloat16, 2> &g) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m.word), "r"(g.word));
+    m.word = r;
+}
+template <typename T> __device__ __forceinline__ bool is_low(const Raw<T, 2> &m) {
+    return to_f32(m.v[0]) < kLowGate || to_f32(m.v[1]) < kLowGate;
+}
+
+// The gates of one channel, each step as above.
 struct Gates {
-    float rho, iota, w, a, beta2, rbeta;  // rbeta = 1 / beta; beta = beta2 rbeta, 0 where w is
+    float rho, iota, w, a, beta2, rbeta;
 };
 template <typename T> __device__ __forceinline__ Gates gates(float r, float i, float k) {
-    Gates g;
-    g.rho = rcp_approx(1.f + exp_of<T>(-r));
-    g.iota = rcp_approx(1.f + exp_of<T>(-i));
-    g.w = k * g.rho;
-    g.a = exp_of<T>(-g.w);
-    g.beta2 = one_minus_a2(g.w, g.a);
-    g.rbeta = rsqrt_approx(fmaxf(g.beta2, 1e-37f));
-    return g;
+    const Gates2 g = gates2<T, false>(f2(r), f2(i), f2(2.f * k), f2(k * kLog2e));
+    Gates o;
+    float other;
+    un2(g.rho, o.rho, other);
+    un2(g.iota, o.iota, other);
+    un2(g.t, o.w, other);
+    o.w *= 0.5f;
+    un2(g.a, o.a, other);
+    un2(g.beta2, o.beta2, other);
+    un2(g.rbeta, o.rbeta, other);
+    return o;
 }
 
 // 8 bits: the values of a group are whole numbers times 2^e, e the least with max |x| <= 127 2^e and e >= -127, kept as the
