@@ -14,6 +14,8 @@
 
 #include "gated_linear.cuh"
 #include "launch.h"
+#include "ssd_scan.h"
+#include "tc_ptx.cuh"
 
 namespace ssd {
 namespace linear {
@@ -41,28 +43,34 @@ template <typename T, bool WIDE> struct Row {  // in shared memory
     static constexpr int kPitch = kTile * (int)sizeof(T) + (WIDE || sizeof(T) == 4 ? 0 : 4);
 };
 
-// Rows 0..n-1 of a tile: channels c0..min(c0 + 64, D) of the rows of `base` ([.., D]) from row `row` on.
-template <typename T, bool WIDE, int R>
-__device__ __forceinline__ void fetch_rows(unsigned char *to, const T *base, int64_t row, int n, int64_t c0, int64_t D, int lane) {
-    constexpr int PITCH = Row<T, WIDE>::kPitch;
+// Rows 0..n-1 of a tile, R at most, of `cols` channels from `base` on, which lie D apart. ACROSS: the bytes from one row to the
+// next in shared memory.
+template <typename T, bool WIDE, int R, int ACROSS>
+__device__ __forceinline__ void fetch_rows(unsigned char *to, const T *base, int n, int cols, int64_t D, int lane) {
     const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
     if constexpr (WIDE) {
         constexpr int PER = kTile * (int)sizeof(T) / 16, ROWS = 32 / PER > R ? R : 32 / PER;  // lanes a row, rows at once
         const int piece = lane % PER, first = lane / PER;
-        const int64_t c = c0 + piece * (16 / (int)sizeof(T));
-        if (c < D && first < ROWS) {
-            const T *from = base + (row + first) * D + c;
+        const int c = piece * (16 / (int)sizeof(T));
+        if (c < cols && first < ROWS) {
+            const T *from = base + first * D + c;
+            const int64_t next = ROWS * D;
 #pragma unroll
-            for (int j = 0; j < R / ROWS; ++j)
-                if (j * ROWS + first < n) copy16(dst + (j * ROWS + first) * PITCH + piece * 16, from + (int64_t)j * ROWS * D);
+            for (int j = 0; j < R / ROWS; ++j, from += next)
+                if (j * ROWS + first < n) copy16(dst + (j * ROWS + first) * ACROSS + piece * 16, from);
         }
     } else {
-        const int64_t have = imin<int64_t>(kTile, D - c0) * (int64_t)sizeof(T);  // bytes of the tile's row
-        for (int t = 0; t < n; ++t) {
-            const unsigned char *from = reinterpret_cast<const unsigned char *>(base + (row + t) * D + c0);
+        const int have = cols * (int)sizeof(T);  // bytes of the tile's row
+        const unsigned char *from = reinterpret_cast<const unsigned char *>(base);
+#pragma unroll 4
+        for (int t = 0; t < n; ++t, from += D * sizeof(T)) {
             const int off = (int)(reinterpret_cast<uintptr_t>(from) & 3);
-            for (int w = lane; w * 4 < off + have; w += 32)
-                copy4(dst + t * PITCH + w * 4, from - off + w * 4, (int)imin<int64_t>(4, off + have - w * 4));
+            const unsigned char *word = from - off;
+#pragma unroll
+            for (int w = 0; w < (kTile * (int)sizeof(T) + 127 + (sizeof(T) == 4 ? 0 : 3)) / 128; ++w) {
+                const int at = 4 * lane + 128 * w, left = off + have - at;
+                if (left > 0) copy4(dst + t * ACROSS + at, word + at, left < 4 ? left : 4);
+            }
         }
     }
 }
@@ -92,193 +100,313 @@ template <typename T, bool WIDE> __device__ __forceinline__ void store_pair(T *p
     store_pair<T, WIDE>(p, r, one, both);
 }
 
+// The same rows from shared memory, where each lane has put its two channels: 16 bytes of T a lane (or as many values of a
+// smaller type U).
+template <typename T, typename U, int R, int ACROSS>
+__device__ __forceinline__ void leave_rows(const unsigned char *from, U *base, int n, int cols, int64_t D, int lane) {
+    constexpr int V = 16 / (int)sizeof(T), PER = kTile / V, ROWS = 32 / PER;
+    const int piece = lane % PER, first = lane / PER;
+    if (piece * V >= cols) return;
+    U *to = base + first * D + piece * V;
+    const int64_t next = ROWS * D;
+#pragma unroll
+    for (int j = 0; j < R / ROWS; ++j, to += next)
+        if (j * ROWS + first < n) {
+            Raw<U, V> r;
+            r.word = *reinterpret_cast<const decltype(r.word) *>(from + (j * ROWS + first) * ACROSS + piece * V * sizeof(U));
+            store<U, V>(to, r);
+        }
+}
+
 // ------------------------------------------------------------ runs, joined in order
 // (A, H) of a lane's two channels: h -> A h + H.
-struct Run2 {
-    float a0, h0, a1, h1;
+struct alignas(16) Run2 {
+    uint64_t a, h;
 };
-__device__ __forceinline__ Run2 after(const Run2 &x, const Run2 &y) {  // x, then y
-    return {x.a0 * y.a0, fmaf(y.a0, x.h0, y.h0), x.a1 * y.a1, fmaf(y.a1, x.h1, y.h1)};
+__device__ __forceinline__ uint64_t after(const Run2 &x, uint64_t h) { return fma2(x.a, h, x.h); }  // x, from h
+__device__ __forceinline__ Run2 after(const Run2 &x, const Run2 &y) { return {mul2(x.a, y.a), fma2(y.a, x.h, y.h)}; }  // x, then y
+
+// A step of a cluster: the tile of a sequence that it is at, as its first thread works out two steps ahead.
+struct Step {
+    int64_t base;      // of the step's first token and the tile's first channel in [B, L, D]
+    int64_t b;
+    int32_t first;     // token
+    int32_t len;       // tokens of the sequence
+    int32_t cols;      // channels of the tile; 0: no more work
+    int32_t c0;
+};
+struct Walk {
+    uint32_t item, items, tiles, clusters;
+    int64_t first;
+    // the step here; then goes on
+    __device__ __forceinline__ Step forward(const LinearArgs &p, int span) {
+        Step s{};
+        if (item >= items) return s;
+        const uint32_t b = item / tiles;
+        s.b = b, s.c0 = (int32_t)(item - b * tiles) * kTile, s.first = (int32_t)first;
+        s.cols = (int32_t)imin<int64_t>(kTile, p.D - s.c0);
+        s.len = (int32_t)seq_len(p.seqlens, b, p.L);
+        s.base = (b * p.L + first) * p.D + s.c0;
+        first += span;
+        if (first >= p.L) first = 0, item += clusters;
+        return s;
+    }
+};
+// Tokens of a run of R from t0 on that are below `end`.
+__device__ __forceinline__ int run_of(int R, int64_t end, int64_t t0) { return (int)imax<int64_t>(0, imin<int64_t>(R, end - t0)); }
+
+// The blocks of a cluster exchange a Run2 a lane: each sends its own to all of them, and the bytes count down the receiver's
+// barrier. (A cluster barrier would have the sender wait for everything that it has written to memory before.) Two of each,
+// taken in turn: a block sends for a step once all of its warps have read the one before.
+struct Exchange {
+    Run2 block[2][kMaxCluster][32];
+    uint64_t bar[2];
+};
+constexpr uint64_t kGiveUpNs = 1000000000ull;
+__device__ int g_gave_up;  // SSD_ERR_TIMEOUT once a wait was given up on this device
+
+__device__ __forceinline__ void exchange_init(Exchange &x, int blocks) {
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&x.bar[0], 1);
+        tc::mbar_init(&x.bar[1], 1);
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    if (blocks > 1) {  // the others are there, with their barriers
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+}
+__device__ __forceinline__ void exchange_send(Exchange &x, int step, int rank, int blocks, int lane, const Run2 &own) {
+    const uint32_t slot = tc::smem_u32(&x.block[step & 1][rank][lane]), bar = tc::smem_u32(&x.bar[step & 1]);
+    uint32_t r0, r1, r2, r3;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(r0), "=r"(r1) : "l"(own.a));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(r2), "=r"(r3) : "l"(own.h));
+    for (int j = 0; j < blocks; ++j)
+        asm volatile(
+            "{\n\t.reg .b32 to, at;\n\t"
+            "mapa.shared::cluster.u32 to, %0, %2;\n\t"
+            "mapa.shared::cluster.u32 at, %1, %2;\n\t"
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [to], {%3, %4, %5, %6}, [at];\n\t}" ::"r"(slot),
+            "r"(bar), "r"(j), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+            : "memory");
+}
+// False, now and from then on, where the others' runs have not come in kGiveUpNs.
+__device__ __forceinline__ bool exchange_wait(Exchange &x, int step, bool alive) {
+    if (!alive) return false;
+    if (tc::mbar_wait(&x.bar[step & 1], (step >> 1) & 1, kGiveUpNs)) return true;
+    atomicCAS(&g_gave_up, SSD_OK, SSD_ERR_TIMEOUT);
+    return false;
 }
 
 // ------------------------------------------------------------------ forward
-// Bound by HBM (8 bytes a token and channel in bf16) with the special function unit and the issue slots close behind it.
+// Bound by HBM (8 bytes a token and channel in bf16) with the issue slots and the special function unit close behind it: so two
+// channels an instruction where there is one for it, and results leave through shared memory, 16 bytes a lane (the rows that were
+// fetched make room for them).
 template <typename T, bool WIDE> struct FwdShared {
-    static constexpr int kPitch = Row<T, WIDE>::kPitch;
-    struct Stage {
-        alignas(16) unsigned char row[3][kFwdRun][kPitch];
-    };
-    Stage stage[2][kWarps];
+    static constexpr int kAcross = Row<T, WIDE>::kPitch;
+    unsigned char row[2][kWarps][3][kFwdRun][kAcross];
     Run2 run[kWarps][32];
-    Run2 block[2][kMaxCluster][32];
+    Exchange exchange;
+    Step step[4];
 };
+
+// A run's values in 8 bits: rows of z (0: x, 1: r, 2: i) from `w`, which holds what `row` held of them.
+template <typename T, bool WIDE, int R, int ACROSS>
+__device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, int z, const Raw<T, 2> (&w)[R], unsigned char *row, const Step &s, int64_t t0,
+                                                int live, int rows, int lane) {
+    const int64_t D = p.D;
+    int8_t *values = p.values + (z * p.B * p.L + t0 - s.first) * D + s.base;
+    const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
+    uint32_t top0 = 0, top1 = 0;
+    if constexpr (sizeof(T) == 2) {
+        uint32_t top = 0;  // bf16 without its sign orders like a whole number: two at once
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+            if (t < live) top = __vmaxu2(top, w[t].word & 0x7fff7fffu);
+        top0 = top << 16, top1 = top & 0xffff0000u;
+    } else {
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+            if (t < live) top0 = max(top0, abs_bits(w[t].v[0])), top1 = max(top1, abs_bits(w[t].v[1]));
+    }
+    Raw<uint8_t, 2> code;
+    code.v[0] = (uint8_t)scale_code(top0), code.v[1] = (uint8_t)scale_code(top1);
+    store_pair<uint8_t, WIDE>(p.scales + ((z * p.B + s.b) * ((p.L + kGroup - 1) / kGroup) + t0 / kGroup) * D + s.c0 + 2 * lane, code, one, both);
+    const uint64_t inv = f2(inverse_scale(code.v[0]), inverse_scale(code.v[1]));
+    const uint32_t mask = (code.v[0] == 255 ? 0u : 0xffu) | (code.v[1] == 255 ? 0u : 0xff00u);
+    __syncwarp();  // every lane has read the row
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+        float q0, q1;
+        un2(fma2(pair_of(w[t]), inv, f2(kToWhole)), q0, q1);
+        Raw<int8_t, 2> q;
+        q.word = (uint16_t)(t < live ? __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x0040) & mask : 0u);
+        if constexpr (WIDE) {
+            *reinterpret_cast<uint16_t *>(row + t * ACROSS + 2 * lane) = q.word;
+        } else {
+            if (t < rows) store_pair<int8_t, WIDE>(values + t * D + 2 * lane, q, one, both);
+        }
+    }
+    if constexpr (WIDE) {
+        __syncwarp();
+        leave_rows<T, int8_t, R, ACROSS>(row, values, rows, s.cols, D, lane);
+        __syncwarp();
+    }
+}
 
 template <typename T, bool WIDE, bool PACK>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_fwd_kernel(LinearArgs p) {
     namespace cg = cooperative_groups;
     pdl_enter();
-    constexpr int R = kFwdRun;
+    constexpr int R = kFwdRun, ACROSS = FwdShared<T, WIDE>::kAcross;
     extern __shared__ __align__(16) unsigned char raw_smem[];
     FwdShared<T, WIDE> &sh = *reinterpret_cast<FwdShared<T, WIDE> *>(raw_smem);
     const cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
     const int64_t D = p.D, L = p.L;
-    const uint32_t tiles = (uint32_t)((D + kTile - 1) / kTile), items = (uint32_t)p.B * tiles;  // below 2^31
-    const uint32_t clusters = gridDim.x / blocks;
-    const int64_t tokens = (int64_t)warps * R, span = tokens * blocks;
-    const int64_t mine = rank * tokens + warp * R;  // of this warp's run, from the step's first token
-    const int64_t n = p.B * L * D;
+    const int span = warps * R * blocks, mine = (rank * warps + warp) * R;  // a step's tokens; of them, where this warp's run is
+    Walk walk{blockIdx.x / (uint32_t)blocks, 0, (uint32_t)((D + kTile - 1) / kTile), gridDim.x / (uint32_t)blocks, 0};
+    walk.items = (uint32_t)p.B * walk.tiles;  // below 2^31
+    if (threadIdx.x == 0) sh.step[0] = walk.forward(p, span), sh.step[1] = walk.forward(p, span);
+    exchange_init(sh.exchange, blocks);
 
-    auto fetch = [&](uint32_t item, int64_t s0, int stage) {
-        if (item < items) {
-            const uint32_t b = item / tiles;
-            const int64_t c0 = (int64_t)(item - b * tiles) * kTile, t0 = s0 + mine;
-            const int live = (int)imax<int64_t>(0, imin<int64_t>(R, seq_len(p.seqlens, b, L) - t0));
-            auto &to = sh.stage[stage][warp];
-            fetch_rows<T, WIDE, R>(to.row[0][0], (const T *)p.x, b * L + t0, live, c0, D, lane);
-            fetch_rows<T, WIDE, R>(to.row[1][0], (const T *)p.r, b * L + t0, live, c0, D, lane);
-            fetch_rows<T, WIDE, R>(to.row[2][0], (const T *)p.i, b * L + t0, live, c0, D, lane);
+    auto fetch = [&](int step) {
+        const Step s = sh.step[step & 3];
+        if (s.cols > 0) {
+            const int live = run_of(R, s.len, (int64_t)s.first + mine);
+            const int64_t at = s.base + mine * D;
+            auto &to = sh.row[step & 1][warp];
+            fetch_rows<T, WIDE, R, ACROSS>(to[0][0], (const T *)p.x + at, live, s.cols, D, lane);
+            fetch_rows<T, WIDE, R, ACROSS>(to[1][0], (const T *)p.r + at, live, s.cols, D, lane);
+            fetch_rows<T, WIDE, R, ACROSS>(to[2][0], (const T *)p.i + at, live, s.cols, D, lane);
         }
         copy_commit();
     };
-    // the step after (item, s0)
-    auto advance = [&](uint32_t &item, int64_t &s0) {
-        s0 += span;
-        if (s0 >= L) s0 = 0, item += clusters;
-    };
-
-    uint32_t item = blockIdx.x / blocks, next_item = item;
-    int64_t s0 = 0, next_s0 = 0;
-    fetch(next_item, next_s0, 0);
-    advance(next_item, next_s0);
-    fetch(next_item, next_s0, 1);
-    float carry[2] = {0.f, 0.f};
-    uint64_t rate2 = 0, rate_log2 = 0;
-    for (int step = 0; item < items; ++step) {
-        const int64_t b = item / tiles, c = (int64_t)(item - (uint32_t)b * tiles) * kTile + 2 * lane, t0 = s0 + mine;
-        const int64_t at = (b * L + t0) * D + c;
-        const bool one = c < D, both = c + 1 < D;
-        const int live = (int)imax<int64_t>(0, imin<int64_t>(R, seq_len(p.seqlens, b, L) - t0));  // tokens of the run that count
-        const int rows = (int)imax<int64_t>(0, imin<int64_t>(R, L - t0));                         // and that exist
-        auto &in = sh.stage[step & 1][warp];
-        float k[2];
-        if (s0 == 0) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                k[v] = c + v < D ? p.lam[c + v] : 0.f;
-                carry[v] = c + v < D && p.init ? p.init[b * D + c + v] : 0.f;
-            }
+    fetch(0);
+    fetch(1);
+    uint64_t carry = 0, rate2 = 0, rate_log2 = 0;
+    bool steep = false, alive = true;
+    for (int step = 0;; ++step) {
+        const Step s = sh.step[step & 3];
+        if (s.cols == 0) break;
+        if (threadIdx.x == 0) {
+            sh.step[(step + 2) & 3] = walk.forward(p, span);
+            tc::mbar_arrive_expect_tx(&sh.exchange.bar[step & 1], blocks * 32 * (uint32_t)sizeof(Run2));
+        }
+        const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
+        const int64_t t0 = (int64_t)s.first + mine, at = s.base + mine * D + 2 * lane;
+        const int live = run_of(R, s.len, t0), rows = run_of(R, L, t0);  // tokens that count, that exist
+        auto &in = sh.row[step & 1][warp];
+        if (s.first == 0) {
+            const int64_t c = s.c0 + 2 * lane;
+            float k0 = one ? p.lam[c] : 0.f, k1 = both ? p.lam[c + 1] : 0.f;
+            carry = p.init ? f2(one ? p.init[s.b * D + c] : 0.f, both ? p.init[s.b * D + c + 1] : 0.f) : 0;
+            k0 = p.c * softplus(k0), k1 = p.c * softplus(k1);
+            rate2 = f2(2.f * k0, 2.f * k1), rate_log2 = f2(kLog2e * k0, kLog2e * k1);
+            steep = __any_sync(0xffffffffu, (one && !(k0 < kSteep)) || (both && !(k1 < kSteep)));
         }
         copy_wait<1>();
         __syncwarp();
-        if (s0 == 0) {
-            k[0] = p.c * softplus(k[0]), k[1] = p.c * softplus(k[1]);
-            rate2 = f2(2.f * k[0], 2.f * k[1]), rate_log2 = f2(kLog2e * k[0], kLog2e * k[1]);
-        }
-        auto offset = [&](const void *base, int t) {  // of a row in its first word
-            return WIDE || sizeof(T) == 4 ? 0 : (int)((reinterpret_cast<uintptr_t>(base) + (uintptr_t)(at - 2 * lane + t * D) * sizeof(T)) & 3);
+        auto pair = [&](int z, int t) {
+            const void *base = z == 0 ? p.x : z == 1 ? p.r : p.i;
+            const int off = WIDE || sizeof(T) == 4
+                                ? 0
+                                : (int)((reinterpret_cast<uintptr_t>(base) + (uintptr_t)(at - 2 * lane + t * D) * sizeof(T)) & 3);
+            return row_pair<T, WIDE>(in[z][t], off, lane, both);
         };
+        uint64_t a[R], h[R];
+        Run2 own;
+        Raw<T, 2> low;
+        auto tokens = [&](auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
+            own.a = f2(1.f), own.h = f2(0.f);
+#pragma unroll
+            for (int t = 0; t < R; ++t) {
+                const Raw<T, 2> r = pair(1, t), i = pair(2, t);
+                if (FAST) {
+                    if (t == 0) low = r; else lower(low, r);
+                    lower(low, i);
+                }
+                const Gates2 g = gates2<T, FAST>(pair_of(r), pair_of(i), rate2, rate_log2);
+                a[t] = g.a;
+                h[t] = mul2(mul2(mul2(g.beta2, g.rbeta), g.iota), pair_of(pair(0, t)));
+                if (!FAST && t >= live) a[t] = f2(1.f), h[t] = f2(0.f);
+                own = after(own, {a[t], h[t]});
+            }
+        };
+        bool fast = live == R && !steep;
+        if (fast) {
+            tokens(std::true_type{});
+            fast = !__any_sync(0xffffffffu, one && is_low(low));
+        }
+        if (!fast) tokens(std::false_type{});
+        sh.run[warp][lane] = own;
+        __syncthreads();
+        Run2 before{f2(1.f), f2(0.f)};  // the block's runs before this one
+        for (int w = 0; w < warp; ++w) before = after(before, sh.run[w][lane]);
+        if (warp == warps - 1) exchange_send(sh.exchange, step, rank, blocks, lane, after(before, own));
+        alive = exchange_wait(sh.exchange, step, alive);
+        if (!alive) carry = f2(__uint_as_float(0x7fc00000u));  // what was not told is not guessed
+        uint64_t e = carry;                                     // the state that enters this run
+        for (int j = 0; j < rank; ++j) e = after(sh.exchange.block[step & 1][j][lane], e);
+        carry = e;
+        for (int j = rank; j < blocks; ++j) carry = after(sh.exchange.block[step & 1][j][lane], carry);
+        e = after(before, e);
+        if (rows > 0 && p.states && t0 % kState == 0) {
+            float e0, e1;
+            un2(e, e0, e1);
+            store_pair<float, WIDE>(p.states + (s.b * ((L + kState - 1) / kState) + t0 / kState) * D + s.c0 + 2 * lane, e0, e1, one, both);
+        }
+        Raw<T, 2> words[R];
+        if constexpr (PACK) {
+#pragma unroll
+            for (int t = 0; t < R; ++t) words[t] = pair(0, t);
+        }
+        __syncwarp();
+        if (p.y) {
+            auto results = [&](auto whole) {
+#pragma unroll
+                for (int t = 0; t < R; ++t) {
+                    float y0, y1;
+                    e = fma2(a[t], e, h[t]);
+                    un2(e, y0, y1);
+                    if (!decltype(whole)::value && t >= live) y0 = y1 = 0.f;
+                    Raw<T, 2> y;
+                    y.v[0] = from_f32<T>(y0), y.v[1] = from_f32<T>(y1);
+                    if constexpr (WIDE) {
+                        *reinterpret_cast<decltype(y.word) *>(in[0][t] + 2 * sizeof(T) * lane) = y.word;
+                    } else {
+                        if (t < rows) store_pair<T, WIDE>((T *)p.y + at + t * D, y, one, both);
+                    }
+                }
+            };
+            if (live == R) results(std::true_type{}); else results(std::false_type{});
+            if constexpr (WIDE) {
+                __syncwarp();
+                leave_rows<T, T, R, ACROSS>(in[0][0], (T *)p.y + at - 2 * lane, rows, s.cols, D, lane);
+                __syncwarp();
+            }
+        }
         if constexpr (PACK) {
             if (rows > 0) {
-                const int64_t groups = (L + kGroup - 1) / kGroup;
-                const void *base[3] = {p.x, p.r, p.i};
+                leave_in_8_bits<T, WIDE, R, ACROSS>(p, 0, words, in[0][0], s, t0, live, rows, lane);
 #pragma unroll
-                for (int z = 0; z < 3; ++z) {
-                    uint32_t top[2] = {0, 0};
+                for (int z = 1; z < 3; ++z) {
 #pragma unroll
-                    for (int t = 0; t < R; ++t) {
-                        const Raw<T, 2> v = row_pair<T, WIDE>(in.row[z][t], offset(base[z], t), lane, both);
-                        if (t < live) {
-                            top[0] = max(top[0], abs_bits(to_f32(v.v[0])));
-                            top[1] = max(top[1], abs_bits(to_f32(v.v[1])));
-                        }
-                    }
-                    Raw<uint8_t, 2> code;
-                    code.v[0] = (uint8_t)scale_code(top[0]), code.v[1] = (uint8_t)scale_code(top[1]);
-                    const To8 to0(code.v[0]), to1(code.v[1]);
-                    store_pair<uint8_t, WIDE>(p.scales + ((z * p.B + b) * groups + t0 / kGroup) * D + c, code, one, both);
-#pragma unroll
-                    for (int t = 0; t < R; ++t) {
-                        const Raw<T, 2> v = row_pair<T, WIDE>(in.row[z][t], offset(base[z], t), lane, both);
-                        Raw<int8_t, 2> q;
-                        q.v[0] = t < live ? to0(to_f32(v.v[0])) : (int8_t)0;
-                        q.v[1] = t < live ? to1(to_f32(v.v[1])) : (int8_t)0;
-                        if (t < rows) store_pair<int8_t, WIDE>(p.values + z * n + at + t * D, q, one, both);
-                    }
+                    for (int t = 0; t < R; ++t) words[t] = pair(z, t);
+                    leave_in_8_bits<T, WIDE, R, ACROSS>(p, z, words, in[z][0], s, t0, live, rows, lane);
                 }
             }
         }
-        uint64_t a[R], h[R];
-        uint64_t A = f2(1.f), H = f2(0.f);
-        const bool full = live == R;
-        Raw<T, 2> low = row_pair<T, WIDE>(in.row[1][0], offset(p.r, 0), lane, both);
-        if (full) {
-#pragma unroll
-            for (int t = 0; t < R; ++t) {
-                if (t > 0) lower(low, row_pair<T, WIDE>(in.row[1][t], offset(p.r, t), lane, both));
-                lower(low, row_pair<T, WIDE>(in.row[2][t], offset(p.i, t), lane, both));
-            }
+        __syncwarp();
+        fetch(step + 2);
+        if (s.first + (int64_t)span >= L && rank == 0 && warp == 0 && p.final_state) {
+            float e0, e1;
+            un2(carry, e0, e1);
+            store_pair<float, WIDE>(p.final_state + s.b * D + s.c0 + 2 * lane, e0, e1, one, both);
         }
-        auto tokens_of = [&](auto fast) {
-            constexpr bool FAST = decltype(fast)::value;
-#pragma unroll
-            for (int t = 0; t < R; ++t) {
-                const Gates2 g = gates2<T, FAST>(pair_of(row_pair<T, WIDE>(in.row[1][t], offset(p.r, t), lane, both)),
-                                                 pair_of(row_pair<T, WIDE>(in.row[2][t], offset(p.i, t), lane, both)), rate2, rate_log2);
-                a[t] = g.a;
-                h[t] = mul2(mul2(mul2(g.beta2, g.rbeta), g.iota), pair_of(row_pair<T, WIDE>(in.row[0][t], offset(p.x, t), lane, both)));
-                if (!FAST && t >= live) a[t] = f2(1.f), h[t] = f2(0.f);
-                A = mul2(A, a[t]);
-                H = fma2(a[t], H, h[t]);
-            }
-        };
-        if (full && !__any_sync(0xffffffffu, one && is_low(low)))
-            tokens_of(std::true_type{});
-        else
-            tokens_of(std::false_type{});
-        Run2 own;
-        un2(A, own.a0, own.a1);
-        un2(H, own.h0, own.h1);
-        sh.run[warp][lane] = own;
-        __syncthreads();
-        Run2 before{1.f, 0.f, 1.f, 0.f};  // the block's runs before this one
-        for (int w = 0; w < warp; ++w) before = after(before, sh.run[w][lane]);
-        if (warp == warps - 1) {
-            const Run2 all = after(before, own);
-            for (int j = 0; j < blocks; ++j) *cluster.map_shared_rank(&sh.block[step & 1][rank][lane], j) = all;
-        }
-        // the stage has been read (by this warp alone): its rows of the step after the next are on their way while the cluster meets
-        if (warp == warps - 1)
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        else  // has written nothing for the others: its stores of y need not arrive first
-            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-        advance(next_item, next_s0);
-        fetch(next_item, next_s0, step & 1);
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        float e[2] = {carry[0], carry[1]};
-        for (int j = 0; j < blocks; ++j) {
-            if (j == rank) e[0] = carry[0], e[1] = carry[1];
-            const Run2 m = sh.block[step & 1][j][lane];
-            carry[0] = fmaf(m.a0, carry[0], m.h0), carry[1] = fmaf(m.a1, carry[1], m.h1);
-        }
-        e[0] = fmaf(before.a0, e[0], before.h0), e[1] = fmaf(before.a1, e[1], before.h1);
-        if (rows > 0 && p.states && t0 % kState == 0)
-            store_pair<float, WIDE>(p.states + (b * ((L + kState - 1) / kState) + t0 / kState) * D + c, e[0], e[1], one, both);
-        if (p.y) {
-            uint64_t y = f2(e[0], e[1]);
-            T *to = (T *)p.y + at;
-#pragma unroll
-            for (int t = 0; t < R; ++t, to += D) {
-                y = fma2(a[t], y, h[t]);
-                un2(y, e[0], e[1]);
-                if (full || t < rows)
-                    store_pair<T, WIDE>(to, full || t < live ? e[0] : 0.f, full || t < live ? e[1] : 0.f, one, both);
-            }
-        }
-        advance(item, s0);
-        if (s0 == 0 && rank == 0 && warp == 0 && p.final_state)
-            store_pair<float, WIDE>(p.final_state + b * D + c, carry[0], carry[1], one, both);
     }
     copy_wait<0>();
 }

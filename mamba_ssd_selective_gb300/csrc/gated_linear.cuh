@@ -96,21 +96,21 @@ template <typename T> __device__ __forceinline__ uint64_t exp_minus(uint64_t x) 
 }
 
 // The gates of one token, for two channels: rho and iota the sigmoids, t = 2 w = 2 k rho, a = exp(-w), beta2 = 1 - a^2 and
-// rbeta = 1 / sqrt(beta2), finite where w is 0, so that beta2 rbeta is 0 there (SHARED: 3e-19). rate2 is 2 k, rate_log2 is
-// k log2(e).
-// SHARED: both sigmoids from one reciprocal, 1 / (1 + e^-r)(1 + e^-i): the special function unit takes twice the time of an
-// exponential for one, and it is what the issue slots wait for next. The product is finite for r, i > kLowGate.
-// beta2 where 1 - a^2 would cancel (t < 1/2) is t times the polynomial of degree 4 through (1 - e^-t) / t at its Chebyshev
-// points on [0, 1/2] (1.1e-7 off at most); above, the difference of 1 and a^2 <= 0.61 costs 5e-7 at most.
-constexpr float kLowGate = -43.f;
+// rbeta = 1 / sqrt(beta2), finite where w is 0, so that beta2 rbeta is 0 there. rate2 is 2 k, rate_log2 is k log2(e).
+// beta2, where 1 - a^2 would cancel (t < 1), is t times the polynomial of degree 5 through (1 - e^-t) / t at its Chebyshev points
+// on [0, 1] (1.7e-7 off at most); above, the difference of 1 and a^2 <= 0.37 costs 2e-7.
+// FAST, for what nearly every run of tokens is: all r and i above kLowGate and k below kSteep. Then both sigmoids come of one
+// reciprocal, 1 / (1 + e^-r)(1 + e^-i), whose product is finite (the special function unit takes twice the time of an
+// exponential for it), and t is below 1. beta2 rbeta is 1e-19 rather than 0 where w is 0.
+constexpr float kLowGate = -43.f, kSteep = 0.5f;
 struct Gates2 {
     uint64_t rho, iota, t, a, beta2, rbeta;
 };
-template <typename T, bool SHARED>
+template <typename T, bool FAST>
 __device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, uint64_t rate2, uint64_t rate_log2) {
     Gates2 g;
     const uint64_t one = f2(1.f), u = add2(exp_minus<T>(r), one), v = add2(exp_minus<T>(i), one);
-    if constexpr (SHARED) {
+    if constexpr (FAST) {
         float d0, d1;
         un2(mul2(u, v), d0, d1);
         const uint64_t q = f2(rcp_approx(d0), rcp_approx(d1));
@@ -121,21 +121,28 @@ __device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, uint64_t rate2,
         un2(v, v0, v1);
         g.rho = f2(rcp_approx(u0), rcp_approx(u1)), g.iota = f2(rcp_approx(v0), rcp_approx(v1));
     }
-    float w0, w1, t0, t1, s0, s1, b0, b1;
+    float w0, w1, b0, b1;
     un2(mul2(g.rho, rate_log2), w0, w1);
     const float a0 = ex2_approx(-w0), a1 = ex2_approx(-w1);
     g.a = f2(a0, a1);
     g.t = mul2(g.rho, rate2);
-    uint64_t s = fma2(g.t, f2(0.0067828623577952385f), f2(-0.0410132110118866f));
-    s = fma2(g.t, s, f2(0.16655193269252777f));
-    s = fma2(g.t, s, f2(-0.49999287724494934f));
+    uint64_t s = fma2(g.t, f2(-0.0009125453652814031f), f2(0.00783736351877451f));
+    s = fma2(g.t, s, f2(-0.04141876474022865f));
+    s = fma2(g.t, s, f2(0.16660967469215393f));
+    s = fma2(g.t, s, f2(-0.4999951720237732f));
     s = fma2(g.t, s, f2(0.9999999403953552f));
-    un2(fma2(g.t, s, f2(SHARED ? 1e-37f : 0.f)), s0, s1);
-    un2(g.t, t0, t1);
-    b0 = t0 < 0.5f ? s0 : fmaf(-a0, a0, 1.f);
-    b1 = t1 < 0.5f ? s1 : fmaf(-a1, a1, 1.f);
-    g.beta2 = f2(b0, b1);
-    g.rbeta = SHARED ? f2(rsqrt_approx(b0), rsqrt_approx(b1)) : f2(rsqrt_approx(fmaxf(b0, 1e-37f)), rsqrt_approx(fmaxf(b1, 1e-37f)));
+    g.beta2 = fma2(g.t, s, f2(FAST ? 1.2e-38f : 0.f));
+    un2(g.beta2, b0, b1);
+    if constexpr (FAST) {
+        g.rbeta = f2(rsqrt_approx(b0), rsqrt_approx(b1));
+    } else {
+        float t0, t1;
+        un2(g.t, t0, t1);
+        b0 = t0 < 1.f ? b0 : fmaf(-a0, a0, 1.f);
+        b1 = t1 < 1.f ? b1 : fmaf(-a1, a1, 1.f);
+        g.beta2 = f2(b0, b1);
+        g.rbeta = f2(rsqrt_approx(fmaxf(b0, 1e-37f)), rsqrt_approx(fmaxf(b1, 1e-37f)));
+    }
     return g;
 }
 // The lesser of the gates seen, to tell whether they are all above kLowGate.
@@ -184,12 +191,13 @@ __device__ __forceinline__ float inverse_scale(uint32_t code) {  // 2^-e
 }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 // The whole number nearest to x 2^-e, as a byte: the sum with 1.5 2^23 has it in its last bits. 0 in a group that is not finite.
+constexpr float kToWhole = 12582912.f;
 struct To8 {
     float inv;
     uint32_t mask;
     __device__ __forceinline__ explicit To8(uint32_t code = 0) : inv(inverse_scale(code)), mask(code == 255u ? 0u : 0xffu) {}
     __device__ __forceinline__ int8_t operator()(float x) const {
-        return (int8_t)(__float_as_uint(fmaf(x, inv, 12582912.f)) & mask);
+        return (int8_t)(__float_as_uint(fmaf(x, inv, kToWhole)) & mask);
     }
 };
 
