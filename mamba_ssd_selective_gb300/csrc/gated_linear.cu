@@ -24,14 +24,17 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTile = 64;                 // channels of a block, two a lane
 constexpr int kFwdRun = kGroup;           // tokens of a warp in the forward: a group of the 8-bit values
 constexpr int kBwdRun = kState / kWarps;  // and in the backward, whose block takes the tokens between two saved states
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8;            // blocks; 4 for rows that are fetched by words, so that two blocks fit an SM
 
 // ------------------------------------------------------- copies to shared memory
 // A warp fetches the rows of its own runs, two steps ahead, and only it reads them: no barrier but its own. WIDE: 16 bytes a
 // lane, for rows that begin at a multiple of 16 bytes. Otherwise 4 bytes: the aligned words around each row, of those at the
 // tensor's end and the tile's only the bytes that belong to the tensor; a row then begins up to 3 bytes into its first word.
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+template <int BYTES> __device__ __forceinline__ void copy(uint32_t to, const void *from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t to, const void *from, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
@@ -44,20 +47,21 @@ template <typename T, bool WIDE> struct Row {  // in shared memory
 };
 
 // Rows 0..n-1 of a tile, R at most, of `cols` channels from `base` on, which lie D apart. ACROSS: the bytes from one row to the
-// next in shared memory.
-template <typename T, bool WIDE, int R, int ACROSS>
+// next in shared memory; V: the channels of a piece, where WIDE.
+template <typename T, bool WIDE, int R, int ACROSS, int V = 16 / (int)sizeof(T)>
 __device__ __forceinline__ void fetch_rows(unsigned char *to, const T *base, int n, int cols, int64_t D, int lane) {
     const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
     if constexpr (WIDE) {
-        constexpr int PER = kTile * (int)sizeof(T) / 16, ROWS = 32 / PER > R ? R : 32 / PER;  // lanes a row, rows at once
+        constexpr int PER = kTile / V, ROWS = 32 / PER;  // lanes a row, rows at once
+        static_assert(R % ROWS == 0, "");
         const int piece = lane % PER, first = lane / PER;
-        const int c = piece * (16 / (int)sizeof(T));
-        if (c < cols && first < ROWS) {
+        const int c = piece * V;
+        if (c < cols) {
             const T *from = base + first * D + c;
             const int64_t next = ROWS * D;
 #pragma unroll
             for (int j = 0; j < R / ROWS; ++j, from += next)
-                if (j * ROWS + first < n) copy16(dst + (j * ROWS + first) * ACROSS + piece * 16, from);
+                if (j * ROWS + first < n) copy<V * (int)sizeof(T)>(dst + (j * ROWS + first) * ACROSS + piece * V * (int)sizeof(T), from);
         }
     } else {
         const int have = cols * (int)sizeof(T);  // bytes of the tile's row
@@ -126,7 +130,7 @@ struct alignas(16) Run2 {
 __device__ __forceinline__ uint64_t after(const Run2 &x, uint64_t h) { return fma2(x.a, h, x.h); }  // x, from h
 __device__ __forceinline__ Run2 after(const Run2 &x, const Run2 &y) { return {mul2(x.a, y.a), fma2(y.a, x.h, y.h)}; }  // x, then y
 
-// A step of a cluster: the tile of a sequence that it is at, as its first thread works out two steps ahead.
+// A step of a cluster: the tile of a sequence that it is at. The first thread works it out three steps ahead, while it would wait.
 struct Step {
     int64_t base;      // of the step's first token and the tile's first channel in [B, L, D]
     int64_t b;
@@ -151,6 +155,22 @@ struct Walk {
         if (first >= p.L) first = 0, item += clusters;
         return s;
     }
+    // the same from a sequence's end, where steps begin at `last`
+    __device__ __forceinline__ Step backward(const LinearArgs &p, int span, int64_t last) {
+        Step s{};
+        if (item >= items) return s;
+        const uint32_t b = item / tiles;
+        s.b = b, s.c0 = (int32_t)(item - b * tiles) * kTile, s.first = (int32_t)first;
+        s.cols = (int32_t)imin<int64_t>(kTile, p.D - s.c0);
+        s.len = (int32_t)seq_len(p.seqlens, b, p.L);
+        s.base = (b * p.L + first) * p.D + s.c0;
+        if (first <= 0) {
+            first = last, item += clusters;
+        } else {
+            first -= span;
+        }
+        return s;
+    }
 };
 // Tokens of a run of R from t0 on that are below `end`.
 __device__ __forceinline__ int run_of(int R, int64_t end, int64_t t0) { return (int)imax<int64_t>(0, imin<int64_t>(R, end - t0)); }
@@ -158,14 +178,15 @@ __device__ __forceinline__ int run_of(int R, int64_t end, int64_t t0) { return (
 // The blocks of a cluster exchange a Run2 a lane: each sends its own to all of them, and the bytes count down the receiver's
 // barrier. (A cluster barrier would have the sender wait for everything that it has written to memory before.) Two of each,
 // taken in turn: a block sends for a step once all of its warps have read the one before.
-struct Exchange {
-    Run2 block[2][kMaxCluster][32];
+template <int MAX> struct Exchange {
+    static constexpr int kMax = MAX;
+    Run2 block[2][MAX][32];
     uint64_t bar[2];
 };
 constexpr uint64_t kGiveUpNs = 1000000000ull;
 __device__ int g_gave_up;  // SSD_ERR_TIMEOUT once a wait was given up on this device
 
-__device__ __forceinline__ void exchange_init(Exchange &x, int blocks) {
+template <int MAX> __device__ __forceinline__ void exchange_init(Exchange<MAX> &x, int blocks) {
     if (threadIdx.x == 0) {
         tc::mbar_init(&x.bar[0], 1);
         tc::mbar_init(&x.bar[1], 1);
@@ -177,12 +198,13 @@ __device__ __forceinline__ void exchange_init(Exchange &x, int blocks) {
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 }
-__device__ __forceinline__ void exchange_send(Exchange &x, int step, int rank, int blocks, int lane, const Run2 &own) {
+// To the ranks first, first + every, ...
+template <int MAX> __device__ __forceinline__ void exchange_send(Exchange<MAX> &x, int step, int rank, int blocks, int first, int every, int lane, const Run2 &own) {
     const uint32_t slot = tc::smem_u32(&x.block[step & 1][rank][lane]), bar = tc::smem_u32(&x.bar[step & 1]);
     uint32_t r0, r1, r2, r3;
     asm("mov.b64 {%0, %1}, %2;" : "=r"(r0), "=r"(r1) : "l"(own.a));
     asm("mov.b64 {%0, %1}, %2;" : "=r"(r2), "=r"(r3) : "l"(own.h));
-    for (int j = 0; j < blocks; ++j)
+    for (int j = first; j < blocks; j += every)
         asm volatile(
             "{\n\t.reg .b32 to, at;\n\t"
             "mapa.shared::cluster.u32 to, %0, %2;\n\t"
@@ -192,7 +214,7 @@ __device__ __forceinline__ void exchange_send(Exchange &x, int step, int rank, i
             : "memory");
 }
 // False, now and from then on, where the others' runs have not come in kGiveUpNs.
-__device__ __forceinline__ bool exchange_wait(Exchange &x, int step, bool alive) {
+template <int MAX> __device__ __forceinline__ bool exchange_wait(Exchange<MAX> &x, int step, bool alive) {
     if (!alive) return false;
     if (tc::mbar_wait(&x.bar[step & 1], (step >> 1) & 1, kGiveUpNs)) return true;
     atomicCAS(&g_gave_up, SSD_OK, SSD_ERR_TIMEOUT);
@@ -206,8 +228,8 @@ __device__ __forceinline__ bool exchange_wait(Exchange &x, int step, bool alive)
 template <typename T, bool WIDE> struct FwdShared {
     static constexpr int kAcross = Row<T, WIDE>::kPitch;
     unsigned char row[2][kWarps][3][kFwdRun][kAcross];
-    Run2 run[kWarps][32];
-    Exchange exchange;
+    Run2 run[2][kWarps][32];  // in turn: a warp may be at its next run while another reads these
+    Exchange<WIDE ? kMaxCluster : 4> exchange;
     Step step[4];
 };
 
@@ -269,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_fwd_k
     const int span = warps * R * blocks, mine = (rank * warps + warp) * R;  // a step's tokens; of them, where this warp's run is
     Walk walk{blockIdx.x / (uint32_t)blocks, 0, (uint32_t)((D + kTile - 1) / kTile), gridDim.x / (uint32_t)blocks, 0};
     walk.items = (uint32_t)p.B * walk.tiles;  // below 2^31
-    if (threadIdx.x == 0) sh.step[0] = walk.forward(p, span), sh.step[1] = walk.forward(p, span);
+    if (threadIdx.x == 0)
+        for (int j = 0; j < 3; ++j) sh.step[j] = walk.forward(p, span);
     exchange_init(sh.exchange, blocks);
 
     auto fetch = [&](int step) {
@@ -286,15 +309,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_fwd_k
     };
     fetch(0);
     fetch(1);
-    uint64_t carry = 0, rate2 = 0, rate_log2 = 0;
+    uint64_t carry = 0;
+    Rate2 rate{};
     bool steep = false, alive = true;
     for (int step = 0;; ++step) {
         const Step s = sh.step[step & 3];
         if (s.cols == 0) break;
-        if (threadIdx.x == 0) {
-            sh.step[(step + 2) & 3] = walk.forward(p, span);
-            tc::mbar_arrive_expect_tx(&sh.exchange.bar[step & 1], blocks * 32 * (uint32_t)sizeof(Run2));
-        }
+        if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&sh.exchange.bar[step & 1], blocks * 32 * (uint32_t)sizeof(Run2));
         const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
         const int64_t t0 = (int64_t)s.first + mine, at = s.base + mine * D + 2 * lane;
         const int live = run_of(R, s.len, t0), rows = run_of(R, L, t0);  // tokens that count, that exist
@@ -304,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_fwd_k
             float k0 = one ? p.lam[c] : 0.f, k1 = both ? p.lam[c + 1] : 0.f;
             carry = p.init ? f2(one ? p.init[s.b * D + c] : 0.f, both ? p.init[s.b * D + c + 1] : 0.f) : 0;
             k0 = p.c * softplus(k0), k1 = p.c * softplus(k1);
-            rate2 = f2(2.f * k0, 2.f * k1), rate_log2 = f2(kLog2e * k0, kLog2e * k1);
+            rate = Rate2::of(k0, k1);
             steep = __any_sync(0xffffffffu, (one && !(k0 < kSteep)) || (both && !(k1 < kSteep)));
         }
         copy_wait<1>();
@@ -329,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_fwd_k
                     if (t == 0) low = r; else lower(low, r);
                     lower(low, i);
                 }
-                const Gates2 g = gates2<T, FAST>(pair_of(r), pair_of(i), rate2, rate_log2);
+                const Gates2 g = gates2<T, FAST, false>(pair_of(r), pair_of(i), rate);
                 a[t] = g.a;
-                h[t] = mul2(mul2(mul2(g.beta2, g.rbeta), g.iota), pair_of(pair(0, t)));
+                h[t] = mul2(g.f, pair_of(pair(0, t)));
                 if (!FAST && t >= live) a[t] = f2(1.f), h[t] = f2(0.f);
                 own = after(own, {a[t], h[t]});
             }
@@ -342,17 +363,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_fwd_k
             fast = !__any_sync(0xffffffffu, one && is_low(low));
         }
         if (!fast) tokens(std::false_type{});
-        sh.run[warp][lane] = own;
+        sh.run[step & 1][warp][lane] = own;
         __syncthreads();
-        Run2 before{f2(1.f), f2(0.f)};  // the block's runs before this one
-        for (int w = 0; w < warp; ++w) before = after(before, sh.run[w][lane]);
-        if (warp == warps - 1) exchange_send(sh.exchange, step, rank, blocks, lane, after(before, own));
+        // The block's runs before this one, and all of them: every warp joins them, and sends to another block.
+        Run2 before{f2(1.f), f2(0.f)}, all = before;
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+            if (w == warp) before = all;
+            all = after(all, sh.run[step & 1][w][lane]);
+        }
+        exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
+        if (threadIdx.x == 0) sh.step[(step + 3) & 3] = walk.forward(p, span);
         alive = exchange_wait(sh.exchange, step, alive);
         if (!alive) carry = f2(__uint_as_float(0x7fc00000u));  // what was not told is not guessed
         uint64_t e = carry;                                     // the state that enters this run
-        for (int j = 0; j < rank; ++j) e = after(sh.exchange.block[step & 1][j][lane], e);
-        carry = e;
-        for (int j = rank; j < blocks; ++j) carry = after(sh.exchange.block[step & 1][j][lane], carry);
+#pragma unroll 4
+        for (int j = 0; j < blocks; ++j) {
+            if (j == rank) e = carry;
+            carry = after(sh.exchange.block[step & 1][j][lane], carry);
+        }
         e = after(before, e);
         if (rows > 0 && p.states && t0 % kState == 0) {
             float e0, e1;
@@ -419,159 +448,283 @@ __global__ void __launch_bounds__(256) linear_keep_kernel(const float *init, flo
 }
 
 // ----------------------------------------------------------------- backward
-// dh_t = dy_t + m_{t+1}, m_t = a_t dh_t (m behind the last token the gradient of the final state): the same kind of
-// recurrence, backwards, a run acting as m -> A m + M. With psi_t = w_t dL/dw_t:
-//     dx = dh beta iota     di = dh b (1 - iota)     psi = dh (a^2 b w / beta^2 - a w h_{t-1})     dr = psi (1 - rho)
+// dh_t = dy_t + m_{t+1}, m_t = a_t dh_t (m behind the last token the gradient of the final state): the same kind of recurrence,
+// backwards, a run acting as m -> A m + M. With f and g as in gates2 and psi_t = w_t dL/dw_t:
+//     b = f x     dx = dh f     di = dh b (1 - iota)     psi = dh (g b - a w h_{t-1})     dr = psi (1 - rho)
 //     dlam = sigmoid(lam) / softplus(lam) sum psi
-// (psi rather than dL/dw, which has 1 / beta: w / beta goes to zero with w.) h_{t-1} is formed again from the state that
-// enters each kState tokens. A block goes over its sequence from the end, kState tokens at a time.
-__device__ __forceinline__ float one_minus_a2(float w, float a) {
-    const float t = 2.f * w;
-    float p = fmaf(t, 0.0067828623577952385f, -0.0410132110118866f);
-    p = fmaf(t, p, 0.16655193269252777f);
-    p = fmaf(t, p, -0.49999287724494934f);
-    p = fmaf(t, p, 0.9999999403953552f);
-    return t < 0.5f ? t * p : fmaf(-a, a, 1.f);
+// (psi rather than dL/dw, which has 1 / sqrt(1 - a^2): w over it goes to zero with w.) h_{t-1} is formed again from the state that
+// enters each kState tokens, which are a block's; the warps and blocks lie one before the other in time.
+// Bound as the forward is (14 bytes a token and channel in bf16, 11 from 8 bits).
+template <typename T, bool WIDE, bool PACK> struct BwdShared {
+    static constexpr int kAcross = Row<T, WIDE>::kPitch;  // 8-bit rows too: the gradients' rows take their place
+    unsigned char row[2][kWarps][4][kBwdRun][kAcross];    // x, r, i and dy; then dx, dr and di
+    float state[4][kTile];
+    unsigned char scale[2][kWarps][3][kTile + 4];
+    Run2 run[2][kWarps][32];
+    uint64_t h[2][kWarps][32], sum[kWarps][32];
+    Exchange<WIDE ? kMaxCluster : 4> exchange;
+    Step step[4];
+};
+
+// The two channels of a lane in 8 bits, as numbers: byte v as 2^23 + 128 + v, less that, exactly; times the scale.
+__device__ __forceinline__ uint64_t from_8(uint32_t two, uint64_t scale) {
+    const uint32_t v = two ^ 0x8080u;
+    const uint64_t n = f2(__uint_as_float(__byte_perm(v, 0x4b000000u, 0x7440)), __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7441)));
+    return mul2(add2(n, f2(-8388736.f)), scale);
 }
-template <typename T, int V, bool PACK> __global__ void __launch_bounds__(kThreads) linear_bwd_kernel(LinearBwdArgs p) {
-    pdl_enter();
-    constexpr int R = kBwdRun;
-    __shared__ float run[3][kWarps][32 * V];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t c0 = ((int64_t)blockIdx.y * 32 + lane) * V, b = blockIdx.z, D = p.f.D, L = p.f.L;
-    const bool on = c0 < D;
-    const int64_t len = seq_len(p.f.seqlens, b, L), n = p.f.B * L * D, groups = (L + kGroup - 1) / kGroup;
-    float k[V], carry[V], sum[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        k[v] = on ? p.f.c * softplus(p.f.lam[c0 + v]) : 0.f;
-        carry[v] = on && p.dfinal ? p.dfinal[b * D + c0 + v] : 0.f;
-        sum[v] = 0.f;
+
+// Whether a run's gates are all above kLowGate.
+template <typename T, bool PACK> struct Low {
+    Raw<T, 2> least;
+    __device__ __forceinline__ void see(const Raw<T, 2> &r, const Raw<T, 2> &i, bool first) {
+        if (first) least = r; else lower(least, r);
+        lower(least, i);
     }
-    for (int64_t chunk = (L + kState - 1) / kState - 1; chunk >= 0; --chunk) {
-        const int64_t t0 = chunk * kState + warp * R, at = (b * L + t0) * D + c0;
-        const int live = on ? (int)imax<int64_t>(0, imin<int64_t>(R, len - t0)) : 0;
-        const int rows = on ? (int)imax<int64_t>(0, imin<int64_t>(R, L - t0)) : 0;
-        float a[R][V], bb[R][V], rho[R][V], iota[R][V], dy[R][V], A[V], H[V], M[V];
-        float scale[3][V];
+    __device__ __forceinline__ bool any() const { return is_low(least); }
+};
+template <typename T> struct Low<T, true> {
+    Raw<float, 2> least;
+    __device__ __forceinline__ void see(uint64_t r, uint64_t i, bool first) {
+        Raw<float, 2> a, b;
+        un2(r, a.v[0], a.v[1]);
+        un2(i, b.v[0], b.v[1]);
+        if (first) least = a; else lower(least, a);
+        lower(least, b);
+    }
+    __device__ __forceinline__ bool any() const { return is_low(least); }
+};
+
+template <typename T, bool WIDE, bool PACK>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) linear_bwd_kernel(LinearBwdArgs p) {
+    namespace cg = cooperative_groups;
+    pdl_enter();
+    constexpr int R = kBwdRun, ACROSS = BwdShared<T, WIDE, PACK>::kAcross;
+    extern __shared__ __align__(16) unsigned char raw_smem[];
+    BwdShared<T, WIDE, PACK> &sh = *reinterpret_cast<BwdShared<T, WIDE, PACK> *>(raw_smem);
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
+    const int64_t D = p.f.D, L = p.f.L, chunks = (L + kState - 1) / kState, groups = (L + kGroup - 1) / kGroup;
+    const int64_t plane = p.f.B * L * D, scales = p.f.B * groups * D;
+    // This warp's run, from the step's first token: rank 0 and warp 0 have the latest. A step begins a cluster's chunks before the
+    // one it came from, at the start of a sequence before its first token.
+    const int mine = (blocks - 1 - rank) * kState + (warps - 1 - warp) * R;
+    Walk walk{blockIdx.x / (uint32_t)blocks, 0, (uint32_t)((D + kTile - 1) / kTile), gridDim.x / (uint32_t)blocks, 0};
+    walk.items = (uint32_t)p.f.B * walk.tiles;  // below 2^31
+    walk.first = (chunks - blocks) * kState;
+    if (threadIdx.x == 0)
+        for (int j = 0; j < 3; ++j) sh.step[j] = walk.backward(p.f, blocks * kState, (chunks - blocks) * kState);
+    exchange_init(sh.exchange, blocks);
+
+    auto fetch = [&](int step) {
+        const Step s = sh.step[step & 3];
+        const int64_t t0 = (int64_t)s.first + mine;
+        if (s.cols > 0 && t0 >= 0) {
+            const int live = run_of(R, s.len, t0);
+            const int64_t at = s.base + mine * D;
+            auto &to = sh.row[step & 1][warp];
+            if constexpr (PACK) {
+                if (live > 0) {
+                    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll
+                    for (int z = 0; z < 3; ++z) {
+                        fetch_rows<int8_t, WIDE, R, ACROSS, V>(to[z][0], p.f.values + z * plane + at, live, s.cols, D, lane);
+                        const uint8_t *scale = p.f.scales + z * scales + (s.b * groups + t0 / kGroup) * D + s.c0;
+                        unsigned char *row = sh.scale[step & 1][warp][z];
+                        if constexpr (WIDE) {
+                            if (lane * 4 < s.cols) copy<4>(tc::smem_u32(row + lane * 4), scale + lane * 4);
+                        } else {
+                            fetch_rows<uint8_t, false, 1, kTile + 4>(row, scale, 1, s.cols, D, lane);
+                        }
+                    }
+                }
+            } else {
+                fetch_rows<T, WIDE, R, ACROSS>(to[0][0], (const T *)p.f.x + at, live, s.cols, D, lane);
+                fetch_rows<T, WIDE, R, ACROSS>(to[1][0], (const T *)p.f.r + at, live, s.cols, D, lane);
+                fetch_rows<T, WIDE, R, ACROSS>(to[2][0], (const T *)p.f.i + at, live, s.cols, D, lane);
+            }
+            fetch_rows<T, WIDE, R, ACROSS>(to[3][0], (const T *)p.dy + at, live, s.cols, D, lane);
+            if (warp == 0) {  // the state that enters the block's tokens: read behind the block's barrier
+                const float *state = p.f.states + (s.b * chunks + t0 / kState) * D + s.c0;
+#pragma unroll
+                for (int c = lane; c < kTile; c += 32)
+                    if (c < s.cols) copy<4>(tc::smem_u32(&sh.state[step & 3][c]), state + c);
+            }
+        }
+        copy_commit();
+    };
+    fetch(0);
+    fetch(1);
+    uint64_t carry = 0, sum = 0;
+    Rate2 rate{};
+    bool steep = false, alive = true;
+    for (int step = 0;; ++step) {
+        const Step s = sh.step[step & 3];
+        if (s.cols == 0) break;
+        if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&sh.exchange.bar[step & 1], blocks * 32 * (uint32_t)sizeof(Run2));
+        const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
+        const int64_t t0 = (int64_t)s.first + mine, at = s.base + mine * D + 2 * lane;
+        const int live = t0 < 0 ? 0 : run_of(R, s.len, t0), rows = t0 < 0 ? 0 : run_of(R, L, t0);
+        auto &in = sh.row[step & 1][warp];
+        if (s.first == (chunks - blocks) * kState) {
+            const int64_t c = s.c0 + 2 * lane;
+            float k0 = one ? p.f.lam[c] : 0.f, k1 = both ? p.f.lam[c + 1] : 0.f;
+            carry = p.dfinal ? f2(one ? p.dfinal[s.b * D + c] : 0.f, both ? p.dfinal[s.b * D + c + 1] : 0.f) : 0;
+            sum = 0;
+            k0 = p.f.c * softplus(k0), k1 = p.f.c * softplus(k1);
+            rate = Rate2::of(k0, k1);
+            steep = __any_sync(0xffffffffu, (one && !(k0 < kSteep)) || (both && !(k1 < kSteep)));
+        }
+        copy_wait<1>();
+        __syncwarp();
+        auto shift = [&](const void *base, int64_t from, int size) {  // bytes that a row begins into its first word
+            return WIDE || size == 4 ? 0 : (int)((reinterpret_cast<uintptr_t>(base) + (uintptr_t)from * size) & 3);
+        };
+        auto pair = [&](int z, int t) {
+            const void *base = z == 0 ? p.f.x : z == 1 ? p.f.r : z == 2 ? p.f.i : p.dy;
+            return row_pair<T, WIDE>(in[z][t], shift(base, at - 2 * lane + t * D, sizeof(T)), lane, both);
+        };
+        uint64_t scale[3];
         if constexpr (PACK) {
 #pragma unroll
             for (int z = 0; z < 3; ++z) {
-                Raw<uint8_t, V> code;
-                if (live > 0) code = load<uint8_t, V>(p.f.scales + ((z * p.f.B + b) * groups + t0 / kGroup) * D + c0);
-#pragma unroll
-                for (int v = 0; v < V; ++v) scale[z][v] = scale_of(code.v[v]);
+                const Raw<uint8_t, 2> code =
+                    row_pair<uint8_t, WIDE>(sh.scale[step & 1][warp][z], shift(p.f.scales, z * scales + (s.b * groups + t0 / kGroup) * D + s.c0, 1), lane, both);
+                scale[z] = f2(scale_of(code.v[0]), scale_of(code.v[1]));
             }
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
-#pragma unroll
-        for (int t = 0; t < R; ++t) {
-            float x[V], r[V], i[V];
-            Raw<T, V> d;
-            if (t < live) d = load<T, V>((const T *)p.dy + at + t * D);
+        auto value = [&](int z, int t) {
             if constexpr (PACK) {
-                Raw<int8_t, V> q[3];
-#pragma unroll
-                for (int z = 0; z < 3; ++z)
-                    if (t < live) q[z] = load<int8_t, V>(p.f.values + z * n + at + t * D);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    x[v] = (float)q[0].v[v] * scale[0][v];
-                    r[v] = (float)q[1].v[v] * scale[1][v];
-                    i[v] = (float)q[2].v[v] * scale[2][v];
-                }
+                const Raw<int8_t, 2> q = row_pair<int8_t, WIDE>(in[z][t], shift(p.f.values, z * plane + at - 2 * lane + t * D, 1), lane, both);
+                return from_8(q.word, scale[z]);
             } else {
-                Raw<T, V> q[3];
-                if (t < live) {
-                    q[0] = load<T, V>((const T *)p.f.x + at + t * D);
-                    q[1] = load<T, V>((const T *)p.f.r + at + t * D);
-                    q[2] = load<T, V>((const T *)p.f.i + at + t * D);
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v) x[v] = to_f32(q[0].v[v]), r[v] = to_f32(q[1].v[v]), i[v] = to_f32(q[2].v[v]);
+                return pair_of(pair(z, t));
             }
+        };
+        uint64_t a[R], b[R], f[R], rho[R], d[R];
+        Run2 own;   // of m, backwards
+        uint64_t H;  // and of h, forwards; its A is the same
+        Low<T, PACK> low;
+        auto tokens = [&](auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
+            const uint64_t minus = f2(-1.f), unit = f2(1.f);
+            H = 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Gates g = gates<T>(r[v], i[v], k[v]);
-                a[t][v] = t < live ? g.a : 1.f;
-                bb[t][v] = t < live ? g.beta2 * g.rbeta * g.iota * x[v] : 0.f;
-                rho[t][v] = g.rho, iota[t][v] = g.iota, dy[t][v] = to_f32(d.v[v]);
-                A[v] *= a[t][v];
-                H[v] = fmaf(a[t][v], H[v], bb[t][v]);
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            M[v] = 0.f;
-#pragma unroll
-            for (int t = R - 1; t >= 0; --t) M[v] = a[t][v] * (dy[t][v] + M[v]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            run[0][warp][lane * V + v] = A[v];
-            run[1][warp][lane * V + v] = H[v];
-            run[2][warp][lane * V + v] = M[v];
-        }
-        __syncthreads();
-        float h[V], m[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            h[v] = on ? p.f.states[(b * ((L + kState - 1) / kState) + chunk) * D + c0 + v] : 0.f;
-            for (int w = 0; w < warp; ++w) h[v] = fmaf(run[0][w][lane * V + v], h[v], run[1][w][lane * V + v]);
-            m[v] = carry[v];
-            for (int w = warps - 1; w >= 0; --w) {
-                if (w == warp) m[v] = carry[v];
-                carry[v] = fmaf(run[0][w][lane * V + v], carry[v], run[2][w][lane * V + v]);
-            }
-        }
-        float before[R][V];
-#pragma unroll
-        for (int t = 0; t < R; ++t)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                before[t][v] = h[v];
-                h[v] = fmaf(a[t][v], h[v], bb[t][v]);
-            }
-#pragma unroll
-        for (int t = R - 1; t >= 0; --t) {
-            float dx[V], dr[V], di[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float av = a[t][v], w = k[v] * rho[t][v], beta2 = one_minus_a2(w, av);
-                const float rb = rsqrt_approx(fmaxf(beta2, 1e-37f));
-                const float dh = dy[t][v] + m[v];
-                const float psi = dh * av * w * (av * bb[t][v] * rb * rb - before[t][v]);
-                dx[v] = dh * beta2 * rb * iota[t][v];
-                di[v] = dh * bb[t][v] * (1.f - iota[t][v]);
-                dr[v] = psi * (1.f - rho[t][v]);
-                if (t < live) {
-                    sum[v] += psi;
+            for (int t = 0; t < R; ++t) {
+                uint64_t r, i;
+                if constexpr (PACK) {
+                    r = value(1, t), i = value(2, t);
+                    if (FAST) low.see(r, i, t == 0);
                 } else {
-                    dx[v] = dr[v] = di[v] = 0.f;
+                    const Raw<T, 2> rw = pair(1, t), iw = pair(2, t);
+                    if (FAST) low.see(rw, iw, t == 0);
+                    r = pair_of(rw), i = pair_of(iw);
                 }
-                m[v] = av * dh;
+                const Gates2 g = gates2<T, FAST, true>(r, i, rate);
+                a[t] = g.a, f[t] = g.f, rho[t] = g.rho;
+                b[t] = mul2(g.f, value(0, t));
+                d[t] = g.iota;
+                if (!FAST && t >= live) a[t] = unit, b[t] = 0;
+                H = fma2(a[t], H, b[t]);
             }
-            if (t < rows) {
-                store_f32<T, V>((T *)p.dx + at + t * D, dx);
-                store_f32<T, V>((T *)p.dr + at + t * D, dr);
-                store_f32<T, V>((T *)p.di + at + t * D, di);
+            own.a = unit, own.h = 0;
+#pragma unroll
+            for (int t = R - 1; t >= 0; --t) {
+                const uint64_t dy = FAST || t < live ? pair_of(pair(3, t)) : 0;
+                own.a = mul2(own.a, a[t]);
+                own.h = mul2(a[t], add2(dy, own.h));
+            }
+        };
+        bool fast = live == R && !steep;
+        if (fast) {
+            tokens(std::true_type{});
+            fast = !__any_sync(0xffffffffu, one && low.any());
+        }
+        if (!fast) tokens(std::false_type{});
+        sh.run[step & 1][warp][lane] = own;
+        sh.h[step & 1][warp][lane] = H;
+        __syncthreads();
+        Run2 before{f2(1.f), 0}, all = before;
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+            if (w == warp) before = all;
+            all = after(all, sh.run[step & 1][w][lane]);
+        }
+        exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
+        if (threadIdx.x == 0) sh.step[(step + 3) & 3] = walk.backward(p.f, blocks * kState, (chunks - blocks) * kState);
+        // h, from the block's state over the earlier runs (the later warps') to this one; with it what multiplies dh in psi
+        uint64_t h = f2(sh.state[step & 3][2 * lane], sh.state[step & 3][2 * lane + 1]);
+        for (int w = warps - 1; w > warp; --w) h = fma2(sh.run[step & 1][w][lane].a, h, sh.h[step & 1][w][lane]);
+        {
+            const uint64_t minus = f2(-1.f), unit = f2(1.f);
+#pragma unroll
+            for (int t = 0; t < R; ++t) {
+                const uint64_t w2 = mul2(rho[t], rate.twice), g = grad_ratio(w2, a[t], steep);
+                const uint64_t c = fma2(mul2(mul2(a[t], w2), f2(-0.5f)), h, mul2(g, b[t]));  // g b - a w h
+                h = fma2(a[t], h, b[t]);
+                d[t] = mul2(b[t], fma2(d[t], minus, unit));
+                b[t] = c;
+                rho[t] = fma2(rho[t], minus, unit);
+            }
+        }
+        alive = exchange_wait(sh.exchange, step, alive);
+        if (!alive) carry = f2(__uint_as_float(0x7fc00000u));  // what was not told is not guessed
+        uint64_t m = carry;                                     // that comes to this run from the later ones
+#pragma unroll 4
+        for (int j = 0; j < blocks; ++j) {
+            if (j == rank) m = carry;
+            carry = after(sh.exchange.block[step & 1][j][lane], carry);
+        }
+        m = after(before, m);
+        auto results = [&](auto whole) {
+#pragma unroll
+            for (int t = R - 1; t >= 0; --t) {
+                constexpr bool ALL = decltype(whole)::value;
+                const uint64_t dh = add2(m, ALL || t < live ? pair_of(pair(3, t)) : 0), psi = mul2(dh, b[t]);
+                const uint64_t out[3] = {mul2(dh, f[t]), mul2(psi, rho[t]), mul2(dh, d[t])};
+                if (ALL || t < live) sum = add2(sum, psi);
+                m = mul2(a[t], dh);
+#pragma unroll
+                for (int z = 0; z < 3; ++z) {
+                    float v0, v1;
+                    un2(out[z], v0, v1);
+                    if (!ALL && t >= live) v0 = v1 = 0.f;
+                    Raw<T, 2> v;
+                    v.v[0] = from_f32<T>(v0), v.v[1] = from_f32<T>(v1);
+                    if constexpr (WIDE) {
+                        *reinterpret_cast<decltype(v.word) *>(in[z][t] + 2 * sizeof(T) * lane) = v.word;
+                    } else {
+                        if (t < rows) store_pair<T, WIDE>((T *)(z == 0 ? p.dx : z == 1 ? p.dr : p.di) + at + t * D, v, one, both);
+                    }
+                }
+            }
+        };
+        __syncwarp();  // the rows of x, r and i have been read
+        if (live == R) results(std::true_type{}); else results(std::false_type{});
+        __syncwarp();
+        if constexpr (WIDE) {
+            leave_rows<T, T, R, ACROSS>(in[0][0], (T *)p.dx + at - 2 * lane, rows, s.cols, D, lane);
+            leave_rows<T, T, R, ACROSS>(in[1][0], (T *)p.dr + at - 2 * lane, rows, s.cols, D, lane);
+            leave_rows<T, T, R, ACROSS>(in[2][0], (T *)p.di + at - 2 * lane, rows, s.cols, D, lane);
+            __syncwarp();
+        }
+        fetch(step + 2);
+        if (s.first <= 0) {  // the sequence is done
+            sh.sum[warp][lane] = sum;
+            __syncthreads();
+            if (warp == 0) {
+                for (int w = 1; w < warps; ++w) sum = add2(sum, sh.sum[w][lane]);
+                float s0, s1;
+                un2(sum, s0, s1);
+                store_pair<float, WIDE>(p.part + (s.b * blocks + rank) * D + s.c0 + 2 * lane, s0, s1, one, both);
+                if (rank == 0 && p.dinit) {
+                    un2(carry, s0, s1);
+                    store_pair<float, WIDE>(p.dinit + s.b * D + s.c0 + 2 * lane, s0, s1, one, both);
+                }
             }
         }
     }
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) run[0][warp][lane * V + v] = sum[v];
-    __syncthreads();
-    if (!on || warp != 0) return;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float s = 0.f;
-        for (int w = 0; w < warps; ++w) s += run[0][w][lane * V + v];
-        p.part[b * D + c0 + v] = s;
-        if (p.dinit) p.dinit[b * D + c0 + v] = carry[v];
-    }
+    copy_wait<0>();
 }
 
 // dlam from the blocks' sums, in float64: their number grows with the batch.
@@ -604,11 +757,13 @@ template <typename T, int V> __global__ void __launch_bounds__(256) linear_step_
         return;
     }
     const Raw<T, V> x = load<T, V>((const T *)p.x + at), r = load<T, V>((const T *)p.r + at), i = load<T, V>((const T *)p.i + at);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const Gates g = gates<T>(to_f32(r.v[v]), to_f32(i.v[v]), p.c * softplus(p.lam[c0 + v]));
-        h[v] = fmaf(g.a, p.state[slot * p.D + c0 + v], g.beta2 * g.rbeta * g.iota * to_f32(x.v[v]));
-    }
+    const float *lam = p.lam + c0, *state = p.state + slot * p.D + c0;
+    auto two = [&](const Raw<T, V> &w) { return f2(to_f32(w.v[0]), to_f32(w.v[V - 1])); };
+    const Rate2 k = Rate2::of(p.c * softplus(lam[0]), p.c * softplus(lam[V - 1]));
+    const Gates2 g = gates2<T, false, false>(two(r), two(i), k);
+    float h0, h1;
+    un2(fma2(g.a, f2(state[0], state[V - 1]), mul2(g.f, two(x))), h0, h1);
+    h[V - 1] = h1, h[0] = h0;
 #pragma unroll
     for (int v = 0; v < V; ++v) p.new_state[slot * p.D + c0 + v] = h[v];
     store_f32<T, V>((T *)p.y + at, h);
@@ -704,11 +859,12 @@ template <auto KERN> cudaError_t clusters_at_once(int blocks, int threads, size_
 
 // Launches KERN over `items` sequences and tiles of `L` tokens in blocks of `tokens`. The cluster's size: the one whose waves
 // times steps are fewest, a step of a cluster counted a tenth dearer than one of a single block for the meeting.
-template <auto KERN, typename Args> cudaError_t launch_clusters(const Args &a, int64_t items, int64_t L, int warps, int run, size_t smem, cudaStream_t stream) {
+template <auto KERN, typename Args> cudaError_t launch_clusters(const Args &a, int64_t items, int64_t L, int most, int warps, int run, size_t smem, cudaStream_t stream,
+                                                         int *blocks_taken = nullptr) {
     const int64_t tokens = (int64_t)warps * run, need = (L + tokens - 1) / tokens;
     int best = 1, held = 1;
     double cost = 0;
-    for (int blocks = 1; blocks <= kMaxCluster && blocks <= need; ++blocks) {
+    for (int blocks = 1; blocks <= most && blocks <= need; ++blocks) {
         int count = 0;
         cudaError_t e = clusters_at_once<KERN>(blocks, kThreads, smem, &count);
         if (e != cudaSuccess) return e;
@@ -716,6 +872,7 @@ template <auto KERN, typename Args> cudaError_t launch_clusters(const Args &a, i
         const double c = (double)((items + count - 1) / count) * (double)((need + blocks - 1) / blocks) * (blocks > 1 ? 1.1 : 1.0);
         if (blocks == 1 || c < cost) best = blocks, held = count, cost = c;
     }
+    if (blocks_taken) *blocks_taken = best;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -734,8 +891,8 @@ template <typename T, bool WIDE> cudaError_t forward_w(const LinearArgs &a, cuda
     const int64_t items = a.B * ((a.D + kTile - 1) / kTile);
     const int warps = warps_for(a.L, kFwdRun);
     const size_t smem = sizeof(FwdShared<T, WIDE>);
-    return a.values ? launch_clusters<linear_fwd_kernel<T, WIDE, true>>(a, items, a.L, warps, kFwdRun, smem, stream)
-                    : launch_clusters<linear_fwd_kernel<T, WIDE, false>>(a, items, a.L, warps, kFwdRun, smem, stream);
+    return a.values ? launch_clusters<linear_fwd_kernel<T, WIDE, true>>(a, items, a.L, WIDE ? kMaxCluster : 4, warps, kFwdRun, smem, stream)
+                    : launch_clusters<linear_fwd_kernel<T, WIDE, false>>(a, items, a.L, WIDE ? kMaxCluster : 4, warps, kFwdRun, smem, stream);
 }
 template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t stream) {
     if (a.L == 0) {
@@ -746,24 +903,30 @@ template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t st
     return wide_rows(a.D, sizeof(T)) ? forward_w<T, true>(a, stream) : forward_w<T, false>(a, stream);
 }
 
+template <typename T, bool WIDE, bool PACK> cudaError_t backward_p(const LinearBwdArgs &a, cudaStream_t stream, int *blocks) {
+    const int64_t items = a.f.B * ((a.f.D + kTile - 1) / kTile);
+    return launch_clusters<linear_bwd_kernel<T, WIDE, PACK>>(a, items, a.f.L, WIDE ? kMaxCluster : 4, warps_for(a.f.L, kBwdRun), kBwdRun, sizeof(BwdShared<T, WIDE, PACK>),
+                                                             stream, blocks);
+}
 template <typename T> cudaError_t backward_t(const LinearBwdArgs &a, cudaStream_t stream) {
-    return for_width(a.f.D, [&](auto vw) {
-        constexpr int V = decltype(vw)::value;
-        cudaError_t e = cudaSuccess;
-        if (a.f.B > 0) {
-            const dim3 grid(1, tiles(a.f.D, V), (unsigned)a.f.B), block(32 * warps_for(a.f.L, kBwdRun));
-            e = a.f.values ? launch_programmatic(linear_bwd_kernel<T, V, true>, grid, block, 0, stream, a)
-                           : launch_programmatic(linear_bwd_kernel<T, V, false>, grid, block, 0, stream, a);
-        }
-        if (e != cudaSuccess) return e;
-        return launch_programmatic(linear_dlam_kernel, dim3((unsigned)((a.f.D + 31) / 32)), dim3(32, 8), 0, stream,
-                                   (const float *)a.part, a.f.lam, a.dlam, a.f.B, a.f.D);
-    });
+    cudaError_t e = cudaSuccess;
+    int blocks = 0;  // none has added to the sum for dlam
+    if (a.f.B > 0 && a.f.L > 0) {
+        const bool wide = wide_rows(a.f.D, sizeof(T));
+        e = a.f.values ? (wide ? backward_p<T, true, true>(a, stream, &blocks) : backward_p<T, false, true>(a, stream, &blocks))
+                       : (wide ? backward_p<T, true, false>(a, stream, &blocks) : backward_p<T, false, false>(a, stream, &blocks));
+    } else if (a.f.B > 0 && a.dinit && a.dinit != a.dfinal) {
+        e = launch_programmatic(linear_keep_kernel, dim3((unsigned)((a.f.B * a.f.D + 255) / 256)), dim3(256), 0, stream, a.dfinal, a.dinit,
+                                a.f.B * a.f.D);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_programmatic(linear_dlam_kernel, dim3((unsigned)((a.f.D + 31) / 32)), dim3(32, 8), 0, stream, (const float *)a.part, a.f.lam,
+                               a.dlam, a.f.B * blocks, a.f.D);
 }
 
 }  // namespace linear
 
-int64_t linear_bwd_parts(int64_t B) { return B; }
+int64_t linear_bwd_parts(int64_t B) { return B * linear::kMaxCluster; }
 
 cudaError_t launch_linear(int io, const LinearArgs &a, cudaStream_t stream) {
     return io == IO_BF16 ? linear::forward_t<__nv_bfloat16>(a, stream) : linear::forward_t<float>(a, stream);

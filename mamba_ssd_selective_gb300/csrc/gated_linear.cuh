@@ -95,53 +95,78 @@ template <typename T> __device__ __forceinline__ uint64_t exp_minus(uint64_t x) 
     return e;
 }
 
-// The gates of one token, for two channels: rho and iota the sigmoids, t = 2 w = 2 k rho, a = exp(-w), beta2 = 1 - a^2 and
-// rbeta = 1 / sqrt(beta2), finite where w is 0, so that beta2 rbeta is 0 there. rate2 is 2 k, rate_log2 is k log2(e).
-// beta2, where 1 - a^2 would cancel (t < 1), is t times the polynomial of degree 5 through (1 - e^-t) / t at its Chebyshev points
-// on [0, 1] (1.7e-7 off at most); above, the difference of 1 and a^2 <= 0.37 costs 2e-7.
-// FAST, for what nearly every run of tokens is: all r and i above kLowGate and k below kSteep. Then both sigmoids come of one
-// reciprocal, 1 / (1 + e^-r)(1 + e^-i), whose product is finite (the special function unit takes twice the time of an
-// exponential for it), and t is below 1. beta2 rbeta is 1e-19 rather than 0 where w is 0.
-constexpr float kLowGate = -43.f, kSteep = 0.5f;
-struct Gates2 {
-    uint64_t rho, iota, t, a, beta2, rbeta;
-};
-template <typename T, bool FAST>
-__device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, uint64_t rate2, uint64_t rate_log2) {
-    Gates2 g;
-    const uint64_t one = f2(1.f), u = add2(exp_minus<T>(r), one), v = add2(exp_minus<T>(i), one);
-    if constexpr (FAST) {
-        float d0, d1;
-        un2(mul2(u, v), d0, d1);
-        const uint64_t q = f2(rcp_approx(d0), rcp_approx(d1));
-        g.rho = mul2(q, v), g.iota = mul2(q, u);
-    } else {
-        float u0, u1, v0, v1;
-        un2(u, u0, u1);
-        un2(v, v0, v1);
-        g.rho = f2(rcp_approx(u0), rcp_approx(u1)), g.iota = f2(rcp_approx(v0), rcp_approx(v1));
+// The gates of one token, for two channels, with rho and iota the sigmoids of r and i, w = k rho and t = 2 w:
+//     a = exp(-w)     f = sqrt(1 - a^2) iota     and for the backward g = a^2 w / (1 - a^2) = w / (exp(2 w) - 1) (grad_ratio).
+// 1 - exp(-t) is t times a smooth function, so its root is sqrt(2 k rho) Q(t) and there is neither a difference that cancels nor a
+// root of its own to take: rho is the square of 1 / sqrt(1 + e^-r). Q(t) = sqrt((1 - e^-t) / t) and g = G(t), t / (e^t - 1) / 2, for
+// t < 1 as polynomials of degree 4 through their Chebyshev points on [0, 1] (1.8e-7 and 4.4e-7 off at most).
+// FAST, for what nearly every run of tokens is: all r and i above kLowGate and k below kSteep. Then t < 1, and one reciprocal root
+// gives sqrt(rho) iota = 1 / sqrt((1 + e^-r) (1 + e^-i)^2), whose argument is finite: four calls of the special function unit a
+// token and channel, which with six of them is what bounds the kernels.
+constexpr float kLowGate = -29.f, kSteep = 0.5f;
+struct Rate2 {  // of two channels: 2 k, k log2(e), sqrt(2 k)
+    uint64_t twice, log2, root;
+    __device__ __forceinline__ static Rate2 of(float k0, float k1) {
+        return {f2(2.f * k0, 2.f * k1), f2(kLog2e * k0, kLog2e * k1), f2(sqrtf(2.f * k0), sqrtf(2.f * k1))};
     }
-    float w0, w1, b0, b1;
-    un2(mul2(g.rho, rate_log2), w0, w1);
-    const float a0 = ex2_approx(-w0), a1 = ex2_approx(-w1);
-    g.a = f2(a0, a1);
-    g.t = mul2(g.rho, rate2);
-    uint64_t s = fma2(g.t, f2(-0.0009125453652814031f), f2(0.00783736351877451f));
-    s = fma2(g.t, s, f2(-0.04141876474022865f));
-    s = fma2(g.t, s, f2(0.16660967469215393f));
-    s = fma2(g.t, s, f2(-0.4999951720237732f));
-    s = fma2(g.t, s, f2(0.9999999403953552f));
-    g.beta2 = fma2(g.t, s, f2(FAST ? 1.2e-38f : 0.f));
-    un2(g.beta2, b0, b1);
+};
+struct Gates2 {
+    uint64_t a, f, rho, iota, t;
+};
+template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, const Rate2 &k) {
+    Gates2 o;
+    const uint64_t one = f2(1.f), u = add2(exp_minus<T>(r), one), v = add2(exp_minus<T>(i), one);
+    uint64_t z;  // sqrt(rho) iota
+    float x0, x1;
     if constexpr (FAST) {
-        g.rbeta = f2(rsqrt_approx(b0), rsqrt_approx(b1));
+        const uint64_t uv = mul2(u, v);
+        un2(mul2(uv, v), x0, x1);
+        z = f2(rsqrt_approx(x0), rsqrt_approx(x1));
+        const uint64_t m = mul2(z, v);
+        o.rho = mul2(m, m);
+        if (GRAD) o.iota = mul2(mul2(z, z), uv);
     } else {
-        float t0, t1;
-        un2(g.t, t0, t1);
-        b0 = t0 < 1.f ? b0 : fmaf(-a0, a0, 1.f);
-        b1 = t1 < 1.f ? b1 : fmaf(-a1, a1, 1.f);
-        g.beta2 = f2(b0, b1);
-        g.rbeta = f2(rsqrt_approx(fmaxf(b0, 1e-37f)), rsqrt_approx(fmaxf(b1, 1e-37f)));
+        un2(u, x0, x1);
+        const uint64_t m = f2(rsqrt_approx(x0), rsqrt_approx(x1));
+        un2(v, x0, x1);
+        o.iota = f2(rcp_approx(x0), rcp_approx(x1));
+        o.rho = mul2(m, m), z = mul2(m, o.iota);
+    }
+    un2(mul2(o.rho, k.log2), x0, x1);
+    const float a0 = ex2_approx(-x0), a1 = ex2_approx(-x1);
+    o.a = f2(a0, a1);
+    o.t = mul2(o.rho, k.twice);
+    uint64_t q = fma2(o.t, f2(0.0006950617535039783f), f2(-0.007676176261156797f));
+    q = fma2(o.t, q, f2(0.052035510540008545f));
+    q = fma2(o.t, q, f2(-0.24999406933784485f));
+    q = fma2(o.t, q, f2(0.9999998807907104f));
+    o.f = mul2(mul2(z, k.root), q);
+    if constexpr (!FAST) {  // t >= 1: 1 - a^2 from a^2 <= 0.37
+        float t0, t1, i0, i1, f0, f1;
+        un2(o.t, t0, t1);
+        un2(o.iota, i0, i1);
+        un2(o.f, f0, f1);
+        const float b0 = fmaf(-a0, a0, 1.f), b1 = fmaf(-a1, a1, 1.f);
+        if (!(t0 < 1.f)) f0 = b0 * rsqrt_approx(b0) * i0;
+        if (!(t1 < 1.f)) f1 = b1 * rsqrt_approx(b1) * i1;
+        o.f = f2(f0, f1);
+    }
+    return o;
+}
+// G(t); `steep`: where t may be 1 and more.
+__device__ __forceinline__ uint64_t grad_ratio(uint64_t t, uint64_t a, bool steep) {
+    uint64_t g = fma2(t, f2(-0.0006299343658611178f), f2(-7.389252277789637e-05f));
+    g = fma2(t, g, f2(0.04169579595327377f));
+    g = fma2(t, g, f2(-0.25000378489494324f));
+    g = fma2(t, g, f2(0.5000000596046448f));
+    if (steep) {
+        float t0, t1, a0, a1, g0, g1;
+        un2(t, t0, t1);
+        un2(a, a0, a1);
+        un2(g, g0, g1);
+        if (!(t0 < 1.f)) g0 = a0 * a0 * 0.5f * t0 * rcp_approx(fmaf(-a0, a0, 1.f));
+        if (!(t1 < 1.f)) g1 = a1 * a1 * 0.5f * t1 * rcp_approx(fmaf(-a1, a1, 1.f));
+        g = f2(g0, g1);
     }
     return g;
 }
@@ -156,24 +181,6 @@ __device__ __forceinline__ void lower(Raw<__nv_bfloat16, 2> &m, const Raw<__nv_b
 }
 template <typename T> __device__ __forceinline__ bool is_low(const Raw<T, 2> &m) {
     return to_f32(m.v[0]) < kLowGate || to_f32(m.v[1]) < kLowGate;
-}
-
-// The gates of one channel, each step as above.
-struct Gates {
-    float rho, iota, w, a, beta2, rbeta;
-};
-template <typename T> __device__ __forceinline__ Gates gates(float r, float i, float k) {
-    const Gates2 g = gates2<T, false>(f2(r), f2(i), f2(2.f * k), f2(k * kLog2e));
-    Gates o;
-    float other;
-    un2(g.rho, o.rho, other);
-    un2(g.iota, o.iota, other);
-    un2(g.t, o.w, other);
-    o.w *= 0.5f;
-    un2(g.a, o.a, other);
-    un2(g.beta2, o.beta2, other);
-    un2(g.rbeta, o.rbeta, other);
-    return o;
 }
 
 // 8 bits: the values of a group are whole numbers times 2^e, e the least with max |x| <= 127 2^e and e >= -127, kept as the
