@@ -100,10 +100,10 @@ template <typename T> __device__ __forceinline__ uint64_t exp_minus(uint64_t x) 
 // 1 - exp(-t) is t times a smooth function, so its root is sqrt(2 k rho) Q(t) and there is neither a difference that cancels nor a
 // root of its own to take: rho is the square of 1 / sqrt(1 + e^-r). Q(t) = sqrt((1 - e^-t) / t) and g = G(t), t / (e^t - 1) / 2, for
 // t < 1 as polynomials of degree 4 through their Chebyshev points on [0, 1] (1.8e-7 and 4.4e-7 off at most).
-// FAST, for what nearly every run of tokens is: all r and i above kLowGate and k below kSteep. Then t < 1, and one reciprocal root
-// gives sqrt(rho) iota = 1 / sqrt((1 + e^-r) (1 + e^-i)^2), whose argument is finite: four calls of the special function unit a
-// token and channel, which with six of them is what bounds the kernels.
-constexpr float kLowGate = -29.f, kSteep = 0.5f;
+// FAST, for what nearly every run of tokens is: k below kSteep, so that t < 1, and r and i (r + 2 i above -88 or so) such that the
+// argument of one reciprocal root, sqrt(rho) iota = 1 / sqrt((1 + e^-r) (1 + e^-i)^2), is finite: `sum` adds them up and tells.
+// Four calls of the special function unit a token and channel instead of six.
+constexpr float kSteep = 0.5f;
 struct Rate2 {  // of two channels: 2 k, k log2(e), sqrt(2 k)
     uint64_t twice, log2, root;
     __device__ __forceinline__ static Rate2 of(float k0, float k1) {
@@ -113,14 +113,15 @@ struct Rate2 {  // of two channels: 2 k, k log2(e), sqrt(2 k)
 struct Gates2 {
     uint64_t a, f, rho, iota, t;
 };
-template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, const Rate2 &k) {
+template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, const Rate2 &k, uint64_t &sum) {
     Gates2 o;
     const uint64_t one = f2(1.f), u = add2(exp_minus<T>(r), one), v = add2(exp_minus<T>(i), one);
     uint64_t z;  // sqrt(rho) iota
     float x0, x1;
     if constexpr (FAST) {
-        const uint64_t uv = mul2(u, v);
-        un2(mul2(uv, v), x0, x1);
+        const uint64_t uv = mul2(u, v), uvv = mul2(uv, v);
+        sum = add2(sum, uvv);
+        un2(uvv, x0, x1);
         z = f2(rsqrt_approx(x0), rsqrt_approx(x1));
         const uint64_t m = mul2(z, v);
         o.rho = mul2(m, m);
@@ -153,6 +154,12 @@ template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 ga
     }
     return o;
 }
+// Whether the sum of gates2's arguments says that one of them was not finite.
+__device__ __forceinline__ bool is_low(uint64_t sum, bool one, bool both) {
+    float s0, s1;
+    un2(sum, s0, s1);
+    return (one && !(s0 < 3.4e38f)) || (both && !(s1 < 3.4e38f));
+}
 // G(t); `steep`: where t may be 1 and more.
 __device__ __forceinline__ uint64_t grad_ratio(uint64_t t, uint64_t a, bool steep) {
     uint64_t g = fma2(t, f2(-0.0006299343658611178f), f2(-7.389252277789637e-05f));
@@ -170,19 +177,6 @@ __device__ __forceinline__ uint64_t grad_ratio(uint64_t t, uint64_t a, bool stee
     }
     return g;
 }
-// The lesser of the gates seen, to tell whether they are all above kLowGate.
-__device__ __forceinline__ void lower(Raw<float, 2> &m, const Raw<float, 2> &g) {
-    m.v[0] = fminf(m.v[0], g.v[0]), m.v[1] = fminf(m.v[1], g.v[1]);
-}
-__device__ __forceinline__ void lower(Raw<__nv_bfloat16, 2> &m, const Raw<__nv_bfloat16, 2> &g) {
-    uint32_t r;
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m.word), "r"(g.word));
-    m.word = r;
-}
-template <typename T> __device__ __forceinline__ bool is_low(const Raw<T, 2> &m) {
-    return to_f32(m.v[0]) < kLowGate || to_f32(m.v[1]) < kLowGate;
-}
-
 // 8 bits: the values of a group are whole numbers times 2^e, e the least with max |x| <= 127 2^e and e >= -127, kept as the
 // byte e + 127. Every step is exact but the rounding to a whole number. 255 marks a group that held a NaN or an infinity.
 // `top` is the largest |x| of the group as bits, which order like the numbers, NaN above infinity.

@@ -25,6 +25,10 @@ bool tma_map_tokens_f32(CUtensorMap *out, const void *base, int64_t inner, int64
 bool tma_map_heads(CUtensorMap *out, const void *base, int64_t inner, int64_t heads, int64_t L, int64_t B, int box_cols,
                    int box_rows, bool swizzle128);
 
+// View of a [B, L, inner] tensor of 1-, 2- (bf16) or 4-byte (float32) elements whose rows are multiples of 16 bytes, box
+// (box_cols, box_rows, 1), rows one behind the other. What lies outside reads as zero and is not written. Encoded anew on each call.
+bool tma_map_rows(CUtensorMap *out, const void *base, int size, int64_t inner, int64_t L, int64_t B, int box_cols, int box_rows);
+
 // Major compute capability of the current device (cached per device), -1 if unknown.
 int device_cc_major_cached();
 
