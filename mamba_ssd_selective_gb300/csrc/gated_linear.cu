@@ -389,8 +389,6 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
                     leave_in_8_bits<T, WIDE>(p, maps, z, pair, sh.q[WIDE ? z * kState + warp * R : 0], s, t0, live, rows, lane);
         }
         __syncthreads();
-        bring(step + 1);
-        if (threadIdx.x == 0) sh.step[(step + 2) & 3] = walk.next(p);
         // the block's runs before this one, and all of them: every warp joins them, and sends to other blocks
         Run2 before = nothing(), all = nothing();
 #pragma unroll
@@ -399,6 +397,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
             if (w < warps) all = after(all, sh.run[step & 1][w][lane]);
         }
         exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
+        bring(step + 1);  // behind the sending, which the others wait for
+        if (threadIdx.x == 0) sh.step[(step + 2) & 3] = walk.next(p);
         uint64_t e = after(before, exchange_receive(sh.exchange, step, rank, blocks, lane, alive, carry));  // the state that enters this run
         if (warp == 0 && rows > 0 && p.states)
             store_pair<float, WIDE>(p.states + (s.b * ((L + kState - 1) / kState) + t0 / kState) * D + s.c0 + 2 * lane, rounded<float>(e), one, both);
@@ -646,8 +646,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
             if (lane == 0) tc::bulk_wait_read_all();
         }
         __syncthreads();
-        bring(step + 1);
-        if (threadIdx.x == 0) sh.step[(step + 2) & 3] = walk.next(p.f);
         Run2 before = nothing(), all = nothing();
 #pragma unroll 4
         for (int w = 0; w < warps; ++w) {
@@ -655,6 +653,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
             all = after(all, sh.run[step & 1][w][lane]);
         }
         exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
+        bring(step + 1);  // behind the sending, which the others wait for
+        if (threadIdx.x == 0) sh.step[(step + 2) & 3] = walk.next(p.f);
         // h over the earlier runs (the later warps') to this one; then b becomes what multiplies dh in psi, and rho 1 - rho
         for (int w = warps - 1; w > warp; --w) h = fma2(sh.run[step & 1][w][lane].a, h, sh.h[step & 1][w][lane]);
 #pragma unroll
