@@ -274,7 +274,7 @@ __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const FwdMa
 template <typename T, bool WIDE, bool PACK>
 __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear_fwd_kernel(LinearArgs p, const __grid_constant__ FwdMaps maps) {
     namespace cg = cooperative_groups;
-    pdl_enter();
+    pdl_wait();
     constexpr int R = kFwdRun, PITCH = Row<T, WIDE>::kPitch;
     extern __shared__ __align__(128) unsigned char raw_smem[];
     FwdShared<T, WIDE, PACK> &sh = *reinterpret_cast<FwdShared<T, WIDE, PACK> *>(raw_smem);
@@ -473,7 +473,7 @@ __device__ __forceinline__ uint64_t from_8(uint32_t two, uint64_t scale) {
 template <typename T, bool WIDE, bool PACK>
 __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear_bwd_kernel(LinearBwdArgs p, const __grid_constant__ BwdMaps maps) {
     namespace cg = cooperative_groups;
-    pdl_enter();
+    pdl_wait();
     constexpr int R = kBwdRun, PITCH = BwdShared<T, WIDE, PACK>::kPitch, DY = Row<T, WIDE>::kPitch, SC = Row<uint8_t, WIDE>::kPitch;
     extern __shared__ __align__(128) unsigned char raw_smem[];
     BwdShared<T, WIDE, PACK> &sh = *reinterpret_cast<BwdShared<T, WIDE, PACK> *>(raw_smem);
@@ -838,8 +838,12 @@ template <auto KERN> cudaError_t clusters_at_once(int blocks, int threads, size_
     return e;
 }
 
-// Launches KERN, `warps` warps a block for kState tokens, over `items` sequences and tiles of L tokens. The cluster's size: the
-// one whose waves times steps are fewest, a step of a cluster counted a tenth dearer than one of a single block for the meeting.
+// Launches KERN over `items` sequences and tiles of L tokens, a run of `run` tokens a warp. The cluster's size: the one whose waves
+// times steps cost least, where a block more in the cluster makes a step 4 % dearer (a step of the forward at B8 L2048 D5120 takes
+// 2.7 us with 2 blocks, 3.05 with 4, 3.4 with 8, 3.7 with 12; of the backward at B4 3.7, 3.95, 4.8 and 5.0).
+// A grid that fills the device is not launched as a programmatic dependent: placed while the kernel before it drains, clusters
+// find holes that no other cluster fits, and the last of them wait for the first (forward 142 us rather than 124, backward 215 rather
+// than 174). One that leaves half of the device free is.
 template <auto KERN, typename Args, typename Maps>
 cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int64_t L, int run, size_t smem, cudaStream_t stream, int *blocks_taken) {
     const int warps = (int)imin<int64_t>(kState / run, (L + run - 1) / run);  // no more than have a token
@@ -851,7 +855,7 @@ cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int6
         cudaError_t e = clusters_at_once<KERN>(blocks, 32 * (kState / run), smem, &count);
         if (e != cudaSuccess) return e;
         if (count < 1) continue;
-        const double c = (double)((items + count - 1) / count) * (double)((need + blocks - 1) / blocks) * (blocks > 1 ? 1.1 : 1.0);
+        const double c = (double)((items + count - 1) / count) * (double)((need + blocks - 1) / blocks) * (1.0 + 0.04 * blocks);
         if (blocks == 1 || c < cost) best = blocks, held = count, cost = c;
     }
     if (blocks_taken) *blocks_taken = best;
@@ -862,7 +866,7 @@ cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int6
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(imin<int64_t>(items, held) * best)), cfg.blockDim = dim3((unsigned)(32 * warps));
-    cfg.dynamicSmemBytes = smem, cfg.stream = stream, cfg.attrs = attr, cfg.numAttrs = 2;
+    cfg.dynamicSmemBytes = smem, cfg.stream = stream, cfg.attrs = attr, cfg.numAttrs = 2 * items <= held ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, KERN, a, maps);
 }
 
