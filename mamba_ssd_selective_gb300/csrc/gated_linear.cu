@@ -114,28 +114,31 @@ __device__ __forceinline__ uint64_t after(const Run2 &x, uint64_t h) { return fm
 __device__ __forceinline__ Run2 after(const Run2 &x, const Run2 &y) { return {mul2(x.a, y.a), fma2(y.a, x.h, y.h)}; }  // x, then y
 __device__ __forceinline__ Run2 nothing() { return {f2(1.f), 0}; }
 
-// A step of a cluster: the tile of a sequence that it is at. The first thread works it out two steps ahead, while it would wait.
-struct Step {
-    int64_t base;   // of the step's first token and the tile's first channel in [B, L, D]
-    int32_t b;
-    int32_t first;  // token
-    int32_t len;    // tokens of the sequence
-    int32_t c0;
-    int32_t cols;   // channels of the tile; 0: no more work
-    int32_t begins, ends;  // its sequence
+// A step of a block: the tile and the tokens of a sequence that it is at. A thread works it out two steps ahead.
+struct alignas(16) Step {
+    int64_t base;          // of the block's first token and the tile's first channel in [B, L, D]
+    int32_t b, t0;         // sequence; the block's first token (below 0: it has none)
+    int32_t live, rows;    // of the block's kState tokens, those that count and those that exist
+    int32_t c0, cols;      // the tile's first channel, its channels; 0: no more work
+    int32_t begins, ends;  // whether the cluster begins, ends the sequence and tile
 };
 struct Walk {
     uint32_t item, items, tiles, clusters;
-    int64_t first;
+    int64_t first;            // token of the cluster
     int64_t start, stop, by;  // a sequence's steps: from token `start` by `by` until past `stop`
+    int ours;                 // the block's first token from the cluster's
     __device__ __forceinline__ Step next(const LinearArgs &p) {
         Step s{};
         if (item >= items) return s;
         const uint32_t b = item / tiles;
-        s.b = (int32_t)b, s.c0 = (int32_t)(item - b * tiles) * kTile, s.first = (int32_t)first;
+        const int64_t t0 = first + ours;
+        s.b = (int32_t)b, s.t0 = (int32_t)t0, s.c0 = (int32_t)(item - b * tiles) * kTile;
         s.cols = (int32_t)imin<int64_t>(kTile, p.D - s.c0);
-        s.len = (int32_t)seq_len(p.seqlens, b, p.L);
-        s.base = (b * p.L + first) * p.D + s.c0;
+        s.base = (b * p.L + t0) * p.D + s.c0;
+        if (t0 >= 0) {
+            s.live = (int32_t)imin<int64_t>(kState, imax<int64_t>(0, seq_len(p.seqlens, b, p.L) - t0));
+            s.rows = (int32_t)imin<int64_t>(kState, imax<int64_t>(0, p.L - t0));
+        }
         s.begins = first == start;
         first += by;
         s.ends = by > 0 ? first >= stop : first <= stop;
@@ -143,10 +146,8 @@ struct Walk {
         return s;
     }
 };
-// Tokens of a run of R from t0 on that are in [0, end).
-__device__ __forceinline__ int run_of(int R, int64_t end, int64_t t0) {
-    return t0 < 0 ? 0 : (int)imax<int64_t>(0, imin<int64_t>(R, end - t0));
-}
+// Of n tokens, those in the run of R from `place` on.
+__device__ __forceinline__ int run_of(int R, int n, int place) { return max(0, min(R, n - place)); }
 
 // The blocks of a cluster exchange a Run2 a lane: each sends its own to all of them, and the bytes count down the receiver's
 // barrier. Two of each, taken in turn: a block sends for a step once all of its warps have read the one before.
@@ -221,6 +222,7 @@ template <typename T, bool WIDE, bool PACK> struct alignas(128) FwdShared {
     Run2 run[2][kFwdWarps][32];  // in turn: a warp may be at its next run while another reads these
     Exchange exchange;
     Step step[4];
+    Walk walk;  // the planner's alone: out of the registers of all
     uint64_t tiles;
 };
 struct FwdMaps {
@@ -230,11 +232,12 @@ struct FwdMaps {
 
 // A run's values in 8 bits: z is 0 for x, 1 for r, 2 for i, and `row` the run's first row of them.
 template <typename T, bool WIDE, typename F>
-__device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const FwdMaps &maps, int z, const F &pair, unsigned char *out, const Step &s, int64_t t0,
+__device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const FwdMaps &maps, int z, const F &pair, unsigned char *out, const Step &s, int place,
                                                 int live, int rows, int lane) {
     constexpr int R = kFwdRun;
     const int64_t D = p.D;
-    int8_t *values = p.values + (z * p.B * p.L + t0 - s.first) * D + s.base;
+    const int t0 = s.t0 + place;
+    int8_t *values = p.values + (z * p.B * p.L + place) * D + s.base;
     const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
     Raw<T, 2> w[R];
 #pragma unroll
@@ -267,7 +270,7 @@ __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const FwdMa
     if constexpr (WIDE) {
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::tma_store_3d(&maps.q, out, s.c0, (int)t0, (int)(z * p.B) + s.b);
+        if (lane == 0) tc::tma_store_3d(&maps.q, out, s.c0, t0, (int)(z * p.B) + s.b);
     }
 }
 
@@ -282,29 +285,30 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
     const int64_t D = p.D, L = p.L;
-    const int mine = rank * kState + warp * R;  // of this warp's run, from the step's first token
-    Walk walk{};
-    if (threadIdx.x == 0) {
+    const int place = warp * R;  // of this warp's run, from the block's first token
+    const bool planner = threadIdx.x == 32 * (warps - 1);
+    if (planner) {
+        Walk walk{};
         walk.tiles = (uint32_t)((D + kTile - 1) / kTile), walk.items = (uint32_t)p.B * walk.tiles;  // below 2^31
         walk.item = blockIdx.x / (uint32_t)blocks, walk.clusters = gridDim.x / (uint32_t)blocks;
-        walk.stop = L, walk.by = blocks * kState;
+        walk.stop = L, walk.by = blocks * kState, walk.ours = rank * kState;
         sh.step[0] = walk.next(p), sh.step[1] = walk.next(p);
+        sh.walk = walk;
     }
     exchange_init(sh.exchange, &sh.tiles, blocks);
 
-    // whether the block waits for anything of a step
-    auto comes = [&](const Step &s) { return s.begins || s.len > (int64_t)s.first + rank * kState; };
+    // Has the next step's tiles brought, by one thread: the others of its warp, and the other warps, wait for the exchange.
     auto bring = [&](int step) {
-        const Step s = sh.step[step & 3];
         if constexpr (WIDE) {
-            if (threadIdx.x == 0 && s.cols > 0 && comes(s)) {
-                const bool live = s.len > (int64_t)s.first + rank * kState;
+            if (threadIdx.x != 0) return;
+            const Step s = sh.step[step & 3];
+            if (s.cols > 0 && (s.begins || s.live > 0)) {
                 const uint32_t some = s.cols * (uint32_t)sizeof(float);
-                tc::mbar_arrive_expect_tx(&sh.tiles, (live ? 3 * kState * PITCH : 0) + (s.begins ? (p.init ? 2 : 1) * some : 0));
-                if (live) {
-                    tc::tma_load_3d(sh.in[0], &maps.x, &sh.tiles, s.c0, s.first + rank * kState, s.b);
-                    tc::tma_load_3d(sh.in[1], &maps.r, &sh.tiles, s.c0, s.first + rank * kState, s.b);
-                    tc::tma_load_3d(sh.in[2], &maps.i, &sh.tiles, s.c0, s.first + rank * kState, s.b);
+                tc::mbar_arrive_expect_tx(&sh.tiles, (s.live > 0 ? 3 * kState * PITCH : 0) + (s.begins ? (p.init ? 2 : 1) * some : 0));
+                if (s.live > 0) {
+                    tc::tma_load_3d(sh.in[0], &maps.x, &sh.tiles, s.c0, s.t0, s.b);
+                    tc::tma_load_3d(sh.in[1], &maps.r, &sh.tiles, s.c0, s.t0, s.b);
+                    tc::tma_load_3d(sh.in[2], &maps.i, &sh.tiles, s.c0, s.t0, s.b);
                 }
                 if (s.begins) {
                     tc::bulk_load(sh.lam, p.lam + s.c0, some, &sh.tiles);
@@ -312,11 +316,12 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
                 }
             }
         } else {
-            const int live = s.cols > 0 ? run_of(R, s.len, (int64_t)s.first + mine) : 0;
-            const int64_t at = s.base + mine * D;
-            fetch_rows<T, PITCH>(sh.in[0][warp * R], (const T *)p.x + at, live, s.cols, D, lane);
-            fetch_rows<T, PITCH>(sh.in[1][warp * R], (const T *)p.r + at, live, s.cols, D, lane);
-            fetch_rows<T, PITCH>(sh.in[2][warp * R], (const T *)p.i + at, live, s.cols, D, lane);
+            const Step s = sh.step[step & 3];
+            const int live = s.cols > 0 ? run_of(R, s.live, place) : 0;
+            const int64_t at = s.base + place * D;
+            fetch_rows<T, PITCH>(sh.in[0][place], (const T *)p.x + at, live, s.cols, D, lane);
+            fetch_rows<T, PITCH>(sh.in[1][place], (const T *)p.r + at, live, s.cols, D, lane);
+            fetch_rows<T, PITCH>(sh.in[2][place], (const T *)p.i + at, live, s.cols, D, lane);
             copy_commit();
         }
     };
@@ -330,10 +335,11 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
         if (s.cols == 0) break;
         if (threadIdx.x == 0) exchange_expect(sh.exchange, step, blocks);
         const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
-        const int64_t t0 = (int64_t)s.first + mine, at = s.base + mine * D + 2 * lane;
-        const int live = run_of(R, s.len, t0), rows = run_of(R, L, t0);  // tokens that count, that exist
+        const int64_t at = s.base + place * D + 2 * lane;
+        const int live = run_of(R, s.live, place), rows = run_of(R, s.rows, place);  // tokens that count, that exist
+        const int t0 = s.t0 + place;                                                  // of the run, where it exists
         if constexpr (WIDE) {
-            if (comes(s)) alive = wait_for(&sh.tiles, parity, alive), parity ^= 1;
+            if (s.begins || s.live > 0) alive = wait_for(&sh.tiles, parity, alive), parity ^= 1;
         } else {
             copy_wait();
             __syncwarp();
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
         }
         auto pair = [&](int z, int t) {
             const void *base = z == 0 ? p.x : z == 1 ? p.r : p.i;
-            return row_pair<T, WIDE>(sh.in[z][warp * R + t], shift<T, WIDE>(base, at - 2 * lane + t * D), lane, both);
+            return row_pair<T, WIDE>(sh.in[z][place + t], shift<T, WIDE>(base, at - 2 * lane + t * D), lane, both);
         };
         uint64_t a[R], h[R];
         Run2 own;
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
             if (rows > 0)
 #pragma unroll
                 for (int z = 0; z < 3; ++z)
-                    leave_in_8_bits<T, WIDE>(p, maps, z, pair, sh.q[WIDE ? z * kState + warp * R : 0], s, t0, live, rows, lane);
+                    leave_in_8_bits<T, WIDE>(p, maps, z, pair, sh.q[WIDE ? z * kState + place : 0], s, place, live, rows, lane);
         }
         __syncthreads();
         // the block's runs before this one, and all of them: every warp joins them, and sends to other blocks
@@ -398,16 +404,16 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
         }
         exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
         bring(step + 1);  // behind the sending, which the others wait for
-        if (threadIdx.x == 0) sh.step[(step + 2) & 3] = walk.next(p);
+        if (planner) sh.step[(step + 2) & 3] = sh.walk.next(p);
         uint64_t e = after(before, exchange_receive(sh.exchange, step, rank, blocks, lane, alive, carry));  // the state that enters this run
         if (warp == 0 && rows > 0 && p.states)
-            store_pair<float, WIDE>(p.states + (s.b * ((L + kState - 1) / kState) + t0 / kState) * D + s.c0 + 2 * lane, rounded<float>(e), one, both);
+            store_pair<float, WIDE>(p.states + (s.b * ((L + kState - 1) / kState) + s.t0 / kState) * D + s.c0 + 2 * lane, rounded<float>(e), one, both);
         if (p.y && rows > 0) {
             auto results = [&](auto whole) {
 #pragma unroll
                 for (int t = 0; t < R; ++t) {
                     e = fma2(a[t], e, h[t]);
-                    put_pair<T, WIDE>(sh.y[WIDE ? warp * R + t : 0], (T *)p.y + at + t * D, rounded<T>(decltype(whole)::value || t < live ? e : 0), t < rows,
+                    put_pair<T, WIDE>(sh.y[WIDE ? place + t : 0], (T *)p.y + at + t * D, rounded<T>(decltype(whole)::value || t < live ? e : 0), t < rows,
                                       one, both, lane);
                 }
             };
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
             if constexpr (WIDE) {
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::tma_store_3d(&maps.y, sh.y[warp * R], s.c0, (int)t0, s.b);
+                if (lane == 0) tc::tma_store_3d(&maps.y, sh.y[place], s.c0, t0, s.b);
             }
         }
         if (WIDE && lane == 0) tc::bulk_commit();
@@ -455,6 +461,7 @@ template <typename T, bool WIDE, bool PACK> struct alignas(128) BwdShared {
     uint64_t h[2][kBwdWarps][32], sum[kBwdWarps][32];
     Exchange exchange;
     Step step[4];
+    Walk walk;  // the planner's alone: out of the registers of all
     uint64_t tiles;
 };
 struct BwdMaps {
@@ -482,59 +489,58 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
     const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
     const int64_t D = p.f.D, L = p.f.L, chunks = (L + kState - 1) / kState, groups = (L + kGroup - 1) / kGroup;
     const int64_t plane = p.f.B * L * D, scales = p.f.B * groups * D;
-    // The block's tokens and this warp's run, from the step's first token: rank 0 and warp 0 have the latest. A step begins a
-    // cluster's chunks before the one it came from, at the start of a sequence before its first token.
-    const int ours = (blocks - 1 - rank) * kState, place = (warps - 1 - warp) * R, mine = ours + place;
-    Walk walk{};
-    if (threadIdx.x == 0) {
+    // Rank 0 and warp 0 have the latest tokens. A step begins a cluster's chunks before the one it came from, at the start of a
+    // sequence before its first token.
+    const int place = (warps - 1 - warp) * R;  // of this warp's run, from the block's first token
+    const bool planner = threadIdx.x == 32 * (warps - 1);
+    if (planner) {
+        Walk walk{};
         walk.tiles = (uint32_t)((D + kTile - 1) / kTile), walk.items = (uint32_t)p.f.B * walk.tiles;  // below 2^31
         walk.item = blockIdx.x / (uint32_t)blocks, walk.clusters = gridDim.x / (uint32_t)blocks;
-        walk.by = -(int64_t)blocks * kState, walk.stop = walk.by;
+        walk.by = -(int64_t)blocks * kState, walk.stop = walk.by, walk.ours = (blocks - 1 - rank) * kState;
         walk.first = walk.start = (chunks - blocks) * kState;
         sh.step[0] = walk.next(p.f), sh.step[1] = walk.next(p.f);
+        sh.walk = walk;
     }
     exchange_init(sh.exchange, &sh.tiles, blocks);
 
-    auto there = [&](const Step &s) { return s.first + (int64_t)ours >= 0; };  // the block has tokens
-    auto lives = [&](const Step &s) { return there(s) && s.len > s.first + (int64_t)ours; };
-    auto comes = [&](const Step &s) { return s.begins || lives(s); };
+    // Has the next step's tiles brought: a warp each, as all of these instructions in one would keep the others waiting.
     auto bring = [&](int step) {
         const Step s = sh.step[step & 3];
-        const int t0 = s.first + ours;
         if constexpr (WIDE) {
-            if (threadIdx.x == 0 && s.cols > 0 && comes(s)) {
-                const bool live = lives(s);
+            if (lane == 0 && s.cols > 0 && (s.begins || s.live > 0)) {
                 const uint32_t some = s.cols * (uint32_t)sizeof(float);
-                tc::mbar_arrive_expect_tx(&sh.tiles, (live ? 3 * kState * PITCH + kState * DY + some + (PACK ? 3 * (kState / kGroup) * SC : 0) : 0) +
-                                                         (s.begins ? (p.dfinal ? 2 : 1) * some : 0));
-                if (live) {
-                    if constexpr (PACK) {
-                        for (int z = 0; z < 3; ++z) {
-                            tc::tma_load_3d(sh.in[z], &maps.q, &sh.tiles, s.c0, t0, z * (int)p.f.B + s.b);
-                            tc::tma_load_3d(sh.scale[z], &maps.scale, &sh.tiles, s.c0, t0 / kGroup, z * (int)p.f.B + s.b);
+                for (int job = warp; job < 6; job += warps) {
+                    if (job == 0)
+                        tc::mbar_arrive_expect_tx(&sh.tiles, (s.live > 0 ? 3 * kState * PITCH + kState * DY + some + (PACK ? 3 * (kState / kGroup) * SC : 0) : 0) +
+                                                                 (s.begins ? (p.dfinal ? 2 : 1) * some : 0));
+                    if (s.live > 0) {
+                        if (job < 3) {
+                            if constexpr (PACK) {
+                                tc::tma_load_3d(sh.in[job], &maps.q, &sh.tiles, s.c0, s.t0, job * (int)p.f.B + s.b);
+                                tc::tma_load_3d(sh.scale[job], &maps.scale, &sh.tiles, s.c0, s.t0 / kGroup, job * (int)p.f.B + s.b);
+                            } else {
+                                tc::tma_load_3d(sh.in[job], job == 0 ? &maps.x : job == 1 ? &maps.r : &maps.i, &sh.tiles, s.c0, s.t0, s.b);
+                            }
                         }
-                    } else {
-                        tc::tma_load_3d(sh.in[0], &maps.x, &sh.tiles, s.c0, t0, s.b);
-                        tc::tma_load_3d(sh.in[1], &maps.r, &sh.tiles, s.c0, t0, s.b);
-                        tc::tma_load_3d(sh.in[2], &maps.i, &sh.tiles, s.c0, t0, s.b);
+                        if (job == 3) tc::tma_load_3d(sh.dy[step & 1], &maps.dy, &sh.tiles, s.c0, s.t0, s.b);
+                        if (job == 4) tc::bulk_load(sh.state, p.f.states + (s.b * chunks + s.t0 / kState) * D + s.c0, some, &sh.tiles);
                     }
-                    tc::tma_load_3d(sh.dy[step & 1], &maps.dy, &sh.tiles, s.c0, t0, s.b);
-                    tc::bulk_load(sh.state, p.f.states + (s.b * chunks + t0 / kState) * D + s.c0, some, &sh.tiles);
-                }
-                if (s.begins) {
-                    tc::bulk_load(sh.lam, p.f.lam + s.c0, some, &sh.tiles);
-                    if (p.dfinal) tc::bulk_load(sh.last, p.dfinal + s.b * D + s.c0, some, &sh.tiles);
+                    if (job == 5 && s.begins) {
+                        tc::bulk_load(sh.lam, p.f.lam + s.c0, some, &sh.tiles);
+                        if (p.dfinal) tc::bulk_load(sh.last, p.dfinal + s.b * D + s.c0, some, &sh.tiles);
+                    }
                 }
             }
         } else {
-            const int live = s.cols > 0 ? run_of(R, s.len, (int64_t)s.first + mine) : 0;
-            const int64_t at = s.base + mine * D;
+            const int live = s.cols > 0 ? run_of(R, s.live, place) : 0;
+            const int64_t at = s.base + place * D;
             if (live > 0) {
                 if constexpr (PACK) {
                     for (int z = 0; z < 3; ++z) {
                         fetch_rows<int8_t, PITCH>(sh.in[z][place], p.f.values + z * plane + at, live, s.cols, D, lane);
                         if (place % kGroup == 0)  // one of a group's two runs brings its scale
-                            fetch_rows<uint8_t, SC>(sh.scale[z][place / kGroup], p.f.scales + z * scales + (s.b * groups + (t0 + place) / kGroup) * D + s.c0, 1,
+                            fetch_rows<uint8_t, SC>(sh.scale[z][place / kGroup], p.f.scales + z * scales + (s.b * groups + (s.t0 + place) / kGroup) * D + s.c0, 1,
                                                     s.cols, D, lane);
                     }
                 } else {
@@ -557,10 +563,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
         if (s.cols == 0) break;
         if (threadIdx.x == 0) exchange_expect(sh.exchange, step, blocks);
         const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
-        const int64_t t0 = (int64_t)s.first + mine, at = s.base + mine * D + 2 * lane;
-        const int live = run_of(R, s.len, t0), rows = run_of(R, L, t0);  // tokens that count, that exist
+        const int64_t at = s.base + place * D + 2 * lane;
+        const int live = run_of(R, s.live, place), rows = run_of(R, s.rows, place);  // tokens that count, that exist
+        const int t0 = s.t0 + place;                                                  // of the run, where it exists
         if constexpr (WIDE) {
-            if (comes(s)) alive = wait_for(&sh.tiles, parity, alive), parity ^= 1;
+            if (s.begins || s.live > 0) alive = wait_for(&sh.tiles, parity, alive), parity ^= 1;
         } else {
             copy_wait();
             if (PACK) __syncthreads(); else __syncwarp();  // scales are shared by two warps
@@ -581,11 +588,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
             steep = __any_sync(0xffffffffu, (one && !(k0 < kSteep)) || (both && !(k1 < kSteep)));
         }
         uint64_t h = 0;  // the state that enters the block's tokens
-        if (lives(s)) {
+        if (s.live > 0) {
             if constexpr (WIDE) {
                 h = f2(sh.state[2 * lane], sh.state[2 * lane + 1]);
             } else {
-                const float *state = p.f.states + (s.b * chunks + (s.first + ours) / kState) * D + c;
+                const float *state = p.f.states + (s.b * chunks + s.t0 / kState) * D + c;
                 h = f2(one ? state[0] : 0.f, both ? state[1] : 0.f);
             }
         }
@@ -654,8 +661,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
         }
         exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
         bring(step + 1);  // behind the sending, which the others wait for
-        if (threadIdx.x == 0) sh.step[(step + 2) & 3] = walk.next(p.f);
+        if (planner) sh.step[(step + 2) & 3] = sh.walk.next(p.f);
         // h over the earlier runs (the later warps') to this one; then b becomes what multiplies dh in psi, and rho 1 - rho
+#pragma unroll 4
         for (int w = warps - 1; w > warp; --w) h = fma2(sh.run[step & 1][w][lane].a, h, sh.h[step & 1][w][lane]);
 #pragma unroll
         for (int t = 0; t < R; ++t) {
@@ -686,9 +694,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tc::tma_store_3d(&maps.dx, sh.out[place], s.c0, (int)t0, s.b);
-                    tc::tma_store_3d(&maps.dr, sh.out[kState + place], s.c0, (int)t0, s.b);
-                    tc::tma_store_3d(&maps.di, sh.out[2 * kState + place], s.c0, (int)t0, s.b);
+                    tc::tma_store_3d(&maps.dx, sh.out[place], s.c0, t0, s.b);
+                    tc::tma_store_3d(&maps.dr, sh.out[kState + place], s.c0, t0, s.b);
+                    tc::tma_store_3d(&maps.di, sh.out[2 * kState + place], s.c0, t0, s.b);
                     tc::bulk_commit();
                 }
             }
