@@ -800,12 +800,18 @@ def _given(**tensors):
 
 def _linear_tokens(x, r, i, lam):
     """Checks the token tensors and weights of a gated-linear call; returns x's shape."""
-    _given(r=r, i=i, lam=lam)
-    _need(x, "x", x.shape, x.dtype, x.device)
-    _need(r, "r", x.shape, x.dtype, x.device)
-    _need(i, "i", x.shape, x.dtype, x.device)
-    _need(lam, "lam", x.shape[-1:], torch.float32, x.device)
-    return x.shape
+    shape, io, dev = x.shape, x.dtype, x.device
+    if (isinstance(r, torch.Tensor) and isinstance(i, torch.Tensor) and isinstance(lam, torch.Tensor)
+            and shape == r.shape == i.shape and lam.shape == shape[-1:] and io is r.dtype is i.dtype
+            and lam.dtype is torch.float32 and dev == r.device == i.device == lam.device
+            and x.is_contiguous() and r.is_contiguous() and i.is_contiguous() and lam.is_contiguous()):
+        return shape
+    _given(r=r, i=i, lam=lam)  # one of these says what is wrong
+    _need(x, "x", shape, io, dev)
+    _need(r, "r", shape, io, dev)
+    _need(i, "i", shape, io, dev)
+    _need(lam, "lam", shape[-1:], torch.float32, dev)
+    return shape
 
 
 def gated_linear_checkpoint(x, packed=True):
@@ -870,9 +876,12 @@ def _linear_grads(dy, lam, dfinal_state, states, seqlens, want_dinit):
     dev = dy.device
     _given(lam=lam)
     _need(lam, "lam", (D,), torch.float32, dev)
-    _need(dfinal_state, "dfinal_state", (Bsz, D), torch.float32, dev)
-    _need(states, "states", (Bsz, -(-L // 64), D), torch.float32, dev)
-    _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
+    if dfinal_state is not None:
+        _need(dfinal_state, "dfinal_state", (Bsz, D), torch.float32, dev)
+    if states is not None:
+        _need(states, "states", (Bsz, -(-L // 64), D), torch.float32, dev)
+    if seqlens is not None:
+        _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
     return dict(dx=torch.empty_like(dy), dr=torch.empty_like(dy), di=torch.empty_like(dy), dlam=torch.empty_like(lam),
                 dinit=torch.empty((Bsz, D), dtype=torch.float32, device=dev) if want_dinit else None)
 
@@ -962,19 +971,21 @@ def pack8(x, seqlens=None, values=None, scales=None, stream=None):
         return _run_on(stream, pack8, locals())
     if x.dim() < 3:
         raise ValueError("x must be [B, L, ...]")
-    Bsz, L = x.shape[:2]
-    rest, dev = tuple(x.shape[2:]), x.device
-    _need(x, "x", tuple(x.shape), x.dtype, dev)
-    _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
+    shape, dev = x.shape, x.device
+    Bsz, L = shape[:2]
+    groups = (Bsz, -(-L // 16), *shape[2:])
+    _need(x, "x", shape, x.dtype, dev)
+    if seqlens is not None:
+        _need(seqlens, "seqlens", (Bsz,), torch.int32, dev)
     if values is None:
-        values = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        values = torch.empty_like(x, dtype=torch.int8)
     else:
-        _need(values, "values", tuple(x.shape), torch.int8, dev)
+        _need(values, "values", shape, torch.int8, dev)
     if scales is None:
-        scales = torch.empty((Bsz, -(-L // 16), *rest), dtype=torch.uint8, device=dev)
+        scales = torch.empty(groups, dtype=torch.uint8, device=dev)
     else:
-        _need(scales, "scales", (Bsz, -(-L // 16), *rest), torch.uint8, dev)
-    _check(load().ssd_pack8(Bsz, L, math.prod(rest), _io_code(x.dtype), _ptr(x), _ptr(seqlens), _ptr(values),
+        _need(scales, "scales", groups, torch.uint8, dev)
+    _check(load().ssd_pack8(Bsz, L, math.prod(shape[2:]), _io_code(x.dtype), _ptr(x), _ptr(seqlens), _ptr(values),
                             _ptr(scales), _stream(stream, dev)))
     return values, scales
 
@@ -985,15 +996,16 @@ def unpack8(values, scales, dtype=torch.bfloat16, out=None, stream=None):
         return _run_on(stream, unpack8, locals())
     if values.dim() < 3:
         raise ValueError("values must be [B, L, ...]")
-    Bsz, L = values.shape[:2]
-    rest, dev = tuple(values.shape[2:]), values.device
+    shape, dev = values.shape, values.device
+    Bsz, L = shape[:2]
     _given(scales=scales)
-    _need(values, "values", tuple(values.shape), torch.int8, dev)
-    _need(scales, "scales", (Bsz, -(-L // 16), *rest), torch.uint8, dev)
+    _need(values, "values", shape, torch.int8, dev)
+    _need(scales, "scales", (Bsz, -(-L // 16), *shape[2:]), torch.uint8, dev)
+    io = _io_code(dtype)
     if out is None:
-        out = torch.empty(values.shape, dtype=dtype, device=dev)
+        out = torch.empty_like(values, dtype=dtype)
     else:
-        _need(out, "out", tuple(values.shape), dtype, dev)
-    _check(load().ssd_unpack8(Bsz, L, math.prod(rest), _io_code(dtype), _ptr(values), _ptr(scales), _ptr(out),
+        _need(out, "out", shape, dtype, dev)
+    _check(load().ssd_unpack8(Bsz, L, math.prod(shape[2:]), io, _ptr(values), _ptr(scales), _ptr(out),
                               _stream(stream, dev)))
     return out

@@ -17,6 +17,8 @@
 // sender wait for everything it has written (B8 L2048 D5120: 193 us so, 176 without).
 #include <cooperative_groups.h>
 
+#include <mutex>
+
 #include "gated_linear.cuh"
 #include "launch.h"
 #include "ssd_scan.h"
@@ -762,7 +764,7 @@ template <typename T, int V> __global__ void __launch_bounds__(256) linear_step_
 }
 
 // ------------------------------------------------------------------- 8 bits
-// A warp takes 32 V channels of one group of tokens.
+// A warp takes 32 V channels of one group of tokens, a lane 16 bytes of each row where rows are multiples of that. Bound by HBM.
 template <typename T, int V> __global__ void __launch_bounds__(32 * kPackWarps) pack8_kernel(Pack8Args p) {
     pdl_enter();
     const int64_t c0 = ((int64_t)blockIdx.y * 32 + (threadIdx.x & 31)) * V, b = blockIdx.z, D = p.D;
@@ -775,7 +777,8 @@ template <typename T, int V> __global__ void __launch_bounds__(32 * kPackWarps) 
 #pragma unroll
     for (int t = 0; t < kGroup; ++t)
         if (t < live) x[t] = load<T, V>((const T *)p.x + at + t * D);
-    To8 to8[V];
+    float inv[V];
+    uint32_t finite[V];
     Raw<uint8_t, V> code;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -783,14 +786,15 @@ template <typename T, int V> __global__ void __launch_bounds__(32 * kPackWarps) 
 #pragma unroll
         for (int t = 0; t < kGroup; ++t) top = max(top, abs_bits(to_f32(x[t].v[v])));
         code.v[v] = (uint8_t)scale_code(top);
-        to8[v] = To8(code.v[v]);
+        inv[v] = inverse_scale(code.v[v]);
+        finite[v] = code.v[v] == 255 ? 0u : 0xffu;
     }
     store<uint8_t, V>(p.scales + (b * groups + g) * D + c0, code);
 #pragma unroll
     for (int t = 0; t < kGroup; ++t) {
         Raw<int8_t, V> q;
 #pragma unroll
-        for (int v = 0; v < V; ++v) q.v[v] = to8[v](to_f32(x[t].v[v]));
+        for (int v = 0; v < V; ++v) q.v[v] = (int8_t)(__float_as_uint(fmaf(to_f32(x[t].v[v]), inv[v], kToWhole)) & finite[v]);
         if (t < rows) store<int8_t, V>(p.values + at + t * D, q);
     }
 }
@@ -807,11 +811,18 @@ template <typename T, int V> __global__ void __launch_bounds__(32 * kPackWarps) 
 #pragma unroll
     for (int t = 0; t < kGroup; ++t)
         if (t < rows) q[t] = load<int8_t, V>(p.values + at + t * D);
+    float scale[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) scale[v] = scale_of(code.v[v]);
 #pragma unroll
     for (int t = 0; t < kGroup; ++t) {
         float f[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) f[v] = (float)q[t].v[v] * scale_of(code.v[v]);
+        for (int v = 0; v < V; ++v) {
+            // byte v as 2^23 + 128 + v, less that: the conversion instruction takes four times as long
+            const uint32_t n = 0x4b000000u | ((uint32_t)(uint8_t)q[t].v[v] ^ 0x80u);
+            f[v] = (__uint_as_float(n) - 8388736.f) * scale[v];
+        }
         if (t < rows) store_f32<T, V>((T *)p.out + at + t * D, f);
     }
 }
@@ -823,26 +834,41 @@ template <typename F> cudaError_t for_width(int64_t D, F &&f) {
     if (D % 2 == 0) return f(std::integral_constant<int, 2>{});
     return f(std::integral_constant<int, 1>{});
 }
-unsigned tiles(int64_t D, int V) { return (unsigned)((D + 32 * V - 1) / (32 * V)); }
-// Clusters of `blocks` blocks of KERN that the device holds at once; asked of the driver once per device and size.
-template <auto KERN> cudaError_t clusters_at_once(int blocks, int threads, size_t smem, int *count) {
-    static std::atomic<int> known[64][kMaxCluster + 1];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::atomic<int> *slot = dev < 64 ? &known[dev][blocks] : nullptr;
-    if (slot && (*count = slot->load(std::memory_order_acquire)) > 0) return cudaSuccess;
-    e = allow_shared<KERN>(smem);
+// Clusters of 1 to kMaxCluster blocks of KERN that the current device holds at once (by index; 0: none), asked of the driver once per
+// device below 64 and else on every call.
+struct ClusterCounts {
+    int at_once[kMaxCluster + 1];
+};
+template <auto KERN> cudaError_t ask_clusters(int threads, size_t smem, ClusterCounts *c) {
+    cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)blocks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)blocks), cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem;
-    cfg.attrs = attr, cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(count, KERN, &cfg);
-    if (e == cudaSuccess && slot) slot->store(*count, std::memory_order_release);
+    for (int blocks = 1; blocks <= kMaxCluster && e == cudaSuccess; ++blocks) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)blocks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)blocks), cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr, cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&c->at_once[blocks], KERN, &cfg);
+    }
+    return e;
+}
+template <auto KERN> cudaError_t cluster_counts(int threads, size_t smem, ClusterCounts *c) {
+    static ClusterCounts known[64];
+    static DeviceOnce asked;
+    static std::mutex one;
+    int dev = 0;
+    cudaError_t e = cudaSuccess;
+    if (asked.pending(&dev, &e)) {
+        std::lock_guard<std::mutex> lock(one);
+        if (asked.pending(&dev, &e)) {
+            e = ask_clusters<KERN>(threads, smem, c);
+            if (e != cudaSuccess || dev < 0 || dev >= 64) return e;
+            known[dev] = *c;
+            asked.done(dev);
+        }
+    }
+    if (e == cudaSuccess) *c = known[dev];
     return e;
 }
 
@@ -856,12 +882,13 @@ template <auto KERN, typename Args, typename Maps>
 cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int64_t L, int run, size_t smem, cudaStream_t stream, int *blocks_taken) {
     const int warps = (int)imin<int64_t>(kState / run, (L + run - 1) / run);  // no more than have a token
     const int64_t need = (L + kState - 1) / kState;
+    ClusterCounts counts{};
+    cudaError_t e = cluster_counts<KERN>(32 * (kState / run), smem, &counts);
+    if (e != cudaSuccess) return e;
     int best = 1, held = 1;
     double cost = 0;
     for (int blocks = 1; blocks <= kMaxCluster && blocks <= need; ++blocks) {
-        int count = 0;
-        cudaError_t e = clusters_at_once<KERN>(blocks, 32 * (kState / run), smem, &count);
-        if (e != cudaSuccess) return e;
+        const int count = counts.at_once[blocks];
         if (count < 1) continue;
         const double c = (double)((items + count - 1) / count) * (double)((need + blocks - 1) / blocks) * (1.0 + 0.04 * blocks);
         if (blocks == 1 || c < cost) best = blocks, held = count, cost = c;
@@ -952,17 +979,20 @@ cudaError_t launch_linear_step(int io, const LinearStepArgs &a, cudaStream_t str
     });
 }
 
+namespace linear {
+template <typename T, int V> cudaError_t pack8_v(const Pack8Args &a, cudaStream_t stream) {
+    const int64_t groups = (a.L + kGroup - 1) / kGroup;
+    const dim3 grid((unsigned)((groups + kPackWarps - 1) / kPackWarps), (unsigned)((a.D + 32 * V - 1) / (32 * V)), (unsigned)a.B), block(32 * kPackWarps);
+    return a.out ? launch_programmatic(unpack8_kernel<T, V>, grid, block, 0, stream, a) : launch_programmatic(pack8_kernel<T, V>, grid, block, 0, stream, a);
+}
+template <typename T> cudaError_t pack8_t(const Pack8Args &a, cudaStream_t stream) {
+    constexpr int V = 16 / (int)sizeof(T);
+    return a.D % V == 0 ? pack8_v<T, V>(a, stream) : a.D % 2 == 0 ? pack8_v<T, 2>(a, stream) : pack8_v<T, 1>(a, stream);
+}
+}  // namespace linear
+
 cudaError_t launch_pack8(int io, const Pack8Args &a, cudaStream_t stream) {
-    return linear::for_width(a.D, [&](auto vw) {
-        constexpr int V = decltype(vw)::value;
-        const dim3 grid((unsigned)((a.L + linear::kGroup * linear::kPackWarps - 1) / (linear::kGroup * linear::kPackWarps)),
-                        linear::tiles(a.D, V), (unsigned)a.B), block(32 * linear::kPackWarps);
-        if (a.out)
-            return io == IO_BF16 ? launch_programmatic(linear::unpack8_kernel<__nv_bfloat16, V>, grid, block, 0, stream, a)
-                                 : launch_programmatic(linear::unpack8_kernel<float, V>, grid, block, 0, stream, a);
-        return io == IO_BF16 ? launch_programmatic(linear::pack8_kernel<__nv_bfloat16, V>, grid, block, 0, stream, a)
-                             : launch_programmatic(linear::pack8_kernel<float, V>, grid, block, 0, stream, a);
-    });
+    return io == IO_BF16 ? linear::pack8_t<__nv_bfloat16>(a, stream) : linear::pack8_t<float>(a, stream);
 }
 
 }  // namespace ssd

@@ -191,16 +191,8 @@ __device__ __forceinline__ float inverse_scale(uint32_t code) {  // 2^-e
     return code == 255u ? 0.f : __uint_as_float((254u - code) << 23);
 }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-// The whole number nearest to x 2^-e, as a byte: the sum with 1.5 2^23 has it in its last bits. 0 in a group that is not finite.
+// x 2^-e + 1.5 2^23 has the whole number nearest to x 2^-e in its last bits.
 constexpr float kToWhole = 12582912.f;
-struct To8 {
-    float inv;
-    uint32_t mask;
-    __device__ __forceinline__ explicit To8(uint32_t code = 0) : inv(inverse_scale(code)), mask(code == 255u ? 0u : 0xffu) {}
-    __device__ __forceinline__ int8_t operator()(float x) const {
-        return (int8_t)(__float_as_uint(fmaf(x, inv, kToWhole)) & mask);
-    }
-};
 
 }  // namespace linear
 }  // namespace ssd
