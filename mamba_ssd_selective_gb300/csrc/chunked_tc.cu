@@ -1171,6 +1171,16 @@ bool tma_map_rows(CUtensorMap *out, const void *base, int size, int64_t inner, i
                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_map_planes(CUtensorMap *out, const void *base, int64_t inner, int64_t L, int64_t B, int planes, int box_cols, int box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)L, (cuuint64_t)B, (cuuint64_t)planes};
+    const cuuint64_t strides[3] = {(cuuint64_t)inner, (cuuint64_t)(L * inner), (cuuint64_t)(B * L * inner)};
+    const cuuint32_t box[4] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1, (cuuint32_t)planes}, estr[4] = {1, 1, 1, 1};
+    return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_cc_major_cached() { return device_cc_major(); }
 
 int sm_count(int fallback) {

@@ -219,7 +219,7 @@ template <typename T, bool WIDE, bool PACK> struct alignas(128) FwdShared {
     static constexpr int kPitch = Row<T, WIDE>::kPitch;
     alignas(128) unsigned char in[3][kState][kPitch];  // x, r, i: brought anew once the block has its a and b
     alignas(128) unsigned char y[WIDE ? kState : 1][kTile * sizeof(T)];
-    alignas(128) unsigned char q[PACK && WIDE ? 3 * kState : 1][kTile];
+    alignas(128) unsigned char q[PACK && WIDE ? 3 * kState : 1][kTile];  // run by run: x, r, i
     alignas(16) float lam[kTile], init[kTile];
     Run2 run[2][kFwdWarps][32];  // in turn: a warp may be at its next run while another reads these
     Exchange exchange;
@@ -229,50 +229,48 @@ template <typename T, bool WIDE, bool PACK> struct alignas(128) FwdShared {
 };
 struct FwdMaps {
     CUtensorMap x, r, i;  // boxes of 64 x 64
-    CUtensorMap y, q;     // of a warp's run
+    CUtensorMap y, q;     // of a warp's run; q of all three in 8 bits
 };
 
-// A run's values in 8 bits: z is 0 for x, 1 for r, 2 for i, and `row` the run's first row of them.
-template <typename T, bool WIDE, typename F>
-__device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const FwdMaps &maps, int z, const F &pair, unsigned char *out, const Step &s, int place,
-                                                int live, int rows, int lane) {
+// A run's x, r and i (z 0, 1, 2) in 8 bits, to `out`, the run's place in FwdShared::q. ALL: every token of it counts.
+template <typename T, bool WIDE, bool ALL, typename F>
+__device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const F &pair, unsigned char (*out)[kTile], const Step &s, int place, int live, int rows,
+                                                int lane) {
     constexpr int R = kFwdRun;
     const int64_t D = p.D;
-    const int t0 = s.t0 + place;
-    int8_t *values = p.values + (z * p.B * p.L + place) * D + s.base;
     const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
-    Raw<T, 2> w[R];
 #pragma unroll
-    for (int t = 0; t < R; ++t) w[t] = pair(z, t);
-    uint32_t top0 = 0, top1 = 0;
-    if constexpr (sizeof(T) == 2) {
-        uint32_t top = 0;  // bf16 without its sign orders like a whole number: two at once
+    for (int z = 0; z < 3; ++z) {
+        Raw<T, 2> w[R];
 #pragma unroll
-        for (int t = 0; t < R; ++t)
-            if (t < live) top = __vmaxu2(top, w[t].word & 0x7fff7fffu);
-        top0 = top << 16, top1 = top & 0xffff0000u;
-    } else {
+        for (int t = 0; t < R; ++t) w[t] = pair(z, t);
+        uint32_t top0 = 0, top1 = 0;
+        if constexpr (sizeof(T) == 2) {
+            uint32_t top = 0;  // bf16 without its sign orders like a whole number: two at once
 #pragma unroll
-        for (int t = 0; t < R; ++t)
-            if (t < live) top0 = max(top0, abs_bits(w[t].v[0])), top1 = max(top1, abs_bits(w[t].v[1]));
-    }
-    Raw<uint8_t, 2> code;
-    code.v[0] = (uint8_t)scale_code(top0), code.v[1] = (uint8_t)scale_code(top1);
-    store_pair<uint8_t, WIDE>(p.scales + ((z * p.B + s.b) * ((p.L + kGroup - 1) / kGroup) + t0 / kGroup) * D + s.c0 + 2 * lane, code, one, both);
-    const uint64_t inv = f2(inverse_scale(code.v[0]), inverse_scale(code.v[1]));
-    const uint32_t mask = (code.v[0] == 255 ? 0u : 0xffu) | (code.v[1] == 255 ? 0u : 0xff00u);
+            for (int t = 0; t < R; ++t)
+                if (ALL || t < live) top = __vmaxu2(top, w[t].word & 0x7fff7fffu);
+            top0 = top << 16, top1 = top & 0xffff0000u;
+        } else {
 #pragma unroll
-    for (int t = 0; t < R; ++t) {
-        float q0, q1;
-        un2(fma2(pair_of(w[t]), inv, f2(kToWhole)), q0, q1);
-        Raw<int8_t, 2> q;
-        q.word = (uint16_t)(t < live ? __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x0040) & mask : 0u);
-        put_pair<int8_t, WIDE>(out + t * kTile, values + t * D + 2 * lane, q, t < rows, one, both, lane);
-    }
-    if constexpr (WIDE) {
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::tma_store_3d(&maps.q, out, s.c0, t0, (int)(z * p.B) + s.b);
+            for (int t = 0; t < R; ++t)
+                if (ALL || t < live) top0 = max(top0, abs_bits(w[t].v[0])), top1 = max(top1, abs_bits(w[t].v[1]));
+        }
+        Raw<uint8_t, 2> code;
+        code.v[0] = (uint8_t)scale_code(top0), code.v[1] = (uint8_t)scale_code(top1);
+        const int64_t groups = (p.L + kGroup - 1) / kGroup;
+        store_pair<uint8_t, WIDE>(p.scales + ((z * p.B + s.b) * groups + (s.t0 + place) / kGroup) * D + s.c0 + 2 * lane, code, one, both);
+        const uint64_t inv = f2(inverse_scale(code.v[0]), inverse_scale(code.v[1]));
+        const uint32_t mask = (code.v[0] == 255 ? 0u : 0xffu) | (code.v[1] == 255 ? 0u : 0xff00u);
+        int8_t *values = p.values + (z * p.B * p.L + place) * D + s.base + 2 * lane;
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+            float q0, q1;
+            un2(fma2(pair_of(w[t]), inv, f2(kToWhole)), q0, q1);
+            Raw<int8_t, 2> q;
+            q.word = (uint16_t)(ALL || t < live ? __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x0040) & mask : 0u);
+            put_pair<int8_t, WIDE>(out[WIDE ? z * R + t : 0], values + t * D, q, t < rows, one, both, lane);
+        }
     }
 }
 
@@ -391,10 +389,18 @@ __global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear
             __syncwarp();
         }
         if constexpr (PACK) {
-            if (rows > 0)
-#pragma unroll
-                for (int z = 0; z < 3; ++z)
-                    leave_in_8_bits<T, WIDE>(p, maps, z, pair, sh.q[WIDE ? z * kState + place : 0], s, place, live, rows, lane);
+            if (rows > 0) {
+                auto *out = &sh.q[WIDE ? 3 * place : 0];
+                if (live == R)
+                    leave_in_8_bits<T, WIDE, true>(p, pair, out, s, place, live, rows, lane);
+                else
+                    leave_in_8_bits<T, WIDE, false>(p, pair, out, s, place, live, rows, lane);
+                if constexpr (WIDE) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::tma_store_4d(&maps.q, out, s.c0, t0, s.b, 0);
+                }
+            }
         }
         __syncthreads();
         // the block's runs before this one, and all of them: every warp joins them, and sends to other blocks
@@ -468,7 +474,7 @@ template <typename T, bool WIDE, bool PACK> struct alignas(128) BwdShared {
 };
 struct BwdMaps {
     CUtensorMap x, r, i, dy;  // boxes of 64 x 64
-    CUtensorMap q, scale;     // the same in 8 bits, and 4 groups of scales
+    CUtensorMap q, scale;     // x, r and i in 8 bits at once, and 4 groups of their scales
     CUtensorMap dx, dr, di;   // of a warp's run
 };
 
@@ -506,35 +512,33 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
     }
     exchange_init(sh.exchange, &sh.tiles, blocks);
 
-    // Has the next step's tiles brought: a warp each, as all of these instructions in one would keep the others waiting.
-    auto bring = [&](int step) {
-        const Step s = sh.step[step & 3];
+    auto bring = [&](int step) {  // as in the forward
         if constexpr (WIDE) {
-            if (lane == 0 && s.cols > 0 && (s.begins || s.live > 0)) {
+            if (threadIdx.x != 0) return;
+            const Step s = sh.step[step & 3];
+            if (s.cols > 0 && (s.begins || s.live > 0)) {
                 const uint32_t some = s.cols * (uint32_t)sizeof(float);
-                for (int job = warp; job < 6; job += warps) {
-                    if (job == 0)
-                        tc::mbar_arrive_expect_tx(&sh.tiles, (s.live > 0 ? 3 * kState * PITCH + kState * DY + some + (PACK ? 3 * (kState / kGroup) * SC : 0) : 0) +
-                                                                 (s.begins ? (p.dfinal ? 2 : 1) * some : 0));
-                    if (s.live > 0) {
-                        if (job < 3) {
-                            if constexpr (PACK) {
-                                tc::tma_load_3d(sh.in[job], &maps.q, &sh.tiles, s.c0, s.t0, job * (int)p.f.B + s.b);
-                                tc::tma_load_3d(sh.scale[job], &maps.scale, &sh.tiles, s.c0, s.t0 / kGroup, job * (int)p.f.B + s.b);
-                            } else {
-                                tc::tma_load_3d(sh.in[job], job == 0 ? &maps.x : job == 1 ? &maps.r : &maps.i, &sh.tiles, s.c0, s.t0, s.b);
-                            }
-                        }
-                        if (job == 3) tc::tma_load_3d(sh.dy[step & 1], &maps.dy, &sh.tiles, s.c0, s.t0, s.b);
-                        if (job == 4) tc::bulk_load(sh.state, p.f.states + (s.b * chunks + s.t0 / kState) * D + s.c0, some, &sh.tiles);
+                tc::mbar_arrive_expect_tx(&sh.tiles, (s.live > 0 ? 3 * kState * PITCH + kState * DY + some + (PACK ? 3 * (kState / kGroup) * SC : 0) : 0) +
+                                                         (s.begins ? (p.dfinal ? 2 : 1) * some : 0));
+                if (s.live > 0) {
+                    if constexpr (PACK) {
+                        tc::tma_load_4d(sh.in, &maps.q, &sh.tiles, s.c0, s.t0, s.b, 0);
+                        tc::tma_load_4d(sh.scale, &maps.scale, &sh.tiles, s.c0, s.t0 / kGroup, s.b, 0);
+                    } else {
+                        tc::tma_load_3d(sh.in[0], &maps.x, &sh.tiles, s.c0, s.t0, s.b);
+                        tc::tma_load_3d(sh.in[1], &maps.r, &sh.tiles, s.c0, s.t0, s.b);
+                        tc::tma_load_3d(sh.in[2], &maps.i, &sh.tiles, s.c0, s.t0, s.b);
                     }
-                    if (job == 5 && s.begins) {
-                        tc::bulk_load(sh.lam, p.f.lam + s.c0, some, &sh.tiles);
-                        if (p.dfinal) tc::bulk_load(sh.last, p.dfinal + s.b * D + s.c0, some, &sh.tiles);
-                    }
+                    tc::tma_load_3d(sh.dy[step & 1], &maps.dy, &sh.tiles, s.c0, s.t0, s.b);
+                    tc::bulk_load(sh.state, p.f.states + (s.b * chunks + s.t0 / kState) * D + s.c0, some, &sh.tiles);
+                }
+                if (s.begins) {
+                    tc::bulk_load(sh.lam, p.f.lam + s.c0, some, &sh.tiles);
+                    if (p.dfinal) tc::bulk_load(sh.last, p.dfinal + s.b * D + s.c0, some, &sh.tiles);
                 }
             }
         } else {
+            const Step s = sh.step[step & 3];
             const int live = s.cols > 0 ? run_of(R, s.live, place) : 0;
             const int64_t at = s.base + place * D;
             if (live > 0) {
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear
         bring(step + 1);  // behind the sending, which the others wait for
         if (planner) sh.step[(step + 2) & 3] = sh.walk.next(p.f);
         // h over the earlier runs (the later warps') to this one; then b becomes what multiplies dh in psi, and rho 1 - rho
-#pragma unroll 4
+#pragma unroll 1
         for (int w = warps - 1; w > warp; --w) h = fma2(sh.run[step & 1][w][lane].a, h, sh.h[step & 1][w][lane]);
 #pragma unroll
         for (int t = 0; t < R; ++t) {
@@ -921,7 +925,7 @@ template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t st
                 tma_map_rows(&m.r, a.r, size, a.D, a.L, a.B, kTile, kState) && tma_map_rows(&m.i, a.i, size, a.D, a.L, a.B, kTile, kState) &&
                 (!a.y || tma_map_rows(&m.y, a.y, size, a.D, a.L, a.B, kTile, kFwdRun));
     if (a.values) {
-        wide = wide && a.D % 16 == 0 && tma_map_rows(&m.q, a.values, 1, a.D, a.L, 3 * a.B, kTile, kFwdRun);
+        wide = wide && a.D % 16 == 0 && tma_map_planes(&m.q, a.values, a.D, a.L, a.B, 3, kTile, kFwdRun);
         return wide ? forward_p<T, true, true>(a, m, stream) : forward_p<T, false, true>(a, m, stream);
     }
     return wide ? forward_p<T, true, false>(a, m, stream) : forward_p<T, false, false>(a, m, stream);
@@ -942,8 +946,8 @@ template <typename T> cudaError_t backward_t(const LinearBwdArgs &a, cudaStream_
                     tma_map_rows(&m.dx, a.dx, size, D, L, B, kTile, kBwdRun) && tma_map_rows(&m.dr, a.dr, size, D, L, B, kTile, kBwdRun) &&
                     tma_map_rows(&m.di, a.di, size, D, L, B, kTile, kBwdRun);
         if (a.f.values) {
-            wide = wide && D % 16 == 0 && tma_map_rows(&m.q, a.f.values, 1, D, L, 3 * B, kTile, kState) &&
-                   tma_map_rows(&m.scale, a.f.scales, 1, D, (L + kGroup - 1) / kGroup, 3 * B, kTile, kState / kGroup);
+            wide = wide && D % 16 == 0 && tma_map_planes(&m.q, a.f.values, D, L, B, 3, kTile, kState) &&
+                   tma_map_planes(&m.scale, a.f.scales, D, (L + kGroup - 1) / kGroup, B, 3, kTile, kState / kGroup);
             e = wide ? backward_p<T, true, true>(a, m, stream, &blocks) : backward_p<T, false, true>(a, m, stream, &blocks);
         } else {
             wide = wide && tma_map_rows(&m.x, a.f.x, size, D, L, B, kTile, kState) && tma_map_rows(&m.r, a.f.r, size, D, L, B, kTile, kState) &&

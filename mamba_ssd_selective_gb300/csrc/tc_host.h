@@ -29,6 +29,9 @@ bool tma_map_heads(CUtensorMap *out, const void *base, int64_t inner, int64_t he
 // (box_cols, box_rows, 1), rows one behind the other. What lies outside reads as zero and is not written. Encoded anew on each call.
 bool tma_map_rows(CUtensorMap *out, const void *base, int size, int64_t inner, int64_t L, int64_t B, int box_cols, int box_rows);
 
+// View of a [planes, B, L, inner] tensor of bytes, inner a multiple of 16, box (box_cols, box_rows, 1, planes); likewise.
+bool tma_map_planes(CUtensorMap *out, const void *base, int64_t inner, int64_t L, int64_t B, int planes, int box_cols, int box_rows);
+
 // Major compute capability of the current device (cached per device), -1 if unknown.
 int device_cc_major_cached();
 
