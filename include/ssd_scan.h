@@ -580,7 +580,12 @@ ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32
  * States, decays and sums are float32. A sequence gives bitwise the same y and
  * states alone as in a batch, and every call repeats itself bitwise. A NaN or
  * an infinity in a token reaches the later tokens of its channel (in the
- * backward the earlier ones too, and the channel's dlam) and no other.
+ * backward the earlier ones too, and the channel's dlam) and no other channel;
+ * where it is in r or i, or a gate is below -29, its neighbours can differ in
+ * the last bits. A sigmoid below 2^-126 counts as zero.
+ * Sequences are taken by clusters of thread blocks, 64 channels each, whose
+ * blocks lie one behind the other in time; rows that are multiples of 16 bytes
+ * (in 8 bits: of 16 channels) move by the TMA, others by 4-byte copies.
  * ------------------------------------------------------------------------- */
 
 #define SSD_GATED_LINEAR_CHUNK 64 /* tokens between two saved states */
@@ -605,7 +610,8 @@ ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32
  *   values     [3, B, L, D]           int8 and
  *   scales     [3, B, ceil(L/16), D]  uint8, with values: x, r and i as
  *              ssd_pack8 keeps them
- * Outputs may not alias x, r or i. Limits here and below: batch <= 65535,
+ * y and what is written for a backward may not alias x, r or i (equal pointers
+ * are refused). Limits here and below: batch <= 65535,
  * dim <= 2097120, seqlen < 2^31.
  */
 ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
@@ -625,7 +631,7 @@ ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, 
  *   dlam         [D] float32             dinit_state [B, D] float32, may be NULL
  *   workspace    ssd_gated_linear_chunked_bwd_workspace_size(..., states given?)
  *                bytes, 256-byte aligned
- * Outputs may not alias inputs. The _packed form takes x, r and i in 8 bits as
+ * Outputs may not alias inputs (equal pointers are refused). The _packed form takes x, r and i in 8 bits as
  * the forward (or ssd_pack8, three times) wrote them, with the states: the
  * gradients are those at the values that the 8 bits stand for, h going on from
  * the given state every 64 tokens.
@@ -644,6 +650,14 @@ ssd_status ssd_gated_linear_chunked_bwd_packed(int64_t batch, int64_t seqlen, in
                                                const float *dfinal_state, void *dx, void *dr, void *di, float *dlam,
                                                float *dinit_state, void *workspace, size_t ws_bytes,
                                                cudaStream_t stream);
+
+/*
+ * Waits for `stream`, then reports SSD_OK, or SSD_ERR_TIMEOUT when a bounded
+ * wait of a gated-linear kernel on the current device gave up since the last
+ * time this was asked: what such a call wrote is NaN from there on. Not to be
+ * called while a stream is captured.
+ */
+ssd_status ssd_gated_linear_status(cudaStream_t stream);
 
 /*
  * One token of the recurrence for a batch of sequences whose states lie in a pool.

@@ -113,11 +113,12 @@ def load() -> ctypes.CDLL:
             lib.ssd_gated_linear_chunked_bwd_packed.argtypes = ([i64, i64, i64, i32] + [vp] * 3 + [f32] + [vp] * 9
                                                                 + [vp, sz, vp])
             lib.ssd_gated_linear_step.argtypes = [i64, i64, i32, i64] + [vp] * 5 + [f32] + [vp] * 4
+            lib.ssd_gated_linear_status.argtypes = [vp]
             lib.ssd_pack8.argtypes = [i64, i64, i64, i32] + [vp] * 5
             lib.ssd_unpack8.argtypes = [i64, i64, i64, i32] + [vp] * 4
             for f in (lib.ssd_gated_linear_chunked, lib.ssd_gated_linear_chunked_bwd,
-                      lib.ssd_gated_linear_chunked_bwd_packed, lib.ssd_gated_linear_step, lib.ssd_pack8,
-                      lib.ssd_unpack8):
+                      lib.ssd_gated_linear_chunked_bwd_packed, lib.ssd_gated_linear_step,
+                      lib.ssd_gated_linear_status, lib.ssd_pack8, lib.ssd_unpack8):
                 f.restype = ctypes.c_int
             lib.ssd_scan_chunked.argtypes = [dp] + [vp] * 7 + [ctypes.c_int, vp, vp, vp, sz, vp]
             lib.ssd_scan_chunked_noalloc.argtypes = [dp] + [vp] * 7 + [ctypes.c_int, vp, vp, vp]
@@ -931,6 +932,12 @@ def gated_linear_chunked_bwd_packed(values, scales, states, lam, dy, c=8.0, dfin
         _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dlam"]), _ptr(g["dinit"]),
         _ptr(workspace), workspace.numel(), _stream(stream, dev)))
     return g
+
+
+def gated_linear_status(stream=None) -> int:
+    """Waits for the stream and returns SSD_OK, or SSD_ERR_TIMEOUT when a bounded
+    wait of a gated-linear kernel on the current device gave up since the last call."""
+    return int(load().ssd_gated_linear_status(_stream(stream, torch.device("cuda", torch.cuda.current_device()))))
 
 
 def gated_linear_step(state, x, r, i, lam, c=8.0, slots=None, new_state=None, y=None, stream=None):

@@ -983,6 +983,13 @@ cudaError_t launch_linear_step(int io, const LinearStepArgs &a, cudaStream_t str
     });
 }
 
+cudaError_t linear_gave_up(int *status) {
+    cudaError_t e = cudaMemcpyFromSymbol(status, linear::g_gave_up, sizeof(int));
+    const int none = SSD_OK;
+    if (e == cudaSuccess && *status != none) e = cudaMemcpyToSymbol(linear::g_gave_up, &none, sizeof(int));
+    return e;
+}
+
 namespace linear {
 template <typename T, int V> cudaError_t pack8_v(const Pack8Args &a, cudaStream_t stream) {
     const int64_t groups = (a.L + kGroup - 1) / kGroup;

@@ -963,6 +963,10 @@ ssd_status linear_bwd(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dty
     const bool some = batch > 0 && seqlen > 0;
     if (!a.f.lam || !a.dlam || (some && (!a.dy || !a.dx || !a.dr || !a.di)))
         return fail(SSD_ERR_INVALID_ARG, "lam, dy, dx, dr, di and dlam must be non-NULL");
+    const void *in[] = {a.f.x, a.f.r, a.f.i, a.dy, a.f.values}, *out[] = {a.dx, a.dr, a.di};
+    for (const void *o : out)
+        for (const void *q : in)
+            if (some && o == q) return fail(SSD_ERR_INVALID_ARG, "dx, dr and di may not be the buffer of an input");
     ssd_status s = check_rate(a.f.c);
     if (s != SSD_OK) return s;
     s = check_aligned({{a.f.x, "x"}, {a.f.r, "r"}, {a.f.i, "i"}, {a.f.values, "values"}, {a.f.scales, "scales"},
@@ -997,6 +1001,7 @@ ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, 
     if (!lam || (seqlen > 0 && (!x || !r || !i || !y)))
         return fail(SSD_ERR_INVALID_ARG, "x, r, i, lam and y must be non-NULL");
     if (!values != !scales) return fail(SSD_ERR_INVALID_ARG, "values and scales must be given together");
+    if (y && (y == x || y == r || y == i)) return fail(SSD_ERR_INVALID_ARG, "y may not be the buffer of x, r or i");
     s = check_aligned({{x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}, {init_state, "init_state"}, {seqlens, "seqlens"},
                        {y, "y"}, {final_state, "final_state"}, {states, "states"}, {values, "values"},
                        {scales, "scales"}});
@@ -1069,6 +1074,15 @@ ssd_status ssd_gated_linear_step(int64_t batch, int64_t dim, int32_t io_dtype, i
     a.x = x, a.r = r, a.i = i, a.lam = lam, a.c = c, a.slots = slots, a.y = y;
     cudaError_t e = ssd::launch_linear_step(io_of(io_dtype), a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_linear_step");
+    return ok();
+}
+
+ssd_status ssd_gated_linear_status(cudaStream_t stream) {
+    cudaError_t e = cudaStreamSynchronize(stream);
+    int word = SSD_OK;
+    if (e == cudaSuccess) e = ssd::linear_gave_up(&word);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_gated_linear_status");
+    if (word != SSD_OK) return fail((ssd_status)word, "a bounded in-kernel wait timed out");
     return ok();
 }
 

@@ -8,12 +8,17 @@ sums. 1e-5 (2-norm) and 1e-4 (largest error over the largest result). bf16 input
 37 units at |r| = 30 and 8 at |r| = 5, so float32 results of bf16 inputs get the same; bf16 results are rounded once: at most
 2^-8 of each value, so of the 2-norm too, and 1e-5 for the float32 value's own error.
 """
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from mamba_ssd_selective_gb300 import inputs
 from oracle import linear
+from tests.conftest import ROOT
 from tests.helpers import IO_TORCH, dev, host
 
 pytestmark = pytest.mark.gpu
@@ -368,3 +373,128 @@ def test_offsets_past_32_bits(ssd):
     del g, g1, kept
     v, s = ssd.pack8(x)
     assert torch.equal(v[2:], k1["values"][0]) and torch.equal(ssd.unpack8(v, s)[2:], ssd.unpack8(v[2:], s[2:]))
+
+
+# widths whose rows are multiples of 16 bytes, tiles of fewer than 64 channels, lengths on both sides of a block's 64 tokens and of
+# clusters of 16 of them, and more sequences and tiles than the device holds clusters
+WIDE = [(1, 1, 8), (2, 63, 16), (2, 64, 72), (3, 65, 200), (2, 1025, 24), (1, 5000, 72), (300, 70, 136), (5, 130, 16), (2, 200, 1000)]
+
+
+@pytest.mark.parametrize("size", WIDE)
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rate", [1.0, 40.0])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_wide_rows(ssd, size, io, rate, ragged):
+    """The forward, its states and 8 bits, and both backwards."""
+    d, t, lens = case(size, io, size[1] + size[2], rate, ragged)
+    args = [d[n] for n in ("x", "r", "i", "lam")]
+    kept = ssd.gated_linear_checkpoint(t["x"])
+    y, final = ssd.gated_linear_chunked(*tokens(t), init_state=t["init"], seqlens=t.get("seqlens"), **kept)
+    wy, wf, ws = linear.linear_seq(*args, 8.0, d["init"], lens)
+    near(y, wy, "y")
+    near(final, wf, "final")
+    near(kept["states"], ws, "states")
+    y2, final2 = ssd.gated_linear_chunked(*tokens(t), init_state=t["init"], seqlens=t.get("seqlens"))
+    assert torch.equal(y, y2) and torch.equal(final, final2)
+    kw = dict(dfinal_state=t["dfinal"], seqlens=t.get("seqlens"))
+    want = linear.linear_seq_bwd(*args, d["dy"], 8.0, d["init"], d["dfinal"], lens)
+    for how in (dict(init_state=t["init"]), dict(states=kept["states"])):
+        got = ssd.gated_linear_chunked_bwd(*tokens(t), t["dy"], **how, **kw)
+        for n, w in want.items():
+            near(got[n], w, n)
+    back = []
+    for z, n in enumerate(("x", "r", "i")):
+        q, code = linear.pack8(d[n], lens)
+        assert np.array_equal(host(kept["values"][z]), q) and np.array_equal(host(kept["scales"][z]), code), n
+        back.append(linear.unpack8(q, code))
+    got = ssd.gated_linear_chunked_bwd_packed(lam=t["lam"], dy=t["dy"], **kept, **kw)
+    want = linear.linear_seq_bwd(*back, d["lam"], d["dy"], 8.0, d["init"], d["dfinal"], lens, states=host(kept["states"]))
+    for n, w in want.items():
+        near(got[n], w, n)
+    assert ssd.gated_linear_status() == ssd.SSD_OK
+
+
+@pytest.mark.parametrize("D", [64, 65, 520])
+def test_states_updated_in_place(ssd, D):
+    d, t, lens = case((30, 100, D), "bf16", 11, 1.0, True)
+    want = ssd.gated_linear_chunked(*tokens(t), init_state=t["init"], seqlens=t["seqlens"])
+    for _ in range(3):
+        state = t["init"].clone()
+        got = ssd.gated_linear_chunked(*tokens(t), init_state=state, final_state=state, seqlens=t["seqlens"])
+        assert got[1] is state and torch.equal(got[0], want[0]) and torch.equal(state, want[1])
+
+
+@pytest.mark.parametrize("D", [72, 33])
+def test_gates_that_are_not_finite(ssd, D):
+    """NaN or an infinity in r or i: NaN (or a gate that is open or shut) in its channel from there on, the others near what they were."""
+    _, t, _ = case((2, 200, D), "bf16", 12)
+    want, _ = ssd.gated_linear_chunked(*tokens(t))
+    others = [c for c in range(D) if c != 7]
+    for n in ("r", "i"):
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            u = dict(t, **{n: t[n].clone()})
+            u[n][1, 100, 7] = bad
+            y, _ = ssd.gated_linear_chunked(*tokens(u))
+            g = ssd.gated_linear_chunked_bwd(*tokens(u), t["dy"])
+            assert torch.isnan(y[1, 100:, 7]).all() if bad != bad else torch.isfinite(y).all()
+            assert torch.equal(y[0], want[0]) and torch.equal(y[1, :96], want[1, :96])
+            diff = (y[1][:, others].float() - want[1][:, others].float()).abs()
+            assert (diff <= 2.0 ** -7 * want[1][:, others].float().abs() + 1e-5).all()
+            assert all(torch.isfinite(v.float()[..., others]).all() for v in g.values())
+            if bad == bad:
+                assert all(torch.isfinite(v.float()).all() for v in g.values())
+
+
+FIRST_CALL = """
+import torch
+from mamba_ssd_selective_gb300 import binding as ops
+x, lam = torch.randn(2, 300, 128, device="cuda").bfloat16(), torch.full((128,), -5.0, device="cuda")
+side = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    kept = ops.gated_linear_checkpoint(x)
+    y, final = ops.gated_linear_chunked(x, x, x, lam, **kept)
+    g = ops.gated_linear_chunked_bwd_packed(lam=lam, dy=x, **kept)
+    g2 = ops.gated_linear_chunked_bwd(x, x, x, lam, x)
+graph.replay()
+torch.cuda.synchronize()
+kept2 = ops.gated_linear_checkpoint(x)
+y2, _ = ops.gated_linear_chunked(x, x, x, lam, **kept2)
+g3 = ops.gated_linear_chunked_bwd_packed(lam=lam, dy=x, **kept2)
+assert torch.equal(y, y2) and all(torch.equal(g[n], g3[n]) for n in g) and torch.equal(kept["values"], kept2["values"])
+assert torch.isfinite(g2["dlam"]).all()
+"""
+
+
+def test_first_call_of_a_process_is_captured(ssd):
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_from_two_threads(ssd):
+    """First and later calls of two host threads, each on its stream."""
+    said = []
+
+    def work(D):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                _, t, _ = case((2, 400, D), "bf16", D)
+                want = None
+                for _ in range(50):
+                    kept = ssd.gated_linear_checkpoint(t["x"])
+                    y, _ = ssd.gated_linear_chunked(*tokens(t), **kept)
+                    g = ssd.gated_linear_chunked_bwd_packed(lam=t["lam"], dy=t["dy"], **kept)
+                    got = [y, *(v for v in g.values() if v is not None)]
+                    assert want is None or all(torch.equal(a, b) for a, b in zip(got, want))
+                    want = got
+        except BaseException as e:  # noqa: B902
+            said.append(e)
+
+    threads = [threading.Thread(target=work, args=(D,)) for D in (64, 520, 33, 64)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not said

@@ -84,22 +84,25 @@ def lib():
     return binding.load()
 
 
+IN, OUT = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)
+
+
 def fwd(lib, B=2, L=100, D=64, io=1, c=8.0, bad=None):
-    a = [P] * 11
+    a = [IN] * 4 + [OUT] * 7
     if bad:
         a[bad[0]] = bad[1]
     return lib.ssd_gated_linear_chunked(B, L, D, io, *a[:4], c, *a[4:], None)
 
 
 def bwd(lib, B=2, L=100, D=64, io=1, c=8.0, bad=None, bytes_=1 << 40):
-    a = [P] * 15
+    a = [IN] * 8 + [OUT] * 7
     if bad:
         a[bad[0]] = bad[1]
     return lib.ssd_gated_linear_chunked_bwd(B, L, D, io, *a[:4], c, *a[4:15], bytes_, None)
 
 
 def bwd_packed(lib, B=2, L=100, D=64, io=1, c=8.0, bad=None, bytes_=1 << 40):
-    a = [P] * 13
+    a = [IN] * 6 + [OUT] * 7
     if bad:
         a[bad[0]] = bad[1]
     return lib.ssd_gated_linear_chunked_bwd_packed(B, L, D, io, *a[:3], c, *a[3:13], bytes_, None)
@@ -153,6 +156,14 @@ def test_missing_and_misaligned_pointers(lib, call, needed, total):
         assert call(lib, bad=(i, None)) == INVALID, i
     for i in range(total):
         assert call(lib, bad=(i, ctypes.c_void_p((1 << 20) + 4))) == INVALID, i
+
+
+def test_results_in_the_place_of_inputs(lib):
+    assert fwd(lib, bad=(6, IN)) == INVALID
+    for i in (9, 10, 11):
+        assert bwd(lib, bad=(i, IN)) == INVALID
+    for i in (7, 8, 9):
+        assert bwd_packed(lib, bad=(i, IN)) == INVALID
 
 
 def test_values_and_scales_go_together(lib):
