@@ -97,17 +97,19 @@ template <typename T> __device__ __forceinline__ uint64_t exp_minus(uint64_t x) 
 
 // The gates of one token, for two channels, with rho and iota the sigmoids of r and i, w = k rho and t = 2 w:
 //     a = exp(-w)     f = sqrt(1 - a^2) iota     and for the backward g = a^2 w / (1 - a^2) = w / (exp(2 w) - 1) (grad_ratio).
-// 1 - exp(-t) is t times a smooth function, so its root is sqrt(2 k rho) Q(t) and there is neither a difference that cancels nor a
-// root of its own to take: rho is the square of 1 / sqrt(1 + e^-r). Q(t) = sqrt((1 - e^-t) / t) and g = G(t), t / (e^t - 1) / 2, for
-// t < 1 as polynomials of degree 4 through their Chebyshev points on [0, 1] (1.8e-7 and 4.4e-7 off at most).
+// For t < 1 all three are polynomials of degree 4 in t, exact at 0 and through Chebyshev points on [0, 1] (their error goes to zero
+// with t, and most tokens' t is small): a as 1 + t E(t) (E 5e-8 off at t = 1/5, 3.5e-7 at 1), f as sqrt(2 k rho) Q(t) iota with
+// Q(t) = sqrt((1 - e^-t) / t) (9e-8, 6e-7), g as G(t) = t / (e^t - 1) / 2 (1.1e-7, 1.2e-6). So there is neither a difference that
+// cancels nor a root of its own to take: rho is the square of 1 / sqrt(1 + e^-r). And a is rounded once: an a off by d counts d / w in
+// h, and the approximate exponential, off by 1e-7 to one side near 1, made h 1.3e-6 wrong where this makes it 2e-7 (float32 B2 L777).
 // FAST, for what nearly every run of tokens is: k below kSteep, so that t < 1, and r and i (r + 2 i above -88 or so) such that the
 // argument of one reciprocal root, sqrt(rho) iota = 1 / sqrt((1 + e^-r) (1 + e^-i)^2), is finite: `sum` adds them up and tells.
-// Four calls of the special function unit a token and channel instead of six.
+// Three calls of the special function unit a token and channel instead of four, and no choice.
 constexpr float kSteep = 0.5f;
-struct Rate2 {  // of two channels: 2 k, k log2(e), sqrt(2 k)
-    uint64_t twice, log2, root;
+struct Rate2 {  // of two channels: 2 k, sqrt(2 k)
+    uint64_t twice, root;
     __device__ __forceinline__ static Rate2 of(float k0, float k1) {
-        return {f2(2.f * k0, 2.f * k1), f2(kLog2e * k0, kLog2e * k1), f2(sqrtf(2.f * k0), sqrtf(2.f * k1))};
+        return {f2(2.f * k0, 2.f * k1), f2(sqrtf(2.f * k0), sqrtf(2.f * k1))};
     }
 };
 struct Gates2 {
@@ -133,24 +135,26 @@ template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 ga
         o.iota = f2(rcp_approx(x0), rcp_approx(x1));
         o.rho = mul2(m, m), z = mul2(m, o.iota);
     }
-    un2(mul2(o.rho, k.log2), x0, x1);
-    const float a0 = ex2_approx(-x0), a1 = ex2_approx(-x1);
-    o.a = f2(a0, a1);
     o.t = mul2(o.rho, k.twice);
-    uint64_t q = fma2(o.t, f2(0.0006950617535039783f), f2(-0.007676176261156797f));
-    q = fma2(o.t, q, f2(0.052035510540008545f));
-    q = fma2(o.t, q, f2(-0.24999406933784485f));
-    q = fma2(o.t, q, f2(0.9999998807907104f));
+    uint64_t e = fma2(o.t, f2(-0.00022097997134551406f), f2(0.002580259693786502f));
+    e = fma2(o.t, e, f2(-0.0208286102861166f));
+    e = fma2(o.t, e, f2(0.12499985098838806f));
+    e = fma2(o.t, e, f2(-0.5f));
+    uint64_t q = fma2(o.t, f2(0.000725092482753098f), f2(-0.007732587866485119f));
+    q = fma2(o.t, q, f2(0.05206755921244621f));
+    q = fma2(o.t, q, f2(-0.2499995082616806f));
+    q = fma2(o.t, q, one);
+    o.a = fma2(o.t, e, one);
     o.f = mul2(mul2(z, k.root), q);
     if constexpr (!FAST) {  // t >= 1: 1 - a^2 from a^2 <= 0.37
-        float t0, t1, i0, i1, f0, f1;
+        float t0, t1, i0, i1, f0, f1, a0, a1;
         un2(o.t, t0, t1);
         un2(o.iota, i0, i1);
         un2(o.f, f0, f1);
-        const float b0 = fmaf(-a0, a0, 1.f), b1 = fmaf(-a1, a1, 1.f);
-        if (!(t0 < 1.f)) f0 = b0 * rsqrt_approx(b0) * i0;
-        if (!(t1 < 1.f)) f1 = b1 * rsqrt_approx(b1) * i1;
-        o.f = f2(f0, f1);
+        un2(o.a, a0, a1);
+        if (!(t0 < 1.f)) a0 = ex2_approx(-0.5f * kLog2e * t0), f0 = fmaf(-a0, a0, 1.f), f0 = f0 * rsqrt_approx(f0) * i0;
+        if (!(t1 < 1.f)) a1 = ex2_approx(-0.5f * kLog2e * t1), f1 = fmaf(-a1, a1, 1.f), f1 = f1 * rsqrt_approx(f1) * i1;
+        o.f = f2(f0, f1), o.a = f2(a0, a1);
     }
     return o;
 }
@@ -162,10 +166,10 @@ __device__ __forceinline__ bool is_low(uint64_t sum, bool one, bool both) {
 }
 // G(t); `steep`: where t may be 1 and more.
 __device__ __forceinline__ uint64_t grad_ratio(uint64_t t, uint64_t a, bool steep) {
-    uint64_t g = fma2(t, f2(-0.0006299343658611178f), f2(-7.389252277789637e-05f));
-    g = fma2(t, g, f2(0.04169579595327377f));
-    g = fma2(t, g, f2(-0.25000378489494324f));
-    g = fma2(t, g, f2(0.5000000596046448f));
+    uint64_t g = fma2(t, f2(-0.0006504057091660798f), f2(-3.583935904316604e-05f));
+    g = fma2(t, g, f2(0.04167448729276657f));
+    g = fma2(t, g, f2(-0.2500002384185791f));
+    g = fma2(t, g, f2(0.5f));
     if (steep) {
         float t0, t1, a0, a1, g0, g1;
         un2(t, t0, t1);
@@ -177,6 +181,7 @@ __device__ __forceinline__ uint64_t grad_ratio(uint64_t t, uint64_t a, bool stee
     }
     return g;
 }
+
 // 8 bits: the values of a group are whole numbers times 2^e, e the least with max |x| <= 127 2^e and e >= -127, kept as the
 // byte e + 127. Every step is exact but the rounding to a whole number. 255 marks a group that held a NaN or an infinity.
 // `top` is the largest |x| of the group as bits, which order like the numbers, NaN above infinity.
