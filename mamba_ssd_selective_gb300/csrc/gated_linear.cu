@@ -17,8 +17,6 @@
 // sender wait for everything it has written (B8 L2048 D5120: 193 us so, 176 without).
 #include <cooperative_groups.h>
 
-#include <mutex>
-
 #include "gated_linear.cuh"
 #include "launch.h"
 #include "ssd_scan.h"
@@ -35,6 +33,10 @@ constexpr int kBwdRun = 8;                // and in the backward, which keeps fi
 constexpr int kBwdWarps = kState / kBwdRun;
 constexpr int kMaxCluster = 16;
 constexpr int kPackWarps = 8;
+
+// Blocks that an SM holds, by registers and shared memory.
+template <typename T, bool PACK> __host__ __device__ constexpr int fwd_per_sm() { return sizeof(T) == 4 ? 2 : PACK ? 3 : 4; }
+template <typename T> __host__ __device__ constexpr int bwd_per_sm() { return sizeof(T) == 4 ? 1 : 2; }
 
 // ------------------------------------------------------- tiles in shared memory
 // WIDE, for rows that begin at a multiple of 16 bytes: a thread has the TMA bring the block's tiles and a lane of each warp
@@ -275,7 +277,7 @@ __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const F &pa
 }
 
 template <typename T, bool WIDE, bool PACK>
-__global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 4 : 2) linear_fwd_kernel(LinearArgs p, const __grid_constant__ FwdMaps maps) {
+__global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_fwd_kernel(LinearArgs p, const __grid_constant__ FwdMaps maps) {
     namespace cg = cooperative_groups;
     pdl_wait();
     constexpr int R = kFwdRun, PITCH = Row<T, WIDE>::kPitch;
@@ -486,7 +488,7 @@ __device__ __forceinline__ uint64_t from_8(uint32_t two, uint64_t scale) {
 }
 
 template <typename T, bool WIDE, bool PACK>
-__global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1) linear_bwd_kernel(LinearBwdArgs p, const __grid_constant__ BwdMaps maps) {
+__global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_kernel(LinearBwdArgs p, const __grid_constant__ BwdMaps maps) {
     namespace cg = cooperative_groups;
     pdl_wait();
     constexpr int R = kBwdRun, PITCH = BwdShared<T, WIDE, PACK>::kPitch, DY = Row<T, WIDE>::kPitch, SC = Row<uint8_t, WIDE>::kPitch;
@@ -838,65 +840,74 @@ template <typename F> cudaError_t for_width(int64_t D, F &&f) {
     if (D % 2 == 0) return f(std::integral_constant<int, 2>{});
     return f(std::integral_constant<int, 1>{});
 }
-// Clusters of 1 to kMaxCluster blocks of KERN that the current device holds at once (by index; 0: none), asked of the driver once per
+constexpr size_t kSmemPerSM = 233472, kSmemPerBlock = 232448;  // a block's also takes 1 KB of the SM's
+constexpr int kMaxPerSM = 4;
+
+// Clusters of KERN that the current device holds at once, by the blocks on an SM and those of a cluster; asked of the driver once per
 // device below 64 and else on every call.
-struct ClusterCounts {
-    int at_once[kMaxCluster + 1];
-};
-template <auto KERN> cudaError_t ask_clusters(int threads, size_t smem, ClusterCounts *c) {
-    cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    for (int blocks = 1; blocks <= kMaxCluster && e == cudaSuccess; ++blocks) {
+template <auto KERN> class ClusterTable {
+  public:
+    ClusterTable(int threads, int per_sm, size_t smem) : threads_(threads), per_sm_(per_sm), smem_(smem) {}
+    // shared memory a block asks for so that an SM takes n
+    size_t smem(int n) const { return n >= per_sm_ ? smem_ : imin(kSmemPerBlock, kSmemPerSM / n - 1024) / 128 * 128; }
+    cudaError_t open() {
+        static DeviceOnce configured;
+        cudaError_t e = cudaSuccess;
+        if (configured.pending(&dev_, &e)) {
+            e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemPerBlock);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) configured.done(dev_);
+        }
+        return e;
+    }
+    cudaError_t at_once(int n, int blocks, int *count) {
+        static std::atomic<int> known[64][kMaxPerSM + 1][kMaxCluster + 1];  // and one
+        std::atomic<int> *slot = dev_ >= 0 && dev_ < 64 ? &known[dev_][n][blocks] : nullptr;
+        if (slot && (*count = slot->load(std::memory_order_acquire) - 1) >= 0) return cudaSuccess;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)blocks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3((unsigned)blocks), cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem;
+        cfg.gridDim = dim3((unsigned)blocks), cfg.blockDim = dim3((unsigned)threads_), cfg.dynamicSmemBytes = smem(n);
         cfg.attrs = attr, cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&c->at_once[blocks], KERN, &cfg);
+        cudaError_t e = cudaOccupancyMaxActiveClusters(count, KERN, &cfg);
+        if (e == cudaSuccess && slot) slot->store(*count + 1, std::memory_order_release);
+        return e;
     }
-    return e;
-}
-template <auto KERN> cudaError_t cluster_counts(int threads, size_t smem, ClusterCounts *c) {
-    static ClusterCounts known[64];
-    static DeviceOnce asked;
-    static std::mutex one;
-    int dev = 0;
-    cudaError_t e = cudaSuccess;
-    if (asked.pending(&dev, &e)) {
-        std::lock_guard<std::mutex> lock(one);
-        if (asked.pending(&dev, &e)) {
-            e = ask_clusters<KERN>(threads, smem, c);
-            if (e != cudaSuccess || dev < 0 || dev >= 64) return e;
-            known[dev] = *c;
-            asked.done(dev);
-        }
-    }
-    if (e == cudaSuccess) *c = known[dev];
-    return e;
-}
 
-// Launches KERN over `items` sequences and tiles of L tokens, a run of `run` tokens a warp. The cluster's size: the one whose waves
-// times steps cost least, where a block more in the cluster makes a step 4 % dearer (a step of the forward at B8 L2048 D5120 takes
-// 2.7 us with 2 blocks, 3.05 with 4, 3.4 with 8, 3.7 with 12; of the backward at B4 3.7, 3.95, 4.8 and 5.0).
+  private:
+    int dev_ = 0, threads_, per_sm_;
+    size_t smem_;
+};
+
+// Launches KERN over `items` sequences and tiles of L tokens, a run of `run` tokens a warp; an SM holds `per_sm` blocks.
+// The blocks of a cluster and those on an SM are those whose waves times steps cost least. A block more in the cluster makes a step
+// 4 % dearer (the forward at B8 L2048 D5120 takes 2.7 us a step with 2, 3.05 with 4, 3.4 with 8, 3.7 with 12; the backward at B4 3.7,
+// 3.95, 4.8 and 5.0), one more on the SM a tenth (the same forward 2.4 us with 2, 2.8 with 3, 3.05 with 4). Fewer blocks on an SM than
+// it holds, by asking for more shared memory than they need, is right where there are few clusters: a cluster's blocks are
+// otherwise put on as few SMs as hold them (B1 L65536 D1536: 235 us in clusters of 16 with 4 on an SM, 213 in clusters of 15 with 3).
 // A grid that fills the device is not launched as a programmatic dependent: placed while the kernel before it drains, clusters
 // find holes that no other cluster fits, and the last of them wait for the first (forward 142 us rather than 124, backward 215 rather
-// than 174). One that leaves half of the device free is.
+// than 174). One that leaves half of the places free is (B1 L512 D1536: 5.2 us rather than 6.4).
 template <auto KERN, typename Args, typename Maps>
-cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int64_t L, int run, size_t smem, cudaStream_t stream, int *blocks_taken) {
+cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int64_t L, int run, int per_sm, size_t smem, cudaStream_t stream,
+                            int *blocks_taken) {
     const int warps = (int)imin<int64_t>(kState / run, (L + run - 1) / run);  // no more than have a token
     const int64_t need = (L + kState - 1) / kState;
-    ClusterCounts counts{};
-    cudaError_t e = cluster_counts<KERN>(32 * (kState / run), smem, &counts);
-    if (e != cudaSuccess) return e;
-    int best = 1, held = 1;
+    ClusterTable<KERN> table(32 * (kState / run), per_sm, smem);
+    cudaError_t e = table.open();
+    int best = 0, on_sm = 0, held = 0;
     double cost = 0;
-    for (int blocks = 1; blocks <= kMaxCluster && blocks <= need; ++blocks) {
-        const int count = counts.at_once[blocks];
-        if (count < 1) continue;
-        const double c = (double)((items + count - 1) / count) * (double)((need + blocks - 1) / blocks) * (1.0 + 0.04 * blocks);
-        if (blocks == 1 || c < cost) best = blocks, held = count, cost = c;
-    }
+    for (int n = per_sm; n >= 1; --n)
+        for (int blocks = 1; blocks <= kMaxCluster && blocks <= need; ++blocks) {
+            int count = 0;
+            if (e == cudaSuccess) e = table.at_once(n, blocks, &count);
+            if (e != cudaSuccess) return e;
+            if (count < 1) continue;
+            const double c = (double)((items + count - 1) / count) * (double)((need + blocks - 1) / blocks) * (1.0 + 0.04 * blocks) * (0.6 + 0.1 * n);
+            if (best == 0 || c < cost) best = blocks, on_sm = n, held = count, cost = c;
+        }
+    if (best == 0) return cudaErrorInvalidConfiguration;
     if (blocks_taken) *blocks_taken = best;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -905,12 +916,13 @@ cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int6
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(imin<int64_t>(items, held) * best)), cfg.blockDim = dim3((unsigned)(32 * warps));
-    cfg.dynamicSmemBytes = smem, cfg.stream = stream, cfg.attrs = attr, cfg.numAttrs = 2 * items <= held ? 2 : 1;
+    cfg.dynamicSmemBytes = table.smem(on_sm), cfg.stream = stream, cfg.attrs = attr;
+    cfg.numAttrs = cfg.gridDim.x * 2 <= (unsigned)(sm_count(1) * per_sm) ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, KERN, a, maps);
 }
 
 template <typename T, bool WIDE, bool PACK> cudaError_t forward_p(const LinearArgs &a, const FwdMaps &maps, cudaStream_t stream) {
-    return launch_clusters<linear_fwd_kernel<T, WIDE, PACK>>(a, maps, a.B * ((a.D + kTile - 1) / kTile), a.L, kFwdRun,
+    return launch_clusters<linear_fwd_kernel<T, WIDE, PACK>>(a, maps, a.B * ((a.D + kTile - 1) / kTile), a.L, kFwdRun, fwd_per_sm<T, PACK>(),
                                                              sizeof(FwdShared<T, WIDE, PACK>), stream, nullptr);
 }
 template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t stream) {
@@ -933,7 +945,7 @@ template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t st
 
 template <typename T, bool WIDE, bool PACK> cudaError_t backward_p(const LinearBwdArgs &a, const BwdMaps &maps, cudaStream_t stream, int *blocks) {
     return launch_clusters<linear_bwd_kernel<T, WIDE, PACK>>(a, maps, a.f.B * ((a.f.D + kTile - 1) / kTile), a.f.L, kBwdRun,
-                                                             sizeof(BwdShared<T, WIDE, PACK>), stream, blocks);
+                                                             bwd_per_sm<T>(), sizeof(BwdShared<T, WIDE, PACK>), stream, blocks);
 }
 template <typename T> cudaError_t backward_t(const LinearBwdArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
