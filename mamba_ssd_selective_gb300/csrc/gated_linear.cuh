@@ -21,6 +21,7 @@ template <> struct Word<16> { using type = uint4; };
 template <typename T, int V> union Raw {
     typename Word<sizeof(T) * V>::type word;
     T v[V];
+    uint32_t u[(sizeof(T) * V + 3) / 4];
     __device__ Raw() : word{} {}
 };
 
