@@ -498,3 +498,21 @@ def test_from_two_threads(ssd):
         th.join()
     torch.cuda.synchronize()
     assert not said
+
+
+@pytest.mark.parametrize("B,D", [(255, 1024), (66, 5120), (1000, 333)])
+def test_step_of_many_rows(ssd, B, D):
+    """Batches of which a thread takes several rows, some of them idle: rows as they are one by one."""
+    _, t, _ = case((B, 1, D), "bf16", 14)
+    one = [t[n][:, 0].contiguous() for n in ("x", "r", "i")]
+    pool = torch.randn(B + 7, D, device="cuda")
+    slots = torch.randperm(B + 7, device="cuda")[:B].to(torch.int32)
+    slots[::9] = -1
+    slots[4::9] = B + 7
+    new, want = pool.clone(), pool.clone()
+    y = ssd.gated_linear_step(new, *one, t["lam"], slots=slots)
+    for b in range(B):
+        yb = ssd.gated_linear_step(want, *(v[b:b + 1] for v in one), t["lam"], slots=slots[b:b + 1].clone()) if D % 8 == 0 else \
+            ssd.gated_linear_step(want, *(v[b:b + 1].clone() for v in one), t["lam"], slots=slots[b:b + 1].clone())
+        assert torch.equal(yb[0], y[b])
+    assert torch.equal(new, want)
