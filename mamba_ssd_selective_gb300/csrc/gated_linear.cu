@@ -17,6 +17,8 @@
 // sender wait for everything it has written (B8 L2048 D5120: 193 us so, 176 without).
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "gated_linear.cuh"
 #include "launch.h"
 #include "ssd_scan.h"
@@ -726,6 +728,140 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
     }
 }
 
+// --------------------------------------------------------- short sequences
+// Up to kShort tokens, a run of the kernels above: a thread goes over V channels of a whole sequence alone, its tokens in registers;
+// there is nothing to join, and the number of sequences is what fills the device (forward B64 L16 D2560 9.8 us, 14.7 as above; B256 L1
+// D5120 17 and 86; backward 19 and 31, 54 and 225; a single sequence of 16 tokens 4.5 and 4.0, its backward 8.4 and 6.6: the rule goes
+// by the length alone, so that a sequence stays bitwise the same in any batch). 64 sequences of 17 tokens take 19 and 37 us.
+constexpr int kShort = kGroup, kShortThreads = 128;
+
+template <typename T, int V> __device__ __forceinline__ uint64_t two_of(const Raw<T, V> &w) { return f2(to_f32(w.v[0]), to_f32(w.v[V - 1])); }
+template <int V> __device__ __forceinline__ uint64_t two_at(const float *p, int64_t at) { return p ? f2(p[at], p[at + V - 1]) : 0; }
+template <typename T, int V> __device__ __forceinline__ void put_two(T *p, uint64_t v) {
+    float v0, v1;
+    un2(v, v0, v1);
+    Raw<T, V> r;
+    r.v[V - 1] = from_f32<T>(v1), r.v[0] = from_f32<T>(v0);
+    store<T, V>(p, r);
+}
+
+template <typename T, int V> __global__ void __launch_bounds__(kShortThreads) linear_fwd_short_kernel(LinearArgs p) {
+    pdl_enter();
+    const int64_t c0 = ((int64_t)blockIdx.x * kShortThreads + threadIdx.x) * V, b = blockIdx.y, D = p.D;
+    if (c0 >= D) return;
+    const int rows = (int)p.L, live = (int)seq_len(p.seqlens, b, p.L);
+    const int64_t at = b * p.L * D + c0;
+    Raw<T, V> w[3][kShort];
+#pragma unroll
+    for (int t = 0; t < kShort; ++t)
+        if (t < live) {
+            w[0][t] = load<T, V>((const T *)p.x + at + t * D);
+            w[1][t] = load<T, V>((const T *)p.r + at + t * D);
+            w[2][t] = load<T, V>((const T *)p.i + at + t * D);
+        }
+    const Rate2 k = Rate2::of(p.c * softplus(p.lam[c0]), p.c * softplus(p.lam[c0 + V - 1]));
+    uint64_t h = two_at<V>(p.init, b * D + c0), unused = 0;
+    if (p.states) put_two<float, V>(p.states + b * D + c0, h);
+#pragma unroll
+    for (int t = 0; t < kShort; ++t) {
+        if (t >= rows) break;
+        if (t < live) {
+            const Gates2 g = gates2<T, false, false>(two_of<T, V>(w[1][t]), two_of<T, V>(w[2][t]), k, unused);
+            h = fma2(g.a, h, mul2(g.f, two_of<T, V>(w[0][t])));
+        }
+        if (p.y) put_two<T, V>((T *)p.y + at + t * D, t < live ? h : 0);
+    }
+    if (p.final_state) put_two<float, V>(p.final_state + b * D + c0, h);
+    if (!p.values) return;
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+        uint32_t top0 = 0, top1 = 0;
+#pragma unroll
+        for (int t = 0; t < kShort; ++t)
+            if (t < live) top0 = max(top0, abs_bits(to_f32(w[z][t].v[0]))), top1 = max(top1, abs_bits(to_f32(w[z][t].v[V - 1])));
+        const uint32_t code0 = scale_code(top0), code1 = scale_code(top1);
+        Raw<uint8_t, V> code;
+        code.v[V - 1] = (uint8_t)code1, code.v[0] = (uint8_t)code0;
+        store<uint8_t, V>(p.scales + (z * p.B + b) * D + c0, code);
+        const uint64_t inv = f2(inverse_scale(code0), inverse_scale(code1));
+#pragma unroll
+        for (int t = 0; t < kShort; ++t) {
+            if (t >= rows) break;
+            float q0, q1;
+            un2(fma2(two_of<T, V>(w[z][t]), inv, f2(kToWhole)), q0, q1);
+            Raw<int8_t, V> q;
+            q.v[V - 1] = t < live && code1 != 255 ? (int8_t)(__float_as_uint(q1) & 0xff) : (int8_t)0;
+            q.v[0] = t < live && code0 != 255 ? (int8_t)(__float_as_uint(q0) & 0xff) : (int8_t)0;
+            store<int8_t, V>(p.values + z * p.B * p.L * D + at + t * D, q);
+        }
+    }
+}
+
+template <typename T, int V, bool PACK> __global__ void __launch_bounds__(kShortThreads) linear_bwd_short_kernel(LinearBwdArgs p) {
+    pdl_enter();
+    using W = std::conditional_t<PACK, int8_t, T>;
+    const int64_t c0 = ((int64_t)blockIdx.x * kShortThreads + threadIdx.x) * V, b = blockIdx.y, D = p.f.D, L = p.f.L;
+    if (c0 >= D) return;
+    const int rows = (int)L, live = (int)seq_len(p.f.seqlens, b, L);
+    const int64_t at = b * L * D + c0, plane = p.f.B * L * D;
+    const W *from[3];
+    if constexpr (PACK) {
+        from[0] = p.f.values, from[1] = p.f.values + plane, from[2] = p.f.values + 2 * plane;
+    } else {
+        from[0] = (const T *)p.f.x, from[1] = (const T *)p.f.r, from[2] = (const T *)p.f.i;
+    }
+    Raw<W, V> w[3][kShort];
+    Raw<T, V> dy[kShort];
+#pragma unroll
+    for (int t = 0; t < kShort; ++t)
+        if (t < live) {
+#pragma unroll
+            for (int z = 0; z < 3; ++z) w[z][t] = load<W, V>(from[z] + at + t * D);
+            dy[t] = load<T, V>((const T *)p.dy + at + t * D);
+        }
+    uint64_t scale[3] = {0, 0, 0};
+    if constexpr (PACK) {
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+            const Raw<uint8_t, V> code = load<uint8_t, V>(p.f.scales + (z * p.f.B + b) * D + c0);
+            scale[z] = f2(scale_of(code.v[0]), scale_of(code.v[V - 1]));
+        }
+    }
+    auto value = [&](int z, int t) {
+        if constexpr (PACK) return mul2(f2((float)w[z][t].v[0], (float)w[z][t].v[V - 1]), scale[z]);
+        else return two_of<T, V>(w[z][t]);
+    };
+    const Rate2 k = Rate2::of(p.f.c * softplus(p.f.lam[c0]), p.f.c * softplus(p.f.lam[c0 + V - 1]));
+    uint64_t before[kShort], h = two_at<V>(p.f.states, b * D + c0), m = two_at<V>(p.dfinal, b * D + c0), sum = 0, unused = 0;
+#pragma unroll
+    for (int t = 0; t < kShort; ++t) {
+        if (t >= live) break;
+        const Gates2 g = gates2<T, false, false>(value(1, t), value(2, t), k, unused);
+        before[t] = h;
+        h = fma2(g.a, h, mul2(g.f, value(0, t)));
+    }
+#pragma unroll
+    for (int t = kShort - 1; t >= 0; --t) {
+        if (t >= rows) continue;
+        uint64_t dx = 0, dr = 0, di = 0;
+        if (t < live) {
+            const Gates2 g = gates2<T, false, true>(value(1, t), value(2, t), k, unused);
+            const uint64_t bt = mul2(g.f, value(0, t)), dh = add2(m, two_of<T, V>(dy[t]));
+            const uint64_t factor = fma2(mul2(mul2(g.a, g.t), f2(-0.5f)), before[t], mul2(grad_ratio(g.t, g.a, true), bt)), psi = mul2(dh, factor);
+            dx = mul2(dh, g.f);
+            di = mul2(dh, mul2(bt, fma2(g.iota, f2(-1.f), f2(1.f))));
+            dr = mul2(psi, fma2(g.rho, f2(-1.f), f2(1.f)));
+            sum = add2(sum, psi);
+            m = mul2(g.a, dh);
+        }
+        put_two<T, V>((T *)p.dx + at + t * D, dx);
+        put_two<T, V>((T *)p.dr + at + t * D, dr);
+        put_two<T, V>((T *)p.di + at + t * D, di);
+    }
+    put_two<float, V>(p.part + b * D + c0, sum);
+    if (p.dinit) put_two<float, V>(p.dinit + b * D + c0, m);
+}
+
 // dlam from the blocks' sums, in float64: their number grows with the batch.
 __global__ void __launch_bounds__(256) linear_dlam_kernel(const float *part, const float *lam, float *dlam, int64_t rows, int64_t D) {
     pdl_enter();
@@ -970,6 +1106,10 @@ cudaError_t launch_clusters(const Args &a, const Maps &maps, int64_t items, int6
     return cudaLaunchKernelEx(&cfg, KERN, a, maps);
 }
 
+template <int V> dim3 short_grid(const LinearArgs &a) {
+    return dim3((unsigned)((a.D / V + kShortThreads - 1) / kShortThreads), (unsigned)a.B);
+}
+
 template <typename T, bool WIDE, bool PACK> cudaError_t forward_p(const LinearArgs &a, const FwdMaps &maps, cudaStream_t stream) {
     return launch_clusters<linear_fwd_kernel<T, WIDE, PACK>>(a, maps, a.B * ((a.D + kTile - 1) / kTile), a.L, kFwdRun, fwd_per_sm<T, PACK>(),
                                                              sizeof(FwdShared<T, WIDE, PACK>), stream, nullptr);
@@ -980,6 +1120,11 @@ template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t st
         return launch_programmatic(linear_keep_kernel, dim3((unsigned)((a.B * a.D + 255) / 256)), dim3(256), 0, stream, a.init,
                                    a.final_state, a.B * a.D);
     }
+    if (a.L <= kShort)
+        return for_width(a.D, [&](auto vw) {
+            constexpr int V = decltype(vw)::value;
+            return launch_programmatic(linear_fwd_short_kernel<T, V>, short_grid<V>(a), dim3(kShortThreads), 0, stream, a);
+        });
     FwdMaps m{};
     const int size = (int)sizeof(T);
     bool wide = a.D * size % 16 == 0 && tma_map_rows(&m.x, a.x, size, a.D, a.L, a.B, kTile, kState) &&
@@ -1000,7 +1145,14 @@ template <typename T> cudaError_t backward_t(const LinearBwdArgs &a, cudaStream_
     cudaError_t e = cudaSuccess;
     int blocks = 0;  // none has added to the sum for dlam
     const int64_t B = a.f.B, L = a.f.L, D = a.f.D;
-    if (B > 0 && L > 0) {
+    if (B > 0 && L > 0 && L <= kShort) {
+        blocks = 1;
+        e = for_width(D, [&](auto vw) {
+            constexpr int V = decltype(vw)::value;
+            return a.f.values ? launch_programmatic(linear_bwd_short_kernel<T, V, true>, short_grid<V>(a.f), dim3(kShortThreads), 0, stream, a)
+                              : launch_programmatic(linear_bwd_short_kernel<T, V, false>, short_grid<V>(a.f), dim3(kShortThreads), 0, stream, a);
+        });
+    } else if (B > 0 && L > 0) {
         BwdMaps m{};
         const int size = (int)sizeof(T);
         bool wide = D * size % 16 == 0 && tma_map_rows(&m.dy, a.dy, size, D, L, B, kTile, kState) &&
