@@ -585,7 +585,9 @@ ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32
  * the last bits. A sigmoid below 2^-126 counts as zero.
  * Sequences are taken by clusters of thread blocks, 64 channels each, whose
  * blocks lie one behind the other in time; rows that are multiples of 16 bytes
- * (in 8 bits: of 16 channels) move by the TMA, others by 4-byte copies.
+ * (in 8 bits: of 16 channels) move by the TMA, others by copies of two channels
+ * or, where dim is odd, of 4 bytes, in 1.4 and 2.8 times the time. Sequences of
+ * up to 16 tokens go a thread each.
  * ------------------------------------------------------------------------- */
 
 #define SSD_GATED_LINEAR_CHUNK 64 /* tokens between two saved states */

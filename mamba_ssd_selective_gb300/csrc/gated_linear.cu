@@ -44,44 +44,55 @@ template <typename T> __host__ __device__ constexpr int bwd_per_sm() { return si
 
 // ------------------------------------------------------- tiles in shared memory
 // WIDE, for rows that begin at a multiple of 16 bytes: a thread has the TMA bring the block's tiles and a lane of each warp
-// has it take the results away. Otherwise each warp fetches the rows of its own run by 4-byte copies: the aligned words around
-// each row, of those at the tensor's end and the tile's only the bytes that belong to the tensor; a row then begins up to 3 bytes
-// into its first word.
+// has it take the results away. Otherwise each warp fetches the rows of its own run: a pair of channels a lane where D is EVEN; else,
+// and bytes always, by 4-byte copies of the aligned words around each row, of those at the tensor's end and the tile's only the bytes
+// that belong to the tensor; a row then begins up to 3 bytes into its first word.
 template <typename T, bool WIDE> struct Row {
     static constexpr int kPitch = kTile * (int)sizeof(T) + (WIDE || sizeof(T) == 4 ? 0 : 4);
 };
 __device__ __forceinline__ void copy4(uint32_t to, const void *from, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
+template <int BYTES> __device__ __forceinline__ void copy_pair(uint32_t to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// Rows 0..n-1 of `cols` elements from `base` on, which lie D apart, by words.
-template <typename T, int PITCH>
+// Rows 0..n-1 of `cols` elements from `base` on, which lie D apart, R at most. EVEN: of pairs of elements.
+template <typename T, int PITCH, int R, bool EVEN>
 __device__ __forceinline__ void fetch_rows(unsigned char *to, const T *base, int n, int cols, int64_t D, int lane) {
     const uint32_t dst = tc::smem_u32(to);
-    const int have = cols * (int)sizeof(T);
-    const unsigned char *from = reinterpret_cast<const unsigned char *>(base);
-#pragma unroll 4
-    for (int t = 0; t < n; ++t, from += D * sizeof(T)) {
-        const int off = (int)(reinterpret_cast<uintptr_t>(from) & 3);
-        const unsigned char *word = from - off;
+    if constexpr (EVEN && sizeof(T) > 1) {  // a pair a lane
+        if (2 * lane >= cols) return;
+        const T *from = base + 2 * lane;
 #pragma unroll
-        for (int w = 0; w < (kTile * (int)sizeof(T) + 127 + (sizeof(T) == 4 ? 0 : 3)) / 128; ++w) {
-            const int at = 4 * lane + 128 * w, left = off + have - at;
-            if (left > 0) copy4(dst + t * PITCH + at, word + at, left < 4 ? left : 4);
+        for (int t = 0; t < R; ++t, from += D)
+            if (t < n) copy_pair<2 * sizeof(T)>(dst + t * PITCH + lane * 2 * (int)sizeof(T), from);
+    } else {
+        const int have = cols * (int)sizeof(T);
+        const unsigned char *from = reinterpret_cast<const unsigned char *>(base);
+#pragma unroll 4
+        for (int t = 0; t < n; ++t, from += D * sizeof(T)) {
+            const int off = (int)(reinterpret_cast<uintptr_t>(from) & 3);
+            const unsigned char *word = from - off;
+#pragma unroll
+            for (int w = 0; w < (kTile * (int)sizeof(T) + 127 + (sizeof(T) == 4 ? 0 : 3)) / 128; ++w) {
+                const int at = 4 * lane + 128 * w, left = off + have - at;
+                if (left > 0) copy4(dst + t * PITCH + at, word + at, left < 4 ? left : 4);
+            }
         }
     }
 }
 // Bytes that a row from `at` elements on begins into its first word.
-template <typename T, bool WIDE> __device__ __forceinline__ int shift(const void *base, int64_t at) {
-    return WIDE || sizeof(T) == 4 ? 0 : (int)((reinterpret_cast<uintptr_t>(base) + (uintptr_t)at * sizeof(T)) & 3);
+template <typename T, bool WIDE, bool EVEN> __device__ __forceinline__ int shift(const void *base, int64_t at) {
+    return WIDE || sizeof(T) == 4 || (EVEN && sizeof(T) == 2) ? 0 : (int)((reinterpret_cast<uintptr_t>(base) + (uintptr_t)at * sizeof(T)) & 3);
 }
 // The two channels of a lane in a row.
-template <typename T, bool WIDE> __device__ __forceinline__ Raw<T, 2> row_pair(const unsigned char *row, int off, int lane, bool both) {
+template <typename T, bool EVEN> __device__ __forceinline__ Raw<T, 2> row_pair(const unsigned char *row, int off, int lane, bool both) {
     Raw<T, 2> r;
     const T *p = reinterpret_cast<const T *>(row + off) + 2 * lane;
-    if constexpr (WIDE) {
+    if constexpr (EVEN) {
         r.word = *reinterpret_cast<const decltype(r.word) *>(p);
     } else {
         r.v[0] = p[0], r.v[1] = both ? p[1] : p[0];
@@ -96,8 +107,8 @@ template <typename T> __device__ __forceinline__ Raw<T, 2> rounded(uint64_t v) {
     return r;
 }
 // The same two channels in global memory; `one` and `both`: whether they exist.
-template <typename T, bool WIDE> __device__ __forceinline__ void store_pair(T *p, const Raw<T, 2> &r, bool one, bool both) {
-    if constexpr (WIDE) {
+template <typename T, bool EVEN> __device__ __forceinline__ void store_pair(T *p, const Raw<T, 2> &r, bool one, bool both) {
+    if constexpr (EVEN) {
         if (one) store<T, 2>(p, r);
     } else {
         if (one) p[0] = r.v[0];
@@ -105,11 +116,12 @@ template <typename T, bool WIDE> __device__ __forceinline__ void store_pair(T *p
     }
 }
 // A lane's two channels of a warp's run, for the TMA to take away or to global memory at once.
-template <typename T, bool WIDE> __device__ __forceinline__ void put_pair(unsigned char *row, T *p, const Raw<T, 2> &r, bool exists, bool one, bool both, int lane) {
+template <typename T, bool WIDE, bool EVEN>
+__device__ __forceinline__ void put_pair(unsigned char *row, T *p, const Raw<T, 2> &r, bool exists, bool one, bool both, int lane) {
     if constexpr (WIDE) {
         *reinterpret_cast<decltype(r.word) *>(row + 2 * sizeof(T) * lane) = r.word;
     } else {
-        if (exists) store_pair<T, WIDE>(p, r, one, both);
+        if (exists) store_pair<T, EVEN>(p, r, one, both);
     }
 }
 
@@ -240,7 +252,7 @@ struct FwdMaps {
 };
 
 // A run's x, r and i (z 0, 1, 2) in 8 bits, to `out`, the run's place in FwdShared::q. ALL: every token of it counts.
-template <typename T, bool WIDE, bool ALL, typename F>
+template <typename T, bool WIDE, bool EVEN, bool ALL, typename F>
 __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const F &pair, unsigned char (*out)[kTile], const Step &s, int place, int live, int rows,
                                                 int lane) {
     constexpr int R = kFwdRun;
@@ -266,7 +278,7 @@ __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const F &pa
         Raw<uint8_t, 2> code;
         code.v[0] = (uint8_t)scale_code(top0), code.v[1] = (uint8_t)scale_code(top1);
         const int64_t groups = (p.L + kGroup - 1) / kGroup;
-        store_pair<uint8_t, WIDE>(p.scales + ((z * p.B + s.b) * groups + (s.t0 + place) / kGroup) * D + s.c0 + 2 * lane, code, one, both);
+        store_pair<uint8_t, EVEN>(p.scales + ((z * p.B + s.b) * groups + (s.t0 + place) / kGroup) * D + s.c0 + 2 * lane, code, one, both);
         const uint64_t inv = f2(inverse_scale(code.v[0]), inverse_scale(code.v[1]));
         const uint32_t mask = (code.v[0] == 255 ? 0u : 0xffu) | (code.v[1] == 255 ? 0u : 0xff00u);
         int8_t *values = p.values + (z * p.B * p.L + place) * D + s.base + 2 * lane;
@@ -276,12 +288,12 @@ __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const F &pa
             un2(fma2(pair_of(w[t]), inv, f2(kToWhole)), q0, q1);
             Raw<int8_t, 2> q;
             q.word = (uint16_t)(ALL || t < live ? __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x0040) & mask : 0u);
-            put_pair<int8_t, WIDE>(out[WIDE ? z * R + t : 0], values + t * D, q, t < rows, one, both, lane);
+            put_pair<int8_t, WIDE, EVEN>(out[WIDE ? z * R + t : 0], values + t * D, q, t < rows, one, both, lane);
         }
     }
 }
 
-template <typename T, bool WIDE, bool PACK>
+template <typename T, bool WIDE, bool EVEN, bool PACK>
 __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_fwd_kernel(LinearArgs p, const __grid_constant__ FwdMaps maps) {
     namespace cg = cooperative_groups;
     pdl_wait();
@@ -326,9 +338,9 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
             const Step s = sh.step[step & 3];
             const int live = s.cols > 0 ? run_of(R, s.live, place) : 0;
             const int64_t at = s.base + place * D;
-            fetch_rows<T, PITCH>(sh.in[0][place], (const T *)p.x + at, live, s.cols, D, lane);
-            fetch_rows<T, PITCH>(sh.in[1][place], (const T *)p.r + at, live, s.cols, D, lane);
-            fetch_rows<T, PITCH>(sh.in[2][place], (const T *)p.i + at, live, s.cols, D, lane);
+            fetch_rows<T, PITCH, R, EVEN>(sh.in[0][place], (const T *)p.x + at, live, s.cols, D, lane);
+            fetch_rows<T, PITCH, R, EVEN>(sh.in[1][place], (const T *)p.r + at, live, s.cols, D, lane);
+            fetch_rows<T, PITCH, R, EVEN>(sh.in[2][place], (const T *)p.i + at, live, s.cols, D, lane);
             copy_commit();
         }
     };
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
         }
         auto pair = [&](int z, int t) {
             const void *base = z == 0 ? p.x : z == 1 ? p.r : p.i;
-            return row_pair<T, WIDE>(sh.in[z][place + t], shift<T, WIDE>(base, at - 2 * lane + t * D), lane, both);
+            return row_pair<T, EVEN>(sh.in[z][place + t], shift<T, WIDE, EVEN>(base, at - 2 * lane + t * D), lane, both);
         };
         uint64_t a[R], h[R];
         Run2 own;
@@ -399,9 +411,9 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
             if (rows > 0) {
                 auto *out = &sh.q[WIDE ? 3 * place : 0];
                 if (live == R)
-                    leave_in_8_bits<T, WIDE, true>(p, pair, out, s, place, live, rows, lane);
+                    leave_in_8_bits<T, WIDE, EVEN, true>(p, pair, out, s, place, live, rows, lane);
                 else
-                    leave_in_8_bits<T, WIDE, false>(p, pair, out, s, place, live, rows, lane);
+                    leave_in_8_bits<T, WIDE, EVEN, false>(p, pair, out, s, place, live, rows, lane);
                 if constexpr (WIDE) {
                     tc::fence_proxy_async_smem();
                     __syncwarp();
@@ -422,13 +434,13 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
         if (planner) sh.step[(step + 2) & 3] = sh.walk.next(p);
         uint64_t e = after(before, exchange_receive(sh.exchange, step, rank, blocks, lane, alive, carry));  // the state that enters this run
         if (warp == 0 && rows > 0 && p.states)
-            store_pair<float, WIDE>(p.states + (s.b * ((L + kState - 1) / kState) + s.t0 / kState) * D + s.c0 + 2 * lane, rounded<float>(e), one, both);
+            store_pair<float, EVEN>(p.states + (s.b * ((L + kState - 1) / kState) + s.t0 / kState) * D + s.c0 + 2 * lane, rounded<float>(e), one, both);
         if (p.y && rows > 0) {
             auto results = [&](auto whole) {
 #pragma unroll
                 for (int t = 0; t < R; ++t) {
                     e = fma2(a[t], e, h[t]);
-                    put_pair<T, WIDE>(sh.y[WIDE ? place + t : 0], (T *)p.y + at + t * D, rounded<T>(decltype(whole)::value || t < live ? e : 0), t < rows,
+                    put_pair<T, WIDE, EVEN>(sh.y[WIDE ? place + t : 0], (T *)p.y + at + t * D, rounded<T>(decltype(whole)::value || t < live ? e : 0), t < rows,
                                       one, both, lane);
                 }
             };
@@ -441,7 +453,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
         }
         if (WIDE && lane == 0) tc::bulk_commit();
         if (s.ends && rank == 0 && warp == 0 && p.final_state)
-            store_pair<float, WIDE>(p.final_state + s.b * D + s.c0 + 2 * lane, rounded<float>(carry), one, both);
+            store_pair<float, EVEN>(p.final_state + s.b * D + s.c0 + 2 * lane, rounded<float>(carry), one, both);
     }
     if constexpr (WIDE) {
         if (lane == 0) tc::bulk_wait_all();
@@ -493,7 +505,7 @@ __device__ __forceinline__ uint64_t from_8(uint32_t two, uint64_t scale) {
     return mul2(add2(n, f2(-8388736.f)), scale);
 }
 
-template <typename T, bool WIDE, bool PACK>
+template <typename T, bool WIDE, bool EVEN, bool PACK>
 __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_kernel(LinearBwdArgs p, const __grid_constant__ BwdMaps maps) {
     namespace cg = cooperative_groups;
     pdl_wait();
@@ -552,17 +564,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
             if (live > 0) {
                 if constexpr (PACK) {
                     for (int z = 0; z < 3; ++z) {
-                        fetch_rows<int8_t, PITCH>(sh.in[z][place], p.f.values + z * plane + at, live, s.cols, D, lane);
+                        fetch_rows<int8_t, PITCH, R, EVEN>(sh.in[z][place], p.f.values + z * plane + at, live, s.cols, D, lane);
                         if (place % kGroup == 0)  // one of a group's two runs brings its scale
-                            fetch_rows<uint8_t, SC>(sh.scale[z][place / kGroup], p.f.scales + z * scales + (s.b * groups + (s.t0 + place) / kGroup) * D + s.c0, 1,
+                            fetch_rows<uint8_t, SC, 1, EVEN>(sh.scale[z][place / kGroup], p.f.scales + z * scales + (s.b * groups + (s.t0 + place) / kGroup) * D + s.c0, 1,
                                                     s.cols, D, lane);
                     }
                 } else {
-                    fetch_rows<T, PITCH>(sh.in[0][place], (const T *)p.f.x + at, live, s.cols, D, lane);
-                    fetch_rows<T, PITCH>(sh.in[1][place], (const T *)p.f.r + at, live, s.cols, D, lane);
-                    fetch_rows<T, PITCH>(sh.in[2][place], (const T *)p.f.i + at, live, s.cols, D, lane);
+                    fetch_rows<T, PITCH, R, EVEN>(sh.in[0][place], (const T *)p.f.x + at, live, s.cols, D, lane);
+                    fetch_rows<T, PITCH, R, EVEN>(sh.in[1][place], (const T *)p.f.r + at, live, s.cols, D, lane);
+                    fetch_rows<T, PITCH, R, EVEN>(sh.in[2][place], (const T *)p.f.i + at, live, s.cols, D, lane);
                 }
-                fetch_rows<T, DY>(sh.dy[step & 1][place], (const T *)p.dy + at, live, s.cols, D, lane);
+                fetch_rows<T, DY, R, EVEN>(sh.dy[step & 1][place], (const T *)p.dy + at, live, s.cols, D, lane);
             }
             copy_commit();
         }
@@ -614,23 +626,23 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
         if constexpr (PACK) {
 #pragma unroll
             for (int z = 0; z < 3; ++z) {
-                const Raw<uint8_t, 2> code = row_pair<uint8_t, WIDE>(
-                    sh.scale[z][place / kGroup], shift<uint8_t, WIDE>(p.f.scales, z * scales + (s.b * groups + t0 / kGroup) * D + s.c0), lane, both);
+                const Raw<uint8_t, 2> code = row_pair<uint8_t, EVEN>(
+                    sh.scale[z][place / kGroup], shift<uint8_t, WIDE, EVEN>(p.f.scales, z * scales + (s.b * groups + t0 / kGroup) * D + s.c0), lane, both);
                 scale[z] = f2(scale_of(code.v[0]), scale_of(code.v[1]));
             }
         }
         auto value = [&](int z, int t) {
             if constexpr (PACK) {
                 const Raw<int8_t, 2> q =
-                    row_pair<int8_t, WIDE>(sh.in[z][place + t], shift<int8_t, WIDE>(p.f.values, z * plane + at - 2 * lane + t * D), lane, both);
+                    row_pair<int8_t, EVEN>(sh.in[z][place + t], shift<int8_t, WIDE, EVEN>(p.f.values, z * plane + at - 2 * lane + t * D), lane, both);
                 return from_8(q.word, scale[z]);
             } else {
                 const void *base = z == 0 ? p.f.x : z == 1 ? p.f.r : p.f.i;
-                return pair_of(row_pair<T, WIDE>(sh.in[z][place + t], shift<T, WIDE>(base, at - 2 * lane + t * D), lane, both));
+                return pair_of(row_pair<T, EVEN>(sh.in[z][place + t], shift<T, WIDE, EVEN>(base, at - 2 * lane + t * D), lane, both));
             }
         };
         auto dy_of = [&](int t) {
-            return pair_of(row_pair<T, WIDE>(sh.dy[step & 1][place + t], shift<T, WIDE>(p.dy, at - 2 * lane + t * D), lane, both));
+            return pair_of(row_pair<T, EVEN>(sh.dy[step & 1][place + t], shift<T, WIDE, EVEN>(p.dy, at - 2 * lane + t * D), lane, both));
         };
         uint64_t a[R], b[R], f[R], rho[R], d[R];
         Run2 own;    // of m, backwards
@@ -699,7 +711,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
                     m = mul2(a[t], dh);
 #pragma unroll
                     for (int z = 0; z < 3; ++z)
-                        put_pair<T, WIDE>(sh.out[WIDE ? z * kState + place + t : 0], (T *)(z == 0 ? p.dx : z == 1 ? p.dr : p.di) + at + t * D,
+                        put_pair<T, WIDE, EVEN>(sh.out[WIDE ? z * kState + place + t : 0], (T *)(z == 0 ? p.dx : z == 1 ? p.dr : p.di) + at + t * D,
                                           rounded<T>(ALL || t < live ? v[z] : 0), t < rows, one, both, lane);
                 }
             };
@@ -720,8 +732,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
             __syncthreads();
             if (warp == 0) {
                 for (int w = 1; w < warps; ++w) sum = add2(sum, sh.sum[w][lane]);
-                store_pair<float, WIDE>(p.part + ((int64_t)s.b * blocks + rank) * D + c, rounded<float>(sum), one, both);
-                if (rank == 0 && p.dinit) store_pair<float, WIDE>(p.dinit + s.b * D + c, rounded<float>(carry), one, both);
+                store_pair<float, EVEN>(p.part + ((int64_t)s.b * blocks + rank) * D + c, rounded<float>(sum), one, both);
+                if (rank == 0 && p.dinit) store_pair<float, EVEN>(p.dinit + s.b * D + c, rounded<float>(carry), one, both);
             }
         }
     }
@@ -1114,8 +1126,8 @@ template <int V> dim3 short_grid(const LinearArgs &a) {
     return dim3((unsigned)((a.D / V + kShortThreads - 1) / kShortThreads), (unsigned)a.B);
 }
 
-template <typename T, bool WIDE, bool PACK> cudaError_t forward_p(const LinearArgs &a, const FwdMaps &maps, cudaStream_t stream) {
-    return launch_clusters<linear_fwd_kernel<T, WIDE, PACK>>(a, maps, a.B * ((a.D + kTile - 1) / kTile), a.L, kFwdRun, fwd_per_sm<T, PACK>(),
+template <typename T, bool WIDE, bool EVEN, bool PACK> cudaError_t forward_p(const LinearArgs &a, const FwdMaps &maps, cudaStream_t stream) {
+    return launch_clusters<linear_fwd_kernel<T, WIDE, EVEN, PACK>>(a, maps, a.B * ((a.D + kTile - 1) / kTile), a.L, kFwdRun, fwd_per_sm<T, PACK>(),
                                                              sizeof(FwdShared<T, WIDE, PACK>), stream, nullptr);
 }
 template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t stream) {
@@ -1136,13 +1148,15 @@ template <typename T> cudaError_t forward_t(const LinearArgs &a, cudaStream_t st
                 (!a.y || tma_map_rows(&m.y, a.y, size, a.D, a.L, a.B, kTile, kFwdRun));
     if (a.values) {
         wide = wide && a.D % 16 == 0 && tma_map_planes(&m.q, a.values, a.D, a.L, a.B, 3, kTile, kFwdRun);
-        return wide ? forward_p<T, true, true>(a, m, stream) : forward_p<T, false, true>(a, m, stream);
+        if (wide) return forward_p<T, true, true, true>(a, m, stream);
+        return a.D % 2 == 0 ? forward_p<T, false, true, true>(a, m, stream) : forward_p<T, false, false, true>(a, m, stream);
     }
-    return wide ? forward_p<T, true, false>(a, m, stream) : forward_p<T, false, false>(a, m, stream);
+    if (wide) return forward_p<T, true, true, false>(a, m, stream);
+    return a.D % 2 == 0 ? forward_p<T, false, true, false>(a, m, stream) : forward_p<T, false, false, false>(a, m, stream);
 }
 
-template <typename T, bool WIDE, bool PACK> cudaError_t backward_p(const LinearBwdArgs &a, const BwdMaps &maps, cudaStream_t stream, int *blocks) {
-    return launch_clusters<linear_bwd_kernel<T, WIDE, PACK>>(a, maps, a.f.B * ((a.f.D + kTile - 1) / kTile), a.f.L, kBwdRun,
+template <typename T, bool WIDE, bool EVEN, bool PACK> cudaError_t backward_p(const LinearBwdArgs &a, const BwdMaps &maps, cudaStream_t stream, int *blocks) {
+    return launch_clusters<linear_bwd_kernel<T, WIDE, EVEN, PACK>>(a, maps, a.f.B * ((a.f.D + kTile - 1) / kTile), a.f.L, kBwdRun,
                                                              bwd_per_sm<T>(), sizeof(BwdShared<T, WIDE, PACK>), stream, blocks);
 }
 template <typename T> cudaError_t backward_t(const LinearBwdArgs &a, cudaStream_t stream) {
@@ -1165,11 +1179,15 @@ template <typename T> cudaError_t backward_t(const LinearBwdArgs &a, cudaStream_
         if (a.f.values) {
             wide = wide && D % 16 == 0 && tma_map_planes(&m.q, a.f.values, D, L, B, 3, kTile, kState) &&
                    tma_map_planes(&m.scale, a.f.scales, D, (L + kGroup - 1) / kGroup, B, 3, kTile, kState / kGroup);
-            e = wide ? backward_p<T, true, true>(a, m, stream, &blocks) : backward_p<T, false, true>(a, m, stream, &blocks);
+            e = wide         ? backward_p<T, true, true, true>(a, m, stream, &blocks)
+                : D % 2 == 0 ? backward_p<T, false, true, true>(a, m, stream, &blocks)
+                             : backward_p<T, false, false, true>(a, m, stream, &blocks);
         } else {
             wide = wide && tma_map_rows(&m.x, a.f.x, size, D, L, B, kTile, kState) && tma_map_rows(&m.r, a.f.r, size, D, L, B, kTile, kState) &&
                    tma_map_rows(&m.i, a.f.i, size, D, L, B, kTile, kState);
-            e = wide ? backward_p<T, true, false>(a, m, stream, &blocks) : backward_p<T, false, false>(a, m, stream, &blocks);
+            e = wide         ? backward_p<T, true, true, false>(a, m, stream, &blocks)
+                : D % 2 == 0 ? backward_p<T, false, true, false>(a, m, stream, &blocks)
+                             : backward_p<T, false, false, false>(a, m, stream, &blocks);
         }
     } else if (B > 0 && a.dinit && a.dinit != a.dfinal) {
         e = launch_programmatic(linear_keep_kernel, dim3((unsigned)((B * D + 255) / 256)), dim3(256), 0, stream, a.dfinal, a.dinit, B * D);
