@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
         auto dy_of = [&](int t) {
             return pair_of(row_pair<T, EVEN>(sh.dy[step & 1][place + t], shift<T, WIDE, EVEN>(p.dy, at - 2 * lane + t * D), lane, both));
         };
-        uint64_t a[R], b[R], f[R], rho[R], d[R];
+        uint64_t a[R], b[R], f[R], er[R], d[R];  // er: e^-r, from which rho and 1 - rho are formed again
         Run2 own;    // of m, backwards
         uint64_t H;  // and of h, forwards; its A is the same
         uint64_t args = 0;
@@ -654,9 +654,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
 #pragma unroll
             for (int t = 0; t < R; ++t) {
                 const Gates2 g = gates2<T, FAST, true>(value(1, t), value(2, t), rate, args);
-                a[t] = g.a, f[t] = g.f, rho[t] = g.rho;
+                a[t] = g.a, f[t] = g.f, er[t] = g.er;
                 b[t] = mul2(g.f, value(0, t));
-                d[t] = mul2(b[t], fma2(g.iota, f2(-1.f), f2(1.f)));
+                d[t] = mul2(b[t], g.not_iota);
                 if (!FAST && t >= live) a[t] = f2(1.f), b[t] = 0;
                 H = fma2(a[t], H, b[t]);
             }
@@ -688,16 +688,18 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
         exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
         bring(step + 1);  // behind the sending, which the others wait for
         if (planner) sh.step[(step + 2) & 3] = sh.walk.next(p.f);
-        // h over the earlier runs (the later warps') to this one; then b becomes what multiplies dh in psi, and rho 1 - rho
+        // h over the earlier runs (the later warps') to this one; then b becomes what multiplies dh in psi, and er 1 - rho
 #pragma unroll 1
         for (int w = warps - 1; w > warp; --w) h = fma2(sh.run[step & 1][w][lane].a, h, sh.h[step & 1][w][lane]);
 #pragma unroll
         for (int t = 0; t < R; ++t) {
-            const uint64_t w2 = mul2(rho[t], rate.twice), g = grad_ratio(w2, a[t], steep);
+            float u0, u1;
+            un2(add2(er[t], f2(1.f)), u0, u1);
+            const uint64_t rho = f2(rcp_approx(u0), rcp_approx(u1)), w2 = mul2(rho, rate.twice), g = grad_ratio(w2, a[t], steep);
             const uint64_t factor = fma2(mul2(mul2(a[t], w2), f2(-0.5f)), h, mul2(g, b[t]));
             h = fma2(a[t], h, b[t]);
             b[t] = factor;
-            rho[t] = fma2(rho[t], f2(-1.f), f2(1.f));
+            er[t] = mul2(er[t], rho);
         }
         uint64_t m = after(before, exchange_receive(sh.exchange, step, rank, blocks, lane, alive, carry));  // from the later runs
         if (rows > 0) {
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
 #pragma unroll
                 for (int t = R - 1; t >= 0; --t) {
                     const uint64_t dh = add2(m, ALL || t < live ? dy_of(t) : 0), psi = mul2(dh, b[t]);
-                    const uint64_t v[3] = {mul2(dh, f[t]), mul2(psi, rho[t]), mul2(dh, d[t])};
+                    const uint64_t v[3] = {mul2(dh, f[t]), mul2(psi, er[t]), mul2(dh, d[t])};
                     if (ALL || t < live) sum = add2(sum, psi);
                     m = mul2(a[t], dh);
 #pragma unroll
@@ -865,8 +867,8 @@ template <typename T, int V, bool PACK> __global__ void __launch_bounds__(kShort
             const uint64_t bt = mul2(g.f, value(0, t)), dh = add2(m, two_of<T, V>(dy[t]));
             const uint64_t factor = fma2(mul2(mul2(g.a, g.t), f2(-0.5f)), before[t], mul2(grad_ratio(g.t, g.a, true), bt)), psi = mul2(dh, factor);
             dx = mul2(dh, g.f);
-            di = mul2(dh, mul2(bt, fma2(g.iota, f2(-1.f), f2(1.f))));
-            dr = mul2(psi, fma2(g.rho, f2(-1.f), f2(1.f)));
+            di = mul2(dh, mul2(bt, g.not_iota));
+            dr = mul2(psi, mul2(g.er, g.rho));
             sum = add2(sum, psi);
             m = mul2(g.a, dh);
         }

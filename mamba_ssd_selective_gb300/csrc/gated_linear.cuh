@@ -106,6 +106,9 @@ template <typename T> __device__ __forceinline__ uint64_t exp_minus(uint64_t x) 
 // FAST, for what nearly every run of tokens is: k below kSteep, so that t < 1, and r and i (r + 2 i above -88 or so) such that the
 // argument of one reciprocal root, sqrt(rho) iota = 1 / sqrt((1 + e^-r) (1 + e^-i)^2), is finite: `sum` adds them up and tells.
 // Three calls of the special function unit a token and channel instead of four, and no choice.
+// The gradients of r and i have 1 - rho and 1 - iota: e^-r rho and e^-i iota, as a difference of an open gate is its error and no more
+// (at r = 16 zero or negative). A gate that is zero has an infinite exponential, which counts as the largest number: the product, zero
+// then, meets nothing but a zero.
 constexpr float kSteep = 0.5f;
 struct Rate2 {  // of two channels: 2 k, sqrt(2 k)
     uint64_t twice, root;
@@ -113,13 +116,20 @@ struct Rate2 {  // of two channels: 2 k, sqrt(2 k)
         return {f2(2.f * k0, 2.f * k1), f2(sqrtf(2.f * k0), sqrtf(2.f * k1))};
     }
 };
+__device__ __forceinline__ uint64_t finite2(uint64_t e) {
+    float e0, e1;
+    un2(e, e0, e1);
+    return f2(fminf(e0, 3.402823466e38f), fminf(e1, 3.402823466e38f));
+}
 struct Gates2 {
-    uint64_t a, f, rho, iota, t;
+    uint64_t a, f, rho, t;
+    uint64_t er, not_iota;  // GRAD: e^-r, finite; 1 - iota
 };
 template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 gates2(uint64_t r, uint64_t i, const Rate2 &k, uint64_t &sum) {
     Gates2 o;
-    const uint64_t one = f2(1.f), u = add2(exp_minus<T>(r), one), v = add2(exp_minus<T>(i), one);
+    const uint64_t one = f2(1.f), er = exp_minus<T>(r), ei = exp_minus<T>(i), u = add2(er, one), v = add2(ei, one);
     uint64_t z;  // sqrt(rho) iota
+    uint64_t iota;
     float x0, x1;
     if constexpr (FAST) {
         const uint64_t uv = mul2(u, v), uvv = mul2(uv, v);
@@ -128,14 +138,16 @@ template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 ga
         z = f2(rsqrt_approx(x0), rsqrt_approx(x1));
         const uint64_t m = mul2(z, v);
         o.rho = mul2(m, m);
-        if (GRAD) o.iota = mul2(mul2(z, z), uv);
+        if (GRAD) o.not_iota = mul2(mul2(z, z), mul2(uv, ei));
     } else {
         un2(u, x0, x1);
         const uint64_t m = f2(rsqrt_approx(x0), rsqrt_approx(x1));
         un2(v, x0, x1);
-        o.iota = f2(rcp_approx(x0), rcp_approx(x1));
-        o.rho = mul2(m, m), z = mul2(m, o.iota);
+        iota = f2(rcp_approx(x0), rcp_approx(x1));
+        o.rho = mul2(m, m), z = mul2(m, iota);
+        if (GRAD) o.not_iota = mul2(finite2(ei), iota);
     }
+    if (GRAD) o.er = FAST ? er : finite2(er);
     o.t = mul2(o.rho, k.twice);
     uint64_t e = fma2(o.t, f2(-0.00022097997134551406f), f2(0.002580259693786502f));
     e = fma2(o.t, e, f2(-0.0208286102861166f));
@@ -150,7 +162,7 @@ template <typename T, bool FAST, bool GRAD> __device__ __forceinline__ Gates2 ga
     if constexpr (!FAST) {  // t >= 1: 1 - a^2 from a^2 <= 0.37
         float t0, t1, i0, i1, f0, f1, a0, a1;
         un2(o.t, t0, t1);
-        un2(o.iota, i0, i1);
+        un2(iota, i0, i1);
         un2(o.f, f0, f1);
         un2(o.a, a0, a1);
         if (!(t0 < 1.f)) a0 = ex2_approx(-0.5f * kLog2e * t0), f0 = fmaf(-a0, a0, 1.f), f0 = f0 * rsqrt_approx(f0) * i0;

@@ -1,0 +1,60 @@
+"""The gated linear recurrence where it can go wrong: gates that are nearly open or shut, number by number."""
+import numpy as np
+import pytest
+import torch
+
+from mamba_ssd_selective_gb300 import inputs
+from oracle import linear
+from tests.helpers import IO_TORCH, dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+def on_device(d, io):
+    return {n: dev(v, IO_TORCH[io] if n in ("x", "r", "i", "dy") else torch.float32) for n, v in d.items()}
+
+
+def tokens(t):
+    return [t[n] for n in ("x", "r", "i", "lam")]
+
+
+# ------------------------------------------------------------- saturated gates
+
+@pytest.mark.parametrize("size", [(2, 7, 64), (1, 16, 5), (2, 100, 72), (1, 130, 33), (2, 90, 6)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rate", [1.0, 40.0])
+@pytest.mark.parametrize("packed", [False, True])
+def test_gradients_of_saturated_gates_number_by_number(ssd, size, io, rate, packed):
+    """r and i from 8 to 30 (a quarter of them from -30 to -8), where 1 - sigmoid is 3e-4 to 1e-13: dr and di each within the error of
+    its own terms. x, dy and the states are positive, so that only the two terms of dr can cancel.
+
+    An exponential at |30| is off by 30e-7 of its argument and 2 units of 2^-23: 3.3e-6. di = dh b (1 - iota): dh 3.3e-6 by the decays and
+    20 units of 2^-24; b 3.3e-6 by iota and half of it by the root of rho; 1 - iota twice: 16e-6. dr has w (3.3e-6), h (that of b and of
+    dh) or the polynomial of the ratio (1.2e-6): 23e-6 of the sum of its terms. Results in bf16 are off by another 2^-8 at most."""
+    d = inputs.linear_inputs(*size, io, seed=21, rate=rate)
+    rng = np.random.default_rng(22)
+    for n in ("r", "i"):
+        d[n] = inputs.round_to(rng.uniform(8, 30, size) * np.where(rng.random(size) < 0.25, -1, 1), io)
+    for n in ("x", "dy", "init", "dfinal"):
+        d[n] = np.abs(d[n])
+    t = on_device(d, io)
+    kept = ssd.gated_linear_checkpoint(t["x"])
+    ssd.gated_linear_chunked(*tokens(t), init_state=t["init"], **kept)
+    if packed:
+        for n in ("x", "r", "i"):
+            d[n] = linear.unpack8(*linear.pack8(d[n]))
+        got = ssd.gated_linear_chunked_bwd_packed(lam=t["lam"], dy=t["dy"], dfinal_state=t["dfinal"], **kept)
+    else:
+        got = ssd.gated_linear_chunked_bwd(*tokens(t), t["dy"], states=kept["states"], dfinal_state=t["dfinal"])
+    want = linear.linear_seq_bwd(*(d[n] for n in ("x", "r", "i", "lam", "dy")), 8.0, d["init"], d["dfinal"], states=host(kept["states"]))
+    w, a, beta, iota = linear.gates(d["x"], d["r"], d["i"], d["lam"], 8.0)
+    y, _, entering = linear.linear_seq(d["x"], d["r"], d["i"], d["lam"], 8.0, d["init"], states=host(kept["states"]))
+    before = np.concatenate([entering[:, :1], y[:, :-1]], 1)
+    before[:, ::64] = entering
+    dh = want["dx"] / (beta * iota)
+    terms = dict(di=np.abs(want["di"]), dr=dh * linear.sigmoid(-d["r"]) * (a * a * w / beta * iota * np.abs(d["x"]) + a * w * before))
+    for n, whole in terms.items():
+        off = np.abs(host(got[n]) - want[n])
+        most = 2.5e-5 * whole + (2.0 ** -8 * np.abs(want[n]) if io == "bf16" else 0)
+        assert (off <= most).all(), f"{n}: {np.max(off / np.maximum(whole, 1e-300)):.2e} of its terms"
+    assert (host(got["di"]) >= 0).all()
