@@ -577,8 +577,10 @@ ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32
  *     w_t = c softplus(lam) sigmoid(r_t)      a_t = exp(-w_t)
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t      y_t = h_t
  *
- * States, decays and sums are float32. A sequence gives bitwise the same y and
- * states alone as in a batch, and every call repeats itself bitwise. A NaN or
+ * States, decays and sums are float32. A sequence gives bitwise the same y,
+ * states and 8 bits alone as in a batch, whatever it is padded to (its gradients
+ * in a batch of the same padded length; dlam is a sum over the batch), and every
+ * call repeats itself bitwise. A NaN or
  * an infinity in a token reaches the later tokens of its channel (in the
  * backward the earlier ones too, and the channel's dlam) and no other channel;
  * where it is in r or i, or a gate is below -29, its neighbours can differ in

@@ -9,7 +9,7 @@
 // block join theirs in shared memory, each block sends its own to the others of its cluster, and every warp goes over its run
 // again from the state that enters it. The cluster then takes the next tokens of the sequence, the state kept by all of its
 // threads, then another tile. Blocks' tokens are always joined one block after the other, so the result depends neither on the
-// cluster's size nor on the batch. Tokens past a sequence's end act as a = 1, b = 0.
+// cluster's size nor on the batch nor on the padding. Tokens past a sequence's end act as a = 1, b = 0.
 //
 // What costs a step is latency more than anything: of the special functions, of the joining. So a block is small and an SM holds
 // four of them, each at another place of its step (with 128 tokens a block and two an SM, B1 L65536 D1536 took 261 us where this took
@@ -37,6 +37,7 @@ constexpr int kBwdRun = 8;                // and in the backward, which keeps fi
 constexpr int kBwdWarps = kState / kBwdRun;
 constexpr int kMaxCluster = 16;
 constexpr int kPackWarps = 8;
+constexpr int kShort = kGroup, kShortThreads = 128;  // tokens of the kernels for short sequences, a run of the forward
 
 // Blocks that an SM holds, by registers and shared memory.
 template <typename T, bool PACK> __host__ __device__ constexpr int fwd_per_sm() { return sizeof(T) == 4 ? 2 : PACK ? 3 : 4; }
@@ -132,7 +133,7 @@ struct alignas(16) Run2 {
 };
 __device__ __forceinline__ uint64_t after(const Run2 &x, uint64_t h) { return fma2(x.a, h, x.h); }  // x, from h
 __device__ __forceinline__ Run2 after(const Run2 &x, const Run2 &y) { return {mul2(x.a, y.a), fma2(y.a, x.h, y.h)}; }  // x, then y
-__device__ __forceinline__ Run2 nothing() { return {f2(1.f), 0}; }
+__device__ __forceinline__ Run2 nothing() { return {f2(1.f), f2(-0.f)}; }  // -0: what is added to zero of either sign and leaves it
 
 // A step of a block: the tile and the tokens of a sequence that it is at. A thread works it out two steps ahead.
 struct alignas(16) Step {
@@ -141,6 +142,7 @@ struct alignas(16) Step {
     int32_t live, rows;    // of the block's kState tokens, those that count and those that exist
     int32_t c0, cols;      // the tile's first channel, its channels; 0: no more work
     int32_t begins, ends;  // whether the cluster begins, ends the sequence and tile
+    int32_t brief;         // whether the sequence has kShort tokens or fewer
 };
 struct Walk {
     uint32_t item, items, tiles, clusters;
@@ -155,8 +157,10 @@ struct Walk {
         s.b = (int32_t)b, s.t0 = (int32_t)t0, s.c0 = (int32_t)(item - b * tiles) * kTile;
         s.cols = (int32_t)imin<int64_t>(kTile, p.D - s.c0);
         s.base = (b * p.L + t0) * p.D + s.c0;
+        const int64_t n = seq_len(p.seqlens, b, p.L);
+        s.brief = n <= kShort;
         if (t0 >= 0) {
-            s.live = (int32_t)imin<int64_t>(kState, imax<int64_t>(0, seq_len(p.seqlens, b, p.L) - t0));
+            s.live = (int32_t)imin<int64_t>(kState, imax<int64_t>(0, n - t0));
             s.rows = (int32_t)imin<int64_t>(kState, imax<int64_t>(0, p.L - t0));
         }
         s.begins = first == start;
@@ -392,11 +396,11 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
                 const Gates2 g = gates2<T, FAST, false>(pair_of(pair(1, t)), pair_of(pair(2, t)), rate, sum);
                 a[t] = g.a;
                 h[t] = mul2(g.f, pair_of(pair(0, t)));
-                if (!FAST && t >= live) a[t] = f2(1.f), h[t] = 0;
+                if (!FAST && t >= live) a[t] = f2(1.f), h[t] = nothing().h;
                 own = after(own, {a[t], h[t]});
             }
         };
-        bool fast = live == R && !steep;
+        bool fast = live == R && !steep && !s.brief;  // brief: the gates as linear_fwd_short_kernel has them
         if (fast) {
             tokens(std::true_type{});
             fast = !__any_sync(0xffffffffu, is_low(sum, one, both));
@@ -750,8 +754,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
 // Up to kShort tokens, a run of the kernels above: a thread goes over V channels of a whole sequence alone, its tokens in registers;
 // there is nothing to join, and the number of sequences is what fills the device (forward B64 L16 D2560 9.8 us, 14.7 as above; B256 L1
 // D5120 17 and 86; backward 19 and 31, 54 and 225; a single sequence of 16 tokens 4.5 and 4.0, its backward 8.4 and 6.6: the rule goes
-// by the length alone, so that a sequence stays bitwise the same in any batch). 64 sequences of 17 tokens take 19 and 37 us.
-constexpr int kShort = kGroup, kShortThreads = 128;
+// by the padded length alone, so that neither results nor times of a sequence hang on how many there are). 64 sequences of 17 tokens
+// take 19 and 39 us. The forward gives bitwise what the kernel above gives a sequence of as many tokens in a batch padded to more:
+// the gates of its slow form, which `Step::brief` has it take there too, and the final state from the run's (A, H).
 
 template <typename T, int V> __device__ __forceinline__ uint64_t two_of(const Raw<T, V> &w) { return f2(to_f32(w.v[0]), to_f32(w.v[V - 1])); }
 template <int V> __device__ __forceinline__ uint64_t two_at(const float *p, int64_t at) { return p ? f2(p[at], p[at + V - 1]) : 0; }
@@ -778,18 +783,22 @@ template <typename T, int V> __global__ void __launch_bounds__(kShortThreads) li
             w[2][t] = load<T, V>((const T *)p.i + at + t * D);
         }
     const Rate2 k = Rate2::of(p.c * softplus(p.lam[c0]), p.c * softplus(p.lam[c0 + V - 1]));
-    uint64_t h = two_at<V>(p.init, b * D + c0), unused = 0;
-    if (p.states) put_two<float, V>(p.states + b * D + c0, h);
+    const uint64_t init = two_at<V>(p.init, b * D + c0);
+    uint64_t h = init, unused = 0;
+    Run2 own = nothing();  // the final state is the run's from the first one, as linear_fwd_kernel has it
+    if (p.states) put_two<float, V>(p.states + b * D + c0, init);
 #pragma unroll
     for (int t = 0; t < kShort; ++t) {
         if (t >= rows) break;
         if (t < live) {
             const Gates2 g = gates2<T, false, false>(two_of<T, V>(w[1][t]), two_of<T, V>(w[2][t]), k, unused);
-            h = fma2(g.a, h, mul2(g.f, two_of<T, V>(w[0][t])));
+            const uint64_t one = mul2(g.f, two_of<T, V>(w[0][t]));
+            h = fma2(g.a, h, one);
+            own = after(own, {g.a, one});
         }
         if (p.y) put_two<T, V>((T *)p.y + at + t * D, t < live ? h : 0);
     }
-    if (p.final_state) put_two<float, V>(p.final_state + b * D + c0, h);
+    if (p.final_state) put_two<float, V>(p.final_state + b * D + c0, after(own, init));
     if (!p.values) return;
 #pragma unroll
     for (int z = 0; z < 3; ++z) {

@@ -1,4 +1,5 @@
-"""The gated linear recurrence where it can go wrong: gates that are nearly open or shut, number by number."""
+"""The gated linear recurrence where it can go wrong: gates that are nearly open or shut, number by number; sequences of every length
+alone and padded, bit by bit."""
 import numpy as np
 import pytest
 import torch
@@ -58,3 +59,31 @@ def test_gradients_of_saturated_gates_number_by_number(ssd, size, io, rate, pack
         most = 2.5e-5 * whole + (2.0 ** -8 * np.abs(want[n]) if io == "bf16" else 0)
         assert (off <= most).all(), f"{n}: {np.max(off / np.maximum(whole, 1e-300)):.2e} of its terms"
     assert (host(got["di"]) >= 0).all()
+
+
+# ------------------------------------------------- alone and in a padded batch
+
+@pytest.mark.parametrize("D", [72, 33, 6])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rate", [1.0, 40.0])
+def test_a_sequence_cut_to_its_length_is_bitwise_the_padded_one(ssd, D, io, rate):
+    """y, the states and the 8 bits do not depend on what a sequence is padded to, zeros' signs in its first state included."""
+    lens = [0, 1, 5, 10, 15, 16, 17, 33, 63, 64, 65, 100, 128, 150]
+    L = max(lens)
+    d = inputs.linear_inputs(len(lens), L, D, io, seed=23, rate=rate)
+    d["init"][:, ::5] = -0.0
+    d["x"][:, ::3, ::5] = 0.0
+    t = on_device(d, io)
+    seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kept = ssd.gated_linear_checkpoint(t["x"])
+    y, final = ssd.gated_linear_chunked(*tokens(t), init_state=t["init"], seqlens=seqlens, **kept)
+    bits = lambda v: v.contiguous().view(torch.uint8)  # noqa: E731
+    for b, n in enumerate(lens):
+        one = [t[k][b:b + 1, :n].clone() for k in ("x", "r", "i")]
+        k1 = ssd.gated_linear_checkpoint(one[0])
+        y1, f1 = ssd.gated_linear_chunked(*one, t["lam"], init_state=t["init"][b:b + 1].clone(), **k1)
+        assert torch.equal(bits(y1[0]), bits(y[b, :n])), f"y, {n} tokens"
+        assert torch.equal(bits(f1[0]), bits(final[b])), f"final state, {n} tokens"
+        assert torch.equal(bits(k1["states"][0]), bits(kept["states"][b, :-(-n // 64)])), f"states, {n} tokens"
+        assert (bits(kept["states"][b, -(-n // 64):]) == bits(final[b][None].expand(-(-L // 64) - -(-n // 64), D))).all()
+        assert torch.equal(k1["values"][:, 0], kept["values"][:, b, :n]) and torch.equal(k1["scales"][:, 0], kept["scales"][:, b, :-(-n // 16)])
