@@ -332,6 +332,16 @@ ssd_status ssd_record_stage_events(cudaEvent_t *events, int count);
 ssd_status ssd_debug_bounds_status(int *site, int64_t *index, int clear);
 
 /*
+ * In a debug build, where bounded waits of gated-linear kernels end after 0.1 or
+ * 0.2 s (1 or 2 s else): has one run out in each later call on the current
+ * device, that of the given step (0, 1, ...) of the block of the given rank in
+ * its cluster, for the step's tiles (what 1; where rows are multiples of 16
+ * bytes) or for the runs of the cluster's blocks (what 2). what 0 ends it. Waits
+ * for the device. A release build returns SSD_ERR_UNSUPPORTED.
+ */
+ssd_status ssd_debug_linear_withhold(int what, int rank, int step);
+
+/*
  * Backward of ssd_scan_chunked (the training step's backward; "Compiler-First
  * State Space Duality ...", appendix Table 13): the gradients of
  *     L = <dy, y> + <dfinal_state, final_state>

@@ -136,6 +136,8 @@ def load() -> ctypes.CDLL:
             lib.ssd_debug_bounds_status.argtypes = [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int64),
                                                     ctypes.c_int]
             lib.ssd_debug_bounds_status.restype = ctypes.c_int
+            lib.ssd_debug_linear_withhold.argtypes = [ctypes.c_int] * 3
+            lib.ssd_debug_linear_withhold.restype = ctypes.c_int
             lib.ssd_record_stage_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int]
             lib.ssd_record_stage_events.restype = ctypes.c_int
             lib.ssd_last_error.argtypes = []
@@ -476,6 +478,12 @@ def ssd_debug_bounds_status(clear=True):
     site, index = ctypes.c_int(0), ctypes.c_int64(-1)
     rc = int(load().ssd_debug_bounds_status(ctypes.byref(site), ctypes.byref(index), 1 if clear else 0))
     return rc, site.value, index.value
+
+
+def ssd_debug_linear_withhold(what, rank=0, step=0) -> None:
+    """Has a bounded wait of later gated-linear calls run out in a debug build: of block `rank` of a cluster in `step`, for its
+    tiles (what 1) or the cluster's runs (what 2); what 0 ends it (see ssd_debug_linear_withhold in ssd_scan.h)."""
+    _check(load().ssd_debug_linear_withhold(int(what), int(rank), int(step)))
 
 
 def ssd_selftest_bounded_wait(workspace, spin_limit, stream=None) -> None:

@@ -179,7 +179,22 @@ struct Exchange {
     Run2 block[2][kMaxCluster][32];
     uint64_t bar[2];
 };
+// A thread whose wait has run out (`alive` false) goes on through its steps with the other threads of its block, but waits, arms
+// barriers, has tiles brought and, from the next step on, sends no more: what it does not send has the other blocks' waits run out in
+// turn, and no barrier counts a step's bytes for another's. A wait for the cluster's runs is twice as long as one for tiles, so that a
+// block whose tiles do not come can still say so. See leave() for the end.
+#ifdef SSD_DEBUG_BOUNDS
+constexpr uint64_t kGiveUpNs = 100000000ull;
+__device__ int g_withhold[3];  // has waits run out: kTiles, kRuns or 0, and the rank and step whose barrier counts bytes that nothing sends
+__device__ __forceinline__ uint32_t withheld(int what, int rank, int step) {
+    return g_withhold[0] == what && g_withhold[1] == rank && g_withhold[2] == step ? 16u : 0u;
+}
+#else
 constexpr uint64_t kGiveUpNs = 1000000000ull;
+__device__ __forceinline__ uint32_t withheld(int, int, int) { return 0; }
+#endif
+constexpr int kTiles = 1, kRuns = 2;
+constexpr uint64_t kUnderWayNs = 100000ull;
 __device__ int g_gave_up;  // SSD_ERR_TIMEOUT once a wait was given up on this device
 
 // Barriers ready in all blocks of the cluster. `tiles`: that of the TMA's tiles.
@@ -196,8 +211,8 @@ __device__ __forceinline__ void exchange_init(Exchange &x, uint64_t *tiles, int 
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 }
-__device__ __forceinline__ void exchange_expect(Exchange &x, int step, int blocks) {
-    tc::mbar_arrive_expect_tx(&x.bar[step & 1], blocks * 32 * (uint32_t)sizeof(Run2));
+__device__ __forceinline__ void exchange_expect(Exchange &x, int step, int rank, int blocks) {
+    tc::mbar_arrive_expect_tx(&x.bar[step & 1], blocks * 32 * (uint32_t)sizeof(Run2) + withheld(kRuns, rank, step));
 }
 // To the ranks first, first + every, ...
 __device__ __forceinline__ void exchange_send(Exchange &x, int step, int rank, int blocks, int first, int every, int lane, const Run2 &own) {
@@ -214,16 +229,16 @@ __device__ __forceinline__ void exchange_send(Exchange &x, int step, int rank, i
             "r"(bar), "r"(j), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
             : "memory");
 }
-// False, now and from then on, where what a barrier counts has not come in kGiveUpNs.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, bool alive) {
+// False, now and from then on, where what a barrier counts has not come in that time.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, bool alive, uint64_t ns = kGiveUpNs) {
     if (!alive) return false;
-    if (tc::mbar_wait(bar, parity, kGiveUpNs)) return true;
+    if (tc::mbar_wait(bar, parity, ns)) return true;
     atomicCAS(&g_gave_up, SSD_OK, SSD_ERR_TIMEOUT);
     return false;
 }
 // The carry over a cluster's blocks up to this one; `carry` goes on to the next step. What was not told is not guessed: NaN.
 __device__ __forceinline__ uint64_t exchange_receive(Exchange &x, int step, int rank, int blocks, int lane, bool &alive, uint64_t &carry) {
-    alive = wait_for(&x.bar[step & 1], (step >> 1) & 1, alive);
+    alive = wait_for(&x.bar[step & 1], (step >> 1) & 1, alive, 2 * kGiveUpNs);
     if (!alive) carry = f2(__uint_as_float(0x7fc00000u));
     uint64_t e = carry;
 #pragma unroll 4
@@ -232,6 +247,20 @@ __device__ __forceinline__ uint64_t exchange_receive(Exchange &x, int step, int 
         carry = after(x.block[step & 1][j][lane], carry);
     }
     return e;
+}
+
+// A block's end. Shared memory is given up once nothing more can come to it: a first thread whose waits all ended knows that all has come.
+// One whose wait ran out sees to the tiles that it had brought, for as long again (`parity`: of the last that it has not seen come); the
+// others' runs are on their way for microseconds once all blocks are here.
+template <bool WIDE> __device__ __forceinline__ void leave(uint64_t *tiles, uint32_t parity, int blocks, bool alive) {
+    if (WIDE && threadIdx.x == 0 && !alive) tc::mbar_wait(tiles, parity, kGiveUpNs);
+    if (blocks > 1) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0 && !alive)
+        for (const uint64_t since = tc::global_ns(); tc::global_ns() - since < kUnderWayNs;) {}
 }
 
 // ------------------------------------------------------------------ forward
@@ -320,14 +349,15 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
     }
     exchange_init(sh.exchange, &sh.tiles, blocks);
 
+    bool alive = true;
     // Has the next step's tiles brought, by one thread: the others of its warp, and the other warps, wait for the exchange.
     auto bring = [&](int step) {
         if constexpr (WIDE) {
-            if (threadIdx.x != 0) return;
+            if (threadIdx.x != 0 || !alive) return;
             const Step s = sh.step[step & 3];
             if (s.cols > 0 && (s.begins || s.live > 0)) {
                 const uint32_t some = s.cols * (uint32_t)sizeof(float);
-                tc::mbar_arrive_expect_tx(&sh.tiles, (s.live > 0 ? 3 * kState * PITCH : 0) + (s.begins ? (p.init ? 2 : 1) * some : 0));
+                tc::mbar_arrive_expect_tx(&sh.tiles, (s.live > 0 ? 3 * kState * PITCH : 0) + (s.begins ? (p.init ? 2 : 1) * some : 0) + withheld(kTiles, rank, step));
                 if (s.live > 0) {
                     tc::tma_load_3d(sh.in[0], &maps.x, &sh.tiles, s.c0, s.t0, s.b);
                     tc::tma_load_3d(sh.in[1], &maps.r, &sh.tiles, s.c0, s.t0, s.b);
@@ -351,18 +381,19 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
     bring(0);
     uint64_t carry = 0;
     Rate2 rate{};
-    bool steep = false, alive = true;
+    bool steep = false;
     uint32_t parity = 0;
     for (int step = 0;; ++step) {
         const Step s = sh.step[step & 3];
         if (s.cols == 0) break;
-        if (threadIdx.x == 0) exchange_expect(sh.exchange, step, blocks);
+        const bool in_step = __all_sync(0xffffffffu, alive);  // with the cluster's other blocks: its run is sent, whatever comes of the tiles
+        if (threadIdx.x == 0 && in_step) exchange_expect(sh.exchange, step, rank, blocks);
         const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
         const int64_t at = s.base + place * D + 2 * lane;
         const int live = run_of(R, s.live, place), rows = run_of(R, s.rows, place);  // tokens that count, that exist
         const int t0 = s.t0 + place;                                                  // of the run, where it exists
         if constexpr (WIDE) {
-            if (s.begins || s.live > 0) alive = wait_for(&sh.tiles, parity, alive), parity ^= 1;
+            if (s.begins || s.live > 0) alive = wait_for(&sh.tiles, parity, alive), parity ^= (uint32_t)alive;
         } else {
             copy_wait();
             __syncwarp();
@@ -433,7 +464,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
             if (w == warp) before = all;
             if (w < warps) all = after(all, sh.run[step & 1][w][lane]);
         }
-        exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
+        if (in_step) exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
         bring(step + 1);  // behind the sending, which the others wait for
         if (planner) sh.step[(step + 2) & 3] = sh.walk.next(p);
         uint64_t e = after(before, exchange_receive(sh.exchange, step, rank, blocks, lane, alive, carry));  // the state that enters this run
@@ -464,6 +495,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
     } else {
         copy_wait();
     }
+    leave<WIDE>(&sh.tiles, parity, blocks, alive);
 }
 
 // A sequence of no tokens: its state goes through.
@@ -536,14 +568,15 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
     }
     exchange_init(sh.exchange, &sh.tiles, blocks);
 
+    bool alive = true;
     auto bring = [&](int step) {  // as in the forward
         if constexpr (WIDE) {
-            if (threadIdx.x != 0) return;
+            if (threadIdx.x != 0 || !alive) return;
             const Step s = sh.step[step & 3];
             if (s.cols > 0 && (s.begins || s.live > 0)) {
                 const uint32_t some = s.cols * (uint32_t)sizeof(float);
                 tc::mbar_arrive_expect_tx(&sh.tiles, (s.live > 0 ? 3 * kState * PITCH + kState * DY + some + (PACK ? 3 * (kState / kGroup) * SC : 0) : 0) +
-                                                         (s.begins ? (p.dfinal ? 2 : 1) * some : 0));
+                                                         (s.begins ? (p.dfinal ? 2 : 1) * some : 0) + withheld(kTiles, rank, step));
                 if (s.live > 0) {
                     if constexpr (PACK) {
                         tc::tma_load_4d(sh.in, &maps.q, &sh.tiles, s.c0, s.t0, s.b, 0);
@@ -586,18 +619,19 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
     bring(0);
     uint64_t carry = 0, sum = 0;
     Rate2 rate{};
-    bool steep = false, alive = true;
+    bool steep = false;
     uint32_t parity = 0;
     for (int step = 0;; ++step) {
         const Step s = sh.step[step & 3];
         if (s.cols == 0) break;
-        if (threadIdx.x == 0) exchange_expect(sh.exchange, step, blocks);
+        const bool in_step = __all_sync(0xffffffffu, alive);  // with the cluster's other blocks: its run is sent, whatever comes of the tiles
+        if (threadIdx.x == 0 && in_step) exchange_expect(sh.exchange, step, rank, blocks);
         const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
         const int64_t at = s.base + place * D + 2 * lane;
         const int live = run_of(R, s.live, place), rows = run_of(R, s.rows, place);  // tokens that count, that exist
         const int t0 = s.t0 + place;                                                  // of the run, where it exists
         if constexpr (WIDE) {
-            if (s.begins || s.live > 0) alive = wait_for(&sh.tiles, parity, alive), parity ^= 1;
+            if (s.begins || s.live > 0) alive = wait_for(&sh.tiles, parity, alive), parity ^= (uint32_t)alive;
         } else {
             copy_wait();
             if (PACK) __syncthreads(); else __syncwarp();  // scales are shared by two warps
@@ -689,7 +723,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
             if (w == warp) before = all;
             all = after(all, sh.run[step & 1][w][lane]);
         }
-        exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
+        if (in_step) exchange_send(sh.exchange, step, rank, blocks, warp, warps, lane, all);
         bring(step + 1);  // behind the sending, which the others wait for
         if (planner) sh.step[(step + 2) & 3] = sh.walk.next(p.f);
         // h over the earlier runs (the later warps') to this one; then b becomes what multiplies dh in psi, and er 1 - rho
@@ -748,6 +782,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
     } else {
         copy_wait();
     }
+    leave<WIDE>(&sh.tiles, parity, blocks, alive);
 }
 
 // --------------------------------------------------------- short sequences
@@ -755,7 +790,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
 // there is nothing to join, and the number of sequences is what fills the device (forward B64 L16 D2560 9.8 us, 14.7 as above; B256 L1
 // D5120 17 and 86; backward 19 and 31, 54 and 225; a single sequence of 16 tokens 4.5 and 4.0, its backward 8.4 and 6.6: the rule goes
 // by the padded length alone, so that neither results nor times of a sequence hang on how many there are). 64 sequences of 17 tokens
-// take 19 and 39 us. The forward gives bitwise what the kernel above gives a sequence of as many tokens in a batch padded to more:
+// take 21 and 39 us. The forward gives bitwise what the kernel above gives a sequence of as many tokens in a batch padded to more:
 // the gates of its slow form, which `Step::brief` has it take there too, and the final state from the run's (A, H).
 
 template <typename T, int V> __device__ __forceinline__ uint64_t two_of(const Raw<T, V> &w) { return f2(to_f32(w.v[0]), to_f32(w.v[V - 1])); }
@@ -1238,6 +1273,15 @@ template <typename T> cudaError_t step_t(const LinearStepArgs &a, cudaStream_t s
 
 cudaError_t launch_linear_step(int io, const LinearStepArgs &a, cudaStream_t stream) {
     return io == IO_BF16 ? linear::step_t<__nv_bfloat16>(a, stream) : linear::step_t<float>(a, stream);
+}
+
+cudaError_t linear_withhold(int what, int rank, int step) {
+#ifdef SSD_DEBUG_BOUNDS
+    const int w[3] = {what, rank, step};
+    return cudaMemcpyToSymbol(linear::g_withhold, w, sizeof(w));
+#else
+    return cudaErrorNotSupported;
+#endif
 }
 
 cudaError_t linear_gave_up(int *status) {

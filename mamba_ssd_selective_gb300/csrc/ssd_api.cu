@@ -1171,6 +1171,19 @@ ssd_status ssd_debug_bounds_status(int *site, int64_t *index, int clear) {
 #endif
 }
 
+ssd_status ssd_debug_linear_withhold(int what, int rank, int step) {
+    if (what < 0 || what > 2 || rank < 0 || step < 0)
+        return fail(SSD_ERR_INVALID_ARG, "what must be 0, 1 or 2 and rank and step >= 0 (got %d, %d, %d)", what, rank, step);
+#ifndef SSD_DEBUG_BOUNDS
+    return fail(SSD_ERR_UNSUPPORTED, "this library was built without SSD_DEBUG_BOUNDS: no wait can be made to run out");
+#else
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = ssd::linear_withhold(what, rank, step);
+    if (e != cudaSuccess) return cuda_fail(e, "ssd_debug_linear_withhold");
+    return ok();
+#endif
+}
+
 ssd_status ssd_selftest_bounded_wait(void *workspace, int spin_limit, cudaStream_t stream) {
     if (!workspace) return fail(SSD_ERR_INVALID_ARG, "workspace is NULL");
     if (!aligned(workspace, 16)) return fail(SSD_ERR_INVALID_ARG, "workspace is not 16-byte aligned");

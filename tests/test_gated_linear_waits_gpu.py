@@ -1,0 +1,90 @@
+"""What a gated-linear kernel leaves when one of its bounded waits runs out. The debug build, in a child process, has a barrier count
+bytes that nothing sends: the wait ends after 0.1 or 0.2 s, the kernel goes on to its end, and the context stays usable."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from tests.conftest import ROOT
+
+pytestmark = pytest.mark.gpu
+
+# 32 chunks of 64 tokens and one tile: a cluster of several blocks, in two steps or more
+CHILD = r"""
+import sys
+import torch
+from mamba_ssd_selective_gb300 import binding as ops
+assert ops.lib_path().endswith("libssdscan_dbg.so")
+TILES, RUNS = 1, 2
+
+
+def data(io, D, L=2000, B=1):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(D)
+    t = {n: torch.randn(B, L, D, generator=gen, device="cuda").to(io) for n in ("x", "r", "i", "dy")}
+    t.update(lam=torch.full((D,), -5.0, device="cuda"), init=torch.randn(B, D, generator=gen, device="cuda"))
+    return t
+
+
+def forward(t):
+    kept = ops.gated_linear_checkpoint(t["x"])
+    y, final = ops.gated_linear_chunked(t["x"], t["r"], t["i"], t["lam"], init_state=t["init"], **kept)
+    plain, _ = ops.gated_linear_chunked(t["x"], t["r"], t["i"], t["lam"], init_state=t["init"])
+    return dict(kept, y=y, final=final, plain=plain)
+
+
+def backward(t, kept):
+    g = ops.gated_linear_chunked_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], states=kept["states"])
+    p = ops.gated_linear_chunked_bwd_packed(kept["values"], kept["scales"], kept["states"], t["lam"], t["dy"])
+    return dict(g, **{"packed_" + n: v for n, v in p.items()})
+
+
+def same(a, b):
+    return all(torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8)) for n in a)
+
+
+CASES = [(torch.bfloat16, 64, TILES), (torch.bfloat16, 64, RUNS), (torch.float32, 64, TILES), (torch.bfloat16, 33, RUNS), (torch.bfloat16, 66, RUNS)]
+"""
+
+ENDS = CHILD + r"""
+for io, D, what in CASES:
+    t = data(io, D)
+    want = forward(t)
+    grads = backward(t, want)
+    assert ops.gated_linear_status() == ops.SSD_OK
+    for rank in (0, 1):
+        for step in (0, 1):
+            ops.ssd_debug_linear_withhold(what, rank, step)
+            got = forward(t)
+            torch.cuda.synchronize()
+            assert ops.gated_linear_status() == ops.SSD_ERR_TIMEOUT, (io, D, what, rank, step)
+            assert ops.gated_linear_status() == ops.SSD_OK
+            if step > 0 or rank > 0:  # the first block's tokens before that
+                for n in ("y", "plain"):
+                    assert torch.equal(got[n][:, :64], want[n][:, :64]), (io, D, what, rank, step, n)
+            backward(t, want)
+            torch.cuda.synchronize()
+            assert ops.gated_linear_status() == ops.SSD_ERR_TIMEOUT, (io, D, what, rank, step)
+            ops.ssd_debug_linear_withhold(0)
+            again = forward(t)
+            assert same(again, want) and same(backward(t, again), grads)
+            assert ops.gated_linear_status() == ops.SSD_OK
+print("ok")
+"""
+
+
+@pytest.fixture(scope="module")
+def debug_library(cuda_device):
+    from mamba_ssd_selective_gb300 import build
+    return build.build(debug_bounds=True)
+
+
+def run(child):
+    r = subprocess.run([sys.executable, "-c", child], capture_output=True, text=True, cwd=ROOT, timeout=300,
+                       env=dict(os.environ, SSD_DEBUG_BOUNDS_LIB="1"))
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-3000:]
+
+
+def test_a_kernel_whose_wait_runs_out_ends_and_leaves_the_rest_as_it_was(debug_library):
+    run(ENDS)
