@@ -668,8 +668,9 @@ ssd_status ssd_gated_linear_chunked_bwd_packed(int64_t batch, int64_t seqlen, in
 /*
  * Waits for `stream`, then reports SSD_OK, or SSD_ERR_TIMEOUT when a bounded
  * wait of a gated-linear kernel on the current device gave up since the last
- * time this was asked: what such a call wrote is NaN from there on. Not to be
- * called while a stream is captured.
+ * time this was asked: what such a call wrote is right up to there, and right or
+ * NaN (in 8 bits a scale of 255) from there on. Not to be called while a stream
+ * is captured.
  */
 ssd_status ssd_gated_linear_status(cudaStream_t stream);
 

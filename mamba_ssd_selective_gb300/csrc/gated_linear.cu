@@ -133,6 +133,7 @@ struct alignas(16) Run2 {
 };
 __device__ __forceinline__ uint64_t after(const Run2 &x, uint64_t h) { return fma2(x.a, h, x.h); }  // x, from h
 __device__ __forceinline__ Run2 after(const Run2 &x, const Run2 &y) { return {mul2(x.a, y.a), fma2(y.a, x.h, y.h)}; }  // x, then y
+__device__ __forceinline__ uint64_t unknown() { return f2(__uint_as_float(0x7fc00000u)); }
 __device__ __forceinline__ Run2 nothing() { return {f2(1.f), f2(-0.f)}; }  // -0: what is added to zero of either sign and leaves it
 
 // A step of a block: the tile and the tokens of a sequence that it is at. A thread works it out two steps ahead.
@@ -182,7 +183,8 @@ struct Exchange {
 // A thread whose wait has run out (`alive` false) goes on through its steps with the other threads of its block, but waits, arms
 // barriers, has tiles brought and, from the next step on, sends no more: what it does not send has the other blocks' waits run out in
 // turn, and no barrier counts a step's bytes for another's. A wait for the cluster's runs is twice as long as one for tiles, so that a
-// block whose tiles do not come can still say so. See leave() for the end.
+// block whose tiles do not come can still say so: its run is NaN, which goes on to all that comes after it, and its groups in 8 bits
+// are marked as NaN too. See leave() for the end.
 #ifdef SSD_DEBUG_BOUNDS
 constexpr uint64_t kGiveUpNs = 100000000ull;
 __device__ int g_withhold[3];  // has waits run out: kTiles, kRuns or 0, and the rank and step whose barrier counts bytes that nothing sends
@@ -239,7 +241,7 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, bool al
 // The carry over a cluster's blocks up to this one; `carry` goes on to the next step. What was not told is not guessed: NaN.
 __device__ __forceinline__ uint64_t exchange_receive(Exchange &x, int step, int rank, int blocks, int lane, bool &alive, uint64_t &carry) {
     alive = wait_for(&x.bar[step & 1], (step >> 1) & 1, alive, 2 * kGiveUpNs);
-    if (!alive) carry = f2(__uint_as_float(0x7fc00000u));
+    if (!alive) carry = unknown();
     uint64_t e = carry;
 #pragma unroll 4
     for (int j = 0; j < blocks; ++j) {
@@ -284,10 +286,11 @@ struct FwdMaps {
     CUtensorMap y, q;     // of a warp's run; q of all three in 8 bits
 };
 
-// A run's x, r and i (z 0, 1, 2) in 8 bits, to `out`, the run's place in FwdShared::q. ALL: every token of it counts.
+// A run's x, r and i (z 0, 1, 2) in 8 bits, to `out`, the run's place in FwdShared::q. ALL: every token of it counts. Not `alive`: what
+// is in the tile is not known, and kept as NaN.
 template <typename T, bool WIDE, bool EVEN, bool ALL, typename F>
 __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const F &pair, unsigned char (*out)[kTile], const Step &s, int place, int live, int rows,
-                                                int lane) {
+                                                int lane, bool alive) {
     constexpr int R = kFwdRun;
     const int64_t D = p.D;
     const bool one = 2 * lane < s.cols, both = 2 * lane + 1 < s.cols;
@@ -308,6 +311,7 @@ __device__ __forceinline__ void leave_in_8_bits(const LinearArgs &p, const F &pa
             for (int t = 0; t < R; ++t)
                 if (ALL || t < live) top0 = max(top0, abs_bits(w[t].v[0])), top1 = max(top1, abs_bits(w[t].v[1]));
         }
+        if (!alive) top0 = top1 = 0x7fc00000u;
         Raw<uint8_t, 2> code;
         code.v[0] = (uint8_t)scale_code(top0), code.v[1] = (uint8_t)scale_code(top1);
         const int64_t groups = (p.L + kGroup - 1) / kGroup;
@@ -437,6 +441,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
             fast = !__any_sync(0xffffffffu, is_low(sum, one, both));
         }
         if (!fast) tokens(std::false_type{});
+        if (!alive) own = {unknown(), unknown()};
         sh.run[step & 1][warp][lane] = own;
         if constexpr (WIDE) {  // the TMA has read what it was given of the step before
             if (lane == 0) tc::bulk_wait_read_all();
@@ -446,9 +451,9 @@ __global__ void __launch_bounds__(32 * kFwdWarps, fwd_per_sm<T, PACK>()) linear_
             if (rows > 0) {
                 auto *out = &sh.q[WIDE ? 3 * place : 0];
                 if (live == R)
-                    leave_in_8_bits<T, WIDE, EVEN, true>(p, pair, out, s, place, live, rows, lane);
+                    leave_in_8_bits<T, WIDE, EVEN, true>(p, pair, out, s, place, live, rows, lane, alive);
                 else
-                    leave_in_8_bits<T, WIDE, EVEN, false>(p, pair, out, s, place, live, rows, lane);
+                    leave_in_8_bits<T, WIDE, EVEN, false>(p, pair, out, s, place, live, rows, lane, alive);
                 if constexpr (WIDE) {
                     tc::fence_proxy_async_smem();
                     __syncwarp();
@@ -711,6 +716,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
             fast = !__any_sync(0xffffffffu, is_low(args, one, both));
         }
         if (!fast) tokens(std::false_type{});
+        if (!alive) own = {unknown(), unknown()}, H = unknown();
         sh.run[step & 1][warp][lane] = own;
         sh.h[step & 1][warp][lane] = H;
         if constexpr (WIDE) {  // the TMA has read what it was given of the step before

@@ -74,6 +74,55 @@ print("ok")
 """
 
 
+LOST = CHILD + r"""
+def right_or_nan(got, want, what):
+    got, want = got.float(), want.float()
+    assert ((got == want) | torch.isnan(got)).all(), what
+
+
+def right_or_lost(got, want, what):  # in 8 bits
+    lost = (got["scales"] == 255)
+    kept = ~lost.repeat_interleave(16, 2)[:, :, :got["values"].shape[2]]
+    assert torch.equal(got["scales"][~lost], want["scales"][~lost]) and torch.equal(got["values"][kept], want["values"][kept]), what
+    assert not got["values"][~kept].any(), what
+
+
+for io, D, what in CASES:
+    t = data(io, D)
+    want = forward(t)
+    grads = backward(t, want)
+    L = t["x"].shape[1]
+    for rank in (0, 1, 2):
+        for step in (0, 1):
+            case = (io, D, what, rank, step)
+            ops.ssd_debug_linear_withhold(what, rank, step)
+            got = forward(t)
+            g = backward(t, want)
+            ops.ssd_debug_linear_withhold(0)
+            for n in ("y", "plain", "states", "final"):
+                right_or_nan(got[n], want[n], (*case, n))
+            right_or_lost(got, want, case)
+            for n in g:
+                right_or_nan(g[n], grads[n], (*case, n))
+                assert n.endswith("dinit") or torch.isnan(g[n].float()).any(), (*case, n)
+            if step > 0:
+                continue
+            # from the block whose wait ran out; all of the others' where its run was not known, else from the next step on
+            first = 64 * rank
+            lost = slice(first, None) if what == TILES else slice(first, min(first + 64, L))
+            for n in ("y", "plain"):
+                assert torch.isnan(got[n][:, lost]).all() and torch.isnan(got[n][:, -1]).all(), (*case, n)
+                assert torch.equal(got[n][:, :first], want[n][:, :first]), (*case, n)
+            assert torch.isnan(got["final"]).all(), case
+            if what == TILES:
+                assert torch.isnan(got["states"][:, rank:]).all() and (got["scales"][:, :, first // 16:first // 16 + 4] == 255).all(), case
+                for n in ("dx", "dr", "di", "dlam", "dinit", "packed_dx", "packed_dlam", "packed_dinit"):
+                    assert torch.isnan(g[n][:, 0] if g[n].dim() == 3 else g[n]).all(), (*case, n)
+assert ops.gated_linear_status() == ops.SSD_ERR_TIMEOUT
+print("ok")
+"""
+
+
 @pytest.fixture(scope="module")
 def debug_library(cuda_device):
     from mamba_ssd_selective_gb300 import build
@@ -88,3 +137,8 @@ def run(child):
 
 def test_a_kernel_whose_wait_runs_out_ends_and_leaves_the_rest_as_it_was(debug_library):
     run(ENDS)
+
+
+def test_what_is_not_known_is_nan(debug_library):
+    """Every number is right or NaN (scale 255 in 8 bits), and what hangs on tiles that did not come is NaN."""
+    run(LOST)
