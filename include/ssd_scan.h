@@ -667,9 +667,11 @@ ssd_status ssd_gated_linear_chunked_bwd_packed(int64_t batch, int64_t seqlen, in
 
 /*
  * Waits for `stream`, then reports SSD_OK, or SSD_ERR_TIMEOUT when a bounded
- * wait of a gated-linear kernel on the current device gave up since the last
- * time this was asked: what such a call wrote is right up to there, and right or
- * NaN (in 8 bits a scale of 255) from there on. Not to be called while a stream
+ * wait of a gated-linear kernel on the current device, which is the stream's,
+ * gave up since this was last asked for the same stream (the first time: since
+ * the library was loaded): what such a call wrote is right up to there, and right
+ * or NaN (in 8 bits a scale of 255) from there on. Every stream that asks is
+ * told, the call having been on another one too. Not to be called while a stream
  * is captured.
  */
 ssd_status ssd_gated_linear_status(cudaStream_t stream);

@@ -943,9 +943,11 @@ def gated_linear_chunked_bwd_packed(values, scales, states, lam, dy, c=8.0, dfin
 
 
 def gated_linear_status(stream=None) -> int:
-    """Waits for the stream and returns SSD_OK, or SSD_ERR_TIMEOUT when a bounded
-    wait of a gated-linear kernel on the current device gave up since the last call."""
-    return int(load().ssd_gated_linear_status(_stream(stream, torch.device("cuda", torch.cuda.current_device()))))
+    """Waits for the stream (None: torch's current one) and returns SSD_OK, or SSD_ERR_TIMEOUT when a bounded wait of a
+    gated-linear kernel on its device gave up since this was last asked for the same stream."""
+    dev = getattr(stream, "device", None) or torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.device(dev):
+        return int(load().ssd_gated_linear_status(_stream(stream, dev)))
 
 
 def gated_linear_step(state, x, r, i, lam, c=8.0, slots=None, new_state=None, y=None, stream=None):

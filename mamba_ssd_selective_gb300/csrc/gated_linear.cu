@@ -23,7 +23,6 @@
 
 #include "gated_linear.cuh"
 #include "launch.h"
-#include "ssd_scan.h"
 #include "tc_host.h"
 #include "tc_ptx.cuh"
 
@@ -197,7 +196,7 @@ __device__ __forceinline__ uint32_t withheld(int, int, int) { return 0; }
 #endif
 constexpr int kTiles = 1, kRuns = 2;
 constexpr uint64_t kUnderWayNs = 100000ull;
-__device__ int g_gave_up;  // SSD_ERR_TIMEOUT once a wait was given up on this device
+__device__ unsigned long long g_gave_up;  // threads whose wait ran out on this device
 
 // Barriers ready in all blocks of the cluster. `tiles`: that of the TMA's tiles.
 __device__ __forceinline__ void exchange_init(Exchange &x, uint64_t *tiles, int blocks) {
@@ -235,7 +234,7 @@ __device__ __forceinline__ void exchange_send(Exchange &x, int step, int rank, i
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, bool alive, uint64_t ns = kGiveUpNs) {
     if (!alive) return false;
     if (tc::mbar_wait(bar, parity, ns)) return true;
-    atomicCAS(&g_gave_up, SSD_OK, SSD_ERR_TIMEOUT);
+    atomicAdd(&g_gave_up, 1ull);
     return false;
 }
 // The carry over a cluster's blocks up to this one; `carry` goes on to the next step. What was not told is not guessed: NaN.
@@ -1290,11 +1289,9 @@ cudaError_t linear_withhold(int what, int rank, int step) {
 #endif
 }
 
-cudaError_t linear_gave_up(int *status) {
-    cudaError_t e = cudaMemcpyFromSymbol(status, linear::g_gave_up, sizeof(int));
-    const int none = SSD_OK;
-    if (e == cudaSuccess && *status != none) e = cudaMemcpyToSymbol(linear::g_gave_up, &none, sizeof(int));
-    return e;
+cudaError_t linear_gave_up(unsigned long long *count, cudaStream_t stream) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(count, linear::g_gave_up, sizeof(*count), 0, cudaMemcpyDeviceToHost, stream);
+    return e == cudaSuccess ? cudaStreamSynchronize(stream) : e;
 }
 
 namespace linear {

@@ -261,7 +261,8 @@ int64_t linear_bwd_parts(int64_t B);
 cudaError_t launch_linear_bwd(int io, const LinearBwdArgs &a, cudaStream_t stream);
 cudaError_t launch_linear_step(int io, const LinearStepArgs &a, cudaStream_t stream);
 cudaError_t linear_withhold(int what, int rank, int step);  // debug builds: see ssd_debug_linear_withhold
-cudaError_t linear_gave_up(int *status);  // reads the current device's word and clears it
+// Waits for the stream; how many threads' waits have run out on the current device, ever.
+cudaError_t linear_gave_up(unsigned long long *count, cudaStream_t stream);
 cudaError_t launch_pack8(int io, const Pack8Args &a, cudaStream_t stream);
 
 // Forward chunk states and entering states only (CUDA-core chunk state, then

@@ -74,6 +74,28 @@ print("ok")
 """
 
 
+TOLD = CHILD + r"""
+import threading
+t = data(torch.bfloat16, 64)
+streams = [torch.cuda.Stream() for _ in range(3)]
+TIMEOUT, OK = ops.SSD_ERR_TIMEOUT, ops.SSD_OK
+for again in range(2):
+    assert [ops.gated_linear_status(s) for s in (None, *streams)] == [OK] * 4
+    ops.ssd_debug_linear_withhold(RUNS, 1, 0)
+    ops.gated_linear_chunked(t["x"], t["r"], t["i"], t["lam"], stream=streams[1])
+    ops.ssd_debug_linear_withhold(0)
+    torch.cuda.synchronize()
+    # others ask first, more than once, and from another thread
+    assert ops.gated_linear_status(streams[0]) == TIMEOUT and ops.gated_linear_status(streams[0]) == OK
+    said = []
+    thread = threading.Thread(target=lambda: said.extend(ops.gated_linear_status(s) for s in (streams[2], streams[2], None)))
+    thread.start()
+    thread.join()
+    assert said == [TIMEOUT, OK, TIMEOUT], said
+    assert ops.gated_linear_status(streams[1]) == TIMEOUT
+print("ok")
+"""
+
 LOST = CHILD + r"""
 def right_or_nan(got, want, what):
     got, want = got.float(), want.float()
@@ -142,3 +164,7 @@ def test_a_kernel_whose_wait_runs_out_ends_and_leaves_the_rest_as_it_was(debug_l
 def test_what_is_not_known_is_nan(debug_library):
     """Every number is right or NaN (scale 255 in 8 bits), and what hangs on tiles that did not come is NaN."""
     run(LOST)
+
+
+def test_every_stream_that_asks_is_told(debug_library):
+    run(TOLD)
