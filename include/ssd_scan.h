@@ -610,23 +610,24 @@ ssd_status ssd_block_norm_bwd(int64_t rows, int64_t dim, int32_t io_dtype, int32
  *   x, r, i    [B, L, D]  io_dtype
  *   lam        [D]        float32
  *   c          positive and finite
- *   init_state [B, D]     float32, may be NULL (zero)
+ *   init_state [B, D]     float32, may be NULL (zero); a result of its size may be
+ *              the same buffer
  *   seqlens    [B]        int32 on the device, may be NULL (L for every b):
  *              sequence b is its first seqlens[b] tokens (values outside
  *              [0, L] are brought into it). What x, r and i hold past them is
  *              not used, y is zero there.
  *   y          [B, L, D]  io_dtype, written
  *   final_state[B, D]     float32, the state after the last token of each
- *              sequence; may be NULL, may be the same buffer as init_state
+ *              sequence; may be NULL
  * For a backward pass, each may be NULL:
  *   states     [B, ceil(L/64), D]     float32: the state before token 0, 64, ...
  *              (past a sequence's end its final state)
  *   values     [3, B, L, D]           int8 and
  *   scales     [3, B, ceil(L/16), D]  uint8, with values: x, r and i as
  *              ssd_pack8 keeps them
- * y and what is written for a backward may not alias x, r or i (equal pointers
- * are refused). Limits here and below: batch <= 65535,
- * dim <= 2097120, seqlen < 2^31.
+ * Here and below, a result that shares memory with another or with anything that
+ * the call reads is refused, but for the pairs that are named. Limits here and
+ * below: batch <= 65535, dim <= 2097120, seqlen < 2^31.
  */
 ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype, const void *x,
                                     const void *r, const void *i, const float *lam, float c, const float *init_state,
@@ -642,13 +643,13 @@ ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, 
  *                only, and may be NULL)
  *   dy           [B, L, D] io_dtype      dfinal_state [B, D] float32, may be NULL (0)
  *   dx, dr, di   [B, L, D] io_dtype, zero past a sequence's length
- *   dlam         [D] float32             dinit_state [B, D] float32, may be NULL
+ *   dlam         [D] float32             dinit_state [B, D] float32, may be NULL,
+ *                may be the same buffer as dfinal_state
  *   workspace    ssd_gated_linear_chunked_bwd_workspace_size(..., states given?)
  *                bytes, 256-byte aligned
- * Outputs may not alias inputs (equal pointers are refused). The _packed form takes x, r and i in 8 bits as
- * the forward (or ssd_pack8, three times) wrote them, with the states: the
- * gradients are those at the values that the 8 bits stand for, h going on from
- * the given state every 64 tokens.
+ * The _packed form takes x, r and i in 8 bits as the forward (or ssd_pack8, three
+ * times) wrote them, with the states: the gradients are those at the values that
+ * the 8 bits stand for, h going on from the given state every 64 tokens.
  */
 size_t ssd_gated_linear_chunked_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtype,
                                                    int32_t have_states);

@@ -948,6 +948,35 @@ ssd_status check_linear(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_d
     if (seqlen > 0x7fffffffLL) return fail(SSD_ERR_UNSUPPORTED, "seqlen must be below 2^31");
     return SSD_OK;
 }
+// A buffer of a call, a * b * c elements of `size` bytes.
+struct Buffer {
+    Buffer(const char *name, const void *p, size_t size, int64_t a, int64_t b = 1, int64_t c = 1)
+        : name(name), at(reinterpret_cast<uintptr_t>(p)) {
+        const unsigned __int128 n = (unsigned __int128)size * (uint64_t)a * (uint64_t)b * (uint64_t)c;
+        bytes = p ? (size_t)(n < SIZE_MAX / 2 ? n : SIZE_MAX / 2) : 0;
+    }
+    bool shares(const Buffer &o) const { return bytes && o.bytes && at < o.at + o.bytes && o.at < at + bytes; }
+    const char *name;
+    uintptr_t at;
+    size_t bytes;
+};
+// Refuses a result that shares memory with another or with what the call reads. `in_place`: pairs of names, of a result and of an input
+// that may be one buffer.
+ssd_status check_apart(std::initializer_list<Buffer> in, std::initializer_list<Buffer> out,
+                       std::initializer_list<std::pair<const char *, const char *>> in_place = {}) {
+    for (const Buffer *o = out.begin(); o != out.end(); ++o) {
+        for (const Buffer *q = out.begin(); q != o; ++q)
+            if (o->shares(*q)) return fail(SSD_ERR_INVALID_ARG, "%s shares memory with %s", o->name, q->name);
+        for (const Buffer &q : in) {
+            if (!o->shares(q)) continue;
+            bool may = false;
+            for (const auto &pair : in_place)
+                may = may || (o->at == q.at && o->bytes == q.bytes && !strcmp(pair.first, o->name) && !strcmp(pair.second, q.name));
+            if (!may) return fail(SSD_ERR_INVALID_ARG, "%s shares memory with %s", o->name, q.name);
+        }
+    }
+    return SSD_OK;
+}
 ssd_status check_rate(float c) {
     if (!(c > 0.f) || !std::isfinite(c)) return fail(SSD_ERR_INVALID_ARG, "c must be positive and finite");
     return SSD_OK;
@@ -965,10 +994,6 @@ ssd_status linear_bwd(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dty
     const bool some = batch > 0 && seqlen > 0;
     if (!a.f.lam || !a.dlam || (some && (!a.dy || !a.dx || !a.dr || !a.di)))
         return fail(SSD_ERR_INVALID_ARG, "lam, dy, dx, dr, di and dlam must be non-NULL");
-    const void *in[] = {a.f.x, a.f.r, a.f.i, a.dy, a.f.values}, *out[] = {a.dx, a.dr, a.di};
-    for (const void *o : out)
-        for (const void *q : in)
-            if (some && o == q) return fail(SSD_ERR_INVALID_ARG, "dx, dr and di may not be the buffer of an input");
     ssd_status s = check_rate(a.f.c);
     if (s != SSD_OK) return s;
     s = check_aligned({{a.f.x, "x"}, {a.f.r, "r"}, {a.f.i, "i"}, {a.f.values, "values"}, {a.f.scales, "scales"},
@@ -977,7 +1002,19 @@ ssd_status linear_bwd(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dty
                        {a.dlam, "dlam"}, {a.dinit, "dinit_state"}});
     if (s != SSD_OK) return s;
     const size_t states = a.f.states ? 0 : linear_states_bytes(batch, seqlen, dim);
-    if ((s = check_ws(workspace, ws_bytes, 256 + states + linear_part_bytes(batch, dim))) != SSD_OK) return s;
+    const size_t need = 256 + states + linear_part_bytes(batch, dim);
+    if ((s = check_ws(workspace, ws_bytes, need)) != SSD_OK) return s;
+    const int64_t tokens = batch * seqlen, chunks = (seqlen + SSD_GATED_LINEAR_CHUNK - 1) / SSD_GATED_LINEAR_CHUNK;
+    const int64_t groups = (seqlen + SSD_PACK8_GROUP - 1) / SSD_PACK8_GROUP;
+    const size_t io = io_dtype == SSD_F32 ? 4 : 2;
+    s = check_apart({{"x", a.f.x, io, tokens, dim}, {"r", a.f.r, io, tokens, dim}, {"i", a.f.i, io, tokens, dim},
+                     {"values", a.f.values, 3, tokens, dim}, {"scales", a.f.scales, 3, batch, groups, dim}, {"lam", a.f.lam, 4, dim},
+                     {"init_state", a.f.states ? nullptr : a.f.init, 4, batch, dim}, {"states", a.f.states, 4, batch, chunks, dim},
+                     {"seqlens", a.f.seqlens, 4, batch}, {"dy", a.dy, io, tokens, dim}, {"dfinal_state", a.dfinal, 4, batch, dim}},
+                    {{"dx", a.dx, io, tokens, dim}, {"dr", a.dr, io, tokens, dim}, {"di", a.di, io, tokens, dim},
+                     {"dlam", a.dlam, 4, dim}, {"dinit_state", a.dinit, 4, batch, dim}, {"workspace", workspace, 1, (int64_t)need}},
+                    {{"dinit_state", "dfinal_state"}});
+    if (s != SSD_OK) return s;
     char *ws = static_cast<char *>(workspace) + 256;
     a.f.B = batch, a.f.L = seqlen, a.f.D = dim;
     a.part = reinterpret_cast<float *>(ws + states);
@@ -1003,10 +1040,18 @@ ssd_status ssd_gated_linear_chunked(int64_t batch, int64_t seqlen, int64_t dim, 
     if (!lam || (seqlen > 0 && (!x || !r || !i || !y)))
         return fail(SSD_ERR_INVALID_ARG, "x, r, i, lam and y must be non-NULL");
     if (!values != !scales) return fail(SSD_ERR_INVALID_ARG, "values and scales must be given together");
-    if (y && (y == x || y == r || y == i)) return fail(SSD_ERR_INVALID_ARG, "y may not be the buffer of x, r or i");
     s = check_aligned({{x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}, {init_state, "init_state"}, {seqlens, "seqlens"},
                        {y, "y"}, {final_state, "final_state"}, {states, "states"}, {values, "values"},
                        {scales, "scales"}});
+    if (s != SSD_OK) return s;
+    const int64_t tokens = batch * seqlen, chunks = (seqlen + SSD_GATED_LINEAR_CHUNK - 1) / SSD_GATED_LINEAR_CHUNK;
+    const int64_t groups = (seqlen + SSD_PACK8_GROUP - 1) / SSD_PACK8_GROUP;
+    const size_t io = io_dtype == SSD_F32 ? 4 : 2;
+    s = check_apart({{"x", x, io, tokens, dim}, {"r", r, io, tokens, dim}, {"i", i, io, tokens, dim}, {"lam", lam, 4, dim},
+                     {"init_state", init_state, 4, batch, dim}, {"seqlens", seqlens, 4, batch}},
+                    {{"y", y, io, tokens, dim}, {"final_state", final_state, 4, batch, dim}, {"states", states, 4, batch, chunks, dim},
+                     {"values", values, 3, tokens, dim}, {"scales", scales, 3, batch, groups, dim}},
+                    {{"final_state", "init_state"}, {"states", "init_state"}, {"y", "init_state"}});
     if (s != SSD_OK) return s;
     ssd::LinearArgs a{};
     a.B = batch, a.L = seqlen, a.D = dim;
@@ -1071,6 +1116,12 @@ ssd_status ssd_gated_linear_step(int64_t batch, int64_t dim, int32_t io_dtype, i
     s = check_aligned({{state, "state"}, {x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}, {slots, "slots"},
                        {new_state, "new_state"}, {y, "y"}});
     if (s != SSD_OK) return s;
+    const size_t io = io_dtype == SSD_F32 ? 4 : 2;
+    s = check_apart({{"state", state, 4, nslots, dim}, {"x", x, io, batch, dim}, {"r", r, io, batch, dim}, {"i", i, io, batch, dim},
+                     {"lam", lam, 4, dim}, {"slots", slots, 4, batch}},
+                    {{"new_state", new_state, 4, nslots, dim}, {"y", y, io, batch, dim}},
+                    {{"new_state", "state"}, {"y", "x"}, {"y", "r"}, {"y", "i"}});
+    if (s != SSD_OK) return s;
     ssd::LinearStepArgs a{};
     a.B = batch, a.D = dim, a.nslots = nslots, a.state = state, a.new_state = new_state;
     a.x = x, a.r = r, a.i = i, a.lam = lam, a.c = c, a.slots = slots, a.y = y;
@@ -1104,6 +1155,10 @@ ssd_status ssd_pack8(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dtyp
     if (!x || !values || !scales) return fail(SSD_ERR_INVALID_ARG, "x, values and scales must be non-NULL");
     s = check_aligned({{x, "x"}, {seqlens, "seqlens"}, {values, "values"}, {scales, "scales"}});
     if (s != SSD_OK) return s;
+    const int64_t groups = (seqlen + SSD_PACK8_GROUP - 1) / SSD_PACK8_GROUP;
+    s = check_apart({{"x", x, io_dtype == SSD_F32 ? 4u : 2u, batch, seqlen, dim}, {"seqlens", seqlens, 4, batch}},
+                    {{"values", values, 1, batch, seqlen, dim}, {"scales", scales, 1, batch, groups, dim}});
+    if (s != SSD_OK) return s;
     ssd::Pack8Args a{};
     a.B = batch, a.L = seqlen, a.D = dim, a.x = x, a.seqlens = seqlens, a.values = values, a.scales = scales;
     cudaError_t e = ssd::launch_pack8(io_of(io_dtype), a, stream);
@@ -1118,6 +1173,10 @@ ssd_status ssd_unpack8(int64_t batch, int64_t seqlen, int64_t dim, int32_t io_dt
     if (batch == 0 || seqlen == 0) return ok();
     if (!values || !scales || !out) return fail(SSD_ERR_INVALID_ARG, "values, scales and out must be non-NULL");
     s = check_aligned({{values, "values"}, {scales, "scales"}, {out, "out"}});
+    if (s != SSD_OK) return s;
+    const int64_t groups = (seqlen + SSD_PACK8_GROUP - 1) / SSD_PACK8_GROUP;
+    s = check_apart({{"values", values, 1, batch, seqlen, dim}, {"scales", scales, 1, batch, groups, dim}},
+                    {{"out", out, io_dtype == SSD_F32 ? 4u : 2u, batch, seqlen, dim}});
     if (s != SSD_OK) return s;
     ssd::Pack8Args a{};
     a.B = batch, a.L = seqlen, a.D = dim, a.out = out;

@@ -1,5 +1,5 @@
 """The gated linear recurrence where it can go wrong: gates that are nearly open or shut, number by number; sequences of every length
-alone and padded, bit by bit."""
+alone and padded, bit by bit; results in the place of inputs."""
 import numpy as np
 import pytest
 import torch
@@ -87,3 +87,42 @@ def test_a_sequence_cut_to_its_length_is_bitwise_the_padded_one(ssd, D, io, rate
         assert torch.equal(bits(k1["states"][0]), bits(kept["states"][b, :-(-n // 64)])), f"states, {n} tokens"
         assert (bits(kept["states"][b, -(-n // 64):]) == bits(final[b][None].expand(-(-L // 64) - -(-n // 64), D))).all()
         assert torch.equal(k1["values"][:, 0], kept["values"][:, b, :n]) and torch.equal(k1["scales"][:, 0], kept["scales"][:, b, :-(-n // 16)])
+
+
+# ------------------------------------------------- results in the place of inputs
+
+@pytest.mark.parametrize("D", [64, 65])
+def test_results_in_the_place_of_what_they_come_from(ssd, D):
+    """The pairs that may be one buffer give the bits that two buffers give, the others are refused."""
+    d = inputs.linear_inputs(4, 50, D, "f32", seed=24)
+    t = on_device(d, "f32")
+    kept = ssd.gated_linear_checkpoint(t["x"], packed=False)
+    y, final = ssd.gated_linear_chunked(*tokens(t), init_state=t["init"], **kept)
+    own = t["init"].clone()
+    y2, _ = ssd.gated_linear_chunked(*tokens(t), init_state=own, final_state=own)
+    assert torch.equal(y, y2) and torch.equal(own, final)
+    own = t["init"].clone()  # the states of up to 64 tokens are the first one
+    y2, final2 = ssd.gated_linear_chunked(*tokens(t), init_state=own, states=own.view(4, 1, D))
+    assert torch.equal(y, y2) and torch.equal(final, final2) and torch.equal(own, t["init"])
+    one = [t[n][:, 0].contiguous() for n in ("x", "r", "i")]
+    pool = t["init"].clone()
+    want = ssd.gated_linear_step(t["init"], *one, t["lam"], new_state=pool)
+    for k in range(3):
+        mine, state = [v.clone() for v in one], t["init"].clone()
+        assert torch.equal(ssd.gated_linear_step(state, *mine, t["lam"], y=mine[k]), want) and torch.equal(state, pool)
+        assert mine[k].equal(want)
+    g = ssd.gated_linear_chunked_bwd(*tokens(t), t["dy"], states=kept["states"], dfinal_state=t["dfinal"])
+    out = {n: torch.empty_like(v) for n, v in g.items() if n != "dinit"}
+    own, ws = t["dfinal"].clone(), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    status = ssd.load().ssd_gated_linear_chunked_bwd(
+        4, 50, D, 0, *(v.data_ptr() for v in tokens(t)), 8.0, None, kept["states"].data_ptr(), None, t["dy"].data_ptr(), own.data_ptr(),
+        out["dx"].data_ptr(), out["dr"].data_ptr(), out["di"].data_ptr(), out["dlam"].data_ptr(), own.data_ptr(), ws.data_ptr(), ws.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    assert status == ssd.SSD_OK and torch.equal(own, g["dinit"]) and all(torch.equal(out[n], g[n]) for n in out)
+    wide = torch.empty(400 * D, device="cuda")
+    x, y = wide[:200 * D].view(4, 50, D), wide[100 * D:300 * D].view(4, 50, D)
+    for refused in (lambda: ssd.gated_linear_chunked(x, t["r"], t["i"], t["lam"], y=y), lambda: ssd.gated_linear_chunked(
+            *tokens(t), init_state=t["init"], final_state=wide[:4 * D].view(4, D), states=wide[:4 * D].view(4, 1, D)),
+            lambda: ssd.pack8(x, values=wide.view(torch.int8)[:200 * D].view(4, 50, D))):
+        with pytest.raises(ssd.SsdError, match="shares memory"):
+            refused()
