@@ -1,5 +1,5 @@
-"""The gated linear recurrence where it can go wrong: gates that are nearly open or shut, number by number; sequences of every length
-alone and padded, bit by bit; results in the place of inputs."""
+"""The gated linear recurrence where it can go wrong: gates that are nearly open or shut, number by number; float32's last digits;
+sequences of every length alone and padded, bit by bit; results in the place of inputs."""
 import numpy as np
 import pytest
 import torch
@@ -59,6 +59,29 @@ def test_gradients_of_saturated_gates_number_by_number(ssd, size, io, rate, pack
         most = 2.5e-5 * whole + (2.0 ** -8 * np.abs(want[n]) if io == "bf16" else 0)
         assert (off <= most).all(), f"{n}: {np.max(off / np.maximum(whole, 1e-300)):.2e} of its terms"
     assert (host(got["di"]) >= 0).all()
+
+
+# ------------------------------------------------------------ float32's digits
+
+@pytest.mark.parametrize("size", [(2, 777, 97), (2, 777, 96), (3, 16, 130), (1, 2000, 34)])
+@pytest.mark.parametrize("rate", [1.0, 40.0])
+def test_float32_keeps_its_digits(ssd, size, rate):
+    """In the 2-norm, 20 units of 2^-24 for y and the states (gates 4, w 6, what h makes of it 6, sums and joints 4) and twice that for
+    gradients, which are products of two such sums; with t up to 1 the polynomials of a and of the root add 3.5e-7 and 6e-7, that of the
+    gradients' ratio 1.2e-6 (dlam, a sum of both signs, is left to the other tests)."""
+    d = inputs.linear_inputs(*size, "f32", seed=25, rate=rate)
+    t = on_device(d, "f32")
+    kept = ssd.gated_linear_checkpoint(t["x"], packed=False)
+    y, final = ssd.gated_linear_chunked(*tokens(t), init_state=t["init"], **kept)
+    g = ssd.gated_linear_chunked_bwd(*tokens(t), t["dy"], states=kept["states"], dfinal_state=t["dfinal"])
+    args = [d[n] for n in ("x", "r", "i", "lam")]
+    want = dict(zip(("y", "final", "states"), linear.linear_seq(*args, 8.0, d["init"])))
+    grads = linear.linear_seq_bwd(*args, d["dy"], 8.0, d["init"], d["dfinal"])
+    one = 20 * 2.0 ** -24 + (9.5e-7 if rate > 1 else 0)
+    for got, w, most in [(y, want["y"], one), (final, want["final"], one), (kept["states"], want["states"], one)] + [
+            (g[n], grads[n], 2 * one + (1.2e-6 if rate > 1 else 0)) for n in ("dx", "dr", "di", "dinit")]:
+        off = np.linalg.norm(host(got) - w) / np.linalg.norm(w)
+        assert off <= most, f"{off:.2e} of {most:.2e}"
 
 
 # ------------------------------------------------- alone and in a padded batch
