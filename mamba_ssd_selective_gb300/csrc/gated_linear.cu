@@ -15,7 +15,7 @@
 // four of them, each at another place of its step (with 128 tokens a block and two an SM, B1 L65536 D1536 took 261 us where this took
 // 242); nothing in a step waits for memory that was not asked for a step before; and the blocks meet on a barrier in shared memory
 // that counts the bytes sent rather than on the cluster's, which would have the sender wait for everything it has written (B8 L2048
-// D5120: 193 us so, 176 without). The whole forward: B8 L2048 D5120 in bf16 122 us, 5.5 TB/s; one block that walks a
+// D5120: 193 us so, 176 without). The whole forward: B8 L2048 D5120 in bf16 123 us, 5.4 TB/s; one block that walks a
 // sequence alone, with plain loads, took 521.
 #include <cooperative_groups.h>
 
@@ -265,9 +265,10 @@ template <bool WIDE> __device__ __forceinline__ void leave(uint64_t *tiles, uint
 }
 
 // ------------------------------------------------------------------ forward
-// Bound by HBM (8 bytes a token and channel in bf16; the same tiles moved without arithmetic take 104 us where this takes 122) with the
-// issue slots close behind it (56 %): so two channels an instruction where there is one for it. Runs of 16 tokens are what the
-// registers of 16 warps an SM hold (a and b of each: 64 of 128). With the 8 bits written too, B4 L2048 D5120: 111 us.
+// Bound by the latency of a step at the 16 warps that an SM's registers hold, which keep neither HBM (8 bytes a token and channel in
+// bf16; B4 L2048 D5120 55 % of its peak) nor the issue slots (57 %) busy; B8 L2048 D5120 123 us, where the same tiles moved without
+// arithmetic take 104. Instructions are time all the same: so two channels each where there is one for it. Runs of 16 tokens are what
+// the registers of those warps hold (a and b of each: 64 of 128). With the 8 bits written too, B4 L2048 D5120: 112 us.
 template <typename T, bool WIDE, bool PACK> struct alignas(128) FwdShared {
     static constexpr int kPitch = Row<T, WIDE>::kPitch;
     alignas(128) unsigned char in[3][kState][kPitch];  // x, r, i: brought anew once the block has its a and b
@@ -516,8 +517,9 @@ __global__ void __launch_bounds__(256) linear_keep_kernel(const float *init, flo
 //     dlam = sigmoid(lam) / softplus(lam) sum psi
 // (psi rather than dL/dw, which has 1 / sqrt(1 - a^2): w over it goes to zero with w.) h_{t-1} is formed again from the state that
 // enters each kState tokens, which are a block's; the warps and blocks lie one before the other in time.
-// Bound by the issue slots (59 %, with 16 warps an SM) before HBM (14 bytes a token and channel in bf16, 11 from 8 bits): B4 L2048
-// D5120 143 us, 4.1 TB/s, and 157 from 8 bits. Five numbers a token wait in registers for the exchange: so runs of 8 tokens.
+// Bound by latency at 16 warps an SM, with 60 % of the issue slots and half of HBM's peak in use (14 bytes a token and channel in bf16, 11
+// from 8 bits): B4 L2048 D5120 146 us, 4.0 TB/s, and 155 from 8 bits. Five numbers a token (a, b, f, e^-r and d) wait in registers for the
+// exchange: so runs of 8 tokens. The 128 registers that two blocks an SM leave spill 4 to 52 bytes a thread, most where rows go by words.
 template <typename T, bool WIDE, bool PACK> struct alignas(128) BwdShared {
     static constexpr int kPitch = PACK ? Row<int8_t, WIDE>::kPitch : Row<T, WIDE>::kPitch;
     alignas(128) unsigned char in[3][kState][kPitch];                     // x, r, i
@@ -792,8 +794,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bwd_per_sm<T>()) linear_bwd_ke
 
 // --------------------------------------------------------- short sequences
 // Up to kShort tokens, a run of the kernels above: a thread goes over V channels of a whole sequence alone, its tokens in registers;
-// there is nothing to join, and the number of sequences is what fills the device (forward B64 L16 D2560 9.8 us, 14.7 as above; B256 L1
-// D5120 17 and 86; backward 19 and 31, 54 and 225; a single sequence of 16 tokens 4.5 and 4.0, its backward 8.4 and 6.6: the rule goes
+// there is nothing to join, and the number of sequences is what fills the device (forward B64 L16 D2560 10.4 us, 14.7 as above; B256 L1
+// D5120 18 and 86; backward 20 and 31, 53 and 225; a single sequence of 16 tokens 4.7 and 4.0, its backward 8.6 and 6.6: the rule goes
 // by the padded length alone, so that neither results nor times of a sequence hang on how many there are). 64 sequences of 17 tokens
 // take 21 and 39 us. The forward gives bitwise what the kernel above gives a sequence of as many tokens in a batch padded to more:
 // the gates of its slow form, which `Step::brief` has it take there too, and the final state from the run's (A, H).
@@ -988,7 +990,8 @@ template <typename T, int V, int ROWS> __global__ void __launch_bounds__(256) li
 
 // ------------------------------------------------------------------- 8 bits
 // A warp takes 32 V channels of one group of tokens, a lane 16 bytes of each row where rows are multiples of that. Bound by HBM: at
-// B8 L2048 D2560 in bf16 22 us each way, 5.8 TB/s (41 us with one channel an instruction, whose registers left an SM one block).
+// B8 L2048 D2560 in bf16 22 us each way, 5.8 TB/s, in float32 36 and 35, 6.0 TB/s (bf16 41 us with one channel an instruction, whose
+// registers left an SM one block).
 template <typename T, int V> __global__ void __launch_bounds__(32 * kPackWarps, 2) pack8_kernel(Pack8Args p) {
     pdl_enter();
     const int64_t c0 = ((int64_t)blockIdx.y * 32 + (threadIdx.x & 31)) * V, b = blockIdx.z, D = p.D;
